@@ -499,7 +499,7 @@ def _power_of_two(e):
 
 
 def _to_8bit(x, u, root):
-    """E4M3 values and block scales of x: rounded down or up by chance u, without bias."""
+    """E4M3 values and block scales of x: rounded down or up by chance u, x (a root: its square) unbiased."""
     n = x.numel()
     b = torch.nn.functional.pad(x, (0, -n % _BLOCK)).view(-1, _BLOCK)
     top = b.abs().amax(1)
@@ -509,9 +509,14 @@ def _to_8bit(x, u, root):
     inv = torch.where(some, (_FMAX / top.double().clamp_min(1e-300)).float(), 0.0)
     t = (b * inv[:, None]).view(-1)[:n]
     e = torch.frexp(t.abs()).exponent.clamp_min(-5) - 4  # the step between E4M3 values is 2^e
-    k = torch.floor(t * _power_of_two(-e) + u)
+    t = t * _power_of_two(-e)
     if root:
+        k = torch.floor(t)
+        odd = 2 * k + 1  # up with the chance (t^2 - k^2) / ((k + 1)^2 - k^2)
+        k = k + ((t - k) * (t + k) + u * odd >= odd)
         k = torch.where(x > 0, k.clamp_min(1.0), k)  # a positive root stays positive
+    else:
+        k = torch.floor(t + u)
     return (k * _power_of_two(e)).clamp(-_FMAX, _FMAX).to(torch.float8_e4m3fn), scale
 
 
