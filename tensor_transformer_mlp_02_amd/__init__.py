@@ -497,3 +497,9 @@ def tp_mlp_shard_bwd_fp8(desc, dYq, dYq_t, Xq_t, Hq_t, Aq, Auq, Bq, Z_save, scal
                 (dA_up, n["dA"], "dA_up"), (dB, n["dB"], "dB"), (dZq, zq, "dZq"),
                 (dZq_t, zq, "dZq_t"), (dz_amax, 4, "dz_amax", "float32")])
     return _check(lib().tp_mlp_shard_bwd_fp8(ctypes.byref(d), *p, _stream(stream)))
+
+
+from .block import *  # noqa: E402,F401,F403  (the operators around the products)
+from .block import __all__ as _block_all  # noqa: E402
+
+__all__ += _block_all

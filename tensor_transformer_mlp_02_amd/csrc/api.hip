@@ -10,6 +10,7 @@
 #include <string>
 #include <vector>
 
+#include "checks.h"
 #include "common.h"
 #include "launch.h"
 
@@ -18,6 +19,10 @@ using namespace tpmlp;
 namespace {
 
 thread_local std::string g_last_error;
+
+}  // namespace
+
+namespace tpmlp {
 
 int fail(int status, const char* fmt, ...) {
   char buf[512];
@@ -35,12 +40,6 @@ int ok() {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Buf {
-  const void* p;
-  size_t bytes;
-  const char* name;
-};
 
 bool overlap(const Buf& a, const Buf& b) {
   if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
@@ -74,7 +73,7 @@ int check_ptrs(const Buf* bufs, int n, bool required) {
 }
 
 // per-device gfx950 check, cached: 0 unknown, 1 yes, 2 no
-std::atomic<int> g_arch[64];
+static std::atomic<int> g_arch[64];
 
 int check_device() {
   int dev = -1;
@@ -98,15 +97,33 @@ int hip_fail(hipError_t e, const char* what) {
   return fail(TP_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-constexpr int64_t kMaxDim = (int64_t)1 << 30;
+// buffers that are required only when they hold something
+int check_sized(const Buf* bufs, int n) {
+  for (int i = 0; i < n; ++i) {
+    if (bufs[i].bytes == 0) continue;
+    if (!bufs[i].p) return fail(TP_ERR_NULL, "%s is NULL", bufs[i].name);
+    if (!aligned16(bufs[i].p)) return fail(TP_ERR_ALIGN, "%s is not 16-byte aligned", bufs[i].name);
+  }
+  return TP_OK;
+}
+// index / weight tables (int32 or fp32 elements): 4-byte alignment
+int check_tables(const Buf* bufs, int n) {
+  for (int i = 0; i < n; ++i) {
+    if (bufs[i].bytes == 0) continue;
+    if (!bufs[i].p) return fail(TP_ERR_NULL, "%s is NULL", bufs[i].name);
+    if (reinterpret_cast<uintptr_t>(bufs[i].p) & 3u)
+      return fail(TP_ERR_ALIGN, "%s is not 4-byte aligned", bufs[i].name);
+  }
+  return TP_OK;
+}
+
+}  // namespace tpmlp
+
+namespace {
+
 // tokens of the FP8 backward: its weight-gradient GEMMs contract over the
 // tokens of K-contiguous code rows, 256 rows x N bytes per 32-bit tile offset
 constexpr int64_t kMaxFp8Tokens = (int64_t)1 << 22;
-// Largest leading dimension (H, and the Z_save width 2 F_shard): the bf16
-// kernels address one 256-row tile through 32-bit buffer offsets, so
-// 256 rows x ld x 2 bytes must stay below 2^31.
-constexpr int64_t kMaxLd = (int64_t)1 << 21;
-
 struct Shard {
   int64_t N, H, Ft;
   int act, dtype;
@@ -154,17 +171,20 @@ GemmArgs dense_args(int M, int N, int K) {
 thread_local std::vector<hipEvent_t> g_events;
 thread_local size_t g_events_used = 0;
 
-template <typename F>
-hipError_t timed(hipStream_t st, F&& launch) {
-  if (g_events_used + 2 > g_events.size()) return launch();
-  hipError_t he = hipEventRecord(g_events[g_events_used], st);
-  if (he != hipSuccess) return he;
-  he = launch();
-  if (he != hipSuccess) return he;
-  he = hipEventRecord(g_events[g_events_used + 1], st);
-  if (he == hipSuccess) g_events_used += 2;
+}  // namespace
+
+namespace tpmlp {
+
+bool timing_armed() { return g_events_used + 2 <= g_events.size(); }
+hipError_t timing_mark(hipStream_t st, bool end) {
+  hipError_t he = hipEventRecord(g_events[g_events_used + (end ? 1 : 0)], st);
+  if (he == hipSuccess && end) g_events_used += 2;
   return he;
 }
+
+}  // namespace tpmlp
+
+namespace {
 
 hipError_t run_gemm(int dtype, GemmKind kind, GemmArgs& g, hipStream_t st) {
   return timed(st, [&] { return dtype == TP_BF16 ? gemm_bf16(kind, g, st) : gemm_f32(kind, g, st); });
@@ -222,25 +242,6 @@ size_t dz_bytes(const Shard& s) {
 
 }  // namespace
 
-// buffers that are required only when they hold something
-int check_sized(const Buf* bufs, int n) {
-  for (int i = 0; i < n; ++i) {
-    if (bufs[i].bytes == 0) continue;
-    if (!bufs[i].p) return fail(TP_ERR_NULL, "%s is NULL", bufs[i].name);
-    if (!aligned16(bufs[i].p)) return fail(TP_ERR_ALIGN, "%s is not 16-byte aligned", bufs[i].name);
-  }
-  return TP_OK;
-}
-// index / weight tables (int32 or fp32 elements): 4-byte alignment
-int check_tables(const Buf* bufs, int n) {
-  for (int i = 0; i < n; ++i) {
-    if (bufs[i].bytes == 0) continue;
-    if (!bufs[i].p) return fail(TP_ERR_NULL, "%s is NULL", bufs[i].name);
-    if (reinterpret_cast<uintptr_t>(bufs[i].p) & 3u)
-      return fail(TP_ERR_ALIGN, "%s is not 4-byte aligned", bufs[i].name);
-  }
-  return TP_OK;
-}
 int check_rows(int32_t dtype, int64_t N, int64_t H, int64_t R) {
   if (dtype != TP_F32 && dtype != TP_BF16) return fail(TP_ERR_DTYPE, "unknown dtype %d", dtype);
   if (N < 0 || R < 0 || H <= 0) return fail(TP_ERR_SHAPE, "N, R must be >= 0 and H > 0");

@@ -1,0 +1,319 @@
+"""Routing on the GPU against the 64-bit definition (oracle/block.py).
+
+Experts and tables are whole numbers and have to be equal.  Weights and
+gradients are fp32 results of exponentials: exp(x) of a rounded argument is
+off by |x| 2^-24 relative and a few roundings, sums of E terms by E 2^-24 at
+most, so an element may be off by half a step of its type plus
+(2 max|l| + E / 4 + 64) 2^-24 of the magnitudes of its terms (twice that
+where scores are divided by their sum once more)."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+import tensor_transformer_mlp_02_amd as tp  # noqa: E402
+from oracle import block as ob  # noqa: E402
+
+F32, BF16 = torch.float32, torch.bfloat16
+HALF = {BF16: 2.0 ** -8, F32: 2.0 ** -24}
+INF = float("inf")
+
+
+def desc(N, E, K, groups=1, kept=1, best=1, sigmoid=False, renorm=False, dtype=F32, scale=1.0):
+    return dict(N=N, E=E, K=K, groups=groups, groups_kept=kept, group_best=best, score=int(sigmoid),
+                renorm=int(renorm), dtype=int(dtype == BF16), scale=scale)
+
+
+def forward(d, logits, bias):
+    e = torch.full((d["N"], d["K"]), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((d["N"], d["K"]), float("nan"), device="cuda")
+    tp.tp_moe_route_fwd(d, logits, bias, e, w)
+    return e, w
+
+
+def want_forward(d, logits, bias):
+    return ob.route_fwd(logits.double().cpu().numpy(), None if bias is None else bias.cpu().numpy(), d["K"],
+                        d["groups"], d["groups_kept"], d["group_best"], bool(d["score"]), bool(d["renorm"]),
+                        float(np.float32(d["scale"])))
+
+
+def gamma(d, logits):
+    l = logits.double().cpu().numpy()
+    l = np.abs(np.where(np.isfinite(l) & (l > ob.LOWEST), l, 0.0))
+    top = np.minimum(l.max(initial=0.0), 104.0)  # exponentials of less are zero in fp32
+    return (2 * top + d["E"] / 4 + 64) * 2.0 ** -24 * (2 if d["renorm"] else 1)
+
+
+def check_forward(d, logits, bias):
+    e, w = forward(d, logits, bias)
+    we, ww = want_forward(d, logits, bias)
+    assert np.array_equal(e.cpu().numpy(), we), np.argwhere(e.cpu().numpy() != we)[:5]
+    got = w.double().cpu().numpy()
+    tol = (2.0 ** -24 + gamma(d, logits)) * np.abs(ww) + 1e-37
+    assert (np.abs(got - ww) <= tol).all(), np.abs(got - ww).max()
+    return e, w
+
+
+def check_backward(d, logits, expert, up, rows=None):
+    """up [N,K]: the weights' gradient; rows: the slots' rows, with the gradient given by rows."""
+    N, E = d["N"], d["E"]
+    dtype = logits.dtype
+    out = torch.full((N, E), float("nan"), dtype=dtype, device="cuda")
+    if rows is None:
+        tp.tp_moe_route_bwd(d, logits, expert, up, None, 0, out)
+        up_np = up.double().cpu().numpy()
+    else:
+        by_row, slot_row, R = rows
+        tp.tp_moe_route_bwd(d, logits, expert, by_row, slot_row, R, out)
+        r = slot_row.cpu().numpy()
+        v = np.append(by_row.double().cpu().numpy(), 0.0)
+        up_np = v[np.where((r >= 0) & (r < R), r, len(v) - 1)]
+    l, ex, scale = logits.double().cpu().numpy(), expert.cpu().numpy(), float(np.float32(d["scale"]))
+    sig, ren = bool(d["score"]), bool(d["renorm"])
+    want = ob.route_bwd(l, ex, up_np, sig, ren, scale)
+    s, _ = ob.scores(l, sig)
+    # magnitudes of the terms
+    mds = np.zeros((N, E))
+    for t in range(N):
+        on = [j for j in range(ex.shape[1]) if 0 <= ex[t, j] < E]
+        total = sum(s[t, ex[t, j]] for j in on) + 1e-20
+        mean = sum(abs(scale * up_np[t, j]) * s[t, ex[t, j]] for j in on) / total
+        for j in on:
+            mds[t, ex[t, j]] += (abs(scale * up_np[t, j]) + mean) / total if ren else abs(scale * up_np[t, j])
+    mag = s * mds if sig else s * (mds + (mds * s).sum(1, keepdims=True))
+    got = out.double().cpu().numpy()
+    tol = HALF[dtype] * np.abs(want) + 2 * gamma(d, logits) * mag + 1e-37
+    assert (np.abs(got - want) <= tol).all(), (np.abs(got - want) / tol).max()
+    return out
+
+
+def inputs(N, E, dtype=F32, bias=False, masked=False, seed=0, std=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    l = torch.randn(N, E, generator=g, device="cuda") * std
+    if masked:
+        l[torch.rand(N, E, generator=g, device="cuda") < 0.3] = -INF
+        l[torch.rand(N, generator=g, device="cuda") < 0.1] = -INF
+    b = torch.randn(E, generator=g, device="cuda") * 0.1 if bias else None
+    return l.to(dtype), b
+
+
+CONFIGS = [  # E, K, groups, kept, best
+    (1, 1, 1, 1, 1), (2, 2, 1, 1, 1), (8, 2, 1, 1, 1), (60, 4, 1, 1, 1), (64, 2, 1, 1, 1), (64, 6, 8, 3, 2),
+    (65, 3, 1, 1, 1), (100, 5, 10, 2, 1), (128, 8, 1, 1, 1), (160, 6, 8, 3, 1), (256, 8, 8, 4, 2),
+    (256, 32, 64, 9, 2), (320, 8, 32, 8, 2), (384, 8, 1, 1, 1), (500, 10, 20, 5, 2), (512, 8, 16, 4, 2), (512, 1, 1, 1, 1),
+    (1000, 7, 1, 1, 1), (1024, 32, 32, 8, 2), (64, 2, 64, 2, 1), (64, 2, 64, 2, 2)]
+
+
+@pytest.mark.parametrize("E,K,groups,kept,best", CONFIGS)
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_forward_and_backward(E, K, groups, kept, best, sigmoid, dtype):
+    for k, (bias, masked, renorm) in enumerate([(False, False, False), (True, False, True), (True, True, True),
+                                                (False, True, False)]):
+        N = 37 + k
+        d = desc(N, E, K, groups, kept, best, sigmoid, renorm, dtype, scale=2.5)
+        l, b = inputs(N, E, dtype, bias, masked, seed=E + k)
+        e, _ = check_forward(d, l, b)
+        g = torch.Generator(device="cuda").manual_seed(k)
+        check_backward(d, l, e, torch.randn(N, K, generator=g, device="cuda"))
+
+
+@pytest.mark.parametrize("N", [0, 1, 2, 3, 4, 5, 63, 64, 65, 1025])
+def test_token_counts(N):
+    d = desc(N, 64, 2, dtype=BF16, renorm=True)
+    l, _ = inputs(N, 64, BF16)
+    e, _ = check_forward(d, l, None)
+    check_backward(d, l, e, torch.ones(N, 2, device="cuda") * torch.arange(2, device="cuda"))
+
+
+def test_many_tokens_past_the_grid():
+    d = desc(70001, 16, 2, sigmoid=True)
+    l, b = inputs(70001, 16, bias=True)
+    e, w = forward(d, l, b)
+    key = (torch.sigmoid(l.double()) + b.double())
+    val, idx = key.sort(dim=1, descending=True, stable=True)
+    assert torch.equal(e.long(), idx[:, :2])
+    torch.testing.assert_close(w, torch.sigmoid(l.double()).gather(1, idx[:, :2]).float(), rtol=1e-6, atol=0)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("groups", [1, 8])
+def test_equal_values_go_to_the_lower_expert(sigmoid, groups):
+    N, E = 50, 64
+    l = torch.randint(0, 3, (N, E), device="cuda").float()
+    for bias in (None, torch.zeros(E, device="cuda"), torch.randint(0, 2, (E,), device="cuda") * 0.5):
+        check_forward(desc(N, E, 8, groups, min(groups, 3), 2, sigmoid), l, bias)
+    l[:] = 1.0
+    e, _ = check_forward(desc(N, E, 8, groups, min(groups, 3), 2, sigmoid), l, None)
+    assert (e == torch.arange(8, device="cuda", dtype=torch.int32)).all()
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_close_values_are_told_apart(sigmoid):
+    """Choice scores that differ by less than fp32 can hold: as in 64 bits."""
+    N, E = 64, 64
+    g = torch.Generator(device="cuda").manual_seed(4)
+    l = 1.0 + torch.randint(0, 8, (N, E), generator=g, device="cuda") * 2.0 ** -23
+    bias = torch.randint(0, 4, (E,), generator=g, device="cuda").float() * 2.0 ** -27
+    check_forward(desc(N, E, 8, sigmoid=sigmoid), l, bias)
+    check_forward(desc(N, E, 8, 8, 3, 2, sigmoid=sigmoid), l, bias)
+    check_forward(desc(N, E, 8, sigmoid=sigmoid), l, None)
+    # saturated scores: without a bias the logits' own order holds
+    l = 40.0 + torch.rand(N, E, generator=g, device="cuda") * 40
+    check_forward(desc(N, E, 8, sigmoid=sigmoid), l, None)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_masked_infinite_and_nan_logits(sigmoid, renorm, dtype):
+    N, E, K = 8, 16, 4
+    l, b = inputs(N, E, bias=True)
+    low = float(torch.finfo(dtype).min)
+    l[0] = -INF
+    l[1] = low
+    l[2] = float("nan")
+    l[3, 1:] = -INF
+    l[4, ::2] = low
+    l[5, 3] = INF
+    l[5, 9] = INF
+    l[6, 5] = float("nan")
+    l[7] = 3e38
+    l = l.to(dtype)
+    for bias in (None, b):
+        for groups, kept in ((1, 1), (4, 2)):
+            d = desc(N, E, K, groups, kept, 2, sigmoid, renorm, dtype)
+            e, w = check_forward(d, l, bias)
+            assert (e[:3] == -1).all() and (w[:3] == 0).all()
+            assert e[3, 0] == 0 and (e[3, 1:] == -1).all()
+            out = check_backward(d, l, e, torch.ones(N, K, device="cuda"))
+            assert (out[:3] == 0).all()
+
+
+def test_wide_ranges_of_logits():
+    for std in (1e-6, 30.0, 1e4):
+        for sigmoid in (False, True):
+            for renorm in (False, True):
+                d = desc(65, 96, 5, sigmoid=sigmoid, renorm=renorm)
+                l, _ = inputs(65, 96, std=std, seed=int(std) + 1)
+                e, _ = check_forward(d, l, None)
+                check_backward(d, l, e, torch.ones(65, 5, device="cuda") * torch.arange(5, device="cuda"))
+
+
+def test_backward_takes_any_table():
+    """The same expert twice, experts out of range, rows out of range."""
+    N, E, K = 6, 20, 4
+    l, _ = inputs(N, E)
+    e = torch.tensor([[3, 3, 5, 7], [-1, 25, 4, 4], [19, 0, 1, 2], [9, 9, 9, 9], [-5, -5, 20, 99], [1, 2, 3, 4]],
+                     dtype=torch.int32, device="cuda")
+    up = torch.randn(N, K, device="cuda")
+    slot = torch.tensor([[0, 1, 2, 3], [4, 5, 6, 7], [-1, 40, 8, 9], [1, 1, 1, 1], [0, 0, 0, 0],
+                         [-2147483648, 2147483647, 11, 12]], dtype=torch.int32, device="cuda")
+    by_row = torch.randn(13, device="cuda")
+    for sigmoid in (False, True):
+        for renorm in (False, True):
+            d = desc(N, E, K, sigmoid=sigmoid, renorm=renorm, scale=1.5)
+            check_backward(d, l, e, up)
+            check_backward(d, l, e, up, rows=(by_row, slot, 13))
+
+
+def tables(N, K, first, n_local, R, e, w, spare=0):
+    i = dict(dtype=torch.int32, device="cuda")
+    o = dict(offsets=torch.full((n_local + 1 + spare,), -9, **i), row_token=torch.full((R + spare,), -9, **i),
+             row_weight=None if w is None else torch.full((R + spare,), float("nan"), device="cuda"),
+             tok_ptr=torch.full((N + 1 + spare,), -9, **i), tok_rows=torch.full((R + spare,), -9, **i),
+             slot_row=torch.full((N + spare, K), -9, **i))
+    nb = tp.tp_moe_route_tables_workspace(N, K, n_local)
+    ws = torch.full((max(nb, 16),), 0x5a, dtype=torch.uint8, device="cuda")
+    tp.tp_moe_route_tables(N, K, first, n_local, R, e, w, *o.values(), ws, nb)
+    return o
+
+
+@pytest.mark.parametrize("N", [0, 1, 2, 7, 64, 255, 256, 257, 1000, 5003])
+@pytest.mark.parametrize("E,K,first,n_local", [(64, 2, 0, 8), (64, 2, 56, 8), (8, 1, 0, 8), (256, 8, 32, 64), (60, 3, 7, 1),
+                                               (1024, 32, 0, 1024), (100, 5, 90, 40)])
+def test_tables(N, E, K, first, n_local):
+    g = torch.Generator(device="cuda").manual_seed(N + E)
+    e = torch.rand(N, E, generator=g, device="cuda").topk(K, dim=1).indices.to(torch.int32) if N else \
+        torch.empty(0, K, dtype=torch.int32, device="cuda")
+    if N > 3:
+        e[1] = -1
+        e[2, 0] = e[2, K - 1]                 # the same expert twice
+        e[3, 0] = 2147483647
+        e[N - 1, 0] = -2147483648
+    w = torch.rand(N, K, generator=g, device="cuda")
+    R = N * K + 5
+    got = tables(N, K, first, n_local, R, e, w, spare=3)
+    want = ob.route_tables(e.cpu().numpy(), w.cpu().numpy(), first, n_local, R)
+    for k, v in want.items():
+        n = len(v)
+        assert np.array_equal(got[k][:n].cpu().numpy(), v), k
+        rest = got[k][n:]
+        assert (torch.isnan(rest).all() if k == "row_weight" else (rest == -9).all()), k   # left alone
+    got = tables(N, K, first, n_local, N * K, e, None)
+    assert np.array_equal(got["slot_row"].cpu().numpy(), want["slot_row"])
+
+
+def test_tables_when_every_token_takes_one_expert():
+    N, K = 3000, 4
+    e = torch.full((N, K), 5, dtype=torch.int32, device="cuda")
+    got = tables(N, K, 0, 8, N * K, e, None)
+    assert got["offsets"].tolist() == [0] * 6 + [N * K] * 3
+    assert torch.equal(got["slot_row"].view(-1), torch.arange(N * K, dtype=torch.int32, device="cuda"))
+    assert torch.equal(got["tok_rows"], torch.arange(N * K, dtype=torch.int32, device="cuda"))
+
+
+def test_two_calls_at_once_on_two_streams():
+    N, E, K = 4096, 256, 8
+    work = []
+    for k in range(2):
+        l, b = inputs(N, E, bias=True, seed=k)
+        work.append((desc(N, E, K, 8, 4, 2, True, True), l, b, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = []
+    for d, l, b, s in work:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            e, w = forward(d, l, b)
+            outs.append((e, w, tables(N, K, 0, 64, N * K, e, w)))
+    torch.cuda.synchronize()
+    for (d, l, b, _), (e, w, t) in zip(work, outs):
+        e2, w2 = forward(d, l, b)
+        assert torch.equal(e, e2) and torch.equal(w, w2)
+        t2 = tables(N, K, 0, 64, N * K, e2, w2)
+        for k in t:
+            assert torch.equal(t[k], t2[k]), k
+
+
+def test_captured_graph_follows_the_logits():
+    N, E, K = 700, 64, 6
+    d = desc(N, E, K, 8, 3, 2, True, True)
+    l, b = inputs(N, E, bias=True)
+    e, w = forward(d, l, b)
+    i = dict(dtype=torch.int32, device="cuda")
+    t = dict(offsets=torch.empty(17, **i), row_token=torch.empty(N * K, **i),
+             row_weight=torch.empty(N * K, device="cuda"), tok_ptr=torch.empty(N + 1, **i),
+             tok_rows=torch.empty(N * K, **i), slot_row=torch.empty(N, K, **i))
+    nb = tp.tp_moe_route_tables_workspace(N, K, 16)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    dl = torch.empty(N, E, device="cuda")
+    up = torch.randn(N * K, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tp.tp_moe_route_fwd(d, l, b, e, w)
+        tp.tp_moe_route_tables(N, K, 16, 16, N * K, e, w, *t.values(), ws, nb)
+        tp.tp_moe_route_bwd(d, l, e, up, t["slot_row"], N * K, dl)
+    for seed in (1, 2, 3):
+        l.copy_(inputs(N, E, seed=seed)[0])
+        graph.replay()
+        torch.cuda.synchronize()
+        e2, w2 = forward(d, l, b)
+        assert torch.equal(e, e2) and torch.equal(w, w2)
+        t2 = tables(N, K, 16, 16, N * K, e2, w2)
+        for k in t:
+            assert torch.equal(t[k], t2[k]), k
+        check_backward(d, l, e, None, rows=(up, t["slot_row"], N * K))
+        dl2 = torch.empty_like(dl)
+        tp.tp_moe_route_bwd(d, l, e, up, t["slot_row"], N * K, dl2)
+        assert torch.equal(dl, dl2)
