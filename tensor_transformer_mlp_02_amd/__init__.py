@@ -152,35 +152,56 @@ def _ptr(t, nbytes: Optional[int] = None, name: str = "tensor",
     when nbytes is given, hold at least that many bytes; tables and scale
     buffers (dtype "int32" / "float32") must hold that element type, since
     the library reads their bytes as such."""
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
-    if dtype is not None and str(getattr(t, "dtype", "")) != f"torch.{dtype}":
+    return _address(t, nbytes, name, dtype, _current_device())
+
+
+def _current_device() -> int:
+    """The current GPU, -1 where there is none."""
+    import torch
+    # the C function behind torch.cuda.current_device(), without its checks
+    # on every call: a process that holds a GPU tensor is initialised
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+
+
+def _address(t, nbytes, name, dtype, device) -> int:
+    if dtype is not None and str(getattr(t, "dtype", "")) != _DTYPE_NAMES[dtype]:
         raise ValueError(f"{name} must be a torch.{dtype} tensor, got {getattr(t, 'dtype', None)}")
     if not getattr(t, "is_cuda", False):
         raise ValueError(f"{name} must be a GPU tensor, got one on {t.device}")
-    import torch
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if nbytes is not None and t.numel() * t.element_size() < nbytes:
-        raise ValueError(f"{name} holds {t.numel() * t.element_size()} bytes, "
-                         f"{nbytes} needed")
+    if nbytes is not None and t.nbytes < nbytes:
+        raise ValueError(f"{name} holds {t.nbytes} bytes, {nbytes} needed")
     return t.data_ptr()
+
+
+_DTYPE_NAMES = {n: f"torch.{n}" for n in ("int32", "float32", "bfloat16")}
 
 
 def _sized(items):
     """_ptr of each (tensor, bytes, name) or (tensor, bytes, name, dtype)."""
-    return [_ptr(*it) for it in items]
+    device = None
+    out = []
+    for t, nbytes, name, *dtype in items:
+        if t is not None and not isinstance(t, int):
+            if device is None:
+                device = _current_device()
+            t = _address(t, nbytes, name, dtype[0] if dtype else None, device)
+        out.append(t)
+    return out
 
 
 def _stream(stream) -> Optional[int]:
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
     import torch
+    if torch.cuda.is_initialized():
+        # the current stream's handle itself (torch.cuda.current_stream() builds an object)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if torch.cuda.is_available():
         return torch.cuda.current_stream().cuda_stream
     return None

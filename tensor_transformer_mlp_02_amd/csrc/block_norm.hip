@@ -17,6 +17,11 @@ namespace tpmlp {
 namespace norm {
 
 constexpr int NT = 256;
+// Threads in flight for each of the 256 compute units where workgroups walk
+// over rows: 512 (8 wavefronts with the next row requested ahead).  Forward,
+// 4096 x 8192 bf16: 53 us at 512 threads, 55 at 1024, 57 at 2048, 74 with a
+// workgroup for each row; 1500 x 5120: 16.2, 17.5, 19.9 us.
+constexpr int CU_THREADS = 512, CUS = 256;
 
 // one 16-byte piece of a row as floats
 template <typename T> struct Piece;
@@ -55,6 +60,237 @@ __device__ __forceinline__ float block_sum(float x, float* red) {
 #pragma unroll
   for (int w = 0; w < NT / 64; ++w) t += red[w];
   return t;
+}
+
+// ---------------------------------------------------------------------------
+// Rows that stay in registers: TPR threads share a row, P 16-byte pieces
+// each, so that every tensor is read from memory once.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint4 load_raw(const void* p, int64_t piece) {
+  return reinterpret_cast<const uint4*>(p)[piece];
+}
+template <typename T>
+__device__ __forceinline__ void store_piece(void* p, int64_t piece, const float v[Piece<T>::V]) {
+  Piece<T>::store(p, piece * Piece<T>::V, v);
+}
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& r, float v[Piece<T>::V]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  if constexpr (Piece<T>::V == 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
+  }
+}
+
+// sum over a wavefront, in every lane: data-parallel moves within rows of
+// 16 lanes and across them, without a trip through shared memory
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float x) {
+  const int y = __builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, ROWS, 0xf, true);
+  return x + __int_as_float(y);
+}
+__device__ __forceinline__ float wave_total(float x) {
+  x = dpp_add<0x111, 0xf>(x);  // row_shr:1, 2, 4, 8
+  x = dpp_add<0x112, 0xf>(x);
+  x = dpp_add<0x114, 0xf>(x);
+  x = dpp_add<0x118, 0xf>(x);
+  x = dpp_add<0x142, 0xa>(x);  // row_bcast:15 into rows 1 and 3
+  x = dpp_add<0x143, 0xc>(x);  // row_bcast:31 into rows 2 and 3
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
+}
+
+template <int TPR>
+struct Rows {
+  static constexpr int THREADS = TPR < 256 ? 256 : TPR;
+  static constexpr int AT_ONCE = THREADS / TPR;  // rows of a workgroup
+};
+
+// K sums over the threads of each row.  `red` has two halves used in turn:
+// one barrier a call, since a wavefront that writes a half again has passed
+// the barrier behind every read of it.
+template <int TPR, int K, int THREADS = Rows<TPR>::THREADS>
+__device__ __forceinline__ void row_sums(float (&v)[K], float* red, int& half) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = wave_total(v[k]);
+  if constexpr (TPR > 64) {
+    constexpr int W = TPR / 64;
+    const int wave = threadIdx.x >> 6;
+    float* mine = red + half * (THREADS / 64) * K;
+    half ^= 1;
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+      for (int k = 0; k < K; ++k) mine[wave * K + k] = v[k];
+    __syncthreads();
+    const float* row = mine + (wave / W) * W * K;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float t = row[k];
+#pragma unroll
+      for (int w = 1; w < W; ++w) t += row[w * K + k];
+      v[k] = t;
+    }
+  }
+}
+
+// The weights are kept in registers over a workgroup's rows, and the next
+// row is requested before the present one is summed.  HBM-bound: 4096 x 8192
+// bf16 with both norms and a gate 53 us, 5.1 TB/s, the rate of a large copy;
+// non-temporal loads or stores change nothing.
+template <typename T, bool LAYER, int TPR, int P>
+__global__ __launch_bounds__(Rows<TPR>::THREADS) void fwd_kernel(NormFwdArgs A) {
+  constexpr int V = Piece<T>::V, R = Rows<TPR>::AT_ONCE;
+  __shared__ float red[2 * (Rows<TPR>::THREADS / 64)];
+  int half = 0;
+  const int tr = threadIdx.x % TPR, rg = threadIdx.x / TPR;
+  const int pieces = A.H / V;
+  const float inv_h = 1.0f / (float)A.H;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  bool in[P];
+  uint4 w_post[P], b_post[P], gate[P], w_pre[P], b_pre[P], x[P], o[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int c = tr + p * TPR;
+    in[p] = c < pieces;
+    w_post[p] = A.w_post && in[p] ? load_raw(A.w_post, c) : zero;
+    b_post[p] = A.b_post && in[p] ? load_raw(A.b_post, c) : zero;
+    gate[p] = A.G == 1 && in[p] ? load_raw(A.gate, c) : zero;
+    w_pre[p] = A.w_pre && in[p] ? load_raw(A.w_pre, c) : zero;
+    b_pre[p] = A.b_pre && in[p] ? load_raw(A.b_pre, c) : zero;
+    x[p] = o[p] = zero;
+  }
+  const int64_t stride = (int64_t)gridDim.x * R;
+  auto request = [&](int64_t n, uint4 (&xx)[P], uint4 (&oo)[P]) {
+    if (n >= A.N) return;
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+      if (in[p]) {
+        xx[p] = load_raw(A.X, n * pieces + tr + p * TPR);
+        if (A.O) oo[p] = load_raw(A.O, n * pieces + tr + p * TPR);
+      }
+  };
+  const int64_t first = (int64_t)blockIdx.x * R;
+  request(first + rg, x, o);
+  for (int64_t base = first; base < A.N; base += stride) {
+    const int64_t n = base + rg;
+    const bool live = n < A.N;
+    uint4 xn[P], on[P], gt[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      xn[p] = on[p] = zero;
+      gt[p] = gate[p];
+    }
+    if (A.G > 1 && live) {
+      const int64_t g = (int64_t)((uint32_t)n % (uint32_t)A.G) * pieces;
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        if (in[p]) gt[p] = load_raw(A.gate, g + tr + p * TPR);
+    }
+    request(n + stride, xn, on);
+    float mo = 0.f, ro = 1.f;
+    if (A.w_post) {
+      if constexpr (LAYER) {
+        float s[1] = {0.f};
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          float t[V];
+          unpack<T>(o[p], t);
+#pragma unroll
+          for (int i = 0; i < V; ++i) s[0] += t[i];
+        }
+        row_sums<TPR>(s, red, half);
+        mo = s[0] * inv_h;
+      }
+      float s[1] = {0.f};
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        float t[V];
+        unpack<T>(o[p], t);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[0] += in[p] || !LAYER ? (t[i] - mo) * (t[i] - mo) : 0.f;
+      }
+      row_sums<TPR>(s, red, half);
+      ro = 1.0f / sqrtf(s[0] * inv_h + A.eps);
+      if (A.stat_post && tr == 0 && live) {
+        A.stat_post[n] = ro;
+        if constexpr (LAYER) A.stat_post[A.N + n] = mo;
+      }
+    }
+    float y[P][V];
+    float sy[1] = {0.f}, sq[1] = {0.f};
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      unpack<T>(x[p], y[p]);
+      if (A.O) {
+        float u[V], w[V];
+        unpack<T>(o[p], u);
+        if (A.w_post) {
+          unpack<T>(w_post[p], w);
+#pragma unroll
+          for (int i = 0; i < V; ++i) u[i] = (u[i] - mo) * ro * w[i];
+          if (A.b_post) {
+            unpack<T>(b_post[p], w);
+#pragma unroll
+            for (int i = 0; i < V; ++i) u[i] += w[i];
+          }
+        }
+        if (A.G > 0) {
+          unpack<T>(gt[p], w);
+#pragma unroll
+          for (int i = 0; i < V; ++i) u[i] *= w[i];
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[p][i] = A.a * y[p][i] + A.b * u[i];
+        if (in[p] && live) store_piece<T>(A.Y, n * pieces + tr + p * TPR, y[p]);
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        sy[0] += y[p][i];
+        sq[0] += y[p][i] * y[p][i];
+      }
+    }
+    if (A.w_pre) {
+      float my = 0.f;
+      if constexpr (LAYER) {
+        row_sums<TPR>(sy, red, half);
+        my = sy[0] * inv_h;
+        sq[0] = 0.f;
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int i = 0; i < V; ++i) sq[0] += in[p] ? (y[p][i] - my) * (y[p][i] - my) : 0.f;
+      }
+      row_sums<TPR>(sq, red, half);
+      const float ry = 1.0f / sqrtf(sq[0] * inv_h + A.eps);
+      if (A.stat_pre && tr == 0 && live) {
+        A.stat_pre[n] = ry;
+        if constexpr (LAYER) A.stat_pre[A.N + n] = my;
+      }
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        float w[V];
+        unpack<T>(w_pre[p], w);
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[p][i] = (y[p][i] - my) * ry * w[i];
+        if (A.b_pre) {
+          unpack<T>(b_pre[p], w);
+#pragma unroll
+          for (int i = 0; i < V; ++i) y[p][i] += w[i];
+        }
+        if (in[p] && live) store_piece<T>(A.Hn, n * pieces + tr + p * TPR, y[p]);
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      x[p] = xn[p];
+      o[p] = on[p];
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -276,143 +512,449 @@ __global__ __launch_bounds__(NT) void bwd_wide_rows_kernel(NormBwdArgs A, float*
 // Column sums.  The rows are dealt to W workers by their gate row, so that
 // a worker holds the sums of one gate row at a time:
 //   G <= W: worker w takes gate row w % G and every (W/G)-th of its tokens,
-//           starting at w / G; its gate sum is a partial one
+//           starting at w / G (W is a multiple of G)
 //   G > W:  worker w takes the gate rows w, w + W, ... with all their
-//           tokens; it finishes each by itself
-// (W is rounded down to a multiple of G in the first case.)  The partial
-// sums [5][W][H] are added over w, in order, by reduce_kernel.
+//           tokens; it finishes each gate row's gradient by itself and
+//           keeps b gate A1, b gate A0 summed over its gate rows
+// The partial sums [4][W][H] are added over w, in order, by reduce_kernel.
 // ---------------------------------------------------------------------------
-enum { SUM_W_PRE = 0, SUM_B_PRE = 1, SUM_W_POST = 2, SUM_B_POST = 3, SUM_GATE = 4, SUMS = 5 };
-
-template <typename Row, typename Flush>
-__device__ __forceinline__ void deal_rows(int64_t N, int64_t G, int w, int W, Row&& row,
-                                          Flush&& flush) {
-  if (G <= W) {
-    const int64_t P = W / G;
-    for (int64_t n = w % G + (w / G) * G; n < N; n += P * G) row(n);
-    flush(-1);
-  } else {
-    for (int64_t g = w; g < G; g += W) {
-      for (int64_t n = g; n < N; n += G) row(n);
-      flush(g);
-    }
-  }
-}
+enum { SUM_W_PRE = 0, SUM_B_PRE = 1, SUM_1 = 2, SUM_0 = 3, SUMS = 4 };
 
 template <typename T, bool LAYER>
 __global__ __launch_bounds__(NT) void bwd_wide_columns_kernel(NormBwdArgs A, const float* means) {
   constexpr int V = Piece<T>::V;
   const int c = (blockIdx.x * NT + threadIdx.x) * V;
   if (c >= A.H) return;
-  const int w = blockIdx.y;
+  const int w = blockIdx.y, W = A.workers;
   const int64_t G = A.G > 0 ? A.G : 1;
-  float acc[SUMS][V];
+  const bool many = G > W;
+  float acc[SUMS][V], s_1[V], s_0[V];
 #pragma unroll
-  for (int k = 0; k < SUMS; ++k)
+  for (int i = 0; i < V; ++i) {
+    s_1[i] = s_0[i] = 0.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[k][i] = 0.f;
-  float wpost[V], bpost[V];
+    for (int k = 0; k < SUMS; ++k) acc[k][i] = 0.f;
+  }
+  auto add_row = [&](int64_t n) {
+    const int64_t row = n * A.H;
+    float ry = 0.f, my = 0.f, ro = 1.f, mo = 0.f, D[V];
+    if (A.w_pre) {
+      ry = A.stat_pre[n];
+      if constexpr (LAYER) my = A.stat_pre[A.N + n];
+      float g[V], y[V];
+      Piece<T>::load(A.dH, row + c, g);
+      Piece<T>::load(A.Y, row + c, y);
 #pragma unroll
-  for (int i = 0; i < V; ++i) { wpost[i] = 1.f; bpost[i] = 0.f; }
-  if (A.w_post) Piece<T>::load(A.w_post, c, wpost);
-  if (A.b_post) Piece<T>::load(A.b_post, c, bpost);
-  deal_rows(
-      A.N, G, w, A.workers,
-      [&](int64_t n) {
-        const int64_t row = n * A.H;
-        float ry = 0.f, my = 0.f, ro = 1.f, mo = 0.f, D[V];
-        if (A.w_pre) {
-          ry = A.stat_pre[n];
-          if constexpr (LAYER) my = A.stat_pre[A.N + n];
-          float g[V], y[V];
-          Piece<T>::load(A.dH, row + c, g);
-          Piece<T>::load(A.Y, row + c, y);
+      for (int i = 0; i < V; ++i) {
+        acc[SUM_W_PRE][i] += g[i] * ((y[i] - my) * ry);
+        acc[SUM_B_PRE][i] += g[i];
+      }
+    }
+    if (!A.O) return;
+    d_at<T, LAYER>(A, row, c, ry, my, means[2 * n], means[2 * n + 1], D);
+    float o[V];
+    Piece<T>::load(A.O, row + c, o);
+    if (A.w_post) {
+      ro = A.stat_post[n];
+      if constexpr (LAYER) mo = A.stat_post[A.N + n];
+    }
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            acc[SUM_W_PRE][i] += g[i] * ((y[i] - my) * ry);
-            acc[SUM_B_PRE][i] += g[i];
-          }
-        }
-        if (!A.O) return;
-        d_at<T, LAYER>(A, row, c, ry, my, means[2 * n], means[2 * n + 1], D);
-        float o[V], g[V];
-        Piece<T>::load(A.O, row + c, o);
-        if (A.w_post) {
-          ro = A.stat_post[n];
-          if constexpr (LAYER) mo = A.stat_post[A.N + n];
-        }
+    for (int i = 0; i < V; ++i) {
+      acc[SUM_1][i] += D[i] * ((o[i] - mo) * ro);
+      acc[SUM_0][i] += D[i];
+    }
+  };
+  if (!many) {
+    for (int64_t n = w % G + (w / G) * G; n < A.N; n += (int64_t)W / G * G) add_row(n);
+  } else {
+    float wp[V], bp[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) g[i] = 1.f;
-        if (A.G > 0) Piece<T>::load(A.gate, (n % A.G) * A.H + c, g);
+    for (int i = 0; i < V; ++i) { wp[i] = 1.f; bp[i] = 0.f; }
+    if (A.w_post) Piece<T>::load(A.w_post, c, wp);
+    if (A.b_post) Piece<T>::load(A.b_post, c, bp);
+    for (int64_t g = w; g < G; g += W) {
+      for (int64_t n = g; n < A.N; n += G) add_row(n);
+      float q[V];
+      Piece<T>::load(A.gate, g * A.H + c, q);
+      float* out = A.dgate + g * A.H + c;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float oh = (o[i] - mo) * ro;
-          const float du = A.b * g[i] * D[i];
-          acc[SUM_W_POST][i] += du * oh;
-          acc[SUM_B_POST][i] += du;
-          acc[SUM_GATE][i] += A.b * D[i] * (oh * wpost[i] + bpost[i]);
-        }
-      },
-      [&](int64_t g) {
-        if (g < 0 || !A.dgate) return;
-        float* out = A.dgate + g * A.H + c;
+      for (int i = 0; i < V; ++i) {
+        const float d = A.b * (wp[i] * acc[SUM_1][i] + bp[i] * acc[SUM_0][i]);
+        out[i] = d + (A.accumulate ? out[i] : 0.f);
+        s_1[i] += A.b * q[i] * acc[SUM_1][i];
+        s_0[i] += A.b * q[i] * acc[SUM_0][i];
+        acc[SUM_1][i] = acc[SUM_0][i] = 0.f;
+      }
+    }
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          out[i] = acc[SUM_GATE][i] + (A.accumulate ? out[i] : 0.f);
-          acc[SUM_GATE][i] = 0.f;
-        }
-      });
+    for (int i = 0; i < V; ++i) {
+      acc[SUM_1][i] = s_1[i];
+      acc[SUM_0][i] = s_0[i];
+    }
+  }
 #pragma unroll
   for (int k = 0; k < SUMS; ++k) {
-    if (k == SUM_GATE && (G > A.workers || !A.dgate)) continue;
-    float* out = A.ws + ((int64_t)k * A.workers + w) * A.H + c;
+    float* out = A.ws + ((int64_t)k * W + w) * A.H + c;
 #pragma unroll
     for (int i = 0; i < V; ++i) out[i] = acc[k][i];
   }
 }
 
-// out[c] (+)= sum over the workers, 64 columns and 16 shares of the workers
-// for each workgroup; the gate's rows g take the workers w = g, g + G, ...
-__global__ __launch_bounds__(NT) void reduce_kernel(NormBwdArgs A, int has_rows) {
-  __shared__ float4 part[NT];
-  int k = blockIdx.y;
-  int first = 0, step = 1;
-  float* out;
-  if (k < SUM_GATE) {
-    out = k == SUM_W_PRE ? A.dw_pre : k == SUM_B_PRE ? A.db_pre : k == SUM_W_POST ? A.dw_post
-                                                                               : A.db_post;
-  } else {
-    first = k - SUM_GATE;
-    step = (int)A.G;
-    k = SUM_GATE;
-    out = A.dgate ? A.dgate + (int64_t)first * A.H : nullptr;
+// ---------------------------------------------------------------------------
+// Backward with rows in registers.  Every tensor is read once, all of a
+// row's sums come from one pass: with k = b gate w_post,
+//   S1 = sum p yh, S2 = sum p, and since q = k D is linear in S1 and S2,
+//   sum q oh = sum k oh (dY + r p) - r (S2/H sum k oh + S1/H sum k oh yh),
+//   sum q likewise without oh.
+// Column sums stay in the thread that owns the columns.  The post norm's
+// need only A1 = sum D oh and A0 = sum D of one gate row at a time:
+//   dw_post = b sum_g gate_g A1_g,  dgate_g = b (w_post A1_g + b_post A0_g).
+// ---------------------------------------------------------------------------
+template <int TPR>
+struct BwdRows {
+  static constexpr int THREADS = CU_THREADS;
+  static constexpr int AT_ONCE = THREADS / TPR;
+};
+
+template <typename T, bool LAYER, bool BIAS, bool MANY, int TPR, int P>
+__global__ __launch_bounds__(BwdRows<TPR>::THREADS) void bwd_kernel(NormBwdArgs A) {
+  constexpr int V = Piece<T>::V, R = BwdRows<TPR>::AT_ONCE, THREADS = BwdRows<TPR>::THREADS;
+  constexpr int SUMS_ROW = LAYER ? 8 : 3;
+  extern __shared__ float lds[];
+  int half = 0;
+  const int tr = threadIdx.x % TPR, rg = threadIdx.x / TPR;
+  const int pieces = A.H / V;
+  const float inv_h = 1.0f / (float)A.H;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  const int w = blockIdx.x, W = A.workers;
+  const uint32_t G = A.G > 0 ? (uint32_t)A.G : 1u;
+
+  bool in[P];
+  uint4 w_post[P], w_pre[P], gate[P];
+  uint4 dy[P], dh[P], yy[P], oo[P];
+  float a_wpre[P][V], a_1[P][V], a_bpre[BIAS ? P : 1][V], a_0[BIAS ? P : 1][V];
+  float s_1[MANY ? P : 1][V], s_0[MANY ? P : 1][V];  // gate-weighted, of the gate rows done
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    in[p] = tr + p * TPR < pieces;
+    w_post[p] = A.w_post && in[p] ? load_raw(A.w_post, tr + p * TPR) : zero;
+    w_pre[p] = A.w_pre && in[p] ? load_raw(A.w_pre, tr + p * TPR) : zero;
+    gate[p] = dy[p] = dh[p] = yy[p] = oo[p] = zero;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      a_wpre[p][i] = a_1[p][i] = 0.f;
+      if constexpr (BIAS) a_bpre[p][i] = a_0[p][i] = 0.f;
+      if constexpr (MANY) s_1[p][i] = s_0[p][i] = 0.f;
+    }
   }
-  if (!out) return;
+  // this row group's rows, turn by turn; all groups of a workgroup take the
+  // same number of turns, some without a row
+  const uint32_t N = (uint32_t)A.N;
+  uint32_t turns, per_gate = 1, g_first, g_step = 0, n_first = 0, n_step = 0;
+  if constexpr (!MANY) {
+    const uint32_t slices = (uint32_t)W / G;
+    g_first = (uint32_t)w % G;
+    const uint32_t n0 = g_first + ((uint32_t)w / G) * G;
+    n_first = n0 + slices * rg * G;
+    n_step = slices * R * G;
+    turns = n0 < N ? (N - n0 + n_step - 1) / n_step : 0;
+  } else {
+    per_gate = (N + G - 1) / G;
+    g_first = (uint32_t)w * R + rg;
+    g_step = (uint32_t)W * R;
+    turns = (G + g_step - 1) / g_step * per_gate;
+  }
+  auto gate_of = [&](uint32_t it) { return g_first + it / per_gate * g_step; };
+  auto row_of = [&](uint32_t it) -> uint32_t {  // N: none
+    if constexpr (!MANY) return min(n_first + it * n_step, N);
+    const uint32_t g = gate_of(it);
+    return g < G ? min(g + it % per_gate * G, N) : N;
+  };
+  auto load_gate = [&](uint32_t g) {
+    if (A.G > 0 && g < G)
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        if (in[p]) gate[p] = load_raw(A.gate, (int64_t)g * pieces + tr + p * TPR);
+  };
+  auto request = [&](uint32_t n, uint4 (&y0)[P], uint4 (&h0)[P], uint4 (&yr)[P], uint4 (&o0)[P],
+                     float (&st)[4]) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) y0[p] = h0[p] = yr[p] = o0[p] = zero;
+    st[0] = st[1] = st[2] = st[3] = 0.f;
+    if (n >= N) return;
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+      if (in[p]) {
+        const int64_t at = (int64_t)n * pieces + tr + p * TPR;
+        if (A.dY) y0[p] = load_raw(A.dY, at);
+        if (A.w_pre) {
+          h0[p] = load_raw(A.dH, at);
+          yr[p] = load_raw(A.Y, at);
+        }
+        if (A.O) o0[p] = load_raw(A.O, at);
+      }
+    if (A.w_pre) {
+      st[0] = A.stat_pre[n];
+      if constexpr (LAYER) st[1] = A.stat_pre[A.N + n];
+    }
+    st[2] = 1.f;
+    if (A.w_post) {
+      st[2] = A.stat_post[n];
+      if constexpr (LAYER) st[3] = A.stat_post[A.N + n];
+    }
+  };
+  float st[4];
+  request(turns > 0 ? row_of(0) : N, dy, dh, yy, oo, st);
+  if constexpr (!MANY) load_gate(g_first);
+
+  for (uint32_t it = 0; it < turns; ++it) {
+    const uint32_t n = row_of(it);
+    const bool live = n < N;
+    if (MANY && it % per_gate == 0) load_gate(gate_of(it));
+    uint4 dyn[P], dhn[P], yyn[P], oon[P];
+    float stn[4];
+    request(it + 1 < turns ? row_of(it + 1) : N, dyn, dhn, yyn, oon, stn);
+    const float ry = st[0], my = st[1], ro = st[2], mo = st[3];
+    float v[SUMS_ROW];
+#pragma unroll
+    for (int k = 0; k < SUMS_ROW; ++k) v[k] = 0.f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      float g[V], x[V], y[V], o[V], kw[V], t[V];
+      unpack<T>(dh[p], g);
+      unpack<T>(w_pre[p], t);
+      unpack<T>(yy[p], y);
+      unpack<T>(oo[p], o);
+      unpack<T>(dy[p], x);
+      unpack<T>(w_post[p], kw);
+      if (A.G > 0) {
+        float q[V];
+        unpack<T>(gate[p], q);
+#pragma unroll
+        for (int i = 0; i < V; ++i) kw[i] *= q[i];
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        // outside the row the weights are zeros: no term counts
+        const float yh = (y[i] - my) * ry, oh = (o[i] - mo) * ro, pw = g[i] * t[i];
+        const float k = A.b * kw[i], f = x[i] + ry * pw;
+        a_wpre[p][i] += g[i] * yh;
+        if constexpr (BIAS) a_bpre[p][i] += g[i];
+        v[0] += pw * yh;
+        v[1] += k * oh * f;
+        v[2] += k * oh * yh;
+        if constexpr (LAYER) {
+          v[3] += pw;
+          v[4] += k * oh;
+          v[5] += k * f;
+          v[6] += k * yh;
+          v[7] += k;
+        }
+      }
+    }
+    row_sums<TPR, SUMS_ROW, THREADS>(v, lds, half);
+    const float m1 = v[0] * inv_h;
+    float m2 = 0.f, t1 = 0.f, t2 = 0.f;
+    if constexpr (LAYER) m2 = v[3] * inv_h;
+    if (A.w_post) {
+      t1 = (v[1] - ry * m1 * v[2]) * inv_h;
+      if constexpr (LAYER) {
+        t1 -= ry * m2 * v[4] * inv_h;
+        t2 = (v[5] - ry * (m2 * v[7] + m1 * v[6])) * inv_h;
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      float g[V], y[V], o[V], D[V], t[V];
+      unpack<T>(dh[p], g);
+      unpack<T>(w_pre[p], t);
+      unpack<T>(yy[p], y);
+      unpack<T>(dy[p], D);
+      unpack<T>(oo[p], o);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float yh = (y[i] - my) * ry;
+        D[i] += ry * (g[i] * t[i] - m2 - yh * m1);
+        o[i] = (o[i] - mo) * ro;
+        if (live) {
+          a_1[p][i] += D[i] * o[i];
+          if constexpr (BIAS) a_0[p][i] += D[i];
+        }
+      }
+      const int64_t at = (int64_t)n * pieces + tr + p * TPR;
+      if (A.O) {
+        float q[V];
+        if (A.G > 0) {
+          unpack<T>(gate[p], q);
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i) q[i] = 1.f;
+        }
+        if (A.w_post) {
+          unpack<T>(w_post[p], t);
+#pragma unroll
+          for (int i = 0; i < V; ++i) q[i] = ro * (A.b * q[i] * t[i] * D[i] - t2 - o[i] * t1);
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i) q[i] = A.b * q[i] * D[i];
+        }
+        if (in[p] && live) store_piece<T>(A.dO, at, q);
+#pragma unroll
+        for (int i = 0; i < V; ++i) D[i] *= A.a;
+      }
+      if (in[p] && live) store_piece<T>(A.dX, at, D);
+    }
+    if constexpr (MANY) {
+      if (it % per_gate == per_gate - 1) {  // this gate row is done
+        const uint32_t g = gate_of(it);
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          float q[V], t[V], c[V];
+          unpack<T>(gate[p], q);
+          unpack<T>(w_post[p], t);
+          if (!A.w_post)
+#pragma unroll
+            for (int i = 0; i < V; ++i) t[i] = 1.f;
+          unpack<T>(A.b_post && in[p] ? load_raw(A.b_post, tr + p * TPR) : zero, c);
+          float* out = A.dgate + (int64_t)g * A.H + (tr + p * TPR) * V;
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float d = A.b * (t[i] * a_1[p][i] + c[i] * a_0[p][i]);
+            s_1[p][i] += A.b * q[i] * a_1[p][i];
+            s_0[p][i] += A.b * q[i] * a_0[p][i];
+            a_1[p][i] = a_0[p][i] = 0.f;
+            if (in[p] && g < G) out[i] = d + (A.accumulate ? out[i] : 0.f);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      dy[p] = dyn[p];
+      dh[p] = dhn[p];
+      yy[p] = yyn[p];
+      oo[p] = oon[p];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) st[k] = stn[k];
+  }
+  // the row groups' sums meet in shared memory, in order
+  auto finish = [&](int k, float (&acc)[P][V]) {
+    float* out = A.ws + ((int64_t)k * W + w) * A.H;
+    __syncthreads();
+    if constexpr (R > 1) {
+      if (rg > 0)
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int i = 0; i < V; ++i) lds[((rg - 1) * P * V + p * V + i) * TPR + tr] = acc[p][i];
+      __syncthreads();
+    }
+    if (rg == 0)
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        if (!in[p]) continue;
+        float t[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          t[i] = acc[p][i];
+#pragma unroll
+          for (int r = 1; r < R; ++r) t[i] += lds[((r - 1) * P * V + p * V + i) * TPR + tr];
+        }
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+          Store4<float>::store(out, (tr + p * TPR) * V + i, t + i);
+      }
+  };
+  if (A.w_pre) finish(SUM_W_PRE, a_wpre);
+  if constexpr (BIAS)
+    if (A.w_pre) finish(SUM_B_PRE, a_bpre);
+  if constexpr (MANY) {
+    finish(SUM_1, s_1);
+    finish(SUM_0, s_0);
+  } else if (A.O) {
+    finish(SUM_1, a_1);
+    if constexpr (BIAS) finish(SUM_0, a_0);
+  }
+}
+
+// The gradients of the weights from the partial sums: 64 columns and 16
+// shares of the workers for each workgroup; blockIdx.y is dw_pre, db_pre,
+// dw_post, db_post, then (G <= W) the gate's rows g with the workers w = g,
+// g + G, ...
+template <typename T>
+__global__ __launch_bounds__(NT) void reduce_kernel(NormBwdArgs A) {
+  __shared__ float4 part[2][NT];
+  const int k = blockIdx.y;
   const int lane = threadIdx.x & 15, share = threadIdx.x >> 4;
   const int c = blockIdx.x * 64 + lane * 4;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (c < A.H && has_rows) {
-    const float* in = A.ws + (int64_t)k * A.workers * A.H + c;
-    for (int64_t w = first + (int64_t)share * step; w < A.workers; w += 16 * (int64_t)step) {
-      const float4 v = *reinterpret_cast<const float4*>(in + w * A.H);
+  const int W = A.workers;
+  float* out = k == 0 ? A.dw_pre : k == 1 ? A.db_pre : k == 2 ? A.dw_post : k == 3 ? A.db_post
+                                                             : A.dgate + (int64_t)(k - 4) * A.H;
+  if (!out) return;
+  const bool is_gate = k >= 4;
+  // dw_post, db_post: the workers' gate rows are still to be applied
+  const bool weigh = (k == 2 || k == 3) && (A.G == 0 || A.G <= W);
+  const int first = is_gate ? k - 4 : 0, step = is_gate ? (int)A.G : 1;
+  const int slot = k == 0 ? SUM_W_PRE : k == 1 ? SUM_B_PRE : k == 3 ? SUM_0 : SUM_1;
+  const bool second = is_gate && A.b_post;  // the gate's other sum
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f), s0 = s;
+  if (c < A.H && A.N > 0) {
+    const float* in = A.ws + (int64_t)slot * W * A.H + c;
+    const float* in0 = A.ws + (int64_t)SUM_0 * W * A.H + c;
+    float4 g = make_float4(A.b, A.b, A.b, A.b);
+    const bool one = A.G == 1;
+    if (weigh && one) {
+      float q[4];
+      Store4<T>::load(A.gate, c, q);
+      g = make_float4(A.b * q[0], A.b * q[1], A.b * q[2], A.b * q[3]);
+    }
+#pragma unroll 4
+    for (int w = first + share * step; w < W; w += 16 * step) {
+      float4 v = *reinterpret_cast<const float4*>(in + (int64_t)w * A.H);
+      if (weigh) {
+        if (A.G > 1) {
+          float q[4];
+          Store4<T>::load(A.gate, (int64_t)(w % (int)A.G) * A.H + c, q);
+          g = make_float4(A.b * q[0], A.b * q[1], A.b * q[2], A.b * q[3]);
+        }
+        v.x *= g.x; v.y *= g.y; v.z *= g.z; v.w *= g.w;
+      }
       s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+      if (second) {
+        const float4 u = *reinterpret_cast<const float4*>(in0 + (int64_t)w * A.H);
+        s0.x += u.x; s0.y += u.y; s0.z += u.z; s0.w += u.w;
+      }
     }
   }
-  part[threadIdx.x] = s;
+  part[0][threadIdx.x] = s;
+  if (second) part[1][threadIdx.x] = s0;
   __syncthreads();
-  if (share == 0 && c < A.H) {
+  if (share != 0 || c >= A.H) return;
 #pragma unroll
-    for (int j = 1; j < 16; ++j) {
-      const float4 v = part[j * 16 + lane];
-      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  for (int j = 1; j < 16; ++j) {
+    const float4 v = part[0][j * 16 + lane];
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    if (second) {
+      const float4 u = part[1][j * 16 + lane];
+      s0.x += u.x; s0.y += u.y; s0.z += u.z; s0.w += u.w;
     }
-    float4* o = reinterpret_cast<float4*>(out + c);
-    if (A.accumulate) {
-      const float4 v = *o;
-      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-    }
-    *o = s;
   }
+  if (is_gate) {
+    float p[4] = {1.f, 1.f, 1.f, 1.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
+    if (A.w_post) Store4<T>::load(A.w_post, c, p);
+    if (A.b_post) Store4<T>::load(A.b_post, c, b);
+    s.x = A.b * (p[0] * s.x + b[0] * s0.x);
+    s.y = A.b * (p[1] * s.y + b[1] * s0.y);
+    s.z = A.b * (p[2] * s.z + b[2] * s0.z);
+    s.w = A.b * (p[3] * s.w + b[3] * s0.w);
+  }
+  float4* o = reinterpret_cast<float4*>(out + c);
+  if (A.accumulate) {
+    const float4 v = *o;
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  }
+  *o = s;
 }
 
 __global__ __launch_bounds__(NT) void zero_kernel(float4* p, int64_t n) {
@@ -420,10 +962,11 @@ __global__ __launch_bounds__(NT) void zero_kernel(float4* p, int64_t n) {
     p[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
-// workers of one call: enough to fill the chip, at least 4 rows each
-static int workers_for(int64_t N, int64_t G) {
-  int64_t w = N / 4;
-  if (w > 256) w = 256;
+// workers of one call, with `at_once` rows to a worker's turn: as many as
+// there are compute units where each then has two turns or more
+static int workers_for(int64_t N, int64_t G, int at_once) {
+  int64_t w = (N + 2 * at_once - 1) / (2 * at_once);
+  if (w > CUS) w = CUS;
   if (w < 1) w = 1;
   if (G > 0 && G <= w) w = w / G * G;
   return (int)w;
@@ -441,52 +984,103 @@ static hipError_t pick(int kind, int dtype, F&& f) {
 
 }  // namespace norm
 
+// f(TPR, P) of the threads a row and pieces a thread that hold `pieces`
+// pieces in registers; false: too wide for any
+template <typename F>
+static bool pick_width(int64_t pieces, F&& f) {
+  using std::integral_constant;
+  if (pieces <= 64) f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  else if (pieces <= 128) f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  else if (pieces <= 256) f(integral_constant<int, 128>{}, integral_constant<int, 2>{});
+  else if (pieces <= 512) f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  else if (pieces <= 1024) f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+  else if (pieces <= 2048) f(integral_constant<int, 512>{}, integral_constant<int, 4>{});
+  else return false;
+  return true;
+}
+
 hipError_t norm_fwd_launch(int kind, int dtype, const NormFwdArgs& a, hipStream_t st) {
   using namespace norm;
   if (a.N == 0) return hipSuccess;
   return pick(kind, dtype, [&](auto t, auto layer) {
     using T = decltype(t);
-    hipLaunchKernelGGL((fwd_wide_kernel<T, decltype(layer)::value>), dim3(grid_rows(a.N)),
-                       dim3(NT), 0, st, a);
+    constexpr bool L = decltype(layer)::value;
+    const bool fits = pick_width(a.H / Piece<T>::V, [&](auto tpr, auto p) {
+      constexpr int TPR = decltype(tpr)::value, P = decltype(p)::value;
+      const int64_t groups = (a.N + Rows<TPR>::AT_ONCE - 1) / Rows<TPR>::AT_ONCE;
+      const int64_t most = (int64_t)CUS * CU_THREADS / Rows<TPR>::THREADS;
+      hipLaunchKernelGGL((fwd_kernel<T, L, TPR, P>), dim3((unsigned)(groups < most ? groups : most)),
+                         dim3(Rows<TPR>::THREADS), 0, st, a);
+    });
+    if (!fits)
+      hipLaunchKernelGGL((fwd_wide_kernel<T, L>), dim3(grid_rows(a.N)), dim3(NT), 0, st, a);
     return hipGetLastError();
   });
 }
 
+// workers of a call, and whether its rows fit the registers
+static int bwd_workers(int64_t N, int64_t G, int64_t pieces, bool* fits) {
+  using namespace norm;
+  int w = 0;
+  *fits = pick_width(pieces, [&](auto tpr, auto) {
+    w = workers_for(N, G, BwdRows<decltype(tpr)::value>::AT_ONCE);
+  });
+  return *fits ? w : workers_for(N, G, 1);
+}
+
 size_t norm_bwd_workspace(const tp_norm_desc& d) {
-  const size_t w = (size_t)norm::workers_for(d.N, d.gate_rows);
-  return (w * norm::SUMS * (size_t)d.H + 2 * (size_t)d.N) * sizeof(float);
+  bool fits;
+  const size_t w = (size_t)bwd_workers(d.N, d.gate_rows, d.H / (d.dtype == TP_BF16 ? 8 : 4), &fits);
+  return (w * norm::SUMS * (size_t)d.H + (fits ? 0 : 2 * (size_t)d.N)) * sizeof(float);
 }
 
 hipError_t norm_bwd_launch(int kind, int dtype, NormBwdArgs& a, hipStream_t st) {
   using namespace norm;
-  a.workers = workers_for(a.N, a.G);
-  if (a.N > 0) {
-    hipError_t he = pick(kind, dtype, [&](auto t, auto layer) {
-      using T = decltype(t);
-      constexpr bool L = decltype(layer)::value;
+  bool fits;
+  a.workers = bwd_workers(a.N, a.G, a.H / (dtype == TP_BF16 ? 8 : 4), &fits);
+  const bool many = a.G > a.workers;
+  // sums without a factor besides them: the biases' gradients, and the
+  // gate's where a bias is in its factor
+  const bool bias = a.db_pre || a.db_post || (a.b_post && a.dgate);
+  return pick(kind, dtype, [&](auto t, auto layer) {
+    using T = decltype(t);
+    constexpr bool L = decltype(layer)::value;
+    hipError_t he = hipSuccess;
+    const unsigned W = (unsigned)a.workers;
+    if (a.N > 0 && fits) {
+      pick_width(a.H / Piece<T>::V, [&](auto tpr, auto p) {
+        constexpr int TPR = decltype(tpr)::value, P = decltype(p)::value;
+        constexpr int THREADS = BwdRows<TPR>::THREADS, R = BwdRows<TPR>::AT_ONCE;
+        const size_t sums = 2 * (THREADS / 64) * (L ? 8 : 3) * sizeof(float);
+        const size_t meet = (size_t)(R - 1) * P * Piece<T>::V * TPR * sizeof(float);
+        const size_t lds = sums > meet ? sums : meet;
+        if (many)
+          hipLaunchKernelGGL((bwd_kernel<T, L, true, true, TPR, P>), dim3(W), dim3(THREADS), lds, st, a);
+        else if (bias)
+          hipLaunchKernelGGL((bwd_kernel<T, L, true, false, TPR, P>), dim3(W), dim3(THREADS), lds, st, a);
+        else
+          hipLaunchKernelGGL((bwd_kernel<T, L, false, false, TPR, P>), dim3(W), dim3(THREADS), lds, st, a);
+      });
+      he = hipGetLastError();
+    } else if (a.N > 0) {
       float* means = a.ws + (size_t)a.workers * SUMS * a.H;
       hipLaunchKernelGGL((bwd_wide_rows_kernel<T, L>), dim3(grid_rows(a.N)), dim3(NT), 0, st, a,
                          means);
-      hipError_t he = hipGetLastError();
-      if (he != hipSuccess) return he;
+      if ((he = hipGetLastError()) != hipSuccess) return he;
       const unsigned cols = (unsigned)((a.H + NT * Piece<T>::V - 1) / (NT * Piece<T>::V));
-      hipLaunchKernelGGL((bwd_wide_columns_kernel<T, L>), dim3(cols, (unsigned)a.workers),
-                         dim3(NT), 0, st, a, means);
-      return hipGetLastError();
-    });
+      hipLaunchKernelGGL((bwd_wide_columns_kernel<T, L>), dim3(cols, W), dim3(NT), 0, st, a, means);
+      he = hipGetLastError();
+    } else if (many && !a.accumulate) {
+      hipLaunchKernelGGL(zero_kernel, dim3(1024), dim3(NT), 0, st,
+                         reinterpret_cast<float4*>(a.dgate), a.G * a.H / 4);
+      he = hipGetLastError();
+    }
     if (he != hipSuccess) return he;
-  }
-  const bool gate_partial = a.dgate && a.G <= a.workers;
-  if (a.N == 0 && a.dgate && !gate_partial && !a.accumulate) {
-    hipLaunchKernelGGL(zero_kernel, dim3(1024), dim3(NT), 0, st,
-                       reinterpret_cast<float4*>(a.dgate), a.G * a.H / 4);
-    hipError_t he = hipGetLastError();
-    if (he != hipSuccess) return he;
-  }
-  hipLaunchKernelGGL(reduce_kernel,
-                     dim3((unsigned)((a.H + 63) / 64), SUM_GATE + (gate_partial ? (unsigned)a.G : 0u)),
-                     dim3(NT), 0, st, a, a.N > 0 ? 1 : 0);
-  return hipGetLastError();
+    const unsigned gates = a.dgate && !many ? (unsigned)a.G : 0u;
+    hipLaunchKernelGGL((reduce_kernel<T>), dim3((unsigned)((a.H + 63) / 64), 4 + gates), dim3(NT), 0,
+                       st, a);
+    return hipGetLastError();
+  });
 }
 
 }  // namespace tpmlp
