@@ -20,8 +20,11 @@ namespace tpmlp {
 namespace adamw {
 
 constexpr int NT = 256;
-constexpr int TENSORS = 48;        // of one launch: the arguments stay under 4 KiB
-constexpr int SPAN = 4096;         // elements of one workgroup's piece of a tensor
+constexpr int TENSORS = 44;        // of one launch: the arguments stay under 4 KiB
+// Elements of one workgroup's piece of a tensor.  fp32 states: 465 us at 4096
+// (88M elements), 479 at 2048, 488 at 1024; 8-bit: 470 us at 1024 (138M), 473
+// at 2048, 489 at 4096 (more registers, fewer wavefronts).
+constexpr int SPAN32 = 4096, SPAN8 = 1024;
 constexpr int BLOCK = TP_ADAMW_BLOCK;
 constexpr float FMAX = 448.f;      // largest finite E4M3
 
@@ -33,11 +36,11 @@ struct Tensor {
   float *ms, *vs;
   int64_t count;
   float wd;
-  int first;  // workgroup of its first piece
 };
 
 struct Args {
   Tensor t[TENSORS];
+  int first[TENSORS];  // workgroup of each one's first piece
   int n, place;  // tensors here; place of the first in the caller's list
   const int32_t* dev_step;
   const float* dev_lr;
@@ -59,6 +62,19 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
   x ^= x >> 15;
   x *= 0xBB67AE85u;
   return x ^ (x >> 16);
+}
+
+// Nothing is used again before the step has passed over everything: past
+// the caches.  88M elements, fp32 states: 465 us so, 474 with plain stores,
+// 487 with plain loads and stores.
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ float4 ld4(const float* p) {
+  const f32x4_t v = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(p));
+  return make_float4(v.x, v.y, v.z, v.w);
+}
+__device__ __forceinline__ void st4(float* p, const float4& q) {
+  const f32x4_t v = {q.x, q.y, q.z, q.w};
+  __builtin_nontemporal_store(v, reinterpret_cast<f32x4_t*>(p));
 }
 
 struct Scalars {
@@ -88,39 +104,97 @@ __device__ __forceinline__ bool scalars(const Args& A, int k, Scalars& s) {
   return true;
 }
 
+// the last tensor whose first piece is not behind workgroup b: one look by
+// all lanes
 __device__ __forceinline__ int find_tensor(const Args& A, int b) {
-  int lo = 0, hi = A.n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (A.t[mid].first <= b) lo = mid; else hi = mid - 1;
-  }
-  return lo;
+  static_assert(TENSORS <= 64, "a lane for each");
+  const int lane = threadIdx.x & 63;
+  const bool before = lane < A.n && A.first[lane < TENSORS ? lane : 0] <= b;
+  return __popcll(__ballot(before)) - 1;
 }
 
-__device__ __forceinline__ float load_grad(const float* g, int64_t i) { return g[i]; }
-__device__ __forceinline__ float load_grad(const bf16_t* g, int64_t i) { return bf16_to_f32(g[i]); }
+// four neighbours; fewer at a tensor's end
+template <typename GT> struct Grad4;
+template <> struct Grad4<float> {
+  float4 q;
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    q = ld4(reinterpret_cast<const float*>(p) + i);
+  }
+  __device__ __forceinline__ void get(float g[4]) const { g[0] = q.x; g[1] = q.y; g[2] = q.z; g[3] = q.w; }
+  static __device__ __forceinline__ float one(const void* p, int64_t i) {
+    return reinterpret_cast<const float*>(p)[i];
+  }
+};
+template <> struct Grad4<bf16_t> {
+  uint2 q;
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    q = *reinterpret_cast<const uint2*>(reinterpret_cast<const bf16_t*>(p) + i);
+  }
+  __device__ __forceinline__ void get(float g[4]) const {
+    g[0] = __uint_as_float(q.x << 16);
+    g[1] = __uint_as_float(q.x & 0xffff0000u);
+    g[2] = __uint_as_float(q.y << 16);
+    g[3] = __uint_as_float(q.y & 0xffff0000u);
+  }
+  static __device__ __forceinline__ float one(const void* p, int64_t i) {
+    return bf16_to_f32(reinterpret_cast<const bf16_t*>(p)[i]);
+  }
+};
 
 __device__ __forceinline__ float new_param(float p, float m, float root, const Scalars& s) {
   return p * s.decay - s.step_size * (m / (root * s.inv_root_c2 + s.eps));
 }
 
-// fp32 states
+// fp32 states: four neighbours a thread, every load of a workgroup's piece
+// before the first store
 template <typename GT>
 __global__ __launch_bounds__(NT) void step32_kernel(Args A) {
   const int k = find_tensor(A, blockIdx.x);
   const Tensor& t = A.t[k];
   Scalars s;
   if (!scalars(A, k, s)) return;
-  const int64_t i0 = (int64_t)(blockIdx.x - t.first) * SPAN;
-  const int64_t i1 = min(i0 + SPAN, t.count);
-  const GT* grad = reinterpret_cast<const GT*>(t.g);
+  const int64_t i0 = (int64_t)(blockIdx.x - A.first[k]) * SPAN32;
   float* mp = reinterpret_cast<float*>(t.m);
   float* vp = reinterpret_cast<float*>(t.v);
-  for (int64_t i = i0 + threadIdx.x; i < i1; i += NT) {
-    const float g = load_grad(grad, i) * s.gs;
-    const float m = mp[i] * A.b1 + g * A.omb1;
-    const float v = vp[i] * A.b2 + g * g * A.omb2;
-    const float p = new_param(t.p[i], m, sqrtf(v), s);
+  auto update = [&](float& p, float g, float& m, float& v) {
+    g *= s.gs;
+    m = m * A.b1 + g * A.omb1;
+    v = v * A.b2 + g * g * A.omb2;
+    p = new_param(p, m, sqrtf(v), s);
+  };
+  if (i0 + SPAN32 <= t.count) {
+    constexpr int U = SPAN32 / (4 * NT);
+    float4 p[U], m[U], v[U];
+    Grad4<GT> g[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = i0 + (u * NT + threadIdx.x) * 4;
+      p[u] = ld4(t.p + i);
+      g[u].load(t.g, i);
+      m[u] = ld4(mp + i);
+      v[u] = ld4(vp + i);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = i0 + (u * NT + threadIdx.x) * 4;
+      float gg[4];
+      g[u].get(gg);
+      update(p[u].x, gg[0], m[u].x, v[u].x);
+      update(p[u].y, gg[1], m[u].y, v[u].y);
+      update(p[u].z, gg[2], m[u].z, v[u].z);
+      update(p[u].w, gg[3], m[u].w, v[u].w);
+      st4(mp + i, m[u]);
+      st4(vp + i, v[u]);
+      st4(t.p + i, p[u]);
+      if (t.p16)
+        *reinterpret_cast<uint2*>(t.p16 + i) =
+            make_uint2(pack_bf16x2(p[u].x, p[u].y), pack_bf16x2(p[u].z, p[u].w));
+    }
+    return;
+  }
+  for (int64_t i = i0 + threadIdx.x; i < t.count; i += NT) {
+    float p = t.p[i], m = mp[i], v = vp[i];
+    update(p, Grad4<GT>::one(t.g, i), m, v);
     mp[i] = m;
     vp[i] = v;
     t.p[i] = p;
@@ -171,60 +245,117 @@ __device__ __forceinline__ float round_e4m3(float t, float u, bool positive) {
   return k > FMAX ? FMAX : k < -FMAX ? -FMAX : k;  // NaN stays NaN
 }
 
-// 8-bit states: a wavefront takes a block of 256, four neighbours a lane
+// 8-bit states: a wavefront takes a block of 256, four neighbours a lane,
+// and requests all its blocks of a workgroup's piece at once
 template <typename GT>
 __global__ __launch_bounds__(NT) void step8_kernel(Args A) {
+  constexpr int U = SPAN8 / (NT / 64) / BLOCK;  // blocks of a wavefront
   const int k = find_tensor(A, blockIdx.x);
   const Tensor& t = A.t[k];
   Scalars s;
   if (!scalars(A, k, s)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t i0 = (int64_t)(blockIdx.x - t.first) * SPAN;
-  const int64_t i1 = min(i0 + SPAN, t.count);
-  const GT* grad = reinterpret_cast<const GT*>(t.g);
+  const int64_t i0 = (int64_t)(blockIdx.x - A.first[k]) * SPAN8 + wave * BLOCK;
   uint8_t* mc = reinterpret_cast<uint8_t*>(t.m);
   uint8_t* vc = reinterpret_cast<uint8_t*>(t.v);
-  for (int64_t b0 = i0 + wave * BLOCK; b0 < i1; b0 += (NT / 64) * BLOCK) {
-    const int64_t blk = b0 / BLOCK;
-    const float ms = t.ms[blk], vs = t.vs[blk];
-    float m[4], r[4];
+  float4 p4[U];
+  Grad4<GT> g4[U];
+  uint32_t m4[U], v4[U];
+  float ms[U], vs[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t b0 = i0 + u * (NT / 64) * BLOCK, i = b0 + lane * 4;
+    if (b0 + BLOCK > t.count) continue;
+    p4[u] = ld4(t.p + i);
+    g4[u].load(t.g, i);
+    m4[u] = *reinterpret_cast<const uint32_t*>(mc + i);
+    v4[u] = *reinterpret_cast<const uint32_t*>(vc + i);
+    ms[u] = t.ms[b0 / BLOCK];
+    vs[u] = t.vs[b0 / BLOCK];
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t b0 = i0 + u * (NT / 64) * BLOCK, i = b0 + lane * 4;
+    if (b0 >= t.count) break;
+    const bool whole = b0 + BLOCK <= t.count;
+    const int here = whole ? 4 : (int)max((int64_t)0, min((int64_t)4, t.count - i));
+    float p[4], g[4], m[4], r[4];
+    float sm = ms[u], sv = vs[u];
+    uint32_t cm = m4[u], cv = v4[u];
+    if (whole) {
+      p[0] = p4[u].x; p[1] = p4[u].y; p[2] = p4[u].z; p[3] = p4[u].w;
+      g4[u].get(g);
+    } else {  // a tensor's last block
+      cm = cv = 0;
+      sm = t.ms[b0 / BLOCK];
+      sv = t.vs[b0 / BLOCK];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        p[j] = g[j] = 0.f;
+        if (j < here) {
+          p[j] = t.p[i + j];
+          g[j] = Grad4<GT>::one(t.g, i + j);
+          cm |= (uint32_t)mc[i + j] << (8 * j);
+          cv |= (uint32_t)vc[i + j] << (8 * j);
+        }
+      }
+    }
+    m[0] = __builtin_amdgcn_cvt_f32_fp8((int)cm, 0) * sm;
+    m[1] = __builtin_amdgcn_cvt_f32_fp8((int)cm, 1) * sm;
+    m[2] = __builtin_amdgcn_cvt_f32_fp8((int)cm, 2) * sm;
+    m[3] = __builtin_amdgcn_cvt_f32_fp8((int)cm, 3) * sm;
+    r[0] = __builtin_amdgcn_cvt_f32_fp8((int)cv, 0) * sv;
+    r[1] = __builtin_amdgcn_cvt_f32_fp8((int)cv, 1) * sv;
+    r[2] = __builtin_amdgcn_cvt_f32_fp8((int)cv, 2) * sv;
+    r[3] = __builtin_amdgcn_cvt_f32_fp8((int)cv, 3) * sv;
     uint32_t mtop = 0, vtop = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int64_t i = b0 + lane * 4 + j;
-      m[j] = r[j] = 0.f;
-      if (i < i1) {
-        const float g = load_grad(grad, i) * s.gs;
-        const float mo = __builtin_amdgcn_cvt_f32_fp8((int)mc[i], 0) * ms;
-        const float ro = __builtin_amdgcn_cvt_f32_fp8((int)vc[i], 0) * vs;
-        m[j] = mo * A.b1 + g * A.omb1;
-        r[j] = sqrtf(ro * ro * A.b2 + g * g * A.omb2);
-        const float p = new_param(t.p[i], m[j], r[j], s);
-        t.p[i] = p;
-        if (t.p16) t.p16[i] = f32_to_bf16(p);
+      const float gj = g[j] * s.gs;
+      m[j] = m[j] * A.b1 + gj * A.omb1;
+      r[j] = sqrtf(r[j] * r[j] * A.b2 + gj * gj * A.omb2);
+      p[j] = new_param(p[j], m[j], r[j], s);
+      // (past the tensor's end the states are zeros unless a scale is NaN)
+      if (j < here) {
+        mtop = max(mtop, __float_as_uint(m[j]) & 0x7fffffffu);
+        vtop = max(vtop, __float_as_uint(r[j]) & 0x7fffffffu);
       }
-      mtop = max(mtop, __float_as_uint(m[j]) & 0x7fffffffu);
-      vtop = max(vtop, __float_as_uint(r[j]) & 0x7fffffffu);
     }
     float msc, minv, vsc, vinv;
     block_scale(wave_max(mtop), msc, minv);
     block_scale(wave_max(vtop), vsc, vinv);
     if (lane == 0) {
-      t.ms[blk] = msc;
-      t.vs[blk] = vsc;
+      t.ms[b0 / BLOCK] = msc;
+      t.vs[b0 / BLOCK] = vsc;
     }
+    float km[4], kr[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int64_t i = b0 + lane * 4 + j;
-      if (i < i1) {
-        const uint32_t h = mix(((uint32_t)i ^ s.key) + (uint32_t)(i >> 32));
-        const float um = (float)(h & 0xffffu) * 0x1p-16f, ur = (float)(h >> 16) * 0x1p-16f;
-        const float cm = round_e4m3<false>(m[j] * minv, um, false);
-        const float cr = round_e4m3<true>(r[j] * vinv, ur, r[j] > 0.f);
-        const int w = __builtin_amdgcn_cvt_pk_fp8_f32(cm, cr, 0, false);
-        mc[i] = (uint8_t)(w & 0xff);
-        vc[i] = (uint8_t)((w >> 8) & 0xff);
-      }
+      const uint32_t h = mix(((uint32_t)(i + j) ^ s.key) + (uint32_t)(i >> 32));
+      km[j] = round_e4m3<false>(m[j] * minv, (float)(h & 0xffffu) * 0x1p-16f, false);
+      kr[j] = round_e4m3<true>(r[j] * vinv, (float)(h >> 16) * 0x1p-16f, r[j] > 0.f);
+    }
+    // exact: the values are E4M3 already
+    int wm = __builtin_amdgcn_cvt_pk_fp8_f32(km[0], km[1], 0, false);
+    wm = __builtin_amdgcn_cvt_pk_fp8_f32(km[2], km[3], wm, true);
+    int wv = __builtin_amdgcn_cvt_pk_fp8_f32(kr[0], kr[1], 0, false);
+    wv = __builtin_amdgcn_cvt_pk_fp8_f32(kr[2], kr[3], wv, true);
+    if (whole) {
+      *reinterpret_cast<uint32_t*>(mc + i) = (uint32_t)wm;
+      *reinterpret_cast<uint32_t*>(vc + i) = (uint32_t)wv;
+      st4(t.p + i, make_float4(p[0], p[1], p[2], p[3]));
+      if (t.p16)
+        *reinterpret_cast<uint2*>(t.p16 + i) =
+            make_uint2(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < here) {
+          mc[i + j] = (uint8_t)((uint32_t)wm >> (8 * j));
+          vc[i + j] = (uint8_t)((uint32_t)wv >> (8 * j));
+          t.p[i + j] = p[j];
+          if (t.p16) t.p16[i + j] = f32_to_bf16(p[j]);
+        }
     }
   }
 }
@@ -254,6 +385,7 @@ hipError_t adamw_launch(const tp_adamw_desc& d, int n, const tp_adamw_tensor* t,
   a.inv_c1 = (float)(1.0 / c1);
   a.step_size = (float)(d.lr / c1);
   a.inv_root_c2 = (float)(1.0 / sqrt(c2));
+  const int64_t span = d.state_bits == 32 ? SPAN32 : SPAN8;
   int k = 0;
   while (k < n) {
     int64_t groups = 0;
@@ -263,10 +395,11 @@ hipError_t adamw_launch(const tp_adamw_desc& d, int n, const tp_adamw_tensor* t,
     // table keeps the numbering)
     for (; k < n && a.n < TENSORS; ++k) {
       const tp_adamw_tensor& x = t[k];
-      const int64_t pieces = (x.count + SPAN - 1) / SPAN;
+      const int64_t pieces = (x.count + span - 1) / span;
       if (groups + pieces > 0x7fffffff) break;
+      a.first[a.n] = (int)groups;
       a.t[a.n++] = Tensor{x.param, (bf16_t*)x.param_bf16, x.grad, x.m, x.v, x.m_scale, x.v_scale,
-                          x.count, x.weight_decay, (int)groups};
+                          x.count, x.weight_decay};
       groups += pieces;
     }
     if (groups == 0) continue;

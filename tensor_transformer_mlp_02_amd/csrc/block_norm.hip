@@ -612,8 +612,10 @@ __global__ __launch_bounds__(NT) void bwd_wide_columns_kernel(NormBwdArgs A, con
 // ---------------------------------------------------------------------------
 template <int TPR>
 struct BwdRows {
-  static constexpr int THREADS = CU_THREADS;
+  static constexpr int THREADS = TPR > CU_THREADS ? TPR : CU_THREADS;
   static constexpr int AT_ONCE = THREADS / TPR;
+  // 16 wavefronts leave 128 registers a lane: no room for the next row
+  static constexpr bool AHEAD = TPR <= CU_THREADS;
 };
 
 template <typename T, bool LAYER, bool BIAS, bool MANY, int TPR, int P>
@@ -633,7 +635,8 @@ __global__ __launch_bounds__(BwdRows<TPR>::THREADS) void bwd_kernel(NormBwdArgs 
   uint4 w_post[P], w_pre[P], gate[P];
   uint4 dy[P], dh[P], yy[P], oo[P];
   float a_wpre[P][V], a_1[P][V], a_bpre[BIAS ? P : 1][V], a_0[BIAS ? P : 1][V];
-  float s_1[MANY ? P : 1][V], s_0[MANY ? P : 1][V];  // gate-weighted, of the gate rows done
+  // gate-weighted, of the gate rows done
+  float s_1[MANY ? P : 1][V], s_0[MANY && BIAS ? P : 1][V];
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     in[p] = tr + p * TPR < pieces;
@@ -644,7 +647,8 @@ __global__ __launch_bounds__(BwdRows<TPR>::THREADS) void bwd_kernel(NormBwdArgs 
     for (int i = 0; i < V; ++i) {
       a_wpre[p][i] = a_1[p][i] = 0.f;
       if constexpr (BIAS) a_bpre[p][i] = a_0[p][i] = 0.f;
-      if constexpr (MANY) s_1[p][i] = s_0[p][i] = 0.f;
+      if constexpr (MANY) s_1[p][i] = 0.f;
+      if constexpr (MANY && BIAS) s_0[p][i] = 0.f;
     }
   }
   // this row group's rows, turn by turn; all groups of a workgroup take the
@@ -711,9 +715,10 @@ __global__ __launch_bounds__(BwdRows<TPR>::THREADS) void bwd_kernel(NormBwdArgs 
     const uint32_t n = row_of(it);
     const bool live = n < N;
     if (MANY && it % per_gate == 0) load_gate(gate_of(it));
+    constexpr bool AHEAD = BwdRows<TPR>::AHEAD;
     uint4 dyn[P], dhn[P], yyn[P], oon[P];
     float stn[4];
-    request(it + 1 < turns ? row_of(it + 1) : N, dyn, dhn, yyn, oon, stn);
+    if constexpr (AHEAD) request(it + 1 < turns ? row_of(it + 1) : N, dyn, dhn, yyn, oon, stn);
     const float ry = st[0], my = st[1], ro = st[2], mo = st[3];
     float v[SUMS_ROW];
 #pragma unroll
@@ -809,34 +814,53 @@ __global__ __launch_bounds__(BwdRows<TPR>::THREADS) void bwd_kernel(NormBwdArgs 
         const uint32_t g = gate_of(it);
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-          float q[V], t[V], c[V];
+          float q[V], t[V], d[V];
           unpack<T>(gate[p], q);
           unpack<T>(w_post[p], t);
           if (!A.w_post)
 #pragma unroll
             for (int i = 0; i < V; ++i) t[i] = 1.f;
-          unpack<T>(A.b_post && in[p] ? load_raw(A.b_post, tr + p * TPR) : zero, c);
-          float* out = A.dgate + (int64_t)g * A.H + (tr + p * TPR) * V;
 #pragma unroll
           for (int i = 0; i < V; ++i) {
-            const float d = A.b * (t[i] * a_1[p][i] + c[i] * a_0[p][i]);
+            d[i] = t[i] * a_1[p][i];
             s_1[p][i] += A.b * q[i] * a_1[p][i];
-            s_0[p][i] += A.b * q[i] * a_0[p][i];
-            a_1[p][i] = a_0[p][i] = 0.f;
-            if (in[p] && g < G) out[i] = d + (A.accumulate ? out[i] : 0.f);
+            a_1[p][i] = 0.f;
+          }
+          if constexpr (BIAS) {
+            unpack<T>(A.b_post && in[p] ? load_raw(A.b_post, tr + p * TPR) : zero, t);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              d[i] += t[i] * a_0[p][i];
+              s_0[p][i] += A.b * q[i] * a_0[p][i];
+              a_0[p][i] = 0.f;
+            }
+          }
+          if (!(in[p] && g < G)) continue;
+          const int64_t out = (int64_t)g * A.H + (tr + p * TPR) * V;
+#pragma unroll
+          for (int i = 0; i < V; i += 4) {
+            float o[4] = {0.f, 0.f, 0.f, 0.f};
+            if (A.accumulate) Store4<float>::load(A.dgate, out + i, o);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] += A.b * d[i + j];
+            Store4<float>::store(A.dgate, out + i, o);
           }
         }
       }
     }
+    if constexpr (AHEAD) {
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      dy[p] = dyn[p];
-      dh[p] = dhn[p];
-      yy[p] = yyn[p];
-      oo[p] = oon[p];
+      for (int p = 0; p < P; ++p) {
+        dy[p] = dyn[p];
+        dh[p] = dhn[p];
+        yy[p] = yyn[p];
+        oo[p] = oon[p];
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) st[k] = stn[k];
+    } else {
+      request(it + 1 < turns ? row_of(it + 1) : N, dy, dh, yy, oo, st);
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) st[k] = stn[k];
   }
   // the row groups' sums meet in shared memory, in order
   auto finish = [&](int k, float (&acc)[P][V]) {
@@ -871,7 +895,7 @@ __global__ __launch_bounds__(BwdRows<TPR>::THREADS) void bwd_kernel(NormBwdArgs 
     if (A.w_pre) finish(SUM_B_PRE, a_bpre);
   if constexpr (MANY) {
     finish(SUM_1, s_1);
-    finish(SUM_0, s_0);
+    if constexpr (BIAS) finish(SUM_0, s_0);
   } else if (A.O) {
     finish(SUM_1, a_1);
     if constexpr (BIAS) finish(SUM_0, a_0);
@@ -985,8 +1009,11 @@ static hipError_t pick(int kind, int dtype, F&& f) {
 }  // namespace norm
 
 // f(TPR, P) of the threads a row and pieces a thread that hold `pieces`
-// pieces in registers; false: too wide for any
-template <typename F>
+// pieces in registers; false: too wide for any.  WIDEST: threads of the
+// widest rows.  Forward, 2048 x 16384 bf16: 57 us with 512 threads, 82 with
+// 1024 (barriers of 16 wavefronts); backward 393 and 256 us (512 threads
+// spill), 2048 x 8192 fp32 with a gate a token 160 and 124.
+template <int WIDEST, typename F>
 static bool pick_width(int64_t pieces, F&& f) {
   using std::integral_constant;
   if (pieces <= 64) f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
@@ -994,7 +1021,7 @@ static bool pick_width(int64_t pieces, F&& f) {
   else if (pieces <= 256) f(integral_constant<int, 128>{}, integral_constant<int, 2>{});
   else if (pieces <= 512) f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
   else if (pieces <= 1024) f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
-  else if (pieces <= 2048) f(integral_constant<int, 512>{}, integral_constant<int, 4>{});
+  else if (pieces <= 2048) f(integral_constant<int, WIDEST>{}, integral_constant<int, 2048 / WIDEST>{});
   else return false;
   return true;
 }
@@ -1005,7 +1032,7 @@ hipError_t norm_fwd_launch(int kind, int dtype, const NormFwdArgs& a, hipStream_
   return pick(kind, dtype, [&](auto t, auto layer) {
     using T = decltype(t);
     constexpr bool L = decltype(layer)::value;
-    const bool fits = pick_width(a.H / Piece<T>::V, [&](auto tpr, auto p) {
+    const bool fits = pick_width<512>(a.H / Piece<T>::V, [&](auto tpr, auto p) {
       constexpr int TPR = decltype(tpr)::value, P = decltype(p)::value;
       const int64_t groups = (a.N + Rows<TPR>::AT_ONCE - 1) / Rows<TPR>::AT_ONCE;
       const int64_t most = (int64_t)CUS * CU_THREADS / Rows<TPR>::THREADS;
@@ -1022,7 +1049,7 @@ hipError_t norm_fwd_launch(int kind, int dtype, const NormFwdArgs& a, hipStream_
 static int bwd_workers(int64_t N, int64_t G, int64_t pieces, bool* fits) {
   using namespace norm;
   int w = 0;
-  *fits = pick_width(pieces, [&](auto tpr, auto) {
+  *fits = pick_width<1024>(pieces, [&](auto tpr, auto) {
     w = workers_for(N, G, BwdRows<decltype(tpr)::value>::AT_ONCE);
   });
   return *fits ? w : workers_for(N, G, 1);
@@ -1048,13 +1075,15 @@ hipError_t norm_bwd_launch(int kind, int dtype, NormBwdArgs& a, hipStream_t st) 
     hipError_t he = hipSuccess;
     const unsigned W = (unsigned)a.workers;
     if (a.N > 0 && fits) {
-      pick_width(a.H / Piece<T>::V, [&](auto tpr, auto p) {
+      pick_width<1024>(a.H / Piece<T>::V, [&](auto tpr, auto p) {
         constexpr int TPR = decltype(tpr)::value, P = decltype(p)::value;
         constexpr int THREADS = BwdRows<TPR>::THREADS, R = BwdRows<TPR>::AT_ONCE;
         const size_t sums = 2 * (THREADS / 64) * (L ? 8 : 3) * sizeof(float);
         const size_t meet = (size_t)(R - 1) * P * Piece<T>::V * TPR * sizeof(float);
         const size_t lds = sums > meet ? sums : meet;
-        if (many)
+        if (many && !bias)
+          hipLaunchKernelGGL((bwd_kernel<T, L, false, true, TPR, P>), dim3(W), dim3(THREADS), lds, st, a);
+        else if (many)
           hipLaunchKernelGGL((bwd_kernel<T, L, true, true, TPR, P>), dim3(W), dim3(THREADS), lds, st, a);
         else if (bias)
           hipLaunchKernelGGL((bwd_kernel<T, L, true, false, TPR, P>), dim3(W), dim3(THREADS), lds, st, a);
