@@ -15,27 +15,103 @@ constexpr int WAVES = NT / 64;
 #define TP_ROUTE_LOWEST (-3.3895313892515355e38f)
 #define TP_ROUTE_LARGEST 3.4028234663852886e38f
 
-template <typename T> __device__ __forceinline__ float load_logit(const T* p, int64_t i);
-template <> __device__ __forceinline__ float load_logit<float>(const float* p, int64_t i) {
-  return p[i];
-}
-template <> __device__ __forceinline__ float load_logit<bf16_t>(const bf16_t* p, int64_t i) {
-  return bf16_to_f32(p[i]);
-}
-__device__ __forceinline__ void store_logit(float* p, int64_t i, float v) { p[i] = v; }
-__device__ __forceinline__ void store_logit(bf16_t* p, int64_t i, float v) { p[i] = f32_to_bf16(v); }
-
-template <typename X>
-__device__ __forceinline__ X wave_max(X x) {
+// One wavefront a token.  Lane i holds the experts i V .. i V + V - 1, so
+// that a lane's logits are one load and the lower expert is in the lower
+// lane.
+template <typename T, int V>
+__device__ __forceinline__ void load_row(const T* row, int E, int lane, bool live, float l[V]) {
+  const int e0 = lane * V;
+  if (V > 1 && E % V == 0) {
+    constexpr int BYTES = V * (int)sizeof(T) < 16 ? V * (int)sizeof(T) : 16;
+    constexpr int PER = BYTES / (int)sizeof(T);  // logits of a load
+    struct alignas(BYTES) Part { T x[PER]; };
 #pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) {
-    const X o = __shfl_xor(x, d, 64);
-    x = o > x ? o : x;
+    for (int i = 0; i < V; i += PER) {
+      Part q;
+      const bool there = live && e0 < E;
+      if (there) q = *reinterpret_cast<const Part*>(row + e0 + i);
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        float x = -__builtin_huge_valf();
+        if (there) {
+          if constexpr (sizeof(T) == 2) x = bf16_to_f32(q.x[j]); else x = q.x[j];
+        }
+        l[i + j] = x;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float x = -__builtin_huge_valf();
+      if (live && e0 + i < E) {
+        if constexpr (sizeof(T) == 2) x = bf16_to_f32(row[e0 + i]); else x = row[e0 + i];
+      }
+      l[i] = x;
+    }
   }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    // NaN compares false
+    if (!(l[i] > TP_ROUTE_LOWEST)) l[i] = -__builtin_huge_valf();
+    l[i] = fminf(l[i], TP_ROUTE_LARGEST);
+  }
+}
+
+// Moves within a wavefront that need no shared memory: lane ^ 1, ^ 2, the
+// mirror of 8 and of 16 lanes (which bring the other half once the halves
+// agree), and lane ^ 16, ^ 32.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+  return __int_as_float(
+      __builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+template <int STEP>  // 0..5: over pairs, 4, 8, 16, 32, 64 lanes
+__device__ __forceinline__ float other(float x) {
+  if constexpr (STEP == 0) return dpp<0xB1>(x);        // quad_perm 1,0,3,2
+  else if constexpr (STEP == 1) return dpp<0x4E>(x);   // quad_perm 2,3,0,1
+  else if constexpr (STEP == 2) return dpp<0x141>(x);  // row_half_mirror
+  else if constexpr (STEP == 3) return dpp<0x140>(x);  // row_mirror
+  else if constexpr (STEP == 4) return __shfl_xor(x, 16, 64);
+  else return __shfl_xor(x, 32, 64);
+}
+template <int STEP>
+__device__ __forceinline__ double other(double x) {
+  const unsigned long long b = __double_as_longlong(x);
+  const uint32_t lo = __float_as_uint(other<STEP>(__uint_as_float((uint32_t)b)));
+  const uint32_t hi = __float_as_uint(other<STEP>(__uint_as_float((uint32_t)(b >> 32))));
+  return __longlong_as_double(((unsigned long long)hi << 32) | lo);
+}
+
+// sums and maxima over the wavefront: 16 lanes by moves, then the four rows
+// through scalar registers
+__device__ __forceinline__ float lane_value(float x, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
+}
+__device__ __forceinline__ float wave_max(float x) {
+  x = fmaxf(x, other<0>(x));
+  x = fmaxf(x, other<1>(x));
+  x = fmaxf(x, other<2>(x));
+  x = fmaxf(x, other<3>(x));
+  return fmaxf(fmaxf(lane_value(x, 0), lane_value(x, 16)),
+               fmaxf(lane_value(x, 32), lane_value(x, 48)));
+}
+__device__ __forceinline__ float wave_sum(float x) {
+  x += other<0>(x);
+  x += other<1>(x);
+  x += other<2>(x);
+  x += other<3>(x);
+  return (lane_value(x, 0) + lane_value(x, 16)) + (lane_value(x, 32) + lane_value(x, 48));
+}
+__device__ __forceinline__ double wave_sum(double x) {
+  x += other<0>(x);
+  x += other<1>(x);
+  x += other<2>(x);
+  x += other<3>(x);
+  x += other<4>(x);
+  x += other<5>(x);
   return x;
 }
-template <typename X>
-__device__ __forceinline__ X wave_sum(X x) {
+__device__ __forceinline__ int wave_sum(int x) {
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) x += __shfl_xor(x, d, 64);
   return x;
@@ -51,112 +127,230 @@ struct FwdArgs {
   float scale;
 };
 
-// One wavefront a token, expert e in lane e % 64; choices in 64 bits.
-template <typename T, int V, bool SIGMOID>
+// The largest and second largest of a run of experts, merged over 2^STEPS
+// lanes
+template <int STEP>
+__device__ __forceinline__ void merge_best(double& b1, double& b2) {
+  const double o1 = other<STEP>(b1), o2 = other<STEP>(b2);
+  b2 = fmax(fmin(b1, o1), fmax(b2, o2));
+  b1 = fmax(b1, o1);
+}
+
+// Which groups stay, one bit each.  worth: this lane's group's, in lane g.
+__device__ __forceinline__ unsigned long long keep_groups(double worth, int groups, int kept,
+                                                          int lane) {
+  const unsigned long long b = __double_as_longlong(worth);
+  int rank = 0;
+  for (int g = 0; g < groups; ++g) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, g);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), g);
+    const double o = __longlong_as_double(((unsigned long long)hi << 32) | lo);
+    rank += o > worth || (o == worth && g < lane);
+  }
+  return __ballot(lane < groups && rank < kept);
+}
+
+// WIDE: scores in 64 bits, where a choice hangs on them (a bias, or groups
+// by the sum of two); otherwise the order of the scores is the logits' own.
+//
+// The k-th choice is a maximum over the wavefront of 32-bit keys: the
+// logits, or the choice scores rounded once, which keeps their order but
+// for equals.  So k + 1 maxima that all differ settle the choice; where two
+// are equal the token is done again on the 64-bit values (tie).
+template <typename T, int V, bool SIGMOID, bool WIDE>
 __global__ __launch_bounds__(NT) void fwd_kernel(FwdArgs A) {
   extern __shared__ double sh[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  double* cs = sh + (size_t)wave * A.E;
   const T* logits = reinterpret_cast<const T*>(A.logits);
   const double NEG = -__builtin_huge_val();
-  const int64_t rounds = (A.N + (int64_t)gridDim.x * WAVES - 1) / ((int64_t)gridDim.x * WAVES);
-  for (int64_t it = 0; it < rounds; ++it) {
-    const int64_t t = (it * gridDim.x + blockIdx.x) * WAVES + wave;
-    const bool live = t < A.N;
-    float l[V];
-    double s[V], key[V];
-    float top = -__builtin_huge_valf();
+  const float NEGF = -__builtin_huge_valf();
+  for (int64_t t = (int64_t)blockIdx.x * WAVES + wave; t < A.N; t += (int64_t)gridDim.x * WAVES) {
+    float l[V], s[V], key[V];
+    double c[WIDE ? V : 1];
+    load_row<T, V>(logits + t * A.E, A.E, lane, true, l);
+    float top = l[0];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = lane + 64 * i;
-      float x = live && e < A.E ? load_logit<T>(logits, t * A.E + e) : -__builtin_huge_valf();
-      if (!(x > TP_ROUTE_LOWEST)) x = -__builtin_huge_valf();
-      l[i] = fminf(x, TP_ROUTE_LARGEST);
-      top = fmaxf(top, l[i]);
-    }
-    if constexpr (SIGMOID) {
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        s[i] = l[i] > TP_ROUTE_LOWEST ? 1.0 / (1.0 + exp(-(double)l[i])) : 0.0;
-    } else {
-      top = wave_max(top);
-      double sum = 0.0;
+    for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
+    if constexpr (!SIGMOID) top = wave_max(top);
+    if constexpr (WIDE) {
+      double s64[V], sum = 0.0;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        s[i] = l[i] > TP_ROUTE_LOWEST ? exp((double)l[i] - (double)top) : 0.0;
-        sum += s[i];
+        if constexpr (SIGMOID) {
+          s64[i] = l[i] > TP_ROUTE_LOWEST ? 1.0 / (1.0 + exp(-(double)l[i])) : 0.0;
+        } else {
+          s64[i] = l[i] > TP_ROUTE_LOWEST ? exp((double)l[i] - (double)top) : 0.0;
+          sum += s64[i];
+        }
       }
-      sum = wave_sum(sum);
-      const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
+      if constexpr (!SIGMOID) {
+        sum = wave_sum(sum);
+        const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
 #pragma unroll
-      for (int i = 0; i < V; ++i) s[i] *= inv;
-    }
+        for (int i = 0; i < V; ++i) s64[i] *= inv;
+      }
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = lane + 64 * i;
-      const bool there = l[i] > TP_ROUTE_LOWEST;
-      double c = s[i];
-      if (A.bias && e < A.E) c += (double)A.bias[e];
-      key[i] = !there ? NEG : A.bias ? c : (double)l[i];
-      if (A.groups > 1 && e < A.E) cs[e] = there ? c : NEG;
+      for (int i = 0; i < V; ++i) {
+        const int e = lane * V + i;
+        s[i] = (float)s64[i];
+        c[i] = s64[i];
+        if (A.bias && e < A.E) c[i] += (double)A.bias[e];
+        if (!(l[i] > TP_ROUTE_LOWEST)) c[i] = NEG;
+        key[i] = A.bias ? (float)c[i] : l[i];
+      }
+    } else {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if constexpr (SIGMOID) {
+          s[i] = l[i] > TP_ROUTE_LOWEST ? 1.f / (1.f + expf(-l[i])) : 0.f;
+        } else {
+          s[i] = l[i] > TP_ROUTE_LOWEST ? expf(l[i] - top) : 0.f;
+          sum += s[i];
+        }
+        key[i] = l[i];
+      }
+      if constexpr (!SIGMOID) {
+        sum = wave_sum(sum);
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] *= inv;
+      }
     }
     if (A.groups > 1) {
-      __syncthreads();
       const int per = A.E / A.groups;
-      double worth = NEG;
-      if (lane < A.groups) {
-        double b1 = NEG, b2 = NEG;
-        for (int j = 0; j < per; ++j) {
-          const double c = cs[lane * per + j];
-          if (c > b1) { b2 = b1; b1 = c; } else if (c > b2) { b2 = c; }
+      double b1 = NEG, b2 = NEG;
+      const int lanes = per / V;
+      const bool aligned = per % V == 0 && lanes <= 16 && (lanes & (lanes - 1)) == 0;
+      if (aligned) {
+        // a group is an aligned power of two of whole lanes
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          double x;
+          if constexpr (WIDE) x = c[i]; else x = (double)key[i];
+          b2 = fmax(b2, fmin(b1, x));
+          b1 = fmax(b1, x);
         }
-        worth = A.best == 2 && b2 > NEG ? b1 + b2 : b1;
+        if (lanes > 1) merge_best<0>(b1, b2);
+        if (lanes > 2) merge_best<1>(b1, b2);
+        if (lanes > 4) merge_best<2>(b1, b2);
+        if (lanes > 8) merge_best<3>(b1, b2);
+        // lane g takes group g's from the group's first lane
+        const double w1 = __shfl(b1, (lane * lanes) & 63, 64), w2 = __shfl(b2, (lane * lanes) & 63, 64);
+        b1 = w1;
+        b2 = w2;
+      } else {
+        double* cs = sh + (size_t)wave * A.E;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          double x;
+          if constexpr (WIDE) x = c[i]; else x = (double)key[i];
+          if (lane * V + i < A.E) cs[lane * V + i] = x;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        if (lane < A.groups)
+          for (int j = 0; j < per; ++j) {
+            const double x = cs[lane * per + j];
+            b2 = fmax(b2, fmin(b1, x));
+            b1 = fmax(b1, x);
+          }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
       }
-      __syncthreads();
-      int rank = 0;
-      for (int g = 0; g < A.groups; ++g) {
-        const double o = __shfl(worth, g, 64);
-        rank += o > worth || (o == worth && g < lane);
-      }
-      const unsigned long long keep = __ballot(lane < A.groups && rank < A.kept);
+      const double worth = A.best == 2 && b2 > NEG ? b1 + b2 : b1;
+      const unsigned long long keep = keep_groups(worth, A.groups, A.kept, lane);
+      const int mine = aligned ? lane >> (__ffs(lanes) - 1) : 0;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int e = lane + 64 * i;
-        if (e < A.E && !((keep >> (e / per)) & 1)) key[i] = NEG;
+        const int g = aligned ? mine : (lane * V + i) / per;
+        if (!((keep >> (g & 63)) & 1)) {
+          key[i] = NEGF;
+          if constexpr (WIDE) c[i] = NEG;
+        }
       }
     }
-    // k rounds: the largest key, the lowest expert among equals
     int my_e = -1;
-    double my_s = 0.0;
-    for (int j = 0; j < A.K; ++j) {
-      double m = NEG;
+    float my_s = 0.f;
+    // a choice by rounded scores needs one more maximum to show that no two
+    // are equal
+    const bool check = WIDE && A.bias;
+    float k32[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) m = key[i] > m ? key[i] : m;
-      m = wave_max(m);
-      int at = 0x7fffffff;
+    for (int i = 0; i < V; ++i) k32[i] = key[i];
+    float before = __builtin_huge_valf();
+    bool tie = false;
+    for (int j = 0; j < A.K + (check ? 1 : 0); ++j) {
+      float head = k32[0], hs = s[0];
+      int hi = 0;
 #pragma unroll
-      for (int i = V - 1; i >= 0; --i)
-        if (key[i] == m && m > NEG) at = lane + 64 * i;
-#pragma unroll
-      for (int d = 32; d >= 1; d >>= 1) at = min(at, __shfl_xor(at, d, 64));
-      const bool none = at == 0x7fffffff;
-      double sc = 0.0;
+      for (int i = 1; i < V; ++i)
+        if (k32[i] > head) {
+          head = k32[i];
+          hs = s[i];
+          hi = i;
+        }
+      const float m = wave_max(head);
+      if (!(m > NEGF)) break;
+      if (check && m == before) {
+        tie = true;
+        break;
+      }
+      before = m;
+      if (j == A.K) break;
+      const int win = __ffsll((unsigned long long)__ballot(head == m)) - 1;
+      const int e = win * V + __builtin_amdgcn_readlane(hi, win);
+      const float sc = lane_value(hs, win);
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (lane + 64 * i == at) {
-          sc = s[i];
-          key[i] = NEG;
-        }
-      sc = __shfl(sc, at & 63, 64);
+        if (lane * V + i == e) k32[i] = NEGF;
       if (lane == j) {
-        my_e = none ? -1 : at;
-        my_s = none ? 0.0 : sc;
+        my_e = e;
+        my_s = sc;
       }
     }
-    if (A.renorm) my_s /= wave_sum(lane < A.K ? my_s : 0.0) + 1e-20;
-    if (live && lane < A.K) {
+    if constexpr (WIDE) {
+      if (tie) {
+        my_e = -1;
+        my_s = 0.f;
+        for (int j = 0; j < A.K; ++j) {
+          double head = c[0];
+          float hs = s[0];
+          int hi = 0;
+#pragma unroll
+          for (int i = 1; i < V; ++i)
+            if (c[i] > head) {
+              head = c[i];
+              hs = s[i];
+              hi = i;
+            }
+          double m = head;
+          m = fmax(m, other<0>(m));
+          m = fmax(m, other<1>(m));
+          m = fmax(m, other<2>(m));
+          m = fmax(m, other<3>(m));
+          m = fmax(m, other<4>(m));
+          m = fmax(m, other<5>(m));
+          if (!(m > NEG)) break;
+          const int win = __ffsll((unsigned long long)__ballot(head == m)) - 1;
+          const int e = win * V + __builtin_amdgcn_readlane(hi, win);
+          const float sc = lane_value(hs, win);
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (lane * V + i == e) c[i] = NEG;
+          if (lane == j) {
+            my_e = e;
+            my_s = sc;
+          }
+        }
+      }
+    }
+    if (A.renorm) my_s /= wave_sum(my_s) + 1e-20f;  // lanes past K hold zeros
+    if (lane < A.K) {
       A.expert[t * A.K + lane] = my_e;
-      A.weight[t * A.K + lane] = (float)(my_s * (double)A.scale);
+      A.weight[t * A.K + lane] = my_s * A.scale;
     }
   }
 }
@@ -174,35 +368,38 @@ struct BwdArgs {
 
 // t_j = scale dw_j; renorm: ds_j = (t_j - sum_i t_i s_i / S) / S with
 // S = sum s + 1e-20, else ds_j = t_j; then softmax: dl = s (ds - sum ds s),
-// sigmoid: dl = s (1 - s) ds.  One wavefront a token.
+// sigmoid: dl = s (1 - s) ds.  One wavefront a token; slot j is lane j's.
 template <typename T, int V, bool SIGMOID>
 __global__ __launch_bounds__(NT) void bwd_kernel(BwdArgs A) {
-  extern __shared__ float shf[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float* ss = shf + (size_t)wave * 2 * A.E;
-  float* ds = ss + A.E;
-  const T* logits = reinterpret_cast<const T*>(A.logits);
-  T* out = reinterpret_cast<T*>(A.dlogits);
-  const int64_t rounds = (A.N + (int64_t)gridDim.x * WAVES - 1) / ((int64_t)gridDim.x * WAVES);
-  for (int64_t it = 0; it < rounds; ++it) {
-    const int64_t t = (it * gridDim.x + blockIdx.x) * WAVES + wave;
-    const bool live = t < A.N;
-    float l[V], s[V];
-    float top = -__builtin_huge_valf();
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = lane + 64 * i;
-      float x = live && e < A.E ? load_logit<T>(logits, t * A.E + e) : -__builtin_huge_valf();
-      if (!(x > TP_ROUTE_LOWEST)) x = -__builtin_huge_valf();
-      l[i] = fminf(x, TP_ROUTE_LARGEST);
-      top = fmaxf(top, l[i]);
+  for (int64_t t = (int64_t)blockIdx.x * WAVES + wave; t < A.N; t += (int64_t)gridDim.x * WAVES) {
+    const T* row = reinterpret_cast<const T*>(A.logits) + t * A.E;
+    int e = -1;
+    int64_t r = -1;
+    if (lane < A.K) {
+      e = A.expert[t * A.K + lane];
+      r = A.slot_row ? (int64_t)A.slot_row[t * A.K + lane] : t * A.K + lane;
     }
+    float l[V], s[V];
+    load_row<T, V>(row, A.E, lane, true, l);
+    if (e < 0 || e >= A.E) e = -1;
+    float up = 0.f, le = -__builtin_huge_valf();
+    if (e >= 0) {
+      if (!A.slot_row || (r >= 0 && r < A.R)) up = A.d_weight[r] * A.scale;
+      if constexpr (sizeof(T) == 2) le = bf16_to_f32(row[e]); else le = row[e];
+    }
+    if (!(le > TP_ROUTE_LOWEST)) le = -__builtin_huge_valf();
+    le = fminf(le, TP_ROUTE_LARGEST);
+    float se;
     if constexpr (SIGMOID) {
 #pragma unroll
       for (int i = 0; i < V; ++i) s[i] = l[i] > TP_ROUTE_LOWEST ? 1.f / (1.f + expf(-l[i])) : 0.f;
+      se = le > TP_ROUTE_LOWEST ? 1.f / (1.f + expf(-le)) : 0.f;
     } else {
+      float top = l[0], sum = 0.f;
+#pragma unroll
+      for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
       top = wave_max(top);
-      float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         s[i] = l[i] > TP_ROUTE_LOWEST ? expf(l[i] - top) : 0.f;
@@ -212,195 +409,230 @@ __global__ __launch_bounds__(NT) void bwd_kernel(BwdArgs A) {
       const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) s[i] *= inv;
+      se = le > TP_ROUTE_LOWEST ? expf(le - top) * inv : 0.f;
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = lane + 64 * i;
-      if (e < A.E) {
-        ss[e] = s[i];
-        ds[e] = 0.f;
-      }
-    }
-    __syncthreads();
-    int e = -1;
-    float up = 0.f;
-    if (live && lane < A.K) {
-      e = A.expert[t * A.K + lane];
-      if (e < 0 || e >= A.E) e = -1;
-      if (A.slot_row) {
-        const int32_t r = A.slot_row[t * A.K + lane];
-        up = r >= 0 && r < A.R ? A.d_weight[r] : 0.f;
-      } else {
-        up = A.d_weight[t * A.K + lane];
-      }
-      up = e < 0 ? 0.f : up * A.scale;
-    }
-    const float se = e >= 0 ? ss[e] : 0.f;
     float d = up;
     if (A.renorm) {
       const float S = wave_sum(se) + 1e-20f;
       d = (up - wave_sum(up * se / S)) / S;
     }
     if (e < 0) d = 0.f;
-    // an expert that stands twice counts twice: each of its slots writes the
-    // same sum, taken in slot order
-    float all = 0.f;
+    float ds[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) ds[i] = 0.f;
+    // an expert that stands twice counts twice, in slot order
     for (int j = 0; j < A.K; ++j) {
-      const int ej = __shfl(e, j, 64);
-      const float dj = __shfl(d, j, 64);
-      if (ej == e) all += dj;
+      const int ej = __builtin_amdgcn_readlane(e, j);
+      const float dj = lane_value(d, j);
+#pragma unroll
+      for (int i = 0; i < V; ++i) ds[i] += lane * V + i == ej ? dj : 0.f;
     }
-    if (e >= 0) ds[e] = all;
-    __syncthreads();
     float dot = 0.f;
     if constexpr (!SIGMOID) dot = wave_sum(d * se);
+    T* out = reinterpret_cast<T*>(A.dlogits) + t * A.E;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int x = lane + 64 * i;
-      if (x < A.E && live) {
-        const float g = SIGMOID ? s[i] * (1.f - s[i]) * ds[x] : s[i] * (ds[x] - dot);
-        store_logit(out, t * A.E + x, g);
+    for (int i = 0; i < V; ++i) ds[i] = SIGMOID ? s[i] * (1.f - s[i]) * ds[i] : s[i] * (ds[i] - dot);
+    const int e0 = lane * V;
+    if (V > 1 && A.E % V == 0) {
+      if (e0 < A.E) {
+        constexpr int BYTES = V * (int)sizeof(T) < 16 ? V * (int)sizeof(T) : 16;
+        constexpr int PER = BYTES / (int)sizeof(T);
+        struct alignas(BYTES) Part { T x[PER]; };
+#pragma unroll
+        for (int i = 0; i < V; i += PER) {
+          Part q;
+#pragma unroll
+          for (int j = 0; j < PER; ++j) {
+            if constexpr (sizeof(T) == 2) q.x[j] = f32_to_bf16(ds[i + j]); else q.x[j] = ds[i + j];
+          }
+          *reinterpret_cast<Part*>(out + e0 + i) = q;
+        }
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (e0 + i < A.E) {
+          if constexpr (sizeof(T) == 2) out[e0 + i] = f32_to_bf16(ds[i]); else out[e0 + i] = ds[i];
+        }
     }
-    __syncthreads();
   }
 }
 
 // ---------------------------------------------------------------------------
 // Dispatch tables: a stable counting sort of the (token, slot) pairs by
-// local expert.  A wavefront takes a run of whole tokens (`run` pairs): it
-// counts its pairs for each expert (count_kernel), scan_kernel turns the
-// counts, expert by expert and run by run, into each run's first row of
-// each expert, and place_kernel deals the rows out.
-//   ws: cnt [n_local][runs], tok [runs]
+// local expert.  A workgroup takes a run of whole tokens, one pair a thread:
+// a pair's row is its expert's first row, plus the expert's pairs in earlier
+// runs, in earlier wavefronts and in lower lanes.
+//   ws: cnt [runs][n_local + 1], pairs of each expert in each run (last: all)
+// One run needs no counts of others.  Up to FEW runs, place_kernel adds up
+// the earlier runs' counts itself; beyond, scan_kernel turns the counts into
+// sums over the earlier runs, and leaves the totals in row `runs`.
 // ---------------------------------------------------------------------------
-constexpr int RUN = 256;  // pairs of a run, at most
+constexpr int RUN = 1024;  // threads of a run
+constexpr int FEW = 128;
 static int run_tokens(int K) { return RUN / K; }
 
-__global__ __launch_bounds__(64) void count_kernel(TablesArgs A, int tokens, int runs) {
+__device__ __forceinline__ int local_expert(const TablesArgs& A, int64_t f, int64_t f1) {
+  if (f >= f1) return -1;
+  const int32_t x = A.expert[f];
+  return x >= A.first && x - A.first < A.n_local ? x - A.first : -1;
+}
+
+__global__ __launch_bounds__(RUN) void count_kernel(TablesArgs A, int pairs) {
   extern __shared__ int hist[];
-  const int run = blockIdx.x, lane = threadIdx.x;
-  for (int e = lane; e < A.n_local; e += 64) hist[e] = 0;
+  const int width = A.n_local + 1;
+  for (int e = threadIdx.x; e < width; e += RUN) hist[e] = 0;
   __syncthreads();
-  const int64_t f0 = (int64_t)run * tokens * A.K;
-  const int64_t f1 = min(f0 + (int64_t)tokens * A.K, A.N * A.K);
-  int mine = 0;
-  for (int64_t f = f0 + lane; f < f1; f += 64) {
-    const int32_t x = A.expert[f];
-    if (x >= A.first && x - A.first < A.n_local) {
-      atomicAdd(&hist[x - A.first], 1);
-      ++mine;
+  const int64_t f0 = (int64_t)blockIdx.x * pairs, f1 = min(f0 + pairs, A.N * A.K);
+  const int e = threadIdx.x < pairs ? local_expert(A, f0 + threadIdx.x, f1) : -1;
+  if (e >= 0) atomicAdd(&hist[e], 1);
+  const unsigned long long on = __ballot(e >= 0);
+  if ((threadIdx.x & 63) == 0) atomicAdd(&hist[A.n_local], (int)__popcll(on));
+  __syncthreads();
+  for (int i = threadIdx.x; i < width; i += RUN) A.ws[(int64_t)blockIdx.x * width + i] = hist[i];
+}
+
+// 64 columns a workgroup, 16 shares of the runs
+__global__ __launch_bounds__(RUN) void scan_kernel(TablesArgs A, int runs) {
+  __shared__ int part[16][64];
+  const int width = A.n_local + 1;
+  const int lane = threadIdx.x & 63, share = threadIdx.x >> 6;
+  const int e = blockIdx.x * 64 + lane;
+  const int each = (runs + 15) / 16, r0 = min(share * each, runs), r1 = min(r0 + each, runs);
+  int sum = 0;
+  if (e < width)
+    for (int r = r0; r < r1; ++r) sum += A.ws[(int64_t)r * width + e];
+  part[share][lane] = sum;
+  __syncthreads();
+  int base = 0;
+  for (int i = 0; i < share; ++i) base += part[i][lane];
+  if (e >= width) return;
+  for (int r = r0; r < r1; ++r) {
+    int* p = A.ws + (int64_t)r * width + e;
+    const int v = *p;
+    *p = base;
+    base += v;
+  }
+  if (share == 15) A.ws[(int64_t)runs * width + e] = base;
+}
+
+__global__ __launch_bounds__(RUN) void place_kernel(TablesArgs A, int pairs, int runs) {
+  extern __shared__ int lds[];
+  const int width = A.n_local + 1;
+  int* first = lds;                 // [n_local + 1] first row of each expert in this run
+  int* total = first + width;       // [n_local + 1] rows of each expert in all
+  int* seen = total + width;        // [RUN] experts of this run's pairs
+  int* red = seen + RUN;            // [32]
+  uint16_t* waves = reinterpret_cast<uint16_t*>(red + 32);  // [16][n_local] pairs in earlier wavefronts
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int run = blockIdx.x;
+  const int64_t f0 = (int64_t)run * pairs, f1 = min(f0 + pairs, A.N * A.K), f = f0 + tid;
+  const int e = tid < pairs ? local_expert(A, f, f1) : -1;
+  seen[tid] = e;
+  for (int i = tid; i < 16 * A.n_local; i += RUN) waves[i] = 0;
+  for (int i = tid; i < 2 * width; i += RUN) lds[i] = 0;
+  __syncthreads();
+  // rank among the lanes with the same expert
+  const unsigned long long below = (1ull << lane) - 1;
+  const unsigned long long on = __ballot(e >= 0);
+  unsigned long long same = on;
+  for (int b = 0; (1 << b) < A.n_local; ++b) {
+    const unsigned long long bit = __ballot((e >> b) & 1);
+    same &= (e >> b) & 1 ? bit : ~bit;
+  }
+  const int rank = __popcll(same & below);
+  if (e >= 0 && rank == 0) waves[wave * A.n_local + e] = (uint16_t)__popcll(same);
+  if (lane == 0) red[wave] = __popcll(on);
+  // the other runs
+  if (runs > FEW) {
+    for (int i = tid; i < width; i += RUN) {
+      first[i] = A.ws[(int64_t)run * width + i];
+      total[i] = A.ws[(int64_t)runs * width + i];
+    }
+  } else if (runs > 1) {
+    // column by column, the runs dealt to as many threads as there are
+    const int shares = max(1, RUN / width);
+    for (int i = tid; i < width * shares; i += RUN) {
+      const int col = i % width, share = i / width;
+      int before = 0, all = 0;
+      for (int r = share; r < runs; r += shares) {
+        const int v = A.ws[(int64_t)r * width + col];
+        all += v;
+        before += r < run ? v : 0;
+      }
+      if (all) atomicAdd(&total[col], all);
+      if (before) atomicAdd(&first[col], before);
     }
   }
   __syncthreads();
-  for (int e = lane; e < A.n_local; e += 64) A.ws[(int64_t)e * runs + run] = hist[e];
-  mine = wave_sum(mine);
-  if (lane == 0) A.ws[(int64_t)A.n_local * runs + run] = mine;
-}
-
-// exclusive sums of one array of `n` ints in place by one workgroup;
-// returns the total
-__device__ int block_exclusive(int* a, int64_t n, int* red) {
-  int carry = 0;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int64_t i0 = 0; i0 < n; i0 += 1024) {
-    const int64_t i = i0 + threadIdx.x;
-    const int v = i < n ? a[i] : 0;
+  // pairs in earlier wavefronts; with one run the sums are the totals
+  for (int i = tid; i < A.n_local; i += RUN) {
+    int sum = 0;
+    for (int w = 0; w < 16; ++w) {
+      const int v = waves[w * A.n_local + i];
+      waves[w * A.n_local + i] = (uint16_t)sum;
+      sum += v;
+    }
+    if (runs <= 1) total[i] = sum;
+  }
+  int mine = 0, listed = 0;  // list entries in earlier wavefronts, and of the run
+  for (int w = 0; w < 16; ++w) {
+    mine += w < wave ? red[w] : 0;
+    listed += red[w];
+  }
+  if (runs <= 1 && tid == 0) total[A.n_local] = listed;
+  __syncthreads();
+  // first rows: exclusive sums of the totals over the experts (n_local <=
+  // RUN: one each)
+  {
+    const int v = tid < A.n_local ? total[tid] : 0;
     int x = v;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int u = __shfl_up(x, d, 64);
       if (lane >= d) x += u;
     }
-    if (lane == 63) red[wave] = x;
+    if (lane == 63) red[16 + wave] = x;
     __syncthreads();
-    int before = carry, all = 0;
-    for (int w = 0; w < 16; ++w) {
-      before += w < wave ? red[w] : 0;
-      all += red[w];
+    int base = x - v;
+    for (int w = 0; w < wave; ++w) base += red[16 + w];
+    if (tid < A.n_local) {
+      first[tid] += base;
+      if (run == 0) A.offsets[tid] = base;
     }
-    if (i < n) a[i] = before + x - v;
-    carry += all;
-    __syncthreads();
   }
-  return carry;
-}
-
-// workgroup 0: rows (all experts' runs in order) and the offsets;
-// workgroup 1: the tokens' lists
-__global__ __launch_bounds__(1024) void scan_kernel(TablesArgs A, int runs) {
-  __shared__ int red[16];
-  if (blockIdx.x == 0) {
-    const int total = block_exclusive(A.ws, (int64_t)A.n_local * runs, red);
-    __syncthreads();
-    for (int e = threadIdx.x; e < A.n_local; e += 1024)
-      A.offsets[e] = runs > 0 ? A.ws[(int64_t)e * runs] : 0;
-    if (threadIdx.x == 0) A.offsets[A.n_local] = total;
-  } else {
-    const int total = block_exclusive(A.ws + (int64_t)A.n_local * runs, runs, red);
-    if (threadIdx.x == 0) A.tok_ptr[A.N] = total;
+  const int rows = total[A.n_local];
+  if (run == 0 && tid == 0) {
+    A.offsets[A.n_local] = rows;
+    A.tok_ptr[A.N] = rows;
   }
-}
-
-__global__ __launch_bounds__(64) void place_kernel(TablesArgs A, int tokens, int runs) {
-  extern __shared__ int next[];
-  const int run = blockIdx.x, lane = threadIdx.x;
-  // rows past the last one
-  const int64_t total = A.tok_ptr[A.N];
-  for (int64_t r = total + (int64_t)run * 64 + lane; r < A.R; r += (int64_t)gridDim.x * 64) {
+  __syncthreads();
+  for (int64_t r = rows + (int64_t)run * RUN + tid; r < A.R; r += (int64_t)gridDim.x * RUN) {
     A.row_token[r] = -1;
     A.tok_rows[r] = -1;
     if (A.row_weight) A.row_weight[r] = 0.f;
   }
-  if (run >= runs) return;
-  for (int e = lane; e < A.n_local; e += 64) next[e] = A.ws[(int64_t)e * runs + run];
-  __syncthreads();
-  int before = A.ws[(int64_t)A.n_local * runs + run];  // list entries of earlier tokens
-  const int64_t f0 = (int64_t)run * tokens * A.K;
-  const int64_t f1 = min(f0 + (int64_t)tokens * A.K, A.N * A.K);
-  const unsigned long long below = (1ull << lane) - 1;
-  for (int64_t base = f0; base < f1; base += 64) {
-    const int64_t f = base + lane;
-    int e = -1;
-    if (f < f1) {
-      const int32_t x = A.expert[f];
-      if (x >= A.first && x - A.first < A.n_local) e = x - A.first;
-    }
-    // the lanes with the same expert
-    const unsigned long long on = __ballot(e >= 0);
-    unsigned long long same = on;
-    for (int b = 0; (1 << b) < A.n_local; ++b) {
-      const unsigned long long bit = __ballot((e >> b) & 1);
-      same &= (e >> b) & 1 ? bit : ~bit;
-    }
-    int row = -1;
-    if (e >= 0) row = next[e] + __popcll(same & below);
-    __syncthreads();
-    if (e >= 0 && !(same & ~below & ~(1ull << lane))) next[e] = row + 1;
-    __syncthreads();
-    if (f < f1) {
-      const int64_t t = f / A.K;
-      const int j = (int)(f - t * A.K);
-      A.slot_row[f] = row;
-      // list entries of earlier slots of this token, and of lower rows
-      int earlier = 0, lower = 0;
-      for (int i = 0; i < A.K; ++i) {
-        const int32_t x = A.expert[t * A.K + i];
-        if (x < A.first || x - A.first >= A.n_local) continue;
-        const int o = x - A.first;
-        earlier += i < j;
-        lower += o < e || (o == e && i < j);
-      }
-      const int start = before + __popcll(on & below) - earlier;
-      if (j == 0) A.tok_ptr[t] = start;
-      if (row >= 0) {
-        A.tok_rows[start + lower] = row;
-        A.row_token[row] = (int32_t)t;
-        if (A.row_weight) A.row_weight[row] = A.weight[f];
-      }
-    }
-    before += __popcll(on);
+  if (tid >= pairs || f >= f1) return;
+  const int slot = tid % A.K, token0 = tid - slot;
+  const int64_t t = (int64_t)run * (pairs / A.K) + tid / A.K;
+  // list entries of this token's earlier slots, and of its lower rows
+  int earlier = 0, lower = 0;
+  for (int i = 0; i < A.K; ++i) {
+    const int o = seen[token0 + i];
+    if (o < 0) continue;
+    earlier += i < slot;
+    lower += o < e || (o == e && i < slot);
   }
+  const int start = first[A.n_local] + mine + __popcll(on & below) - earlier;
+  if (slot == 0) A.tok_ptr[t] = start;
+  int row = -1;
+  if (e >= 0) {
+    row = first[e] + waves[wave * A.n_local + e] + rank;
+    A.tok_rows[start + lower] = row;
+    A.row_token[row] = (int32_t)t;
+    if (A.row_weight) A.row_weight[row] = A.weight[f];
+  }
+  A.slot_row[f] = row;
 }
 
 template <typename F>
@@ -431,10 +663,16 @@ hipError_t route_fwd_launch(const tp_route_desc& d, const void* logits, const fl
   if (d.N == 0) return hipSuccess;
   FwdArgs a{logits, bias, expert, weight, d.N, d.E, d.K, d.groups, d.groups_kept, d.group_best,
             d.renorm, d.scale};
+  const bool wide = bias || (d.groups > 1 && d.group_best == 2);
   return pick(d.dtype, d.E, d.score, [&](auto t, auto v, auto sig) {
     const size_t lds = d.groups > 1 ? (size_t)WAVES * d.E * sizeof(double) : 0;
-    hipLaunchKernelGGL((fwd_kernel<decltype(t), decltype(v)::value, decltype(sig)::value>),
-                       dim3(grid_tokens(d.N)), dim3(NT), lds, st, a);
+    const dim3 grid(grid_tokens(d.N));
+    if (wide)
+      hipLaunchKernelGGL((fwd_kernel<decltype(t), decltype(v)::value, decltype(sig)::value, true>),
+                         grid, dim3(NT), lds, st, a);
+    else
+      hipLaunchKernelGGL((fwd_kernel<decltype(t), decltype(v)::value, decltype(sig)::value, false>),
+                         grid, dim3(NT), lds, st, a);
     return hipGetLastError();
   });
 }
@@ -447,8 +685,7 @@ hipError_t route_bwd_launch(const tp_route_desc& d, const void* logits, const in
   BwdArgs a{logits, expert, d_weight, slot_row, dlogits, d.N, R, d.E, d.K, d.renorm, d.scale};
   return pick(d.dtype, d.E, d.score, [&](auto t, auto v, auto sig) {
     hipLaunchKernelGGL((bwd_kernel<decltype(t), decltype(v)::value, decltype(sig)::value>),
-                       dim3(grid_tokens(d.N)), dim3(NT), (size_t)WAVES * 2 * d.E * sizeof(float),
-                       st, a);
+                       dim3(grid_tokens(d.N)), dim3(NT), 0, st, a);
     return hipGetLastError();
   });
 }
@@ -456,27 +693,28 @@ hipError_t route_bwd_launch(const tp_route_desc& d, const void* logits, const in
 size_t route_tables_workspace(int64_t N, int K, int n_local) {
   const int64_t tokens = route::run_tokens(K);
   const int64_t runs = (N + tokens - 1) / tokens;
-  return (size_t)(runs * ((int64_t)n_local + 1)) * sizeof(int32_t);
+  if (runs <= 1) return 16;  // not used; a caller need not tell sizes apart
+  return (size_t)(runs + (runs > route::FEW ? 1 : 0)) * ((size_t)n_local + 1) * sizeof(int32_t);
 }
 
 hipError_t route_tables_launch(const TablesArgs& a, hipStream_t st) {
   using namespace route;
-  const int tokens = run_tokens(a.K);
+  const int tokens = run_tokens(a.K), pairs = tokens * a.K;
   const int runs = (int)((a.N + tokens - 1) / tokens);
-  const size_t lds = (size_t)a.n_local * sizeof(int);
+  const size_t width = (size_t)a.n_local + 1;
   hipError_t he = hipSuccess;
-  if (runs > 0) {
-    hipLaunchKernelGGL(count_kernel, dim3((unsigned)runs), dim3(64), lds, st, a, tokens, runs);
+  if (runs > 1) {
+    hipLaunchKernelGGL(count_kernel, dim3((unsigned)runs), dim3(RUN), width * sizeof(int), st, a, pairs);
     if ((he = hipGetLastError()) != hipSuccess) return he;
   }
-  hipLaunchKernelGGL(scan_kernel, dim3(2), dim3(1024), 0, st, a, runs);
-  if ((he = hipGetLastError()) != hipSuccess) return he;
-  if (runs > 0 || a.R > 0) {
-    hipLaunchKernelGGL(place_kernel, dim3((unsigned)(runs > 0 ? runs : 64)), dim3(64), lds, st, a,
-                       tokens, runs);
-    he = hipGetLastError();
+  if (runs > FEW) {
+    hipLaunchKernelGGL(scan_kernel, dim3((unsigned)((width + 63) / 64)), dim3(RUN), 0, st, a, runs);
+    if ((he = hipGetLastError()) != hipSuccess) return he;
   }
-  return he;
+  const size_t lds = (2 * width + RUN + 32) * sizeof(int) + 16 * (size_t)a.n_local * sizeof(uint16_t);
+  hipLaunchKernelGGL(place_kernel, dim3((unsigned)(runs > 0 ? runs : 1)), dim3(RUN), lds, st, a,
+                     pairs, runs);
+  return hipGetLastError();
 }
 
 }  // namespace tpmlp
