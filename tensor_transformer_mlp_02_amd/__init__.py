@@ -157,12 +157,23 @@ def _ptr(t, nbytes: Optional[int] = None, name: str = "tensor",
     return _address(t, nbytes, name, dtype, _current_device())
 
 
+_torch = None
+
+
+def _get_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _current_device() -> int:
     """The current GPU, -1 where there is none."""
-    import torch
+    t = _get_torch()
     # the C function behind torch.cuda.current_device(), without its checks
     # on every call: a process that holds a GPU tensor is initialised
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+    return t._C._cuda_getDevice() if t.cuda.is_initialized() else -1
 
 
 def _address(t, nbytes, name, dtype, device) -> int:
@@ -182,14 +193,26 @@ def _address(t, nbytes, name, dtype, device) -> int:
 _DTYPE_NAMES = {n: f"torch.{n}" for n in ("int32", "float32", "bfloat16")}
 
 
+_addresses = None
+
+
 def _sized(items):
     """_ptr of each (tensor, bytes, name) or (tensor, bytes, name, dtype)."""
-    device = None
+    global _addresses
+    device = _current_device()
+    if device >= 0:
+        if _addresses is None:
+            try:
+                from ._marshal import addresses as _addresses
+            except ImportError:  # not built: the loop below does the same, slower
+                _addresses = False
+        if _addresses:
+            out = _addresses(items, device)
+            if out is not None:
+                return out
     out = []
     for t, nbytes, name, *dtype in items:
         if t is not None and not isinstance(t, int):
-            if device is None:
-                device = _current_device()
             t = _address(t, nbytes, name, dtype[0] if dtype else None, device)
         out.append(t)
     return out
@@ -198,7 +221,7 @@ def _sized(items):
 def _stream(stream) -> Optional[int]:
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
+    torch = _get_torch()
     if torch.cuda.is_initialized():
         # the current stream's handle itself (torch.cuda.current_stream() builds an object)
         return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())

@@ -46,6 +46,25 @@ def _compile(src: str, verbose: bool, build_dir: str, defines) -> str:
     return obj
 
 
+def build_marshal(verbose: bool = False) -> str:
+    """_marshal.so: the binding's check of a call's tensors, against torch's C++ headers."""
+    import importlib.util
+    import sysconfig
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    out = os.path.join(HERE, "_marshal.so")
+    tmp = out + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-I" + sysconfig.get_path("include"), "-I" + os.path.join(torch_dir, "include"),
+           "-I" + os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           os.path.join(CSRC, "marshal.cpp"), "-o", tmp, "-L" + os.path.join(torch_dir, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, out)
+    return out
+
+
 def build(verbose: bool = False, defines=(), out=None) -> str:
     defines = list(defines)
     build_dir = BUILD_DIR
@@ -57,8 +76,11 @@ def build(verbose: bool = False, defines=(), out=None) -> str:
     if defines and os.path.abspath(out) == OUT:
         raise ValueError("a build with defines may not replace the default library")
     os.makedirs(build_dir, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        marshal = None if defines else ex.submit(build_marshal, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose, build_dir, defines), SOURCES))
+        if marshal:
+            marshal.result()
     tmp = out + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     if verbose:
