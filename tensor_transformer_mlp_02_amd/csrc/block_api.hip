@@ -72,36 +72,36 @@ int check_tables_shape(int64_t N, int32_t K, int32_t n_local) {
   return TP_OK;
 }
 
+// The step's buffers, to see that no two overlap.  Those of one kind usually
+// lie in the list's order: then each has to start behind the one before and
+// the kinds have to lie apart as wholes, told in one walk; otherwise they are
+// all sorted.
 struct Span {
   uintptr_t lo, hi;
   int32_t tensor;
   const char* name;
 };
-
-// no two of the step's buffers overlap.  Buffers of one kind usually lie in
-// the list's order: then each kind is checked by neighbours and the kinds
-// by their hulls; otherwise everything is sorted.
-int check_spans(std::vector<Span>* kinds, int nk) {
+struct Kind {
+  uintptr_t lo = 0, hi = 0;
   bool ordered = true;
-  Span hull[16];
-  int nh = 0;
-  for (int k = 0; k < nk && ordered; ++k) {
-    const std::vector<Span>& v = kinds[k];
-    for (size_t i = 1; i < v.size() && ordered; ++i) ordered = v[i].lo >= v[i - 1].hi;
-    if (!v.empty()) hull[nh++] = Span{v.front().lo, v.back().hi, -1, v.front().name};
+  void add(const Buf& b) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(b.p);
+    if (!hi) lo = p;
+    else if (p < hi) ordered = false;
+    hi = p + b.bytes;
   }
-  for (int i = 0; i < nh && ordered; ++i)
-    for (int j = 0; j < i && ordered; ++j)
-      ordered = hull[i].hi <= hull[j].lo || hull[j].hi <= hull[i].lo;
-  if (ordered) return TP_OK;
-  std::vector<Span> all;
-  for (int k = 0; k < nk; ++k) all.insert(all.end(), kinds[k].begin(), kinds[k].end());
-  std::sort(all.begin(), all.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
-  for (size_t i = 1; i < all.size(); ++i)
-    if (all[i].lo < all[i - 1].hi)
-      return fail(TP_ERR_ALIAS, "%s of tensor %d and %s of tensor %d overlap", all[i - 1].name,
-                  all[i - 1].tensor, all[i].name, all[i].tensor);
-  return TP_OK;
+};
+
+constexpr int kKinds = 7;
+void step_buffers(const tp_adamw_tensor& t, size_t ge, size_t se, bool q, Buf (&b)[kKinds]) {
+  const size_t c = (size_t)t.count, blocks = (c + TP_ADAMW_BLOCK - 1) / TP_ADAMW_BLOCK;
+  b[0] = {t.param, c * 4, "param"};
+  b[1] = {t.grad, c * ge, "grad"};
+  b[2] = {t.m, c * se, "m"};
+  b[3] = {t.v, c * se, "v"};
+  b[4] = {t.param_bf16, t.param_bf16 ? c * 2 : 0, "param_bf16"};
+  b[5] = {t.m_scale, q ? blocks * 4 : 0, "m_scale"};
+  b[6] = {t.v_scale, q ? blocks * 4 : 0, "v_scale"};
 }
 
 }  // namespace
@@ -337,45 +337,61 @@ int tp_adamw_step(const tp_adamw_desc* desc, int32_t n, const tp_adamw_tensor* t
   const bool q = d.state_bits == 8;
   const size_t ge = d.grad_dtype == TP_BF16 ? 2 : 4, se = q ? 1 : 4;
   int rc;
-  try {
-    std::vector<Span> kinds[8];
-    for (int k = 0; k < 7; ++k) kinds[k].reserve((size_t)n);
-    for (int32_t i = 0; i < n; ++i) {
-      const tp_adamw_tensor& t = tensors[i];
-      if (t.count < 0 || t.count > ((int64_t)1 << 40))
-        return fail(TP_ERR_SHAPE, "count of tensor %d must be in 0..2^40", i);
-      if (!isfinite(t.weight_decay))
-        return fail(TP_ERR_SHAPE, "weight_decay of tensor %d must be finite", i);
-      if (t.reserved != 0) return fail(TP_ERR_SHAPE, "reserved of tensor %d must be 0", i);
-      if (!q && (t.m_scale || t.v_scale))
-        return fail(TP_ERR_SHAPE, "m_scale and v_scale of tensor %d must be NULL with 32-bit states", i);
-      const size_t c = (size_t)t.count, blocks = (c + TP_ADAMW_BLOCK - 1) / TP_ADAMW_BLOCK;
-      const Buf b[] = {{t.param, c * 4, "param"},
-                       {t.grad, c * ge, "grad"},
-                       {t.m, c * se, "m"},
-                       {t.v, c * se, "v"},
-                       {t.param_bf16, t.param_bf16 ? c * 2 : 0, "param_bf16"},
-                       {t.m_scale, q ? blocks * 4 : 0, "m_scale"},
-                       {t.v_scale, q ? blocks * 4 : 0, "v_scale"}};
-      if ((rc = check_sized(b, 5)) || (rc = check_tables(b + 5, 2))) return rc;
-      for (int k = 0; k < 7; ++k)
-        if (b[k].bytes > 0) {
-          const uintptr_t lo = reinterpret_cast<uintptr_t>(b[k].p);
-          kinds[k].push_back(Span{lo, lo + b[k].bytes, i, b[k].name});
-        }
+  Kind kinds[kKinds];
+  Buf b[kKinds];
+  for (int32_t i = 0; i < n; ++i) {
+    const tp_adamw_tensor& t = tensors[i];
+    if (t.count < 0 || t.count > ((int64_t)1 << 40))
+      return fail(TP_ERR_SHAPE, "count of tensor %d must be in 0..2^40", i);
+    if (!isfinite(t.weight_decay))
+      return fail(TP_ERR_SHAPE, "weight_decay of tensor %d must be finite", i);
+    if (t.reserved != 0) return fail(TP_ERR_SHAPE, "reserved of tensor %d must be 0", i);
+    if (!q && (t.m_scale || t.v_scale))
+      return fail(TP_ERR_SHAPE, "m_scale and v_scale of tensor %d must be NULL with 32-bit states", i);
+    step_buffers(t, ge, se, q, b);
+    if ((rc = check_sized(b, 5)) || (rc = check_tables(b + 5, 2))) return rc;
+    for (int k = 0; k < kKinds; ++k)
+      if (b[k].bytes > 0) kinds[k].add(b[k]);
+  }
+  bool apart = true;
+  for (int k = 0; k < kKinds; ++k) {
+    apart = apart && kinds[k].ordered;
+    for (int j = 0; j < k; ++j)
+      if (kinds[k].hi && kinds[j].hi)
+        apart = apart && (kinds[k].hi <= kinds[j].lo || kinds[j].hi <= kinds[k].lo);
+  }
+  // the device scalars are read throughout the step
+  const void* scalars[] = {dev_step, dev_lr, grad_scale};
+  for (const void* p : scalars)
+    for (int k = 0; p && k < kKinds; ++k) {
+      const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+      if (kinds[k].hi && lo < kinds[k].hi && kinds[k].lo < lo + 4) apart = false;
     }
-    // the device scalars are read throughout the step
-    for (const void* p : {(const void*)dev_step, (const void*)dev_lr, (const void*)grad_scale})
-      if (p) {
-        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-        for (int k = 0; k < 7; ++k)
-          for (const Span& s : kinds[k])
-            if (lo < s.hi && s.lo < lo + 4)
-              return fail(TP_ERR_ALIAS, "a device scalar lies in %s of tensor %d", s.name, s.tensor);
+  if (!apart) {
+    try {
+      std::vector<Span> all;
+      all.reserve((size_t)n * kKinds + 3);
+      for (int32_t i = 0; i < n; ++i) {
+        step_buffers(tensors[i], ge, se, q, b);
+        for (int k = 0; k < kKinds; ++k) {
+          const uintptr_t lo = reinterpret_cast<uintptr_t>(b[k].p);
+          if (b[k].bytes > 0) all.push_back(Span{lo, lo + b[k].bytes, i, b[k].name});
+        }
       }
-    if ((rc = check_spans(kinds, 7))) return rc;
-  } catch (const std::bad_alloc&) {
-    return fail(TP_ERR_SHAPE, "out of host memory for %d tensors", n);
+      std::sort(all.begin(), all.end(), [](const Span& x, const Span& y) { return x.lo < y.lo; });
+      for (size_t i = 1; i < all.size(); ++i)
+        if (all[i].lo < all[i - 1].hi)
+          return fail(TP_ERR_ALIAS, "%s of tensor %d and %s of tensor %d overlap", all[i - 1].name,
+                      all[i - 1].tensor, all[i].name, all[i].tensor);
+      for (const void* p : scalars) {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+        for (const Span& x : all)
+          if (p && lo < x.hi && x.lo < lo + 4)
+            return fail(TP_ERR_ALIAS, "a device scalar lies in %s of tensor %d", x.name, x.tensor);
+      }
+    } catch (const std::bad_alloc&) {
+      return fail(TP_ERR_SHAPE, "out of host memory for %d tensors", n);
+    }
   }
   if ((rc = check_device())) return rc;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);

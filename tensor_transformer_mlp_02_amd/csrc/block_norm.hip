@@ -989,7 +989,10 @@ __global__ __launch_bounds__(NT) void zero_kernel(float4* p, int64_t n) {
 // workers of one call, with `at_once` rows to a worker's turn: as many as
 // there are compute units where each then has two turns or more
 static int workers_for(int64_t N, int64_t G, int at_once) {
-  int64_t w = (N + 2 * at_once - 1) / (2 * at_once);
+#ifndef TURNS
+#define TURNS 2
+#endif
+  int64_t w = (N + TURNS * at_once - 1) / (TURNS * at_once);
   if (w > CUS) w = CUS;
   if (w < 1) w = 1;
   if (G > 0 && G <= w) w = w / G * G;

@@ -57,6 +57,14 @@ __device__ __forceinline__ void load_row(const T* row, int E, int lane, bool liv
   }
 }
 
+// Shared memory that one wavefront writes and reads by itself: its accesses
+// are in order, the compiler has to keep them so.
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Moves within a wavefront that need no shared memory: lane ^ 1, ^ 2, the
 // mirror of 8 and of 16 lanes (which bring the other half once the halves
 // agree), and lane ^ 16, ^ 32.
@@ -125,233 +133,471 @@ struct FwdArgs {
   int64_t N;
   int E, K, groups, kept, best, renorm;
   float scale;
+  // groups: experts of one; whole lanes of one as a power of two (-1: it is
+  // none); x / per = x magic >> 20 for x < 1024
+  int per, lanes_log2;
+  uint32_t magic;
+  int wide_log2;  // lanes_log2 of the 64-bit choice
 };
 
-// The largest and second largest of a run of experts, merged over 2^STEPS
-// lanes
-template <int STEP>
-__device__ __forceinline__ void merge_best(double& b1, double& b2) {
-  const double o1 = other<STEP>(b1), o2 = other<STEP>(b2);
+// Keys in unsigned integers that order like the floats, 0 for an expert that
+// is not there: maxima need no canonical NaNs, and equal bits are equal keys.
+__device__ __forceinline__ uint32_t to_key(float x) {
+  const uint32_t u = __float_as_uint(x + 0.f);  // -0 is 0
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_key(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_with(uint32_t x) {
+  return max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ uint32_t key_of_lane(uint32_t x, int lane) {
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, lane);
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  x = max_with<0xB1>(x);
+  x = max_with<0x4E>(x);
+  x = max_with<0x141>(x);
+  x = max_with<0x140>(x);
+  return max(max(key_of_lane(x, 0), key_of_lane(x, 16)), max(key_of_lane(x, 32), key_of_lane(x, 48)));
+}
+__device__ __forceinline__ double lane_value(double x, int lane) {
+  const unsigned long long b = __double_as_longlong(x);
+  return __longlong_as_double(((unsigned long long)key_of_lane((uint32_t)(b >> 32), lane) << 32) |
+                              key_of_lane((uint32_t)b, lane));
+}
+__device__ __forceinline__ double wave_max(double x) {
+  x = fmax(x, other<0>(x));
+  x = fmax(x, other<1>(x));
+  x = fmax(x, other<2>(x));
+  x = fmax(x, other<3>(x));
+  return fmax(fmax(lane_value(x, 0), lane_value(x, 16)), fmax(lane_value(x, 32), lane_value(x, 48)));
+}
+
+// The largest and second largest of a run of experts, merged over lanes
+template <int STEP, typename X>
+__device__ __forceinline__ void merge_best(X& b1, X& b2) {
+  const X o1 = other<STEP>(b1), o2 = other<STEP>(b2);
   b2 = fmax(fmin(b1, o1), fmax(b2, o2));
   b1 = fmax(b1, o1);
 }
 
-// Which groups stay, one bit each.  worth: this lane's group's, in lane g.
-__device__ __forceinline__ unsigned long long keep_groups(double worth, int groups, int kept,
-                                                          int lane) {
-  const unsigned long long b = __double_as_longlong(worth);
-  int rank = 0;
-  for (int g = 0; g < groups; ++g) {
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, g);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), g);
-    const double o = __longlong_as_double(((unsigned long long)hi << 32) | lo);
-    rank += o > worth || (o == worth && g < lane);
+// What lane g's group of experts is worth: the sum of its `best` largest
+// choice scores c (-inf: none there).  `cs`: E values of shared memory.
+template <typename X, int V>
+__device__ __forceinline__ X group_worth(const X (&c)[V], const FwdArgs& A, int lane, X* cs) {
+  const X NEG = (X)-__builtin_huge_val();
+  X b1 = NEG, b2 = NEG;
+  if (A.lanes_log2 >= 0) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      b2 = fmax(b2, fmin(b1, c[i]));
+      b1 = fmax(b1, c[i]);
+    }
+    if (A.lanes_log2 > 0) merge_best<0>(b1, b2);
+    if (A.lanes_log2 > 1) merge_best<1>(b1, b2);
+    if (A.lanes_log2 > 2) merge_best<2>(b1, b2);
+    if (A.lanes_log2 > 3) merge_best<3>(b1, b2);
+    const X worth = A.best == 2 && b2 > NEG ? b1 + b2 : b1;
+    return __shfl(worth, (lane << A.lanes_log2) & 63, 64);
   }
-  return __ballot(lane < groups && rank < kept);
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (lane * V + i < A.E) cs[lane * V + i] = c[i];
+  wave_lds_sync();
+  if (lane < A.groups)
+    for (int j = 0; j < A.per; ++j) {
+      const X x = cs[lane * A.per + j];
+      b2 = fmax(b2, fmin(b1, x));
+      b1 = fmax(b1, x);
+    }
+  wave_lds_sync();
+  return A.best == 2 && b2 > NEG ? b1 + b2 : b1;
 }
 
-// WIDE: scores in 64 bits, where a choice hangs on them (a bias, or groups
-// by the sum of two); otherwise the order of the scores is the logits' own.
-//
-// The k-th choice is a maximum over the wavefront of 32-bit keys: the
-// logits, or the choice scores rounded once, which keeps their order but
-// for equals.  So k + 1 maxima that all differ settle the choice; where two
-// are equal the token is done again on the 64-bit values (tie).
-template <typename T, int V, bool SIGMOID, bool WIDE>
+// Which groups stay, one bit each: the `kept` worth most, the lower of equals
+template <typename X>
+__device__ __forceinline__ unsigned long long keep_groups(X worth, const FwdArgs& A, int lane) {
+  int rank = 0;
+  for (int g = 0; g < A.groups; ++g) {
+    const X o = lane_value(worth, g);
+    rank += o > worth || (o == worth && g < lane);
+  }
+  return __ballot(lane < A.groups && rank < A.kept);
+}
+
+// Whether this lane's i-th expert is in a group kept
+template <int V>
+__device__ __forceinline__ bool in_kept(unsigned long long keep, const FwdArgs& A, int lane, int i) {
+  const int g = A.lanes_log2 >= 0 ? lane >> A.lanes_log2
+                                  : (int)(((uint32_t)(lane * V + i) * A.magic) >> 20);
+  return (keep >> (g & 63)) & 1;
+}
+
+// The choice in 64 bits: lane j gets the j-th expert.
+template <int V, bool SIGMOID>
+__device__ __forceinline__ int choose_wide(const FwdArgs& A, const float (&l)[V], float top, int lane,
+                                           double* cs) {
+  const double NEG = -__builtin_huge_val();
+  double c[V], sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if constexpr (SIGMOID) {
+      c[i] = 1.0 / (1.0 + exp(-(double)l[i]));
+    } else {
+      c[i] = l[i] > TP_ROUTE_LOWEST ? exp((double)l[i] - (double)top) : 0.0;
+      sum += c[i];
+    }
+  }
+  if constexpr (!SIGMOID) {
+    sum = wave_sum(sum);
+    const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] *= inv;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (A.bias && lane * V + i < A.E) c[i] += (double)A.bias[lane * V + i];
+    if (!(l[i] > TP_ROUTE_LOWEST)) c[i] = NEG;
+  }
+  if (A.groups > 1) {
+    const unsigned long long keep = keep_groups(group_worth<double, V>(c, A, lane, cs), A, lane);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (!in_kept<V>(keep, A, lane, i)) c[i] = NEG;
+  }
+  if (!A.bias)  // the order of the scores is the logits'
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = c[i] > NEG ? (double)l[i] : NEG;
+  int my_e = -1;
+  for (int j = 0; j < A.K; ++j) {
+    double head = c[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) head = fmax(head, c[i]);
+    const double m = wave_max(head);
+    if (!(m > NEG)) break;
+    const int win = __ffsll((unsigned long long)__ballot(head == m)) - 1;
+    int at = 0;
+#pragma unroll
+    for (int i = V - 1; i >= 0; --i)
+      if ((__ballot(c[i] == m) >> win) & 1) at = i;
+    const int e = win * V + at;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (lane * V + i == e) c[i] = NEG;
+    if (lane == j) my_e = e;
+  }
+  return my_e;
+}
+
+// e^x by the hardware's 2^x: off by |x| 2^-23 relative at most (the rounded
+// argument), a unit in the last place more
+__device__ __forceinline__ float fast_exp(float x) {
+  return __builtin_amdgcn_exp2f(x * 1.4426950408889634f);
+}
+
+// One wavefront a token.  Choices are to be those of 64-bit arithmetic, made
+// in 32 bits: without a bias the experts' order is the logits' own, exact.
+// With one, a key c = s + bias is off by at most 2^-19 max s (an exponential
+// of a rounded argument, a sum of E <= 1024 terms, a quotient) plus 2^-24
+// |c|; so the order of the first k + 1 keys is right if neighbours differ by
+// more than 2^-18 max s + 2^-22 |c|, and the groups kept are if the worth of
+// the last one and of the first left out differ by twice that.  A token
+// where they do not (one in a hundred or fewer at 256 experts) is done again
+// in 64 bits.
+// Bound by instruction issue: the k maxima take about 25 vector
+// instructions each at V = 4, the scores 15 for each of a lane's experts.
+template <typename T, int V, bool SIGMOID>
 __global__ __launch_bounds__(NT) void fwd_kernel(FwdArgs A) {
   extern __shared__ double sh[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const T* logits = reinterpret_cast<const T*>(A.logits);
-  const double NEG = -__builtin_huge_val();
-  const float NEGF = -__builtin_huge_valf();
-  for (int64_t t = (int64_t)blockIdx.x * WAVES + wave; t < A.N; t += (int64_t)gridDim.x * WAVES) {
-    float l[V], s[V], key[V];
-    double c[WIDE ? V : 1];
-    load_row<T, V>(logits + t * A.E, A.E, lane, true, l);
-    float top = l[0];
+  const float NEG = -__builtin_huge_valf();
+  double* cs = sh + (size_t)wave * A.E;
+  float* scores = reinterpret_cast<float*>(cs);
+  float bias[V];
 #pragma unroll
-    for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
-    if constexpr (!SIGMOID) top = wave_max(top);
-    if constexpr (WIDE) {
-      double s64[V], sum = 0.0;
+  for (int i = 0; i < V; ++i)
+    bias[i] = A.bias && lane * V + i < A.E ? A.bias[lane * V + i] : 0.f;
+  const int64_t stride = (int64_t)gridDim.x * WAVES;
+  int64_t t = (int64_t)blockIdx.x * WAVES + wave;
+  float l[V];
+  load_row<T, V>(logits + t * A.E, A.E, lane, t < A.N, l);
+  for (; t < A.N; t += stride) {
+    float ahead[V];
+    load_row<T, V>(logits + (t + stride) * A.E, A.E, lane, t + stride < A.N, ahead);
+    float s[V];
+    float top = 0.f, largest = 1.f;  // of the logits; of the scores
+    if constexpr (SIGMOID) {
+      // (the exponential of an absent expert is infinite: score 0)
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if constexpr (SIGMOID) {
-          s64[i] = l[i] > TP_ROUTE_LOWEST ? 1.0 / (1.0 + exp(-(double)l[i])) : 0.0;
-        } else {
-          s64[i] = l[i] > TP_ROUTE_LOWEST ? exp((double)l[i] - (double)top) : 0.0;
-          sum += s64[i];
-        }
-      }
-      if constexpr (!SIGMOID) {
-        sum = wave_sum(sum);
-        const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
-#pragma unroll
-        for (int i = 0; i < V; ++i) s64[i] *= inv;
-      }
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = lane * V + i;
-        s[i] = (float)s64[i];
-        c[i] = s64[i];
-        if (A.bias && e < A.E) c[i] += (double)A.bias[e];
-        if (!(l[i] > TP_ROUTE_LOWEST)) c[i] = NEG;
-        key[i] = A.bias ? (float)c[i] : l[i];
-      }
+      for (int i = 0; i < V; ++i) s[i] = __builtin_amdgcn_rcpf(1.f + fast_exp(-l[i]));
     } else {
+      top = l[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
+      top = wave_max(top);
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        if constexpr (SIGMOID) {
-          s[i] = l[i] > TP_ROUTE_LOWEST ? 1.f / (1.f + expf(-l[i])) : 0.f;
-        } else {
-          s[i] = l[i] > TP_ROUTE_LOWEST ? expf(l[i] - top) : 0.f;
-          sum += s[i];
-        }
-        key[i] = l[i];
+        s[i] = l[i] > TP_ROUTE_LOWEST ? fast_exp(l[i] - top) : 0.f;
+        sum += s[i];
       }
-      if constexpr (!SIGMOID) {
-        sum = wave_sum(sum);
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      sum = wave_sum(sum);
+      largest = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) s[i] *= inv;
-      }
+      for (int i = 0; i < V; ++i) s[i] *= largest;
     }
+    uint32_t key[V];
+    bool close = false;  // too close for 32 bits
+    const float slack = 0x1p-18f * largest;
     if (A.groups > 1) {
-      const int per = A.E / A.groups;
-      double b1 = NEG, b2 = NEG;
-      const int lanes = per / V;
-      const bool aligned = per % V == 0 && lanes <= 16 && (lanes & (lanes - 1)) == 0;
-      if (aligned) {
-        // a group is an aligned power of two of whole lanes
+      float c[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          double x;
-          if constexpr (WIDE) x = c[i]; else x = (double)key[i];
-          b2 = fmax(b2, fmin(b1, x));
-          b1 = fmax(b1, x);
-        }
-        if (lanes > 1) merge_best<0>(b1, b2);
-        if (lanes > 2) merge_best<1>(b1, b2);
-        if (lanes > 4) merge_best<2>(b1, b2);
-        if (lanes > 8) merge_best<3>(b1, b2);
-        // lane g takes group g's from the group's first lane
-        const double w1 = __shfl(b1, (lane * lanes) & 63, 64), w2 = __shfl(b2, (lane * lanes) & 63, 64);
-        b1 = w1;
-        b2 = w2;
-      } else {
-        double* cs = sh + (size_t)wave * A.E;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          double x;
-          if constexpr (WIDE) x = c[i]; else x = (double)key[i];
-          if (lane * V + i < A.E) cs[lane * V + i] = x;
-        }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-        if (lane < A.groups)
-          for (int j = 0; j < per; ++j) {
-            const double x = cs[lane * per + j];
-            b2 = fmax(b2, fmin(b1, x));
-            b1 = fmax(b1, x);
-          }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-      }
-      const double worth = A.best == 2 && b2 > NEG ? b1 + b2 : b1;
-      const unsigned long long keep = keep_groups(worth, A.groups, A.kept, lane);
-      const int mine = aligned ? lane >> (__ffs(lanes) - 1) : 0;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int g = aligned ? mine : (lane * V + i) / per;
-        if (!((keep >> (g & 63)) & 1)) {
-          key[i] = NEGF;
-          if constexpr (WIDE) c[i] = NEG;
-        }
-      }
-    }
-    int my_e = -1;
-    float my_s = 0.f;
-    // a choice by rounded scores needs one more maximum to show that no two
-    // are equal
-    const bool check = WIDE && A.bias;
-    float k32[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) k32[i] = key[i];
-    float before = __builtin_huge_valf();
-    bool tie = false;
-    for (int j = 0; j < A.K + (check ? 1 : 0); ++j) {
-      float head = k32[0], hs = s[0];
-      int hi = 0;
-#pragma unroll
-      for (int i = 1; i < V; ++i)
-        if (k32[i] > head) {
-          head = k32[i];
-          hs = s[i];
-          hi = i;
-        }
-      const float m = wave_max(head);
-      if (!(m > NEGF)) break;
-      if (check && m == before) {
-        tie = true;
-        break;
-      }
-      before = m;
-      if (j == A.K) break;
-      const int win = __ffsll((unsigned long long)__ballot(head == m)) - 1;
-      const int e = win * V + __builtin_amdgcn_readlane(hi, win);
-      const float sc = lane_value(hs, win);
+      for (int i = 0; i < V; ++i) c[i] = l[i] > TP_ROUTE_LOWEST ? s[i] + bias[i] : NEG;
+      const float worth = group_worth<float, V>(c, A, lane, scores);
+      const unsigned long long keep = keep_groups(worth, A, lane);
+      const bool mine = (keep >> lane) & 1;
+      const float last = -wave_max(mine ? -worth : NEG);
+      const float next = wave_max(lane < A.groups && !mine ? worth : NEG);
+      close = next > NEG && !(last - next > 2.f * slack + 0x1p-21f * (fabsf(last) + fabsf(next)));
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (lane * V + i == e) k32[i] = NEGF;
+        key[i] = c[i] > NEG && in_kept<V>(keep, A, lane, i) ? to_key(A.bias ? c[i] : l[i]) : 0u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        key[i] = l[i] > TP_ROUTE_LOWEST ? to_key(A.bias ? s[i] + bias[i] : l[i]) : 0u;
+    }
+    // for the chosen ones' lanes to read
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (lane * V + i < A.E) scores[lane * V + i] = s[i];
+    wave_lds_sync();
+    int my_e = -1;
+    uint32_t my_key = 0;
+    const int rounds = A.K + (A.bias ? 1 : 0);
+    for (int j = 0; j < rounds; ++j) {
+      uint32_t head = key[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) head = max(head, key[i]);
+      const uint32_t m = wave_max(head);
+      if (m == 0) break;
+      const int win = __ffsll((unsigned long long)__ballot(head == m)) - 1;
+      int at = 0;
+#pragma unroll
+      for (int i = V - 1; i >= 0; --i)
+        if ((__ballot(key[i] == m) >> win) & 1) at = i;
+      const int e = win * V + at;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (lane * V + i == e) key[i] = 0;
       if (lane == j) {
         my_e = e;
-        my_s = sc;
+        my_key = m;
       }
     }
-    if constexpr (WIDE) {
-      if (tie) {
-        my_e = -1;
-        my_s = 0.f;
-        for (int j = 0; j < A.K; ++j) {
-          double head = c[0];
-          float hs = s[0];
-          int hi = 0;
+    if (A.bias) {
+      // lane j's key against lane j + 1's
+      const uint32_t below = (uint32_t)__shfl_down((int)my_key, 1, 64);
+      const float m = from_key(my_key), n = from_key(below);
+      const bool tight = lane < A.K && below != 0 && !(m - n > slack + 0x1p-22f * fabsf(m));
+      close = close || __ballot(tight) != 0;
+    }
+    if (lane >= A.K) my_e = -1;
+    float my_s = my_e >= 0 ? scores[my_e] : 0.f;
+    wave_lds_sync();
+    if (close) {
+      my_e = choose_wide<V, SIGMOID>(A, l, top, lane, cs);
+      my_s = 0.f;
+      wave_lds_sync();
 #pragma unroll
-          for (int i = 1; i < V; ++i)
-            if (c[i] > head) {
-              head = c[i];
-              hs = s[i];
-              hi = i;
-            }
-          double m = head;
-          m = fmax(m, other<0>(m));
-          m = fmax(m, other<1>(m));
-          m = fmax(m, other<2>(m));
-          m = fmax(m, other<3>(m));
-          m = fmax(m, other<4>(m));
-          m = fmax(m, other<5>(m));
-          if (!(m > NEG)) break;
-          const int win = __ffsll((unsigned long long)__ballot(head == m)) - 1;
-          const int e = win * V + __builtin_amdgcn_readlane(hi, win);
-          const float sc = lane_value(hs, win);
-#pragma unroll
-          for (int i = 0; i < V; ++i)
-            if (lane * V + i == e) c[i] = NEG;
-          if (lane == j) {
-            my_e = e;
-            my_s = sc;
-          }
-        }
-      }
+      for (int i = 0; i < V; ++i)
+        if (lane * V + i < A.E) scores[lane * V + i] = s[i];
+      wave_lds_sync();
+      if (my_e >= 0) my_s = scores[my_e];
+      wave_lds_sync();
     }
     if (A.renorm) my_s /= wave_sum(my_s) + 1e-20f;  // lanes past K hold zeros
     if (lane < A.K) {
       A.expert[t * A.K + lane] = my_e;
       A.weight[t * A.K + lane] = my_s * A.scale;
     }
+#pragma unroll
+    for (int i = 0; i < V; ++i) l[i] = ahead[i];
+  }
+}
+
+// Many tokens: four to a wavefront, 16 lanes each, so that the moves within
+// 16 lanes serve four maxima at once.  V experts a lane, E <= 16 V, K <= 15,
+// groups of whole lanes only.
+template <typename X, typename F>
+__device__ __forceinline__ X row_all(X x, F&& f) {
+  x = f(x, other<0>(x));
+  x = f(x, other<1>(x));
+  x = f(x, other<2>(x));
+  return f(x, other<3>(x));
+}
+// rank of this lane's group among the row's: groups of 2^LOG lanes
+template <int LOG, int N = 1>
+__device__ __forceinline__ int group_rank(float worth, int lane) {
+  if constexpr ((N << LOG) >= 16) {
+    return 0;
+  } else {
+    constexpr int CTRL = 0x120 + (N << LOG);  // row_ror
+    const float o = dpp<CTRL>(worth);
+    const int from = __builtin_amdgcn_update_dpp(0, lane, CTRL, 0xf, 0xf, true);
+    return (o > worth || (o == worth && from < lane)) + group_rank<LOG, N + 1>(worth, lane);
+  }
+}
+
+template <typename T, int V, bool SIGMOID>
+__global__ __launch_bounds__(NT) void fwd_rows_kernel(FwdArgs A) {
+  constexpr int V64 = V < 4 ? 1 : V / 4;
+  constexpr int ROW = 16 * V + 16;  // scores, chosen
+  __shared__ alignas(16) float lds[WAVES * 4 * ROW + (V < 4 ? WAVES * 128 : 0)];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
+  const T* logits = reinterpret_cast<const T*>(A.logits);
+  const float NEG = -__builtin_huge_valf();
+  float* scores = lds + (wave * 4 + q) * ROW;
+  int* chosen = reinterpret_cast<int*>(scores + 16 * V);
+  float bias[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) bias[i] = A.bias && r * V + i < A.E ? A.bias[r * V + i] : 0.f;
+  const int64_t stride = (int64_t)gridDim.x * WAVES * 4;
+  int64_t t = ((int64_t)blockIdx.x * WAVES + wave) * 4 + q;
+  float l[V];
+  load_row<T, V>(logits + t * A.E, A.E, r, t < A.N, l);
+  for (; t - q < A.N; t += stride) {
+    float ahead[V];
+    load_row<T, V>(logits + (t + stride) * A.E, A.E, r, t + stride < A.N, ahead);
+    float s[V];
+    float top = 0.f, largest = 1.f;
+    auto fmaxf_ = [](float a, float b) { return fmaxf(a, b); };
+    if constexpr (SIGMOID) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[i] = __builtin_amdgcn_rcpf(1.f + fast_exp(-l[i]));
+    } else {
+      top = l[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
+      top = row_all(top, fmaxf_);
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        s[i] = l[i] > TP_ROUTE_LOWEST ? fast_exp(l[i] - top) : 0.f;
+        sum += s[i];
+      }
+      sum = row_all(sum, [](float a, float b) { return a + b; });
+      largest = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[i] *= largest;
+    }
+#pragma unroll
+    for (int i = 0; i < V; i += V < 4 ? V : 4) {
+      if constexpr (V >= 4)
+        *reinterpret_cast<float4*>(scores + r * V + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+      else
+#pragma unroll
+        for (int j = 0; j < V; ++j) scores[r * V + j] = s[j];
+    }
+    uint32_t key[V];
+    bool close = false;
+    const float slack = 0x1p-18f * largest;
+    bool kept = true;
+    if (A.groups > 1) {
+      float b1 = NEG, b2 = NEG;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float c = l[i] > TP_ROUTE_LOWEST ? s[i] + bias[i] : NEG;
+        b2 = fmaxf(b2, fminf(b1, c));
+        b1 = fmaxf(b1, c);
+      }
+      if (A.lanes_log2 > 0) merge_best<0>(b1, b2);
+      if (A.lanes_log2 > 1) merge_best<1>(b1, b2);
+      if (A.lanes_log2 > 2) merge_best<2>(b1, b2);
+      const float worth = A.best == 2 && b2 > NEG ? b1 + b2 : b1;
+      const int rank = A.lanes_log2 == 0   ? group_rank<0>(worth, r)
+                       : A.lanes_log2 == 1 ? group_rank<1>(worth, r)
+                       : A.lanes_log2 == 2 ? group_rank<2>(worth, r)
+                                           : group_rank<3>(worth, r);
+      kept = rank < A.kept;
+      const float last = -row_all(kept ? -worth : NEG, fmaxf_);
+      const float next = row_all(kept ? NEG : worth, fmaxf_);
+      close = next > NEG && !(last - next > 2.f * slack + 0x1p-21f * (fabsf(last) + fabsf(next)));
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      key[i] = kept && l[i] > TP_ROUTE_LOWEST ? to_key(A.bias ? s[i] + bias[i] : l[i]) : 0u;
+    uint32_t my_key = 0;
+    const int rounds = A.K + (A.bias ? 1 : 0);
+    for (int j = 0; j < rounds; ++j) {
+      uint32_t head = key[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) head = max(head, key[i]);
+      uint32_t m = max_with<0xB1>(head);
+      m = max_with<0x4E>(m);
+      m = max_with<0x141>(m);
+      m = max_with<0x140>(m);
+      // the lowest of the row's lanes that hold it, and there the lowest i
+      const uint32_t holders = (uint32_t)(__ballot(head == m) >> (lane & 48)) & 0xffffu;
+      bool mine = m != 0 && r == __ffs((int)holders) - 1;
+      int at = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const bool hit = mine && key[i] == m;
+        key[i] = hit ? 0u : key[i];
+        at = hit ? i : at;
+        mine = mine && !hit;
+      }
+      if (m != 0 && r == __ffs((int)holders) - 1) chosen[j] = r * V + at;
+      my_key = r == j ? m : my_key;
+    }
+    wave_lds_sync();
+    int my_e = r < A.K && my_key != 0 ? chosen[r] : -1;
+    float my_s = my_e >= 0 ? scores[my_e] : 0.f;
+    if (A.bias) {
+      const uint32_t below = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)my_key, 0x101, 0xf, 0xf, true);
+      const float m = from_key(my_key), n = from_key(below);
+      close = close || (r < A.K && below != 0 && !(m - n > slack + 0x1p-22f * fabsf(m)));
+    }
+    wave_lds_sync();
+    const unsigned long long redo = __ballot(close);
+    if (redo) {
+      FwdArgs W = A;
+      W.lanes_log2 = A.wide_log2;
+      double* cs = reinterpret_cast<double*>(lds + wave * 4 * ROW);
+      if constexpr (V < 4) cs = reinterpret_cast<double*>(lds + WAVES * 4 * ROW + wave * 128);
+      for (int k = 0; k < 4; ++k) {
+        if (!((redo >> (16 * k)) & 0xffff)) continue;
+        const int64_t tk = t - q + k;
+        float w[V64];
+        load_row<T, V64>(logits + tk * A.E, A.E, lane, tk < A.N, w);
+        const float tw = __shfl(top, 16 * k, 64);
+        const int e = __shfl(choose_wide<V64, SIGMOID>(W, w, tw, lane, cs), r, 64);
+        if (q == k) {
+          my_e = r < A.K ? e : -1;
+          my_s = 0.f;
+          if (my_e >= 0) {
+            float x;
+            if constexpr (sizeof(T) == 2) x = bf16_to_f32(logits[t * A.E + my_e]);
+            else x = logits[t * A.E + my_e];
+            x = fminf(x, TP_ROUTE_LARGEST);
+            my_s = SIGMOID ? __builtin_amdgcn_rcpf(1.f + fast_exp(-x)) : fast_exp(x - top) * largest;
+          }
+        }
+        wave_lds_sync();
+      }
+    }
+    if (A.renorm) my_s /= row_all(my_s, [](float a, float b) { return a + b; }) + 1e-20f;
+    if (r < A.K && t < A.N) {
+      A.expert[t * A.K + r] = my_e;
+      A.weight[t * A.K + r] = my_s * A.scale;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) l[i] = ahead[i];
   }
 }
 
@@ -468,9 +714,7 @@ __global__ __launch_bounds__(NT) void bwd_kernel(BwdArgs A) {
 // the earlier runs' counts itself; beyond, scan_kernel turns the counts into
 // sums over the earlier runs, and leaves the totals in row `runs`.
 // ---------------------------------------------------------------------------
-constexpr int RUN = 1024;  // threads of a run
 constexpr int FEW = 128;
-static int run_tokens(int K) { return RUN / K; }
 
 __device__ __forceinline__ int local_expert(const TablesArgs& A, int64_t f, int64_t f1) {
   if (f >= f1) return -1;
@@ -478,13 +722,14 @@ __device__ __forceinline__ int local_expert(const TablesArgs& A, int64_t f, int6
   return x >= A.first && x - A.first < A.n_local ? x - A.first : -1;
 }
 
+template <int RUN>
 __global__ __launch_bounds__(RUN) void count_kernel(TablesArgs A, int pairs) {
   extern __shared__ int hist[];
   const int width = A.n_local + 1;
-  for (int e = threadIdx.x; e < width; e += RUN) hist[e] = 0;
-  __syncthreads();
   const int64_t f0 = (int64_t)blockIdx.x * pairs, f1 = min(f0 + pairs, A.N * A.K);
   const int e = threadIdx.x < pairs ? local_expert(A, f0 + threadIdx.x, f1) : -1;
+  for (int i = threadIdx.x; i < width; i += RUN) hist[i] = 0;
+  __syncthreads();
   if (e >= 0) atomicAdd(&hist[e], 1);
   const unsigned long long on = __ballot(e >= 0);
   if ((threadIdx.x & 63) == 0) atomicAdd(&hist[A.n_local], (int)__popcll(on));
@@ -493,7 +738,7 @@ __global__ __launch_bounds__(RUN) void count_kernel(TablesArgs A, int pairs) {
 }
 
 // 64 columns a workgroup, 16 shares of the runs
-__global__ __launch_bounds__(RUN) void scan_kernel(TablesArgs A, int runs) {
+__global__ __launch_bounds__(1024) void scan_kernel(TablesArgs A, int runs) {
   __shared__ int part[16][64];
   const int width = A.n_local + 1;
   const int lane = threadIdx.x & 63, share = threadIdx.x >> 6;
@@ -516,22 +761,52 @@ __global__ __launch_bounds__(RUN) void scan_kernel(TablesArgs A, int runs) {
   if (share == 15) A.ws[(int64_t)runs * width + e] = base;
 }
 
+// shared memory of place_kernel, in ints
+template <int RUN>
+static size_t place_lds(int n_local) {
+  const size_t width = (size_t)n_local + 1;
+  const size_t shares = width < (size_t)RUN ? RUN / width : 1;
+  return 2 * width + RUN + RUN / 64 * 2 + 2 * shares * width + ((size_t)RUN / 64 * n_local + 1) / 2;
+}
+
+template <int RUN>
 __global__ __launch_bounds__(RUN) void place_kernel(TablesArgs A, int pairs, int runs) {
+  constexpr int WV = RUN / 64;
   extern __shared__ int lds[];
   const int width = A.n_local + 1;
-  int* first = lds;                 // [n_local + 1] first row of each expert in this run
-  int* total = first + width;       // [n_local + 1] rows of each expert in all
-  int* seen = total + width;        // [RUN] experts of this run's pairs
-  int* red = seen + RUN;            // [32]
-  uint16_t* waves = reinterpret_cast<uint16_t*>(red + 32);  // [16][n_local] pairs in earlier wavefronts
+  const int shares = max(1, RUN / width);
+  int* first = lds;            // [width] first row of each expert in this run
+  int* total = first + width;  // [width] rows of each expert in all
+  int* seen = total + width;   // [RUN] experts of this run's pairs
+  int* red = seen + RUN;       // [2 WV]
+  int* sums = red + 2 * WV;    // [2][shares][width] other runs' counts: earlier, all
+  uint16_t* waves = reinterpret_cast<uint16_t*>(sums + 2 * shares * width);  // [WV][n_local]
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int run = blockIdx.x;
   const int64_t f0 = (int64_t)run * pairs, f1 = min(f0 + pairs, A.N * A.K), f = f0 + tid;
   const int e = tid < pairs ? local_expert(A, f, f1) : -1;
+  // the other runs' counts, column by column
+  if (runs > FEW) {
+    for (int i = tid; i < width; i += RUN) {
+      sums[i] = A.ws[(int64_t)run * width + i];
+      sums[width + i] = A.ws[(int64_t)runs * width + i];
+    }
+  } else if (runs > 1) {
+    for (int i = tid; i < width * shares; i += RUN) {
+      const int share = i / width, col = i - share * width;
+      int before = 0, all = 0;
+#pragma unroll 4
+      for (int r = share; r < runs; r += shares) {
+        const int v = A.ws[r * width + col];
+        all += v;
+        before += r < run ? v : 0;
+      }
+      sums[i] = before;
+      sums[shares * width + i] = all;
+    }
+  }
+  const int parts = runs > FEW ? 1 : shares;
   seen[tid] = e;
-  for (int i = tid; i < 16 * A.n_local; i += RUN) waves[i] = 0;
-  for (int i = tid; i < 2 * width; i += RUN) lds[i] = 0;
-  __syncthreads();
   // rank among the lanes with the same expert
   const unsigned long long below = (1ull << lane) - 1;
   const unsigned long long on = __ballot(e >= 0);
@@ -541,98 +816,139 @@ __global__ __launch_bounds__(RUN) void place_kernel(TablesArgs A, int pairs, int
     same &= (e >> b) & 1 ? bit : ~bit;
   }
   const int rank = __popcll(same & below);
-  if (e >= 0 && rank == 0) waves[wave * A.n_local + e] = (uint16_t)__popcll(same);
+  uint16_t* mine = waves + wave * A.n_local;
+  for (int i = lane; i < A.n_local; i += 64) mine[i] = 0;
+  wave_lds_sync();
+  if (e >= 0 && rank == 0) mine[e] = (uint16_t)__popcll(same);
   if (lane == 0) red[wave] = __popcll(on);
-  // the other runs
-  if (runs > FEW) {
-    for (int i = tid; i < width; i += RUN) {
-      first[i] = A.ws[(int64_t)run * width + i];
-      total[i] = A.ws[(int64_t)runs * width + i];
-    }
-  } else if (runs > 1) {
-    // column by column, the runs dealt to as many threads as there are
-    const int shares = max(1, RUN / width);
-    for (int i = tid; i < width * shares; i += RUN) {
-      const int col = i % width, share = i / width;
-      int before = 0, all = 0;
-      for (int r = share; r < runs; r += shares) {
-        const int v = A.ws[(int64_t)r * width + col];
-        all += v;
-        before += r < run ? v : 0;
-      }
-      if (all) atomicAdd(&total[col], all);
-      if (before) atomicAdd(&first[col], before);
-    }
-  }
   __syncthreads();
-  // pairs in earlier wavefronts; with one run the sums are the totals
-  for (int i = tid; i < A.n_local; i += RUN) {
+  // each expert's pairs in earlier wavefronts, in earlier runs and in all
+  int all = 0, before = 0;
+  if (tid < A.n_local) {
     int sum = 0;
-    for (int w = 0; w < 16; ++w) {
-      const int v = waves[w * A.n_local + i];
-      waves[w * A.n_local + i] = (uint16_t)sum;
+#pragma unroll
+    for (int w = 0; w < WV; ++w) {
+      const int v = waves[w * A.n_local + tid];
+      waves[w * A.n_local + tid] = (uint16_t)sum;
       sum += v;
     }
-    if (runs <= 1) total[i] = sum;
+    all = sum;
   }
-  int mine = 0, listed = 0;  // list entries in earlier wavefronts, and of the run
-  for (int w = 0; w < 16; ++w) {
-    mine += w < wave ? red[w] : 0;
-    listed += red[w];
+  if (runs > 1 && tid < width) {
+    all = 0;
+    for (int p = 0; p < parts; ++p) {
+      before += sums[p * width + tid];
+      all += sums[(parts + p) * width + tid];
+    }
   }
-  if (runs <= 1 && tid == 0) total[A.n_local] = listed;
-  __syncthreads();
-  // first rows: exclusive sums of the totals over the experts (n_local <=
-  // RUN: one each)
-  {
-    const int v = tid < A.n_local ? total[tid] : 0;
+  int earlier_waves = 0, listed = 0;  // list entries in earlier wavefronts, and of the run
+#pragma unroll
+  for (int w = 0; w < WV; ++w) {
+    const int v = red[w];
+    earlier_waves += w < wave ? v : 0;
+    listed += v;
+  }
+  // an expert's first row: the totals of the experts before it, chunks of
+  // RUN experts (one where n_local fits the workgroup)
+  int carry = 0;
+  for (int e0 = 0; e0 < A.n_local; e0 += RUN) {
+    if (e0 > 0) {  // n_local > RUN: this thread's next expert
+      const int i = e0 + tid;
+      all = before = 0;
+      if (i < A.n_local) {
+        int sum = 0;
+        for (int w = 0; w < WV; ++w) {
+          const int v = waves[w * A.n_local + i];
+          waves[w * A.n_local + i] = (uint16_t)sum;
+          sum += v;
+        }
+        all = sum;
+        if (runs > 1) {
+          all = 0;
+          for (int p = 0; p < parts; ++p) {
+            before += sums[p * width + i];
+            all += sums[(parts + p) * width + i];
+          }
+        }
+      }
+    }
+    const int v = e0 + tid < A.n_local ? all : 0;
     int x = v;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int u = __shfl_up(x, d, 64);
       if (lane >= d) x += u;
     }
-    if (lane == 63) red[16 + wave] = x;
-    __syncthreads();
-    int base = x - v;
-    for (int w = 0; w < wave; ++w) base += red[16 + w];
-    if (tid < A.n_local) {
-      first[tid] += base;
-      if (run == 0) A.offsets[tid] = base;
+    int base = carry + x - v;
+    if (A.n_local > 64) {
+      __syncthreads();
+      if (lane == 63) red[WV + wave] = x;
+      __syncthreads();
+      for (int w = 0; w < wave; ++w) base += red[WV + w];
+      for (int w = 0; w < WV; ++w) carry += red[WV + w];
+    }
+    if (e0 + tid < A.n_local) {
+      first[e0 + tid] = base + before;
+      total[e0 + tid] = all;
+      if (run == 0) A.offsets[e0 + tid] = base;
     }
   }
-  const int rows = total[A.n_local];
-  if (run == 0 && tid == 0) {
-    A.offsets[A.n_local] = rows;
-    A.tok_ptr[A.N] = rows;
+  // the lists' own sums: column n_local
+  if (tid == RUN - 1) {
+    int b = 0, t = listed;
+    if (runs > 1) {
+      t = 0;
+      for (int p = 0; p < parts; ++p) {
+        b += sums[p * width + A.n_local];
+        t += sums[(parts + p) * width + A.n_local];
+      }
+    }
+    first[A.n_local] = b;
+    total[A.n_local] = t;
+    if (run == 0) {
+      A.offsets[A.n_local] = t;
+      A.tok_ptr[A.N] = t;
+    }
   }
   __syncthreads();
-  for (int64_t r = rows + (int64_t)run * RUN + tid; r < A.R; r += (int64_t)gridDim.x * RUN) {
+  for (int64_t r = total[A.n_local] + (int64_t)run * RUN + tid; r < A.R; r += (int64_t)gridDim.x * RUN) {
     A.row_token[r] = -1;
     A.tok_rows[r] = -1;
     if (A.row_weight) A.row_weight[r] = 0.f;
   }
   if (tid >= pairs || f >= f1) return;
-  const int slot = tid % A.K, token0 = tid - slot;
-  const int64_t t = (int64_t)run * (pairs / A.K) + tid / A.K;
+  const int token = tid / A.K, slot = tid - token * A.K;
+  const int t = run * (pairs / A.K) + token;
   // list entries of this token's earlier slots, and of its lower rows
   int earlier = 0, lower = 0;
   for (int i = 0; i < A.K; ++i) {
-    const int o = seen[token0 + i];
+    const int o = seen[token * A.K + i];
     if (o < 0) continue;
     earlier += i < slot;
     lower += o < e || (o == e && i < slot);
   }
-  const int start = first[A.n_local] + mine + __popcll(on & below) - earlier;
+  const int start = first[A.n_local] + earlier_waves + __popcll(on & below) - earlier;
   if (slot == 0) A.tok_ptr[t] = start;
   int row = -1;
   if (e >= 0) {
     row = first[e] + waves[wave * A.n_local + e] + rank;
     A.tok_rows[start + lower] = row;
-    A.row_token[row] = (int32_t)t;
+    A.row_token[row] = t;
     if (A.row_weight) A.row_weight[row] = A.weight[f];
   }
   A.slot_row[f] = row;
+}
+
+// Threads of a run, a pair each: one run where that is possible (one launch),
+// else the smallest runs whose counts place_kernel adds up itself (two).  32768
+// pairs of 8 local experts: 11.9 us for the routing with runs of 256 threads,
+// 12.5 with 512, 14.5 with 1024; 65528 pairs of 64: 25.5 with 512, 25.3 with
+// 1024, 32 with 256 (256 runs, a scan between).
+static int run_threads(int64_t N, int K) {
+  if (N * K > 256 && (N + 1024 / K - 1) / (1024 / K) <= 1) return 1024;
+  for (int run = 256; run < 1024; run *= 2)
+    if ((N + run / K - 1) / (run / K) <= FEW) return run;
+  return 1024;
 }
 
 template <typename F>
@@ -650,9 +966,26 @@ static hipError_t pick(int dtype, int E, int score, F&& f) {
   return dtype == TP_BF16 ? by_size(bf16_t{}) : by_size(0.f);
 }
 
-static unsigned grid_tokens(int64_t N) {
+template <typename F>
+static void pick_rows(int dtype, int V, int score, F&& f) {
+  auto by_score = [&](auto t, auto v) {
+    score == TP_SCORE_SIGMOID ? f(t, v, std::true_type{}) : f(t, v, std::false_type{});
+  };
+  auto by_size = [&](auto t) {
+    V == 1   ? by_score(t, std::integral_constant<int, 1>{})
+    : V == 2 ? by_score(t, std::integral_constant<int, 2>{})
+    : V == 4 ? by_score(t, std::integral_constant<int, 4>{})
+    : V == 8 ? by_score(t, std::integral_constant<int, 8>{})
+             : by_score(t, std::integral_constant<int, 16>{});
+  };
+  dtype == TP_BF16 ? by_size(bf16_t{}) : by_size(0.f);
+}
+
+constexpr int64_t ROWS_FROM = 4096, ROWS_GRID = 1024;
+
+static unsigned grid_tokens(int64_t N, int64_t most) {
   const int64_t b = (N + WAVES - 1) / WAVES;
-  return (unsigned)(b > 8192 ? 8192 : b);
+  return (unsigned)(b > most ? most : b);
 }
 
 }  // namespace route
@@ -661,18 +994,34 @@ hipError_t route_fwd_launch(const tp_route_desc& d, const void* logits, const fl
                             int32_t* expert, float* weight, hipStream_t st) {
   using namespace route;
   if (d.N == 0) return hipSuccess;
+  const int per = d.E / d.groups;
   FwdArgs a{logits, bias, expert, weight, d.N, d.E, d.K, d.groups, d.groups_kept, d.group_best,
-            d.renorm, d.scale};
-  const bool wide = bias || (d.groups > 1 && d.group_best == 2);
+            d.renorm, d.scale, per, -1, (uint32_t)(((1 << 20) + per - 1) / per), -1};
+  auto log2_lanes = [&](int V) {
+    for (int b = 0; b <= 4; ++b)
+      if (per == V << b) return b;
+    return -1;
+  };
+  // Four tokens to a wavefront once those wavefronts fill the chip: 16384
+  // tokens top 2 of 64 4.8 us (7.4 with one), 8191 top 8 of 256 in groups 16.6
+  // (18.0); 8 tokens take 5.0 us with one and 6.6 with four.
+  const int v16 = d.E <= 16 ? 1 : d.E <= 32 ? 2 : d.E <= 64 ? 4 : d.E <= 128 ? 8 : 16;
+  if (d.N >= ROWS_FROM && d.E <= 256 && d.K <= 15 && (d.groups == 1 || (log2_lanes(v16) >= 0 && log2_lanes(v16) <= 3))) {
+    const int64_t groups = (d.N + 4 * WAVES - 1) / (4 * WAVES);
+    const dim3 grid((unsigned)(groups > ROWS_GRID ? ROWS_GRID : groups));
+    a.lanes_log2 = log2_lanes(v16);
+    a.wide_log2 = log2_lanes(v16 < 4 ? 1 : v16 / 4);
+    pick_rows(d.dtype, v16, d.score, [&](auto t, auto v, auto sig) {
+      hipLaunchKernelGGL((fwd_rows_kernel<decltype(t), decltype(v)::value, decltype(sig)::value>),
+                         grid, dim3(NT), 0, st, a);
+    });
+    return hipGetLastError();
+  }
   return pick(d.dtype, d.E, d.score, [&](auto t, auto v, auto sig) {
-    const size_t lds = d.groups > 1 ? (size_t)WAVES * d.E * sizeof(double) : 0;
-    const dim3 grid(grid_tokens(d.N));
-    if (wide)
-      hipLaunchKernelGGL((fwd_kernel<decltype(t), decltype(v)::value, decltype(sig)::value, true>),
-                         grid, dim3(NT), lds, st, a);
-    else
-      hipLaunchKernelGGL((fwd_kernel<decltype(t), decltype(v)::value, decltype(sig)::value, false>),
-                         grid, dim3(NT), lds, st, a);
+    constexpr int V = decltype(v)::value;
+    a.lanes_log2 = log2_lanes(V);
+    hipLaunchKernelGGL((fwd_kernel<decltype(t), V, decltype(sig)::value>), dim3(grid_tokens(d.N, 1024)),
+                       dim3(NT), (size_t)WAVES * d.E * sizeof(double), st, a);
     return hipGetLastError();
   });
 }
@@ -685,36 +1034,45 @@ hipError_t route_bwd_launch(const tp_route_desc& d, const void* logits, const in
   BwdArgs a{logits, expert, d_weight, slot_row, dlogits, d.N, R, d.E, d.K, d.renorm, d.scale};
   return pick(d.dtype, d.E, d.score, [&](auto t, auto v, auto sig) {
     hipLaunchKernelGGL((bwd_kernel<decltype(t), decltype(v)::value, decltype(sig)::value>),
-                       dim3(grid_tokens(d.N)), dim3(NT), 0, st, a);
+                       dim3(grid_tokens(d.N, 8192)), dim3(NT), 0, st, a);
     return hipGetLastError();
   });
 }
 
 size_t route_tables_workspace(int64_t N, int K, int n_local) {
-  const int64_t tokens = route::run_tokens(K);
+  const int64_t tokens = route::run_threads(N, K) / K;
   const int64_t runs = (N + tokens - 1) / tokens;
   if (runs <= 1) return 16;  // not used; a caller need not tell sizes apart
   return (size_t)(runs + (runs > route::FEW ? 1 : 0)) * ((size_t)n_local + 1) * sizeof(int32_t);
 }
 
-hipError_t route_tables_launch(const TablesArgs& a, hipStream_t st) {
+template <int RUN>
+static hipError_t tables_launch(const TablesArgs& a, hipStream_t st) {
   using namespace route;
-  const int tokens = run_tokens(a.K), pairs = tokens * a.K;
+  const int tokens = RUN / a.K, pairs = tokens * a.K;
   const int runs = (int)((a.N + tokens - 1) / tokens);
   const size_t width = (size_t)a.n_local + 1;
   hipError_t he = hipSuccess;
   if (runs > 1) {
-    hipLaunchKernelGGL(count_kernel, dim3((unsigned)runs), dim3(RUN), width * sizeof(int), st, a, pairs);
+    hipLaunchKernelGGL(count_kernel<RUN>, dim3((unsigned)runs), dim3(RUN), width * sizeof(int), st, a,
+                       pairs);
     if ((he = hipGetLastError()) != hipSuccess) return he;
   }
   if (runs > FEW) {
-    hipLaunchKernelGGL(scan_kernel, dim3((unsigned)((width + 63) / 64)), dim3(RUN), 0, st, a, runs);
+    hipLaunchKernelGGL(scan_kernel, dim3((unsigned)((width + 63) / 64)), dim3(1024), 0, st, a, runs);
     if ((he = hipGetLastError()) != hipSuccess) return he;
   }
-  const size_t lds = (2 * width + RUN + 32) * sizeof(int) + 16 * (size_t)a.n_local * sizeof(uint16_t);
-  hipLaunchKernelGGL(place_kernel, dim3((unsigned)(runs > 0 ? runs : 1)), dim3(RUN), lds, st, a,
-                     pairs, runs);
+  hipLaunchKernelGGL(place_kernel<RUN>, dim3((unsigned)(runs > 0 ? runs : 1)), dim3(RUN),
+                     place_lds<RUN>(a.n_local) * sizeof(int), st, a, pairs, runs);
   return hipGetLastError();
+}
+
+hipError_t route_tables_launch(const TablesArgs& a, hipStream_t st) {
+  switch (route::run_threads(a.N, a.K)) {
+    case 256: return tables_launch<256>(a, st);
+    case 512: return tables_launch<512>(a, st);
+    default: return tables_launch<1024>(a, st);
+  }
 }
 
 }  // namespace tpmlp

@@ -317,3 +317,81 @@ def test_captured_graph_follows_the_logits():
         dl2 = torch.empty_like(dl)
         tp.tp_moe_route_bwd(d, l, e, up, t["slot_row"], N * K, dl2)
         assert torch.equal(dl, dl2)
+
+
+def by_pieces(d, l, b, piece=1000):
+    """The same tokens in calls of few tokens, which take a wavefront each."""
+    es, ws = [], []
+    for i in range(0, d["N"], piece):
+        part = l[i:i + piece].contiguous()
+        e, w = forward({**d, "N": len(part)}, part, b)
+        es.append(e)
+        ws.append(w)
+    return torch.cat(es), torch.cat(ws)
+
+
+def check_many(d, l, b):
+    e, w = forward(d, l, b)
+    e2, w2 = by_pieces(d, l, b)
+    assert torch.equal(e, e2), (e != e2).nonzero()[:4]
+    g = 2 * (gamma(d, l) + 2.0 ** -24)       # either side may be off by that much
+    assert bool(((w - w2).abs() <= g * w2.abs() + 1e-37).all())
+    pick = list(range(0, d["N"], d["N"] // 40)) + [d["N"] - 1]
+    part = l[pick].contiguous()
+    we, ww = want_forward({**d, "N": len(pick)}, part, b)
+    assert np.array_equal(e[pick].cpu().numpy(), we)
+    assert (np.abs(w[pick].double().cpu().numpy() - ww) <= (2.0 ** -24 + gamma(d, l)) * np.abs(ww) + 1e-37).all()
+
+
+@pytest.mark.parametrize("E,K,groups,kept,best", CONFIGS)
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_many_tokens(E, K, groups, kept, best, sigmoid, dtype):
+    for k, (bias, masked, renorm) in enumerate([(True, True, True), (False, True, False), (True, False, False)]):
+        N = 4096 + 7 * k
+        d = desc(N, E, K, groups, kept, best, sigmoid, renorm, dtype, scale=1.5)
+        l, b = inputs(N, E, dtype, bias, masked, seed=E + k)
+        check_many(d, l, b)
+
+
+@pytest.mark.parametrize("E,K,groups,kept", [(16, 4, 1, 1), (32, 4, 2, 1), (64, 8, 8, 3), (128, 8, 4, 2), (256, 8, 8, 4),
+                                             (256, 15, 1, 1), (256, 16, 1, 1)])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_many_tokens_with_equal_and_close_values(E, K, groups, kept, sigmoid):
+    N = 4099
+    g = torch.Generator(device="cuda").manual_seed(E)
+    close = 1.0 + torch.randint(0, 8, (N, E), generator=g, device="cuda") * 2.0 ** -23
+    ties = torch.randint(0, 3, (N, E), generator=g, device="cuda").float()
+    ties[5] = float("nan")
+    ties[6] = -INF
+    ties[7, 1:] = -INF
+    ties[8, ::3] = INF
+    small = torch.randint(0, 4, (E,), generator=g, device="cuda").float() * 2.0 ** -27
+    for l in (close, ties):
+        for b in (None, small, torch.zeros(E, device="cuda"), -3 * torch.ones(E, device="cuda")):
+            check_many(desc(N, E, K, groups, kept, 2, sigmoid), l, b)
+
+
+@pytest.mark.parametrize("N,K", [(40000, 2), (20000, 8), (16384, 2), (140000, 1), (9000, 32), (66000, 6)])
+@pytest.mark.parametrize("E,first,n_local", [(64, 0, 64), (64, 8, 1), (1024, 0, 1024), (256, 100, 70)])
+def test_tables_of_many_runs(N, K, E, first, n_local):
+    """Runs beyond what a workgroup adds up itself; against a stable sort."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    e = torch.randint(-1, E, (N, K), generator=g, device="cuda", dtype=torch.int32)
+    w = torch.rand(N, K, generator=g, device="cuda")
+    R = N * K
+    got = tables(N, K, first, n_local, R, e, w)
+    flat = e.view(-1).long() - first
+    on = (flat >= 0) & (flat < n_local)
+    order = torch.where(on, flat, n_local).sort(stable=True).indices
+    total = int(on.sum())
+    count = torch.bincount(flat[on], minlength=n_local)
+    assert torch.equal(got["offsets"].long(), torch.cat([count.new_zeros(1), count.cumsum(0)]))
+    assert torch.equal(got["row_token"][:total].long(), order[:total] // K) and bool((got["row_token"][total:] == -1).all())
+    assert torch.equal(got["row_weight"][:total], w.view(-1)[order[:total]]) and bool((got["row_weight"][total:] == 0).all())
+    slot = torch.full((R,), -1, dtype=torch.int64, device="cuda")
+    slot[order[:total]] = torch.arange(total, device="cuda")
+    assert torch.equal(got["slot_row"].view(-1).long(), slot)
+    assert torch.equal(got["tok_ptr"].long(), torch.cat([count.new_zeros(1), on.view(N, K).sum(1).cumsum(0)]))
+    per_token = torch.where(got["row_token"] >= 0, got["row_token"].long(), N).sort(stable=True).indices
+    assert torch.equal(got["tok_rows"][:total].long(), per_token[:total]) and bool((got["tok_rows"][total:] == -1).all())
