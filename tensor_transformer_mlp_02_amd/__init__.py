@@ -193,23 +193,30 @@ def _address(t, nbytes, name, dtype, device) -> int:
 _DTYPE_NAMES = {n: f"torch.{n}" for n in ("int32", "float32", "bfloat16")}
 
 
-_addresses = None
+_compiled = None
+
+
+def _marshaller():
+    """The compiled part of the binding, False where it is not built (every
+    call then marshals in Python: the same checks, slower)."""
+    global _compiled
+    if _compiled is None:
+        try:
+            _get_torch()
+            from . import _marshal as module
+            _compiled = module
+        except ImportError:
+            _compiled = False
+    return _compiled
 
 
 def _sized(items):
     """_ptr of each (tensor, bytes, name) or (tensor, bytes, name, dtype)."""
-    global _addresses
     device = _current_device()
-    if device >= 0:
-        if _addresses is None:
-            try:
-                from ._marshal import addresses as _addresses
-            except ImportError:  # not built: the loop below does the same, slower
-                _addresses = False
-        if _addresses:
-            out = _addresses(items, device)
-            if out is not None:
-                return out
+    if device >= 0 and _marshaller():
+        out = _compiled.addresses(items, device)
+        if out is not None:
+            return out
     out = []
     for t, nbytes, name, *dtype in items:
         if t is not None and not isinstance(t, int):

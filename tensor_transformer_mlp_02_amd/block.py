@@ -10,7 +10,8 @@ from __future__ import annotations
 import ctypes
 from typing import Optional
 
-from . import TP_BF16, _check, _elt, _ptr, _sized, _stream, _vp
+from . import (TP_BF16, TpError, _check, _current_device, _elt, _marshaller, _ptr, _sized,
+               _stream, _vp, tp_last_error)
 from . import lib as _base_lib
 
 __all__ = [
@@ -58,8 +59,7 @@ def _lib() -> ctypes.CDLL:
     global _ready
     if _ready is None:
         L = _base_lib()
-        ND, RD = ctypes.POINTER(tp_norm_desc), ctypes.POINTER(tp_route_desc)
-        AD, AT = ctypes.POINTER(tp_adamw_desc), ctypes.POINTER(tp_adamw_tensor)
+        ND = RD = AD = AT = _vp  # structures, by address
         for name, args, res in (
                 ("tp_block_norm_fwd", [ND] + [_vp] * 12, ctypes.c_int),
                 ("tp_block_norm_bwd_workspace", [ND], _sz),
@@ -72,8 +72,27 @@ def _lib() -> ctypes.CDLL:
                 ("tp_adamw_step", [AD, _i32, AT] + [_vp] * 4, ctypes.c_int)):
             fn = getattr(L, name)
             fn.argtypes, fn.restype = args, res
+            _entry[name] = ctypes.cast(fn, _vp).value
         _ready = L
     return _ready
+
+
+_entry = {}
+
+
+def _call(name: str, args: tuple) -> int:
+    """Entry point `name` with args: items as _sized takes them, ints, None."""
+    L = _ready or _lib()
+    m = _marshaller()
+    if m:
+        device = _current_device()
+        if device >= 0:
+            rc = m.call(_entry[name], device, args)
+            if rc == 0:
+                return 0
+            if rc is not None:
+                raise TpError(rc, tp_last_error())
+    return _check(getattr(L, name)(*[_sized([a])[0] if isinstance(a, tuple) else a for a in args]))
 
 
 def _as(cls, desc, **defaults):
@@ -101,11 +120,12 @@ def tp_block_norm_fwd(desc, X, O, w_post, b_post, gate, w_pre, b_pre, Y, Hn, sta
     defaults, gate_rows 0, kind TP_NORM_RMS, dtype TP_BF16, eps 1e-5, res_scale 1, branch_scale 1."""
     d = _norm(desc)
     rows, vec, gate_n, _, _, stat = _norm_sizes(d)
-    p = _sized([(X, rows, "X"), (O, rows, "O"), (w_post, vec, "w_post"), (b_post, vec, "b_post"),
-                (gate, gate_n, "gate"), (w_pre, vec, "w_pre"), (b_pre, vec, "b_pre"),
-                (Y, rows, "Y"), (Hn, rows, "Hn"), (stat_post, stat, "stat_post", "float32"),
-                (stat_pre, stat, "stat_pre", "float32")])
-    return _check(_lib().tp_block_norm_fwd(ctypes.byref(d), *p, _stream(stream)))
+    return _call("tp_block_norm_fwd", (
+        ctypes.addressof(d), (X, rows, "X"), (O, rows, "O"), (w_post, vec, "w_post"),
+        (b_post, vec, "b_post"), (gate, gate_n, "gate"), (w_pre, vec, "w_pre"),
+        (b_pre, vec, "b_pre"), (Y, rows, "Y"), (Hn, rows, "Hn"),
+        (stat_post, stat, "stat_post", "float32"), (stat_pre, stat, "stat_pre", "float32"),
+        _stream(stream)))
 
 
 def tp_block_norm_bwd_workspace(desc) -> int:
@@ -119,15 +139,15 @@ def tp_block_norm_bwd(desc, dY, dHn, Y, O, w_post, b_post, gate, w_pre, stat_pos
     accumulate=True adds into the fp32 gradients."""
     d = _norm(desc)
     rows, vec, gate_n, out, gate_out, stat = _norm_sizes(d)
-    p = _sized([(dY, rows, "dY"), (dHn, rows, "dHn"), (Y, rows, "Y"), (O, rows, "O"),
-                (w_post, vec, "w_post"), (b_post, vec, "b_post"), (gate, gate_n, "gate"),
-                (w_pre, vec, "w_pre"), (stat_post, stat, "stat_post", "float32"),
-                (stat_pre, stat, "stat_pre", "float32"), (dX, rows, "dX"), (dO, rows, "dO"),
-                (dw_post, out, "dw_post", "float32"), (db_post, out, "db_post", "float32"),
-                (dgate, gate_out, "dgate", "float32"), (dw_pre, out, "dw_pre", "float32"),
-                (db_pre, out, "db_pre", "float32"), (workspace, int(ws_bytes), "workspace")])
-    return _check(_lib().tp_block_norm_bwd(ctypes.byref(d), *p, int(ws_bytes),
-                                           1 if accumulate else 0, _stream(stream)))
+    return _call("tp_block_norm_bwd", (
+        ctypes.addressof(d), (dY, rows, "dY"), (dHn, rows, "dHn"), (Y, rows, "Y"), (O, rows, "O"),
+        (w_post, vec, "w_post"), (b_post, vec, "b_post"), (gate, gate_n, "gate"),
+        (w_pre, vec, "w_pre"), (stat_post, stat, "stat_post", "float32"),
+        (stat_pre, stat, "stat_pre", "float32"), (dX, rows, "dX"), (dO, rows, "dO"),
+        (dw_post, out, "dw_post", "float32"), (db_post, out, "db_post", "float32"),
+        (dgate, gate_out, "dgate", "float32"), (dw_pre, out, "dw_pre", "float32"),
+        (db_pre, out, "db_pre", "float32"), (workspace, int(ws_bytes), "workspace"),
+        int(ws_bytes), 1 if accumulate else 0, _stream(stream)))
 
 
 def tp_moe_route_fwd(desc, logits, bias, topk_expert, topk_weight, stream=None) -> int:
@@ -135,10 +155,10 @@ def tp_moe_route_fwd(desc, logits, bias, topk_expert, topk_weight, stream=None) 
     groups 1, groups_kept 1, group_best 1, score TP_SCORE_SOFTMAX, renorm 0, dtype TP_F32, scale 1."""
     d = _route(desc)
     n, e, k = max(d.N, 0), max(d.E, 0), max(d.K, 0)
-    p = _sized([(logits, n * e * _elt(d.dtype), "logits"), (bias, e * 4, "bias", "float32"),
-                (topk_expert, n * k * 4, "topk_expert", "int32"),
-                (topk_weight, n * k * 4, "topk_weight", "float32")])
-    return _check(_lib().tp_moe_route_fwd(ctypes.byref(d), *p, _stream(stream)))
+    return _call("tp_moe_route_fwd", (
+        ctypes.addressof(d), (logits, n * e * _elt(d.dtype), "logits"),
+        (bias, e * 4, "bias", "float32"), (topk_expert, n * k * 4, "topk_expert", "int32"),
+        (topk_weight, n * k * 4, "topk_weight", "float32"), _stream(stream)))
 
 
 def tp_moe_route_bwd(desc, logits, topk_expert, d_weight, slot_row, R: int, dlogits,
@@ -147,12 +167,12 @@ def tp_moe_route_bwd(desc, logits, topk_expert, d_weight, slot_row, R: int, dlog
     d = _route(desc)
     n, e, k = max(d.N, 0), max(d.E, 0), max(d.K, 0)
     dw = n * k * 4 if slot_row is None else max(int(R), 0) * 4
-    p = _sized([(logits, n * e * _elt(d.dtype), "logits"),
-                (topk_expert, n * k * 4, "topk_expert", "int32"),
-                (d_weight, dw, "d_weight", "float32"), (slot_row, n * k * 4, "slot_row", "int32")])
-    return _check(_lib().tp_moe_route_bwd(ctypes.byref(d), *p, int(R),
-                                          _ptr(dlogits, n * e * _elt(d.dtype), "dlogits"),
-                                          _stream(stream)))
+    whole = n * e * _elt(d.dtype)
+    return _call("tp_moe_route_bwd", (
+        ctypes.addressof(d), (logits, whole, "logits"),
+        (topk_expert, n * k * 4, "topk_expert", "int32"), (d_weight, dw, "d_weight", "float32"),
+        (slot_row, n * k * 4, "slot_row", "int32"), int(R), (dlogits, whole, "dlogits"),
+        _stream(stream)))
 
 
 def tp_moe_route_tables_workspace(N: int, K: int, n_local: int) -> int:
@@ -163,16 +183,17 @@ def tp_moe_route_tables(N: int, K: int, first_expert: int, n_local: int, R: int,
                         topk_weight, offsets, row_token, row_weight, tok_ptr, tok_rows, slot_row,
                         workspace, ws_bytes: int, stream=None) -> int:
     """Dispatch tables of the experts [first_expert, first_expert + n_local), on the device."""
-    n, k, r, e = max(int(N), 0), max(int(K), 0), max(int(R), 0), max(int(n_local), 0)
-    p = _sized([(topk_expert, n * k * 4, "topk_expert", "int32"),
-                (topk_weight, n * k * 4, "topk_weight", "float32"),
-                (offsets, (e + 1) * 4, "offsets", "int32"), (row_token, r * 4, "row_token", "int32"),
-                (row_weight, r * 4, "row_weight", "float32"),
-                (tok_ptr, (n + 1) * 4, "tok_ptr", "int32"), (tok_rows, r * 4, "tok_rows", "int32"),
-                (slot_row, n * k * 4, "slot_row", "int32"),
-                (workspace, int(ws_bytes), "workspace")])
-    return _check(_lib().tp_moe_route_tables(int(N), int(K), int(first_expert), int(n_local),
-                                             int(R), *p, int(ws_bytes), _stream(stream)))
+    N, K, first_expert, n_local, R, ws_bytes = (int(N), int(K), int(first_expert), int(n_local),
+                                                int(R), int(ws_bytes))
+    n, r = max(N, 0) * 4, max(R, 0) * 4
+    nk = n * max(K, 0)
+    return _call("tp_moe_route_tables", (
+        N, K, first_expert, n_local, R, (topk_expert, nk, "topk_expert", "int32"),
+        (topk_weight, nk, "topk_weight", "float32"),
+        (offsets, (max(n_local, 0) + 1) * 4, "offsets", "int32"), (row_token, r, "row_token", "int32"),
+        (row_weight, r, "row_weight", "float32"), (tok_ptr, n + 4, "tok_ptr", "int32"),
+        (tok_rows, r, "tok_rows", "int32"), (slot_row, nk, "slot_row", "int32"),
+        (workspace, ws_bytes, "workspace"), ws_bytes, _stream(stream)))
 
 
 class AdamwTensors:
@@ -186,6 +207,7 @@ class AdamwTensors:
         self.formats = (d.grad_dtype, d.state_bits)
         self.n = len(tensors)
         self.array = (tp_adamw_tensor * max(1, self.n))()
+        self.address = ctypes.addressof(self.array)
         self.tensors = [dict(t) for t in tensors]
         self.device = None
         state = None if small else "float32"
@@ -229,11 +251,10 @@ def tp_adamw_step(desc, tensors, dev_step=None, dev_lr=None, grad_scale=None,
     t = tensors if isinstance(tensors, AdamwTensors) else AdamwTensors(d, tensors)
     if t.formats != (d.grad_dtype, d.state_bits):
         raise ValueError(f"the table is for (grad_dtype, state_bits) = {t.formats}")
-    if t.device is not None:
-        import torch
-        if torch.cuda.current_device() != t.device:
-            raise ValueError(f"the table is on cuda:{t.device}, the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
-    p = _sized([(dev_step, 4, "dev_step", "int32"), (dev_lr, 4, "dev_lr", "float32"),
-                (grad_scale, 4, "grad_scale", "float32")])
-    return _check(_lib().tp_adamw_step(ctypes.byref(d), t.n, t.array, *p, _stream(stream)))
+    if t.device is not None and _current_device() != t.device:
+        raise ValueError(f"the table is on cuda:{t.device}, the current device is "
+                         f"cuda:{_current_device()}")
+    return _call("tp_adamw_step", (
+        ctypes.addressof(d), t.n, t.address, (dev_step, 4, "dev_step", "int32"),
+        (dev_lr, 4, "dev_lr", "float32"), (grad_scale, 4, "grad_scale", "float32"),
+        _stream(stream)))

@@ -1,12 +1,19 @@
-// Checks and device addresses of a call's tensors for the Python binding.
+// Calls of the library from the Python binding.
 //
-// A call of this library passes 5 to 18 tensors; looking at each from Python
-// (device, contiguity, size, type, address) takes longer than the launch.
-// addresses(items, device) does it here, on the same items as the binding's
-// own loop: tuples (tensor | int | None, bytes | None, name[, type name]).
-// It returns the list of addresses, or None where any item does not pass:
-// the binding's loop then finds the item and words the error.
+// A call passes 5 to 18 tensors; looking at each from Python (device,
+// contiguity, size, type, address) takes longer than the launch.  Here it is
+// done in one step, on the same items as the binding's own loop: tuples
+// (tensor | int | None, bytes | None, name[, type name]).
+//   addresses(items, device) -> the list of addresses
+//   call(function, device, args) -> the function's int result; `args` is a
+//       tuple of items and of plain ints / None, `function` the address of an
+//       entry point whose arguments are all pointers or integers and whose
+//       result is an int
+// Both return None where an item does not pass: the binding's loop then finds
+// the item and words the error.
 #include <torch/csrc/autograd/python_variable.h>
+
+#include <cstdint>
 
 namespace {
 
@@ -24,72 +31,129 @@ bool type_is(const at::Tensor& t, PyObject* name) {
   }
 }
 
+// The address that an item stands for; false: it does not pass (or an error
+// is set).
+bool address_of(PyObject* it, long device, uintptr_t& out) {
+  if (!PyTuple_Check(it) || PyTuple_GET_SIZE(it) < 3) return false;
+  PyObject* t = PyTuple_GET_ITEM(it, 0);
+  if (t == Py_None) {
+    out = 0;
+    return true;
+  }
+  if (PyLong_Check(t)) {
+    out = (uintptr_t)PyLong_AsUnsignedLongLong(t);
+    return !PyErr_Occurred();
+  }
+  if (!THPVariable_Check(t)) return false;
+  const at::Tensor& x = THPVariable_Unpack(t);
+  PyObject* nb = PyTuple_GET_ITEM(it, 1);
+  PyObject* type = PyTuple_GET_SIZE(it) > 3 ? PyTuple_GET_ITEM(it, 3) : Py_None;
+  if (!x.is_cuda() || x.get_device() != device || !x.is_contiguous()) return false;
+  if (type != Py_None && !(PyUnicode_Check(type) && type_is(x, type))) return false;
+  if (nb != Py_None) {
+    const long long need = PyLong_AsLongLong(nb);
+    if (need == -1 && PyErr_Occurred()) return false;
+    if ((long long)x.nbytes() < need) return false;
+  }
+  out = reinterpret_cast<uintptr_t>(x.data_ptr());
+  return true;
+}
+
+PyObject* refused() {
+  PyErr_Clear();
+  Py_RETURN_NONE;
+}
+
 PyObject* addresses(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   if (nargs != 2 || !PyList_Check(args[0])) {
     PyErr_SetString(PyExc_TypeError, "addresses(list, device)");
     return nullptr;
   }
-  PyObject* items = args[0];
   const long device = PyLong_AsLong(args[1]);
   if (device == -1 && PyErr_Occurred()) return nullptr;
-  const Py_ssize_t n = PyList_GET_SIZE(items);
+  const Py_ssize_t n = PyList_GET_SIZE(args[0]);
   Owned list{PyList_New(n)};
   if (!list.p) return nullptr;
-  PyObject* out = list.p;
   for (Py_ssize_t i = 0; i < n; ++i) {
-    PyObject* it = PyList_GET_ITEM(items, i);
-    bool fine = PyTuple_Check(it) && PyTuple_GET_SIZE(it) >= 3;
+    uintptr_t a = 0;
+    PyObject* it = PyList_GET_ITEM(args[0], i);
+    if (!address_of(it, device, a)) return refused();
     PyObject* value = nullptr;
-    if (fine) {
-      PyObject* t = PyTuple_GET_ITEM(it, 0);
-      if (t == Py_None || PyLong_Check(t)) {
-        Py_INCREF(t);
-        value = t;
-      } else if (THPVariable_Check(t)) {
-        const at::Tensor& x = THPVariable_Unpack(t);
-        PyObject* nb = PyTuple_GET_ITEM(it, 1);
-        PyObject* type = PyTuple_GET_SIZE(it) > 3 ? PyTuple_GET_ITEM(it, 3) : Py_None;
-        fine = x.is_cuda() && x.get_device() == device && x.is_contiguous() &&
-               (type == Py_None || (PyUnicode_Check(type) && type_is(x, type)));
-        if (fine && nb != Py_None) {
-          const long long need = PyLong_AsLongLong(nb);
-          if (need == -1 && PyErr_Occurred()) {
-            PyErr_Clear();
-            fine = false;
-          } else {
-            fine = (long long)x.nbytes() >= need;
-          }
-        }
-        if (fine) value = PyLong_FromVoidPtr(x.data_ptr());
-      } else {
-        fine = false;
-      }
+    if (PyTuple_GET_ITEM(it, 0) == Py_None) {
+      Py_INCREF(Py_None);
+      value = Py_None;
+    } else {
+      value = PyLong_FromUnsignedLongLong(a);
     }
-    if (!fine || !value) {
-      Py_XDECREF(value);
-      if (PyErr_Occurred()) return nullptr;
-      Py_RETURN_NONE;
-    }
-    PyList_SET_ITEM(out, i, value);
+    if (!value) return nullptr;
+    PyList_SET_ITEM(list.p, i, value);
   }
+  PyObject* out = list.p;
   list.p = nullptr;
   return out;
 }
 
+// Every argument is a pointer or an integer of at most 64 bits and the C
+// calling convention of x86-64 passes each in a whole register or stack
+// slot, so one function type serves all entry points; slots past a
+// function's own arguments are not looked at.
+constexpr int SLOTS = 24;
+typedef int (*Entry)(uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t,
+                     uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t,
+                     uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t,
+                     uintptr_t, uintptr_t, uintptr_t);
+
+PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  if (nargs != 3 || !PyTuple_Check(args[2]) || PyTuple_GET_SIZE(args[2]) > SLOTS) {
+    PyErr_SetString(PyExc_TypeError, "call(function, device, tuple of at most 24)");
+    return nullptr;
+  }
+  const uintptr_t fn = (uintptr_t)PyLong_AsUnsignedLongLong(args[0]);
+  if (PyErr_Occurred()) return nullptr;
+  const long device = PyLong_AsLong(args[1]);
+  if (device == -1 && PyErr_Occurred()) return nullptr;
+  uintptr_t v[SLOTS] = {0};
+  const Py_ssize_t n = PyTuple_GET_SIZE(args[2]);
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    PyObject* it = PyTuple_GET_ITEM(args[2], i);
+    if (it == Py_None) continue;
+    if (PyLong_Check(it)) {
+      int over = 0;
+      const long long x = PyLong_AsLongLongAndOverflow(it, &over);
+      v[i] = over > 0 ? (uintptr_t)PyLong_AsUnsignedLongLong(it) : (uintptr_t)x;
+      if (over < 0 || PyErr_Occurred()) return refused();
+    } else if (!address_of(it, device, v[i])) {
+      return refused();
+    }
+  }
+  int rc;
+  Py_BEGIN_ALLOW_THREADS  // a full queue makes a launch wait
+  rc = reinterpret_cast<Entry>(fn)(
+      v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], v[8], v[9], v[10], v[11], v[12], v[13], v[14],
+      v[15], v[16], v[17], v[18], v[19], v[20], v[21], v[22], v[23]);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(rc);
+}
+
 // x.data_ptr() and the like may throw (a tensor without storage): the
 // binding's loop meets the same and words it
-PyObject* addresses_safe(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyObject* guarded(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
   try {
-    return addresses(self, args, nargs);
+    return F(self, args, nargs);
   } catch (...) {
-    PyErr_Clear();
-    Py_RETURN_NONE;
+    return refused();
   }
 }
 
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyCFunction method() {
+  return reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&guarded<F>));
+}
+
 PyMethodDef methods[] = {
-    {"addresses", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(addresses_safe)),
-     METH_FASTCALL, "addresses(items, device) -> list of addresses, or None"},
+    {"addresses", method<addresses>(), METH_FASTCALL, "addresses(items, device)"},
+    {"call", method<call>(), METH_FASTCALL, "call(function, device, args)"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
