@@ -12,8 +12,8 @@ namespace route {
 constexpr int NT = 256;
 constexpr int WAVES = NT / 64;
 // a logit at or below the lowest finite bf16 (or NaN) is no choice
-#define TP_ROUTE_LOWEST (-3.3895313892515355e38f)
-#define TP_ROUTE_LARGEST 3.4028234663852886e38f
+constexpr float LOWEST = -3.3895313892515355e38f;
+constexpr float LARGEST = 3.4028234663852886e38f;
 
 // One wavefront a token.  Lane i holds the experts i V .. i V + V - 1, so
 // that a lane's logits are one load and the lower expert is in the lower
@@ -52,8 +52,8 @@ __device__ __forceinline__ void load_row(const T* row, int E, int lane, bool liv
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     // NaN compares false
-    if (!(l[i] > TP_ROUTE_LOWEST)) l[i] = -__builtin_huge_valf();
-    l[i] = fminf(l[i], TP_ROUTE_LARGEST);
+    if (!(l[i] > LOWEST)) l[i] = -__builtin_huge_valf();
+    l[i] = fminf(l[i], LARGEST);
   }
 }
 
@@ -247,7 +247,7 @@ __device__ __forceinline__ int choose_wide(const FwdArgs& A, const float (&l)[V]
     if constexpr (SIGMOID) {
       c[i] = 1.0 / (1.0 + exp(-(double)l[i]));
     } else {
-      c[i] = l[i] > TP_ROUTE_LOWEST ? exp((double)l[i] - (double)top) : 0.0;
+      c[i] = l[i] > LOWEST ? exp((double)l[i] - (double)top) : 0.0;
       sum += c[i];
     }
   }
@@ -260,7 +260,7 @@ __device__ __forceinline__ int choose_wide(const FwdArgs& A, const float (&l)[V]
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     if (A.bias && lane * V + i < A.E) c[i] += (double)A.bias[lane * V + i];
-    if (!(l[i] > TP_ROUTE_LOWEST)) c[i] = NEG;
+    if (!(l[i] > LOWEST)) c[i] = NEG;
   }
   if (A.groups > 1) {
     const unsigned long long keep = keep_groups(group_worth<double, V>(c, A, lane, cs), A, lane);
@@ -327,7 +327,7 @@ __global__ __launch_bounds__(NT) void fwd_kernel(FwdArgs A) {
   load_row<T, V>(logits + t * A.E, A.E, lane, t < A.N, l);
   for (; t < A.N; t += stride) {
     float ahead[V];
-    load_row<T, V>(logits + (t + stride) * A.E, A.E, lane, t + stride < A.N, ahead);
+    if (t + stride < A.N) load_row<T, V>(logits + (t + stride) * A.E, A.E, lane, true, ahead);
     float s[V];
     float top = 0.f, largest = 1.f;  // of the logits; of the scores
     if constexpr (SIGMOID) {
@@ -342,7 +342,7 @@ __global__ __launch_bounds__(NT) void fwd_kernel(FwdArgs A) {
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        s[i] = l[i] > TP_ROUTE_LOWEST ? fast_exp(l[i] - top) : 0.f;
+        s[i] = l[i] > LOWEST ? fast_exp(l[i] - top) : 0.f;
         sum += s[i];
       }
       sum = wave_sum(sum);
@@ -356,7 +356,7 @@ __global__ __launch_bounds__(NT) void fwd_kernel(FwdArgs A) {
     if (A.groups > 1) {
       float c[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) c[i] = l[i] > TP_ROUTE_LOWEST ? s[i] + bias[i] : NEG;
+      for (int i = 0; i < V; ++i) c[i] = l[i] > LOWEST ? s[i] + bias[i] : NEG;
       const float worth = group_worth<float, V>(c, A, lane, scores);
       const unsigned long long keep = keep_groups(worth, A, lane);
       const bool mine = (keep >> lane) & 1;
@@ -369,7 +369,7 @@ __global__ __launch_bounds__(NT) void fwd_kernel(FwdArgs A) {
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        key[i] = l[i] > TP_ROUTE_LOWEST ? to_key(A.bias ? s[i] + bias[i] : l[i]) : 0u;
+        key[i] = l[i] > LOWEST ? to_key(A.bias ? s[i] + bias[i] : l[i]) : 0u;
     }
     // for the chosen ones' lanes to read
 #pragma unroll
@@ -472,7 +472,8 @@ __global__ __launch_bounds__(NT) void fwd_rows_kernel(FwdArgs A) {
   load_row<T, V>(logits + t * A.E, A.E, r, t < A.N, l);
   for (; t - q < A.N; t += stride) {
     float ahead[V];
-    load_row<T, V>(logits + (t + stride) * A.E, A.E, r, t + stride < A.N, ahead);
+    if (t - q + stride < A.N)
+      load_row<T, V>(logits + (t + stride) * A.E, A.E, r, t + stride < A.N, ahead);
     float s[V];
     float top = 0.f, largest = 1.f;
     auto fmaxf_ = [](float a, float b) { return fmaxf(a, b); };
@@ -487,7 +488,7 @@ __global__ __launch_bounds__(NT) void fwd_rows_kernel(FwdArgs A) {
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        s[i] = l[i] > TP_ROUTE_LOWEST ? fast_exp(l[i] - top) : 0.f;
+        s[i] = l[i] > LOWEST ? fast_exp(l[i] - top) : 0.f;
         sum += s[i];
       }
       sum = row_all(sum, [](float a, float b) { return a + b; });
@@ -511,7 +512,7 @@ __global__ __launch_bounds__(NT) void fwd_rows_kernel(FwdArgs A) {
       float b1 = NEG, b2 = NEG;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float c = l[i] > TP_ROUTE_LOWEST ? s[i] + bias[i] : NEG;
+        const float c = l[i] > LOWEST ? s[i] + bias[i] : NEG;
         b2 = fmaxf(b2, fminf(b1, c));
         b1 = fmaxf(b1, c);
       }
@@ -530,7 +531,7 @@ __global__ __launch_bounds__(NT) void fwd_rows_kernel(FwdArgs A) {
     }
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      key[i] = kept && l[i] > TP_ROUTE_LOWEST ? to_key(A.bias ? s[i] + bias[i] : l[i]) : 0u;
+      key[i] = kept && l[i] > LOWEST ? to_key(A.bias ? s[i] + bias[i] : l[i]) : 0u;
     uint32_t my_key = 0;
     const int rounds = A.K + (A.bias ? 1 : 0);
     for (int j = 0; j < rounds; ++j) {
@@ -584,7 +585,7 @@ __global__ __launch_bounds__(NT) void fwd_rows_kernel(FwdArgs A) {
             float x;
             if constexpr (sizeof(T) == 2) x = bf16_to_f32(logits[t * A.E + my_e]);
             else x = logits[t * A.E + my_e];
-            x = fminf(x, TP_ROUTE_LARGEST);
+            x = fminf(x, LARGEST);
             my_s = SIGMOID ? __builtin_amdgcn_rcpf(1.f + fast_exp(-x)) : fast_exp(x - top) * largest;
           }
         }
@@ -634,13 +635,13 @@ __global__ __launch_bounds__(NT) void bwd_kernel(BwdArgs A) {
       if (!A.slot_row || (r >= 0 && r < A.R)) up = A.d_weight[r] * A.scale;
       if constexpr (sizeof(T) == 2) le = bf16_to_f32(row[e]); else le = row[e];
     }
-    if (!(le > TP_ROUTE_LOWEST)) le = -__builtin_huge_valf();
-    le = fminf(le, TP_ROUTE_LARGEST);
+    if (!(le > LOWEST)) le = -__builtin_huge_valf();
+    le = fminf(le, LARGEST);
     float se;
     if constexpr (SIGMOID) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) s[i] = l[i] > TP_ROUTE_LOWEST ? 1.f / (1.f + expf(-l[i])) : 0.f;
-      se = le > TP_ROUTE_LOWEST ? 1.f / (1.f + expf(-le)) : 0.f;
+      for (int i = 0; i < V; ++i) s[i] = l[i] > LOWEST ? 1.f / (1.f + expf(-l[i])) : 0.f;
+      se = le > LOWEST ? 1.f / (1.f + expf(-le)) : 0.f;
     } else {
       float top = l[0], sum = 0.f;
 #pragma unroll
@@ -648,14 +649,14 @@ __global__ __launch_bounds__(NT) void bwd_kernel(BwdArgs A) {
       top = wave_max(top);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        s[i] = l[i] > TP_ROUTE_LOWEST ? expf(l[i] - top) : 0.f;
+        s[i] = l[i] > LOWEST ? expf(l[i] - top) : 0.f;
         sum += s[i];
       }
       sum = wave_sum(sum);
       const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) s[i] *= inv;
-      se = le > TP_ROUTE_LOWEST ? expf(le - top) * inv : 0.f;
+      se = le > LOWEST ? expf(le - top) * inv : 0.f;
     }
     float d = up;
     if (A.renorm) {
