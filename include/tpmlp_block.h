@@ -99,8 +99,8 @@ int tp_block_norm_fwd(const tp_norm_desc *desc, const void *X, const void *O, co
  * gate_rows > 0.  b_post is read for dgate only.  Nothing may overlap.
  * Sums over tokens are fp32 in a fixed order: equal calls give equal bits.
  * workspace: tp_block_norm_bwd_workspace(desc) bytes, 16-byte aligned, not
- * shared with a call that may run at the same time; its contents do not
- * matter before or after.
+ * shared with a call that may run at the same time (two graphs replayed
+ * together, say); its contents do not matter before or after.
  */
 size_t tp_block_norm_bwd_workspace(const tp_norm_desc *desc);
 int tp_block_norm_bwd(const tp_norm_desc *desc, const void *dY, const void *dHn, const void *Y,
@@ -184,7 +184,10 @@ int tp_moe_route_bwd(const tp_route_desc *desc, const void *logits, const int32_
  * tables may be given any smaller R that offsets[n_local] does not exceed.
  * topk_expert values outside the local range give no row.  n_local in
  * 1..1024 (the grouped calls take 64), first_expert >= 0.  topk_weight and
- * row_weight may both be NULL.  Pointers 4-byte aligned, workspace 16.
+ * row_weight may both be NULL.  Pointers 4-byte aligned.  workspace:
+ * tp_moe_route_tables_workspace(N, K, n_local) bytes (at least 16), 16-byte
+ * aligned, not shared with a call that may run at the same time (two graphs
+ * replayed together, say); its contents do not matter before or after.
  */
 size_t tp_moe_route_tables_workspace(int64_t N, int32_t K, int32_t n_local);
 int tp_moe_route_tables(int64_t N, int32_t K, int32_t first_expert, int32_t n_local, int64_t R,

@@ -738,26 +738,39 @@ __global__ __launch_bounds__(RUN) void count_kernel(TablesArgs A, int pairs) {
   for (int i = threadIdx.x; i < width; i += RUN) A.ws[(int64_t)blockIdx.x * width + i] = hist[i];
 }
 
-// 64 columns a workgroup, 16 shares of the runs
+// 64 columns a workgroup, 16 shares of the runs, eight counts on their way at
+// a time
 __global__ __launch_bounds__(1024) void scan_kernel(TablesArgs A, int runs) {
+  constexpr int AT_ONCE = 8;
   __shared__ int part[16][64];
   const int width = A.n_local + 1;
   const int lane = threadIdx.x & 63, share = threadIdx.x >> 6;
   const int e = blockIdx.x * 64 + lane;
   const int each = (runs + 15) / 16, r0 = min(share * each, runs), r1 = min(r0 + each, runs);
+  int v[AT_ONCE];
+  auto load = [&](int r) {
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) v[i] = r + i < r1 ? A.ws[(int64_t)(r + i) * width + e] : 0;
+  };
   int sum = 0;
   if (e < width)
-    for (int r = r0; r < r1; ++r) sum += A.ws[(int64_t)r * width + e];
+    for (int r = r0; r < r1; r += AT_ONCE) {
+      load(r);
+#pragma unroll
+      for (int i = 0; i < AT_ONCE; ++i) sum += v[i];
+    }
   part[share][lane] = sum;
   __syncthreads();
   int base = 0;
   for (int i = 0; i < share; ++i) base += part[i][lane];
   if (e >= width) return;
-  for (int r = r0; r < r1; ++r) {
-    int* p = A.ws + (int64_t)r * width + e;
-    const int v = *p;
-    *p = base;
-    base += v;
+  for (int r = r0; r < r1; r += AT_ONCE) {
+    load(r);
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) {
+      if (r + i < r1) A.ws[(int64_t)(r + i) * width + e] = base;
+      base += v[i];
+    }
   }
   if (share == 15) A.ws[(int64_t)runs * width + e] = base;
 }

@@ -316,3 +316,31 @@ def test_long_batch_past_32_bit_offsets():
     x = host(X[pick])
     want, _, _, mag = ob.norm(x, False, np.ones(H), None, float(np.float32(EPS)))
     close("Hn", Hn[pick], want, mag, torch.bfloat16, (H / 4 + 64) * 2.0 ** -24)
+
+
+def test_backward_past_32_bit_offsets():
+    H, N = 8192, (1 << 19) + 3
+    g = torch.Generator(device="cuda").manual_seed(2)
+    bf = lambda: torch.empty(N, H, dtype=torch.bfloat16, device="cuda").normal_(generator=g)  # noqa: E731
+    X, dY, dH = bf(), bf(), bf()
+    w = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    r = torch.empty(N, device="cuda")
+    Hn = torch.empty_like(X)
+    d = dict(N=N, H=H)
+    tp.tp_block_norm_fwd(d, X, None, None, None, None, w, None, None, Hn, None, r)
+    dX, dw = Hn.fill_(float("nan")), torch.empty(H, device="cuda")
+    nb = tp.tp_block_norm_bwd_workspace(d)
+    tp.tp_block_norm_bwd(d, dY, dH, X, None, None, None, None, w, None, r, dX, None, None, None, None, dw, None,
+                         torch.empty(nb, dtype=torch.uint8, device="cuda"), nb)
+    pick = [0, 1, (1 << 18) - 1, 1 << 18, (1 << 18) + 1, (1 << 19) - 1, 1 << 19, N - 1]
+    want = ob.norm_bwd(host(dY[pick]), host(dH[pick]), host(X[pick]), None, None, None, None, np.ones(H), None, None,
+                       host(r[pick]), None, layer=False, a=1.0, b=1.0)
+    close("dX", dX[pick], want["dX"], want["mag_dX"], torch.bfloat16, (H / 2 + 128) * 2.0 ** -24)
+    # sums of half a million terms of size 1, in chains of 2049 and 256: far below 1e-5 of their magnitudes
+    part = torch.zeros(H, dtype=torch.float64, device="cuda")
+    mag = torch.zeros(H, dtype=torch.float64, device="cuda")
+    for i in range(0, N, 1 << 15):
+        t = dH[i:i + (1 << 15)].double() * X[i:i + (1 << 15)].double() * r[i:i + (1 << 15), None].double()
+        part += t.sum(0)
+        mag += t.abs().sum(0)
+    assert bool(((dw.double() - part).abs() <= (2049 + 256 + 64) * 2.0 ** -24 * mag).all())

@@ -395,3 +395,23 @@ def test_tables_of_many_runs(N, K, E, first, n_local):
     assert torch.equal(got["tok_ptr"].long(), torch.cat([count.new_zeros(1), on.view(N, K).sum(1).cumsum(0)]))
     per_token = torch.where(got["row_token"] >= 0, got["row_token"].long(), N).sort(stable=True).indices
     assert torch.equal(got["tok_rows"][:total].long(), per_token[:total]) and bool((got["tok_rows"][total:] == -1).all())
+
+
+@pytest.mark.parametrize("N,E", [((1 << 23) + 5, 512), ((1 << 24) + 3, 256)])
+def test_more_logits_than_32_bits_count(N, E):
+    K = 2
+    d = desc(N, E, K, renorm=True)
+    l = torch.empty(N, E, device="cuda").normal_()
+    e, w = forward(d, l, None)
+    up = torch.ones(N, K, device="cuda") * torch.arange(K, device="cuda")
+    dl = torch.empty_like(l)
+    tp.tp_moe_route_bwd(d, l, e, up, None, 0, dl)
+    pick = [0, 1, N // 2 - 1, N // 2, N // 2 + 1, N - 2, N - 1]
+    part = l[pick].contiguous()
+    p = {**d, "N": len(pick)}
+    we, ww = want_forward(p, part, None)
+    assert np.array_equal(e[pick].cpu().numpy(), we)
+    small = torch.empty_like(part)
+    tp.tp_moe_route_bwd(p, part, e[pick].contiguous(), up[pick].contiguous(), None, 0, small)
+    assert torch.equal(small, dl[pick])
+    check_backward(p, part, e[pick].contiguous(), up[pick].contiguous())
