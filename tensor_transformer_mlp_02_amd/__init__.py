@@ -202,10 +202,11 @@ def _marshaller():
     global _compiled
     if _compiled is None:
         try:
-            _get_torch()
+            c = _get_torch()._C
             from . import _marshal as module
+            module.setup(c._cuda_getDevice, c._cuda_getCurrentRawStream)
             _compiled = module
-        except ImportError:
+        except (ImportError, AttributeError):
             _compiled = False
     return _compiled
 

@@ -10,8 +10,7 @@ from __future__ import annotations
 import ctypes
 from typing import Optional
 
-from . import (TP_BF16, TpError, _check, _current_device, _elt, _marshaller, _ptr, _sized,
-               _stream, _vp, tp_last_error)
+from . import TP_BF16, _check, _current_device, _elt, _marshaller, _ptr, _sized, _stream, _vp
 from . import lib as _base_lib
 
 __all__ = [
@@ -80,19 +79,17 @@ def _lib() -> ctypes.CDLL:
 _entry = {}
 
 
-def _call(name: str, args: tuple) -> int:
-    """Entry point `name` with args: items as _sized takes them, ints, None."""
+def _call(name: str, args: tuple, stream) -> int:
+    """Entry point `name` with args (items as _sized takes them, ints, None) and the stream."""
     L = _ready or _lib()
+    if stream is not None:
+        stream = _stream(stream)
     m = _marshaller()
-    if m:
-        device = _current_device()
-        if device >= 0:
-            rc = m.call(_entry[name], device, args)
-            if rc == 0:
-                return 0
-            if rc is not None:
-                raise TpError(rc, tp_last_error())
-    return _check(getattr(L, name)(*[_sized([a])[0] if isinstance(a, tuple) else a for a in args]))
+    rc = m.call(_entry[name], args, stream) if m else None
+    if rc is None:
+        rc = getattr(L, name)(*[_sized([a])[0] if isinstance(a, tuple) else a for a in args],
+                              _stream(stream))
+    return rc if rc == 0 else _check(rc)
 
 
 def _as(cls, desc, **defaults):
@@ -110,8 +107,10 @@ def _route(desc) -> tp_route_desc:
 
 
 def _norm_sizes(d: tp_norm_desc):
-    n, h, g, e = max(d.N, 0), max(d.H, 0), max(d.gate_rows, 0), _elt(d.dtype)
-    return n * h * e, h * e, g * h * e, h * 4, g * h * 4, n * (8 if d.kind == TP_NORM_LAYER else 4)
+    # (a negative size asks for nothing here: the library refuses it)
+    n, h = d.N, d.H
+    vec = h * _elt(d.dtype)
+    return n * vec, vec, d.gate_rows * vec, h * 4, d.gate_rows * h * 4, n * (8 if d.kind else 4)
 
 
 def tp_block_norm_fwd(desc, X, O, w_post, b_post, gate, w_pre, b_pre, Y, Hn, stat_post=None,
@@ -124,8 +123,7 @@ def tp_block_norm_fwd(desc, X, O, w_post, b_post, gate, w_pre, b_pre, Y, Hn, sta
         ctypes.addressof(d), (X, rows, "X"), (O, rows, "O"), (w_post, vec, "w_post"),
         (b_post, vec, "b_post"), (gate, gate_n, "gate"), (w_pre, vec, "w_pre"),
         (b_pre, vec, "b_pre"), (Y, rows, "Y"), (Hn, rows, "Hn"),
-        (stat_post, stat, "stat_post", "float32"), (stat_pre, stat, "stat_pre", "float32"),
-        _stream(stream)))
+        (stat_post, stat, "stat_post", "float32"), (stat_pre, stat, "stat_pre", "float32")), stream)
 
 
 def tp_block_norm_bwd_workspace(desc) -> int:
@@ -147,32 +145,31 @@ def tp_block_norm_bwd(desc, dY, dHn, Y, O, w_post, b_post, gate, w_pre, stat_pos
         (dw_post, out, "dw_post", "float32"), (db_post, out, "db_post", "float32"),
         (dgate, gate_out, "dgate", "float32"), (dw_pre, out, "dw_pre", "float32"),
         (db_pre, out, "db_pre", "float32"), (workspace, int(ws_bytes), "workspace"),
-        int(ws_bytes), 1 if accumulate else 0, _stream(stream)))
+        int(ws_bytes), 1 if accumulate else 0), stream)
 
 
 def tp_moe_route_fwd(desc, logits, bias, topk_expert, topk_weight, stream=None) -> int:
     """The K experts of each token and their weights.  ``desc``: N, E, K and, with their defaults,
     groups 1, groups_kept 1, group_best 1, score TP_SCORE_SOFTMAX, renorm 0, dtype TP_F32, scale 1."""
     d = _route(desc)
-    n, e, k = max(d.N, 0), max(d.E, 0), max(d.K, 0)
+    n, e, k = d.N, d.E, d.K
     return _call("tp_moe_route_fwd", (
         ctypes.addressof(d), (logits, n * e * _elt(d.dtype), "logits"),
         (bias, e * 4, "bias", "float32"), (topk_expert, n * k * 4, "topk_expert", "int32"),
-        (topk_weight, n * k * 4, "topk_weight", "float32"), _stream(stream)))
+        (topk_weight, n * k * 4, "topk_weight", "float32")), stream)
 
 
 def tp_moe_route_bwd(desc, logits, topk_expert, d_weight, slot_row, R: int, dlogits,
                      stream=None) -> int:
     """dlogits from the weights' gradient: d_weight [N,K] with slot_row None, else [R] by rows."""
     d = _route(desc)
-    n, e, k = max(d.N, 0), max(d.E, 0), max(d.K, 0)
-    dw = n * k * 4 if slot_row is None else max(int(R), 0) * 4
+    n, e, k = d.N, d.E, d.K
+    dw = n * k * 4 if slot_row is None else int(R) * 4
     whole = n * e * _elt(d.dtype)
     return _call("tp_moe_route_bwd", (
         ctypes.addressof(d), (logits, whole, "logits"),
         (topk_expert, n * k * 4, "topk_expert", "int32"), (d_weight, dw, "d_weight", "float32"),
-        (slot_row, n * k * 4, "slot_row", "int32"), int(R), (dlogits, whole, "dlogits"),
-        _stream(stream)))
+        (slot_row, n * k * 4, "slot_row", "int32"), int(R), (dlogits, whole, "dlogits")), stream)
 
 
 def tp_moe_route_tables_workspace(N: int, K: int, n_local: int) -> int:
@@ -185,15 +182,15 @@ def tp_moe_route_tables(N: int, K: int, first_expert: int, n_local: int, R: int,
     """Dispatch tables of the experts [first_expert, first_expert + n_local), on the device."""
     N, K, first_expert, n_local, R, ws_bytes = (int(N), int(K), int(first_expert), int(n_local),
                                                 int(R), int(ws_bytes))
-    n, r = max(N, 0) * 4, max(R, 0) * 4
-    nk = n * max(K, 0)
+    n, r = N * 4, R * 4
+    nk = n * K
     return _call("tp_moe_route_tables", (
         N, K, first_expert, n_local, R, (topk_expert, nk, "topk_expert", "int32"),
         (topk_weight, nk, "topk_weight", "float32"),
-        (offsets, (max(n_local, 0) + 1) * 4, "offsets", "int32"), (row_token, r, "row_token", "int32"),
+        (offsets, (n_local + 1) * 4, "offsets", "int32"), (row_token, r, "row_token", "int32"),
         (row_weight, r, "row_weight", "float32"), (tok_ptr, n + 4, "tok_ptr", "int32"),
         (tok_rows, r, "tok_rows", "int32"), (slot_row, nk, "slot_row", "int32"),
-        (workspace, ws_bytes, "workspace"), ws_bytes, _stream(stream)))
+        (workspace, ws_bytes, "workspace"), ws_bytes), stream)
 
 
 class AdamwTensors:
@@ -256,5 +253,4 @@ def tp_adamw_step(desc, tensors, dev_step=None, dev_lr=None, grad_scale=None,
                          f"cuda:{_current_device()}")
     return _call("tp_adamw_step", (
         ctypes.addressof(d), t.n, t.address, (dev_step, 4, "dev_step", "int32"),
-        (dev_lr, 4, "dev_lr", "float32"), (grad_scale, 4, "grad_scale", "float32"),
-        _stream(stream)))
+        (dev_lr, 4, "dev_lr", "float32"), (grad_scale, 4, "grad_scale", "float32")), stream)

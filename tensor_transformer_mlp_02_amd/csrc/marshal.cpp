@@ -5,12 +5,15 @@
 // done in one step, on the same items as the binding's own loop: tuples
 // (tensor | int | None, bytes | None, name[, type name]).
 //   addresses(items, device) -> the list of addresses
-//   call(function, device, args) -> the function's int result; `args` is a
+//   call(function, args, stream) -> the function's int result; `args` is a
 //       tuple of items and of plain ints / None, `function` the address of an
-//       entry point whose arguments are all pointers or integers and whose
-//       result is an int
-// Both return None where an item does not pass: the binding's loop then finds
-// the item and words the error.
+//       entry point whose arguments are all pointers or integers, a stream
+//       the last, and whose result is an int; stream None: the current one
+//   setup(device, stream): torch's functions for the current device and for
+//       a device's current raw stream
+// The first two return None where an item does not pass, call also where no
+// item is a tensor (nothing shows that the GPU is in use): the binding's own
+// loop then does the work, or finds the item and words the error.
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
@@ -98,34 +101,70 @@ PyObject* addresses(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
 // slot, so one function type serves all entry points; slots past a
 // function's own arguments are not looked at.
 constexpr int SLOTS = 24;
+PyObject* current_device = nullptr;
+PyObject* current_stream = nullptr;
+
+PyObject* setup(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  if (nargs != 2 || !PyCallable_Check(args[0]) || !PyCallable_Check(args[1])) {
+    PyErr_SetString(PyExc_TypeError, "setup(device function, stream function)");
+    return nullptr;
+  }
+  for (int i = 0; i < 2; ++i) {
+    PyObject*& to = i == 0 ? current_device : current_stream;
+    Py_INCREF(args[i]);
+    Py_XDECREF(to);
+    to = args[i];
+  }
+  Py_RETURN_NONE;
+}
+
 typedef int (*Entry)(uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t,
                      uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t,
                      uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t,
                      uintptr_t, uintptr_t, uintptr_t);
 
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
-  if (nargs != 3 || !PyTuple_Check(args[2]) || PyTuple_GET_SIZE(args[2]) > SLOTS) {
-    PyErr_SetString(PyExc_TypeError, "call(function, device, tuple of at most 24)");
+  if (nargs != 3 || !PyTuple_Check(args[1]) || PyTuple_GET_SIZE(args[1]) >= SLOTS || !current_device) {
+    PyErr_SetString(PyExc_TypeError, "call(function, tuple of at most 23, stream), after setup()");
     return nullptr;
   }
   const uintptr_t fn = (uintptr_t)PyLong_AsUnsignedLongLong(args[0]);
   if (PyErr_Occurred()) return nullptr;
-  const long device = PyLong_AsLong(args[1]);
-  if (device == -1 && PyErr_Occurred()) return nullptr;
+  PyObject* list = args[1];
+  const Py_ssize_t n = PyTuple_GET_SIZE(list);
+  long device = -1;
+  PyObject* device_object = nullptr;
   uintptr_t v[SLOTS] = {0};
-  const Py_ssize_t n = PyTuple_GET_SIZE(args[2]);
+  Owned holder{nullptr};
   for (Py_ssize_t i = 0; i < n; ++i) {
-    PyObject* it = PyTuple_GET_ITEM(args[2], i);
+    PyObject* it = PyTuple_GET_ITEM(list, i);
     if (it == Py_None) continue;
     if (PyLong_Check(it)) {
       int over = 0;
       const long long x = PyLong_AsLongLongAndOverflow(it, &over);
       v[i] = over > 0 ? (uintptr_t)PyLong_AsUnsignedLongLong(it) : (uintptr_t)x;
       if (over < 0 || PyErr_Occurred()) return refused();
-    } else if (!address_of(it, device, v[i])) {
-      return refused();
+      continue;
     }
+    if (!PyTuple_Check(it) || PyTuple_GET_SIZE(it) < 3) return refused();
+    if (!device_object && THPVariable_Check(PyTuple_GET_ITEM(it, 0))) {
+      // a GPU tensor: torch is set up for the GPU
+      if (!THPVariable_Unpack(PyTuple_GET_ITEM(it, 0)).is_cuda()) return refused();
+      holder.p = device_object = PyObject_CallNoArgs(current_device);
+      if (!device_object) return refused();
+      device = PyLong_AsLong(device_object);
+    }
+    if (!address_of(it, device, v[i])) return refused();
   }
+  if (!device_object) return refused();
+  if (args[2] == Py_None) {
+    Owned s{PyObject_CallOneArg(current_stream, device_object)};
+    if (!s.p) return refused();
+    v[n] = (uintptr_t)PyLong_AsUnsignedLongLong(s.p);
+  } else {
+    v[n] = (uintptr_t)PyLong_AsUnsignedLongLong(args[2]);
+  }
+  if (PyErr_Occurred()) return refused();
   int rc;
   Py_BEGIN_ALLOW_THREADS  // a full queue makes a launch wait
   rc = reinterpret_cast<Entry>(fn)(
@@ -153,7 +192,8 @@ PyCFunction method() {
 
 PyMethodDef methods[] = {
     {"addresses", method<addresses>(), METH_FASTCALL, "addresses(items, device)"},
-    {"call", method<call>(), METH_FASTCALL, "call(function, device, args)"},
+    {"call", method<call>(), METH_FASTCALL, "call(function, args, stream)"},
+    {"setup", method<setup>(), METH_FASTCALL, "setup(device function, stream function)"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
