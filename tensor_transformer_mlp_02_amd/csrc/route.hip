@@ -57,6 +57,32 @@ __device__ __forceinline__ void load_row(const T* row, int E, int lane, bool liv
   }
 }
 
+template <typename T, int V>
+__device__ __forceinline__ void store_row(T* row, int E, int lane, const float (&g)[V]) {
+  const int e0 = lane * V;
+  if (V > 1 && E % V == 0) {
+    if (e0 >= E) return;
+    constexpr int BYTES = V * (int)sizeof(T) < 16 ? V * (int)sizeof(T) : 16;
+    constexpr int PER = BYTES / (int)sizeof(T);
+    struct alignas(BYTES) Part { T x[PER]; };
+#pragma unroll
+    for (int i = 0; i < V; i += PER) {
+      Part q;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        if constexpr (sizeof(T) == 2) q.x[j] = f32_to_bf16(g[i + j]); else q.x[j] = g[i + j];
+      }
+      *reinterpret_cast<Part*>(row + e0 + i) = q;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (e0 + i < E) {
+        if constexpr (sizeof(T) == 2) row[e0 + i] = f32_to_bf16(g[i]); else row[e0 + i] = g[i];
+      }
+  }
+}
+
 // Shared memory that one wavefront writes and reads by itself: its accesses
 // are in order, the compiler has to keep them so.
 __device__ __forceinline__ void wave_lds_sync() {
@@ -679,29 +705,101 @@ __global__ __launch_bounds__(NT) void bwd_kernel(BwdArgs A) {
     T* out = reinterpret_cast<T*>(A.dlogits) + t * A.E;
 #pragma unroll
     for (int i = 0; i < V; ++i) ds[i] = SIGMOID ? s[i] * (1.f - s[i]) * ds[i] : s[i] * (ds[i] - dot);
-    const int e0 = lane * V;
-    if (V > 1 && A.E % V == 0) {
-      if (e0 < A.E) {
-        constexpr int BYTES = V * (int)sizeof(T) < 16 ? V * (int)sizeof(T) : 16;
-        constexpr int PER = BYTES / (int)sizeof(T);
-        struct alignas(BYTES) Part { T x[PER]; };
-#pragma unroll
-        for (int i = 0; i < V; i += PER) {
-          Part q;
-#pragma unroll
-          for (int j = 0; j < PER; ++j) {
-            if constexpr (sizeof(T) == 2) q.x[j] = f32_to_bf16(ds[i + j]); else q.x[j] = ds[i + j];
-          }
-          *reinterpret_cast<Part*>(out + e0 + i) = q;
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (e0 + i < A.E) {
-          if constexpr (sizeof(T) == 2) out[e0 + i] = f32_to_bf16(ds[i]); else out[e0 + i] = ds[i];
-        }
+    store_row<T, V>(out, A.E, lane, ds);
+  }
+}
+
+// Many tokens: four to a wavefront, as fwd_rows_kernel: 16384 x 64 fp32 4.4 us
+// (6.3 with one), 8191 x 256 bf16 top 8 5.8 (7.7).  The slots' gradients
+// meet the experts through shared memory: every slot of an expert writes the
+// same sum over the expert's slots, taken in slot order.  K <= 16.
+template <int J>
+__device__ __forceinline__ float slot_sum(float all, int e, float d, int K) {
+  if constexpr (J == 16) {
+    return all;
+  } else {
+    if (J >= K) return all;
+    constexpr int CTRL = 0x150 + J;  // row_newbcast: lane J of each row
+    const int ej = __builtin_amdgcn_update_dpp(0, e, CTRL, 0xf, 0xf, true);
+    const float dj = dpp<CTRL>(d);
+    return slot_sum<J + 1>(all + (ej == e ? dj : 0.f), e, d, K);
+  }
+}
+
+template <typename T, int V, bool SIGMOID>
+__global__ __launch_bounds__(NT) void bwd_rows_kernel(BwdArgs A) {
+  __shared__ alignas(16) float lds[WAVES * 4 * 16 * V];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
+  float* mine = lds + (wave * 4 + q) * 16 * V;
+  const int64_t stride = (int64_t)gridDim.x * WAVES * 4;
+  for (int64_t t = ((int64_t)blockIdx.x * WAVES + wave) * 4 + q; t - q < A.N; t += stride) {
+    const bool live = t < A.N;
+    const T* row = reinterpret_cast<const T*>(A.logits) + t * A.E;
+    int e = -1;
+    int64_t at = -1;
+    if (live && r < A.K) {
+      e = A.expert[t * A.K + r];
+      at = A.slot_row ? (int64_t)A.slot_row[t * A.K + r] : t * A.K + r;
     }
+    float l[V], s[V];
+    load_row<T, V>(row, A.E, r, live, l);
+    if (e < 0 || e >= A.E) e = -1;
+    float up = 0.f, le = -__builtin_huge_valf();
+    if (e >= 0) {
+      if (!A.slot_row || (at >= 0 && at < A.R)) up = A.d_weight[at] * A.scale;
+      if constexpr (sizeof(T) == 2) le = bf16_to_f32(row[e]); else le = row[e];
+    }
+    if (!(le > LOWEST)) le = -__builtin_huge_valf();
+    le = fminf(le, LARGEST);
+#pragma unroll
+    for (int i = 0; i < V; i += V < 4 ? V : 4) {
+      if constexpr (V >= 4)
+        *reinterpret_cast<float4*>(mine + r * V + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+      else
+#pragma unroll
+        for (int j = 0; j < V; ++j) mine[r * V + j] = 0.f;
+    }
+    auto sum_ = [](float a, float b) { return a + b; };
+    float se;
+    if constexpr (SIGMOID) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[i] = l[i] > LOWEST ? 1.f / (1.f + expf(-l[i])) : 0.f;
+      se = le > LOWEST ? 1.f / (1.f + expf(-le)) : 0.f;
+    } else {
+      float top = l[0], sum = 0.f;
+#pragma unroll
+      for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
+      top = row_all(top, [](float a, float b) { return fmaxf(a, b); });
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        s[i] = l[i] > LOWEST ? expf(l[i] - top) : 0.f;
+        sum += s[i];
+      }
+      sum = row_all(sum, sum_);
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[i] *= inv;
+      se = le > LOWEST ? expf(le - top) * inv : 0.f;
+    }
+    float d = up;
+    if (A.renorm) {
+      const float S = row_all(se, sum_) + 1e-20f;
+      d = (up - row_all(up * se / S, sum_)) / S;
+    }
+    if (e < 0) d = 0.f;
+    const float all = slot_sum<0>(0.f, e, d, A.K);
+    wave_lds_sync();
+    if (e >= 0) mine[e] = all;
+    wave_lds_sync();
+    float dot = 0.f;
+    if constexpr (!SIGMOID) dot = row_all(d * se, sum_);
+    float ds[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) ds[i] = mine[r * V + i];
+    wave_lds_sync();
+#pragma unroll
+    for (int i = 0; i < V; ++i) ds[i] = SIGMOID ? s[i] * (1.f - s[i]) * ds[i] : s[i] * (ds[i] - dot);
+    if (live) store_row<T, V>(reinterpret_cast<T*>(A.dlogits) + t * A.E, A.E, r, ds);
   }
 }
 
@@ -996,6 +1094,8 @@ static void pick_rows(int dtype, int V, int score, F&& f) {
 }
 
 constexpr int64_t ROWS_FROM = 4096, ROWS_GRID = 1024;
+// experts of a lane with 16 lanes a token
+static int rows_experts(int E) { return E <= 16 ? 1 : E <= 32 ? 2 : E <= 64 ? 4 : E <= 128 ? 8 : 16; }
 
 static unsigned grid_tokens(int64_t N, int64_t most) {
   const int64_t b = (N + WAVES - 1) / WAVES;
@@ -1019,7 +1119,7 @@ hipError_t route_fwd_launch(const tp_route_desc& d, const void* logits, const fl
   // Four tokens to a wavefront once those wavefronts fill the chip: 16384
   // tokens top 2 of 64 4.8 us (7.4 with one), 8191 top 8 of 256 in groups 16.6
   // (18.0); 8 tokens take 5.0 us with one and 6.6 with four.
-  const int v16 = d.E <= 16 ? 1 : d.E <= 32 ? 2 : d.E <= 64 ? 4 : d.E <= 128 ? 8 : 16;
+  const int v16 = rows_experts(d.E);
   if (d.N >= ROWS_FROM && d.E <= 256 && d.K <= 15 && (d.groups == 1 || (log2_lanes(v16) >= 0 && log2_lanes(v16) <= 3))) {
     const int64_t groups = (d.N + 4 * WAVES - 1) / (4 * WAVES);
     const dim3 grid((unsigned)(groups > ROWS_GRID ? ROWS_GRID : groups));
@@ -1046,6 +1146,15 @@ hipError_t route_bwd_launch(const tp_route_desc& d, const void* logits, const in
   using namespace route;
   if (d.N == 0) return hipSuccess;
   BwdArgs a{logits, expert, d_weight, slot_row, dlogits, d.N, R, d.E, d.K, d.renorm, d.scale};
+  if (d.N >= ROWS_FROM && d.E <= 256 && d.K <= 16) {
+    const int64_t groups = (d.N + 4 * WAVES - 1) / (4 * WAVES);
+    const dim3 grid((unsigned)(groups > 2 * ROWS_GRID ? 2 * ROWS_GRID : groups));
+    pick_rows(d.dtype, rows_experts(d.E), d.score, [&](auto t, auto v, auto sig) {
+      hipLaunchKernelGGL((bwd_rows_kernel<decltype(t), decltype(v)::value, decltype(sig)::value>),
+                         grid, dim3(NT), 0, st, a);
+    });
+    return hipGetLastError();
+  }
   return pick(d.dtype, d.E, d.score, [&](auto t, auto v, auto sig) {
     hipLaunchKernelGGL((bwd_kernel<decltype(t), decltype(v)::value, decltype(sig)::value>),
                        dim3(grid_tokens(d.N, 8192)), dim3(NT), 0, st, a);

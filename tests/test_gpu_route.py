@@ -55,17 +55,22 @@ def check_forward(d, logits, bias):
     return e, w
 
 
-def check_backward(d, logits, expert, up, rows=None):
-    """up [N,K]: the weights' gradient; rows: the slots' rows, with the gradient given by rows."""
+def check_backward(d, logits, expert, up, rows=None, out=None):
+    """up [N,K]: the weights' gradient; rows: the slots' rows, with the gradient given by rows;
+    out: the result to check, where it is there (these tokens' part of a larger call's)."""
     N, E = d["N"], d["E"]
     dtype = logits.dtype
-    out = torch.full((N, E), float("nan"), dtype=dtype, device="cuda")
+    called = out is not None
+    if not called:
+        out = torch.full((N, E), float("nan"), dtype=dtype, device="cuda")
     if rows is None:
-        tp.tp_moe_route_bwd(d, logits, expert, up, None, 0, out)
+        if not called:
+            tp.tp_moe_route_bwd(d, logits, expert, up, None, 0, out)
         up_np = up.double().cpu().numpy()
     else:
         by_row, slot_row, R = rows
-        tp.tp_moe_route_bwd(d, logits, expert, by_row, slot_row, R, out)
+        if not called:
+            tp.tp_moe_route_bwd(d, logits, expert, by_row, slot_row, R, out)
         r = slot_row.cpu().numpy()
         v = np.append(by_row.double().cpu().numpy(), 0.0)
         up_np = v[np.where((r >= 0) & (r < R), r, len(v) - 1)]
@@ -411,7 +416,33 @@ def test_more_logits_than_32_bits_count(N, E):
     p = {**d, "N": len(pick)}
     we, ww = want_forward(p, part, None)
     assert np.array_equal(e[pick].cpu().numpy(), we)
-    small = torch.empty_like(part)
-    tp.tp_moe_route_bwd(p, part, e[pick].contiguous(), up[pick].contiguous(), None, 0, small)
-    assert torch.equal(small, dl[pick])
-    check_backward(p, part, e[pick].contiguous(), up[pick].contiguous())
+    check_backward(p, part, e[pick].contiguous(), up[pick].contiguous(), out=dl[pick].contiguous())
+
+
+@pytest.mark.parametrize("E,K", [(1, 1), (16, 4), (20, 3), (32, 2), (60, 4), (64, 2), (100, 16), (128, 8), (160, 6), (256, 8),
+                                 (256, 16), (256, 17), (300, 8)])
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_backward_of_many_tokens(E, K, sigmoid, dtype):
+    """A sample of a large call's tokens against the definition."""
+    N = 4101
+    l, _ = inputs(N, E, dtype, masked=True, seed=E)
+    g = torch.Generator(device="cuda").manual_seed(E)
+    e = torch.randint(-1, E + 1, (N, K), generator=g, device="cuda", dtype=torch.int32)   # some twice, some out of range
+    slot = torch.randint(-2, N * K + 5, (N, K), generator=g, device="cuda", dtype=torch.int32)
+    by_row = torch.randn(N * K, generator=g, device="cuda")
+    up = torch.randn(N, K, generator=g, device="cuda")
+    for renorm in (False, True):
+        d = desc(N, E, K, sigmoid=sigmoid, renorm=renorm, dtype=dtype, scale=1.5)
+        for rows in (False, True):
+            out = torch.full((N, E), float("nan"), dtype=dtype, device="cuda")
+            tp.tp_moe_route_bwd(d, l, e, by_row if rows else up, slot if rows else None, N * K if rows else 0, out)
+            pick = list(range(0, N, 100)) + [N - 1]
+            p = {**d, "N": len(pick)}
+            part, ep = l[pick].contiguous(), e[pick].contiguous()
+            got = out[pick].contiguous()
+            if rows:
+                check_backward(p, part, ep, None, rows=(by_row, slot[pick].contiguous(), N * K), out=got)
+            else:
+                check_backward(p, part, ep, up[pick].contiguous(), out=got)
+            assert bool(torch.isfinite(out).all())
