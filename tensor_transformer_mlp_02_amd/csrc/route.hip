@@ -324,15 +324,24 @@ __device__ __forceinline__ float fast_exp(float x) {
   return __builtin_amdgcn_exp2f(x * 1.4426950408889634f);
 }
 
+// How far apart two keys c = s + bias must be for their order to be sure,
+// before 2^-22 |c| for the sums' own roundings.
+//   sigmoid: the argument's rounding, the hardware's 2^x and reciprocal leave
+//     s off by s (1 - s) (1.5 |l| + 2) 2^-24 + 3 s 2^-24 < 2^-22
+//   softmax: the exponential off by (1.5 |x| + 2) 2^-24 with e^-|x| |x| < 0.4,
+//     the sum of E <= 1024 terms and the quotient: < 2^-19 of the largest s
+// and twice that separates two of them, twice again to be on the safe side.
+template <bool SIGMOID>
+__device__ __forceinline__ float key_slack(float largest) {
+  return SIGMOID ? 0x1p-20f : 0x1p-17f * largest;
+}
+
 // One wavefront a token.  Choices are to be those of 64-bit arithmetic, made
 // in 32 bits: without a bias the experts' order is the logits' own, exact.
-// With one, a key c = s + bias is off by at most 2^-19 max s (an exponential
-// of a rounded argument, a sum of E <= 1024 terms, a quotient) plus 2^-24
-// |c|; so the order of the first k + 1 keys is right if neighbours differ by
-// more than 2^-18 max s + 2^-22 |c|, and the groups kept are if the worth of
-// the last one and of the first left out differ by twice that.  A token
-// where they do not (one in a hundred or fewer at 256 experts) is done again
-// in 64 bits.
+// With one, the order of the first k + 1 keys is right if neighbours differ
+// by more than the slack, and the groups kept are if the worth of the last
+// one and of the first left out differ by twice that.  A token where they do
+// not (about one in a thousand at 256 experts) is done again in 64 bits.
 // Bound by instruction issue: the k maxima take about 25 vector
 // instructions each at V = 4, the scores 15 for each of a lane's experts.
 template <typename T, int V, bool SIGMOID>
@@ -378,7 +387,7 @@ __global__ __launch_bounds__(NT) void fwd_kernel(FwdArgs A) {
     }
     uint32_t key[V];
     bool close = false;  // too close for 32 bits
-    const float slack = 0x1p-18f * largest;
+    const float slack = key_slack<SIGMOID>(largest);
     if (A.groups > 1) {
       float c[V];
 #pragma unroll
@@ -532,7 +541,7 @@ __global__ __launch_bounds__(NT) void fwd_rows_kernel(FwdArgs A) {
     }
     uint32_t key[V];
     bool close = false;
-    const float slack = 0x1p-18f * largest;
+    const float slack = key_slack<SIGMOID>(largest);
     bool kept = true;
     if (A.groups > 1) {
       float b1 = NEG, b2 = NEG;
@@ -1093,7 +1102,12 @@ static void pick_rows(int dtype, int V, int score, F&& f) {
   dtype == TP_BF16 ? by_size(bf16_t{}) : by_size(0.f);
 }
 
-constexpr int64_t ROWS_FROM = 4096, ROWS_GRID = 1024;
+// Tokens from which four of them share a wavefront: then those wavefronts
+// fill the chip.  Forward, top 2 of 64: 2048 tokens 3.3 us so and 3.1 with a
+// wavefront each, 4096 3.3 and 3.6, 32768 6.4 and 12.5; top 8 of 256 in groups
+// (16 experts a lane): 4096 13.2 and 11.7, 8192 16.3 and 16.9, 32768 33 and 49.
+static int64_t rows_from(int E) { return E <= 128 ? 4096 : 7168; }
+constexpr int64_t ROWS_GRID = 1024;
 // experts of a lane with 16 lanes a token
 static int rows_experts(int E) { return E <= 16 ? 1 : E <= 32 ? 2 : E <= 64 ? 4 : E <= 128 ? 8 : 16; }
 
@@ -1116,11 +1130,8 @@ hipError_t route_fwd_launch(const tp_route_desc& d, const void* logits, const fl
       if (per == V << b) return b;
     return -1;
   };
-  // Four tokens to a wavefront once those wavefronts fill the chip: 16384
-  // tokens top 2 of 64 4.8 us (7.4 with one), 8191 top 8 of 256 in groups 16.6
-  // (18.0); 8 tokens take 5.0 us with one and 6.6 with four.
   const int v16 = rows_experts(d.E);
-  if (d.N >= ROWS_FROM && d.E <= 256 && d.K <= 15 && (d.groups == 1 || (log2_lanes(v16) >= 0 && log2_lanes(v16) <= 3))) {
+  if (d.N >= rows_from(d.E) && d.E <= 256 && d.K <= 15 && (d.groups == 1 || (log2_lanes(v16) >= 0 && log2_lanes(v16) <= 3))) {
     const int64_t groups = (d.N + 4 * WAVES - 1) / (4 * WAVES);
     const dim3 grid((unsigned)(groups > ROWS_GRID ? ROWS_GRID : groups));
     a.lanes_log2 = log2_lanes(v16);
@@ -1146,7 +1157,8 @@ hipError_t route_bwd_launch(const tp_route_desc& d, const void* logits, const in
   using namespace route;
   if (d.N == 0) return hipSuccess;
   BwdArgs a{logits, expert, d_weight, slot_row, dlogits, d.N, R, d.E, d.K, d.renorm, d.scale};
-  if (d.N >= ROWS_FROM && d.E <= 256 && d.K <= 16) {
+  // fp32, 256 experts: 8192 tokens 8.1 us so, 7.5 with a wavefront each
+  if (d.N >= rows_from(d.E) && d.E <= 256 && d.K <= 16 && (d.E <= 128 || d.dtype == TP_BF16)) {
     const int64_t groups = (d.N + 4 * WAVES - 1) / (4 * WAVES);
     const dim3 grid((unsigned)(groups > 2 * ROWS_GRID ? 2 * ROWS_GRID : groups));
     pick_rows(d.dtype, rows_experts(d.E), d.score, [&](auto t, auto v, auto sig) {

@@ -353,7 +353,7 @@ def check_many(d, l, b):
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_many_tokens(E, K, groups, kept, best, sigmoid, dtype):
     for k, (bias, masked, renorm) in enumerate([(True, True, True), (False, True, False), (True, False, False)]):
-        N = 4096 + 7 * k
+        N = (4096 if E <= 128 else 7168) + 7 * k
         d = desc(N, E, K, groups, kept, best, sigmoid, renorm, dtype, scale=1.5)
         l, b = inputs(N, E, dtype, bias, masked, seed=E + k)
         check_many(d, l, b)
@@ -363,7 +363,7 @@ def test_many_tokens(E, K, groups, kept, best, sigmoid, dtype):
                                              (256, 15, 1, 1), (256, 16, 1, 1)])
 @pytest.mark.parametrize("sigmoid", [False, True])
 def test_many_tokens_with_equal_and_close_values(E, K, groups, kept, sigmoid):
-    N = 4099
+    N = 4099 if E <= 128 else 7171
     g = torch.Generator(device="cuda").manual_seed(E)
     close = 1.0 + torch.randint(0, 8, (N, E), generator=g, device="cuda") * 2.0 ** -23
     ties = torch.randint(0, 3, (N, E), generator=g, device="cuda").float()
@@ -425,7 +425,7 @@ def test_more_logits_than_32_bits_count(N, E):
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_backward_of_many_tokens(E, K, sigmoid, dtype):
     """A sample of a large call's tokens against the definition."""
-    N = 4101
+    N = 4101 if E <= 128 else 7173
     l, _ = inputs(N, E, dtype, masked=True, seed=E)
     g = torch.Generator(device="cuda").manual_seed(E)
     e = torch.randint(-1, E + 1, (N, K), generator=g, device="cuda", dtype=torch.int32)   # some twice, some out of range
