@@ -138,6 +138,12 @@ __device__ __forceinline__ void row_sums(float (&v)[K], float* red, int& half) {
   }
 }
 
+// the compiler forgets what it knows of v: values unpacked from it do not
+// stay in registers past here
+__device__ __forceinline__ void hold(uint4& v) {
+  asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w));
+}
+
 // The weights are kept in registers over a workgroup's rows, and the next
 // row is requested before the present one is summed.  HBM-bound: 4096 x 8192
 // bf16 with both norms and a gate 53 us, 5.1 TB/s, the rate of a large copy;
@@ -191,7 +197,12 @@ __global__ __launch_bounds__(Rows<TPR>::THREADS) void fwd_kernel(NormFwdArgs A) 
       for (int p = 0; p < P; ++p)
         if (in[p]) gt[p] = load_raw(A.gate, g + tr + p * TPR);
     }
-    request(n + stride, xn, on);
+    // the next row is asked for at once; where four bf16 pieces fill the
+    // registers, when this row's are free, and its values are unpacked again
+    // after the sums (2048 x 16384: 46 us so, 50 otherwise, with biases and
+    // means 56 and 169)
+    constexpr bool AHEAD = V * P < 32;
+    if constexpr (AHEAD) request(n + stride, xn, on);
     float mo = 0.f, ro = 1.f;
     if (A.w_post) {
       if constexpr (LAYER) {
@@ -219,6 +230,13 @@ __global__ __launch_bounds__(Rows<TPR>::THREADS) void fwd_kernel(NormFwdArgs A) 
       if (A.stat_post && tr == 0 && live) {
         A.stat_post[n] = ro;
         if constexpr (LAYER) A.stat_post[A.N + n] = mo;
+      }
+    }
+    if constexpr (!AHEAD) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        hold(o[p]);
+        hold(x[p]);
       }
     }
     float y[P][V];
@@ -254,6 +272,7 @@ __global__ __launch_bounds__(Rows<TPR>::THREADS) void fwd_kernel(NormFwdArgs A) 
         sq[0] += y[p][i] * y[p][i];
       }
     }
+    if constexpr (!AHEAD) request(n + stride, x, o);
     if (A.w_pre) {
       float my = 0.f;
       if constexpr (LAYER) {
@@ -285,10 +304,12 @@ __global__ __launch_bounds__(Rows<TPR>::THREADS) void fwd_kernel(NormFwdArgs A) 
         if (in[p] && live) store_piece<T>(A.Hn, n * pieces + tr + p * TPR, y[p]);
       }
     }
+    if constexpr (AHEAD) {
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      x[p] = xn[p];
-      o[p] = on[p];
+      for (int p = 0; p < P; ++p) {
+        x[p] = xn[p];
+        o[p] = on[p];
+      }
     }
   }
 }
@@ -614,8 +635,6 @@ template <int TPR>
 struct BwdRows {
   static constexpr int THREADS = TPR > CU_THREADS ? TPR : CU_THREADS;
   static constexpr int AT_ONCE = THREADS / TPR;
-  // 16 wavefronts leave 128 registers a lane: no room for the next row
-  static constexpr bool AHEAD = TPR <= CU_THREADS;
 };
 
 template <typename T, bool LAYER, bool BIAS, bool MANY, int TPR, int P>
@@ -634,7 +653,11 @@ __global__ __launch_bounds__(BwdRows<TPR>::THREADS) void bwd_kernel(NormBwdArgs 
   bool in[P];
   uint4 w_post[P], w_pre[P], gate[P];
   uint4 dy[P], dh[P], yy[P], oo[P];
-  float a_wpre[P][V], a_1[P][V], a_bpre[BIAS ? P : 1][V], a_0[BIAS ? P : 1][V];
+  // 16 wavefronts leave 128 registers a lane: there the two sums that every
+  // call may ask for are kept in shared memory, each thread's own
+  constexpr bool KEPT = TPR > CU_THREADS && !MANY && !BIAS;
+  __shared__ float kept[KEPT ? 2 * P * V * THREADS : 1];
+  float a_wpre[KEPT ? 1 : P][V], a_1[KEPT ? 1 : P][V], a_bpre[BIAS ? P : 1][V], a_0[BIAS ? P : 1][V];
   // gate-weighted, of the gate rows done
   float s_1[MANY ? P : 1][V], s_0[MANY && BIAS ? P : 1][V];
 #pragma unroll
@@ -645,7 +668,11 @@ __global__ __launch_bounds__(BwdRows<TPR>::THREADS) void bwd_kernel(NormBwdArgs 
     gate[p] = dy[p] = dh[p] = yy[p] = oo[p] = zero;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      a_wpre[p][i] = a_1[p][i] = 0.f;
+      if constexpr (KEPT) {
+        kept[(p * V + i) * THREADS + tr] = kept[((P + p) * V + i) * THREADS + tr] = 0.f;
+      } else {
+        a_wpre[p][i] = a_1[p][i] = 0.f;
+      }
       if constexpr (BIAS) a_bpre[p][i] = a_0[p][i] = 0.f;
       if constexpr (MANY) s_1[p][i] = 0.f;
       if constexpr (MANY && BIAS) s_0[p][i] = 0.f;
@@ -715,7 +742,10 @@ __global__ __launch_bounds__(BwdRows<TPR>::THREADS) void bwd_kernel(NormBwdArgs 
     const uint32_t n = row_of(it);
     const bool live = n < N;
     if (MANY && it % per_gate == 0) load_gate(gate_of(it));
-    constexpr bool AHEAD = BwdRows<TPR>::AHEAD;
+    // the next row's loads on their way, where registers are left for it (eight
+    // sums of two bf16 pieces leave none: 8192 x 4096 with biases and a gate a
+    // token 272 us so, 178 without; 65536 x 512, of one piece, 156 and 180)
+    constexpr bool AHEAD = TPR <= CU_THREADS && !(MANY && BIAS && V * P == 16);
     uint4 dyn[P], dhn[P], yyn[P], oon[P];
     float stn[4];
     if constexpr (AHEAD) request(it + 1 < turns ? row_of(it + 1) : N, dyn, dhn, yyn, oon, stn);
@@ -743,7 +773,8 @@ __global__ __launch_bounds__(BwdRows<TPR>::THREADS) void bwd_kernel(NormBwdArgs 
         // outside the row the weights are zeros: no term counts
         const float yh = (y[i] - my) * ry, oh = (o[i] - mo) * ro, pw = g[i] * t[i];
         const float k = A.b * kw[i], f = x[i] + ry * pw;
-        a_wpre[p][i] += g[i] * yh;
+        if constexpr (KEPT) kept[(p * V + i) * THREADS + tr] += g[i] * yh;
+        else a_wpre[p][i] += g[i] * yh;
         if constexpr (BIAS) a_bpre[p][i] += g[i];
         v[0] += pw * yh;
         v[1] += k * oh * f;
@@ -768,6 +799,23 @@ __global__ __launch_bounds__(BwdRows<TPR>::THREADS) void bwd_kernel(NormBwdArgs 
         t2 = (v[5] - ry * (m2 * v[7] + m1 * v[6])) * inv_h;
       }
     }
+    // From here the values are unpacked again: kept unpacked over the sums they
+    // would take twice the registers.  Without it 8192 x 4096 with biases takes
+    // 119 us for 102, with a gate a token besides 379 for 178, and 2048 x 16384
+    // 173 for 123; where the registers do hold them it costs (8192 x 4096
+    // without biases 91 us for 84).
+    if constexpr (V == 8 && BIAS != (TPR > CU_THREADS)) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        hold(dy[p]);
+        hold(dh[p]);
+        hold(yy[p]);
+        hold(oo[p]);
+        hold(w_post[p]);
+        hold(w_pre[p]);
+        hold(gate[p]);
+      }
+    }
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       float g[V], y[V], o[V], D[V], t[V];
@@ -782,7 +830,8 @@ __global__ __launch_bounds__(BwdRows<TPR>::THREADS) void bwd_kernel(NormBwdArgs 
         D[i] += ry * (g[i] * t[i] - m2 - yh * m1);
         o[i] = (o[i] - mo) * ro;
         if (live) {
-          a_1[p][i] += D[i] * o[i];
+          if constexpr (KEPT) kept[((P + p) * V + i) * THREADS + tr] += D[i] * o[i];
+          else a_1[p][i] += D[i] * o[i];
           if constexpr (BIAS) a_0[p][i] += D[i];
         }
       }
@@ -862,43 +911,72 @@ __global__ __launch_bounds__(BwdRows<TPR>::THREADS) void bwd_kernel(NormBwdArgs 
       request(it + 1 < turns ? row_of(it + 1) : N, dy, dh, yy, oo, st);
     }
   }
-  // the row groups' sums meet in shared memory, in order
-  auto finish = [&](int k, float (&acc)[P][V]) {
-    float* out = A.ws + ((int64_t)k * W + w) * A.H;
-    __syncthreads();
-    if constexpr (R > 1) {
-      if (rg > 0)
+  // The row groups' sums meet in shared memory, two arrays at a time (64 KiB
+  // at most); each group then adds up its share of the columns, in order.
+  constexpr int PV = P * V, EACH = THREADS * PV;
+  constexpr int SHARE = PV >= R ? PV / R : 1;
+  auto out_of = [&](int k) { return A.ws + ((int64_t)k * W + w) * A.H; };
+  auto put = [&](int k, int at, float (&acc)[P][V]) {
+    if constexpr (R == 1) {
 #pragma unroll
-        for (int p = 0; p < P; ++p)
+      for (int p = 0; p < P; ++p)
+        if (in[p])
 #pragma unroll
-          for (int i = 0; i < V; ++i) lds[((rg - 1) * P * V + p * V + i) * TPR + tr] = acc[p][i];
-      __syncthreads();
+          for (int i = 0; i < V; i += 4)
+            Store4<float>::store(out_of(k), (tr + p * TPR) * V + i, acc[p] + i);
+    } else {
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int i = 0; i < V; ++i) lds[at * EACH + (rg * PV + p * V + i) * TPR + tr] = acc[p][i];
     }
-    if (rg == 0)
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        if (!in[p]) continue;
-        float t[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          t[i] = acc[p][i];
-#pragma unroll
-          for (int r = 1; r < R; ++r) t[i] += lds[((r - 1) * P * V + p * V + i) * TPR + tr];
-        }
-#pragma unroll
-        for (int i = 0; i < V; i += 4)
-          Store4<float>::store(out, (tr + p * TPR) * V + i, t + i);
-      }
   };
-  if (A.w_pre) finish(SUM_W_PRE, a_wpre);
-  if constexpr (BIAS)
-    if (A.w_pre) finish(SUM_B_PRE, a_bpre);
-  if constexpr (MANY) {
-    finish(SUM_1, s_1);
-    if constexpr (BIAS) finish(SUM_0, s_0);
-  } else if (A.O) {
-    finish(SUM_1, a_1);
-    if constexpr (BIAS) finish(SUM_0, a_0);
+  auto add = [&](int k, int at) {
+    const int j0 = rg * SHARE, c = tr + j0 / V * TPR;
+    if (j0 >= PV || c >= pieces) return;
+    float t[SHARE];
+#pragma unroll
+    for (int j = 0; j < SHARE; ++j) {
+      t[j] = lds[at * EACH + (j0 + j) * TPR + tr];
+#pragma unroll
+      for (int r = 1; r < R; ++r) t[j] += lds[at * EACH + (r * PV + j0 + j) * TPR + tr];
+    }
+    float* out = out_of(k) + c * V + j0 % V;
+    if constexpr (SHARE % 4 == 0) {
+#pragma unroll
+      for (int j = 0; j < SHARE; j += 4) Store4<float>::store(out, j, t + j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < SHARE; ++j) out[j] = t[j];
+    }
+  };
+  auto finish = [&](bool one, int k1, float (&a1)[P][V], bool two, int k2, float (&a2)[P][V]) {
+    if constexpr (R > 1) __syncthreads();
+    if (one) put(k1, 0, a1);
+    if (two) put(k2, 1, a2);
+    if constexpr (R > 1) {
+      __syncthreads();
+      if (one) add(k1, 0);
+      if (two) add(k2, 1);
+    }
+  };
+  const bool pre = A.w_pre != nullptr, block = A.O != nullptr;
+  if constexpr (KEPT) {
+    float t[P][V];
+    for (int k = 0; k < 2; ++k) {
+      if (!(k ? block : pre)) continue;
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int i = 0; i < V; ++i) t[p][i] = kept[((k * P + p) * V + i) * THREADS + tr];
+      put(k ? SUM_1 : SUM_W_PRE, 0, t);
+    }
+  } else if constexpr (MANY) {
+    finish(pre, SUM_W_PRE, a_wpre, block, SUM_1, s_1);
+    if constexpr (BIAS) finish(pre, SUM_B_PRE, a_bpre, block, SUM_0, s_0);
+  } else {
+    finish(pre, SUM_W_PRE, a_wpre, block, SUM_1, a_1);
+    if constexpr (BIAS) finish(pre, SUM_B_PRE, a_bpre, block, SUM_0, a_0);
   }
 }
 
@@ -991,10 +1069,12 @@ __global__ __launch_bounds__(NT) void zero_kernel(float4* p, int64_t n) {
 }
 
 // workers of one call, with `at_once` rows to a worker's turn: as many as
-// there are compute units where each then has two turns or more (999 x 1004
-// fp32: 14.2 us so, 14.5 with one turn or more; 200 x 8192 bf16: 15.5, 16.5)
+// there are compute units where each then has a turn and two rows or more
+// (bwd and reduction, 200 x 8192 bf16: 16.5 us so, 19.1 with one row or more,
+// 18.2 with four; 999 x 1004 fp32 14.0, 15.5 with two turns)
 static int workers_for(int64_t N, int64_t G, int at_once) {
-  int64_t w = (N + 2 * at_once - 1) / (2 * at_once);
+  const int64_t least = at_once > 2 ? at_once : 2;
+  int64_t w = (N + least - 1) / least;
   if (w > CUS) w = CUS;
   if (w < 1) w = 1;
   if (G > 0 && G <= w) w = w / G * G;
@@ -1015,9 +1095,9 @@ static hipError_t pick(int kind, int dtype, F&& f) {
 
 // f(TPR, P) of the threads a row and pieces a thread that hold `pieces`
 // pieces in registers; false: too wide for any.  WIDEST: threads of the
-// widest rows.  Forward, 2048 x 16384 bf16: 57 us with 512 threads, 82 with
-// 1024 (barriers of 16 wavefronts); backward 393 and 256 us (512 threads
-// spill), 2048 x 8192 fp32 with a gate a token 160 and 124.
+// widest rows.  Forward, 2048 x 16384 bf16: 46 us with 512 threads, 82 with
+// 1024 (barriers of 16 wavefronts); backward, whose 512 threads would spill,
+// 393 and 123 us.
 template <int WIDEST, typename F>
 static bool pick_width(int64_t pieces, F&& f) {
   using std::integral_constant;
@@ -1050,6 +1130,14 @@ hipError_t norm_fwd_launch(int kind, int dtype, const NormFwdArgs& a, hipStream_
   });
 }
 
+// 16 wavefronts a workgroup leave too few registers for bf16 rows with more
+// sums than two: those take the wide kernels (2048 x 16384: with biases 221 us
+// so, 502 with registers spilled; with a gate a token 326, 342; with both 319,
+// 762; fp32 rows do fit: 2048 x 8192 with both 213 us, 269 in the wide kernels)
+static bool two_sums_only(int dtype, int64_t H) {
+  return dtype == TP_BF16 && H > norm::CU_THREADS * 2 * norm::Piece<bf16_t>::V;
+}
+
 // workers of a call, and whether its rows fit the registers
 static int bwd_workers(int64_t N, int64_t G, int64_t pieces, bool* fits) {
   using namespace norm;
@@ -1063,7 +1151,9 @@ static int bwd_workers(int64_t N, int64_t G, int64_t pieces, bool* fits) {
 size_t norm_bwd_workspace(const tp_norm_desc& d) {
   bool fits;
   const size_t w = (size_t)bwd_workers(d.N, d.gate_rows, d.H / (d.dtype == TP_BF16 ? 8 : 4), &fits);
-  return (w * norm::SUMS * (size_t)d.H + (fits ? 0 : 2 * (size_t)d.N)) * sizeof(float);
+  // (the descriptor does not say whether there are biases: as for wide rows)
+  const bool wide = !fits || two_sums_only(d.dtype, d.H);
+  return (w * norm::SUMS * (size_t)d.H + (wide ? 2 * (size_t)d.N : 0)) * sizeof(float);
 }
 
 hipError_t norm_bwd_launch(int kind, int dtype, NormBwdArgs& a, hipStream_t st) {
@@ -1074,6 +1164,7 @@ hipError_t norm_bwd_launch(int kind, int dtype, NormBwdArgs& a, hipStream_t st) 
   // sums without a factor besides them: the biases' gradients, and the
   // gate's where a bias is in its factor
   const bool bias = a.db_pre || a.db_post || (a.b_post && a.dgate);
+  if ((bias || many) && two_sums_only(dtype, a.H)) fits = false;
   return pick(kind, dtype, [&](auto t, auto layer) {
     using T = decltype(t);
     constexpr bool L = decltype(layer)::value;
@@ -1084,15 +1175,17 @@ hipError_t norm_bwd_launch(int kind, int dtype, NormBwdArgs& a, hipStream_t st) 
         constexpr int TPR = decltype(tpr)::value, P = decltype(p)::value;
         constexpr int THREADS = BwdRows<TPR>::THREADS, R = BwdRows<TPR>::AT_ONCE;
         const size_t sums = 2 * (THREADS / 64) * (L ? 8 : 3) * sizeof(float);
-        const size_t meet = (size_t)(R - 1) * P * Piece<T>::V * TPR * sizeof(float);
+        const size_t meet = R == 1 ? 0 : 2 * sizeof(float) * THREADS * P * Piece<T>::V;
         const size_t lds = sums > meet ? sums : meet;
-        if (many && !bias)
-          hipLaunchKernelGGL((bwd_kernel<T, L, false, true, TPR, P>), dim3(W), dim3(THREADS), lds, st, a);
-        else if (many)
-          hipLaunchKernelGGL((bwd_kernel<T, L, true, true, TPR, P>), dim3(W), dim3(THREADS), lds, st, a);
-        else if (bias)
-          hipLaunchKernelGGL((bwd_kernel<T, L, true, false, TPR, P>), dim3(W), dim3(THREADS), lds, st, a);
-        else
+        if constexpr (sizeof(T) == 4 || TPR <= CU_THREADS) {  // see two_sums_only
+          if (many && !bias)
+            hipLaunchKernelGGL((bwd_kernel<T, L, false, true, TPR, P>), dim3(W), dim3(THREADS), lds, st, a);
+          else if (many)
+            hipLaunchKernelGGL((bwd_kernel<T, L, true, true, TPR, P>), dim3(W), dim3(THREADS), lds, st, a);
+          else if (bias)
+            hipLaunchKernelGGL((bwd_kernel<T, L, true, false, TPR, P>), dim3(W), dim3(THREADS), lds, st, a);
+        }
+        if (!many && !bias)
           hipLaunchKernelGGL((bwd_kernel<T, L, false, false, TPR, P>), dim3(W), dim3(THREADS), lds, st, a);
       });
       he = hipGetLastError();

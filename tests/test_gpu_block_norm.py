@@ -201,7 +201,17 @@ def test_scales_and_a_large_stream(H):
     c.check_backward(c.backward())
 
 
-@pytest.mark.parametrize("H", [256, 8192, 20000])
+@pytest.mark.parametrize("H,dtype", [(8200, torch.bfloat16), (16384, torch.bfloat16), (4100, torch.float32),
+                                     (8192, torch.float32)])
+@pytest.mark.parametrize("G,bias,layer", [(1, False, False), (1, True, True), (600, False, True), (600, True, False)])
+def test_several_turns_of_the_widest_rows(H, dtype, G, bias, layer):
+    # the widest rows that a workgroup holds, more of them than workgroups
+    c = Case(600, H, G=G, dtype=dtype, layer=layer, bias=bias, seed=H)
+    c.check_forward(c.forward())
+    c.check_backward(c.backward(db=bias))
+
+
+@pytest.mark.parametrize("H", [256, 8192, 16384, 20000])
 def test_stream_updated_in_place(H):
     c = Case(19, H, G=1)
     a, b = c.forward(), c.forward(in_place=True)
