@@ -5,7 +5,7 @@
 // Nothing is reused: the kernel is HBM-bound at 30 bytes an element with
 // fp32 states (fp32 gradient, bf16 copy) and 18 with 8-bit ones.
 //
-// The tensors travel by value in the kernel's arguments, up to CHUNK_TENSORS
+// The tensors travel by value in the kernel's arguments, up to TENSORS
 // of them in a launch, so that nothing has to be copied to the device and a
 // captured graph holds its own table.
 #include "block_launch.h"
@@ -25,6 +25,8 @@ constexpr int TENSORS = 44;        // of one launch: the arguments stay under 4 
 // (88M elements), 479 at 2048, 488 at 1024; 8-bit: 470 us at 1024 (138M), 473
 // at 2048, 489 at 4096 (more registers, fewer wavefronts).
 constexpr int SPAN32 = 4096, SPAN8 = 1024;
+// Workgroups of one launch: a grid holds fewer than 2^32 threads.
+constexpr int64_t GROUPS = ((int64_t)1 << 32) / NT - 1;
 constexpr int BLOCK = TP_ADAMW_BLOCK;
 constexpr float FMAX = 448.f;      // largest finite E4M3
 
@@ -42,6 +44,7 @@ struct Args {
   Tensor t[TENSORS];
   int first[TENSORS];  // workgroup of each one's first piece
   int n, place;  // tensors here; place of the first in the caller's list
+  int64_t done;  // pieces of the first that earlier launches did
   const int32_t* dev_step;
   const float* dev_lr;
   const float* grad_scale;
@@ -113,6 +116,11 @@ __device__ __forceinline__ int find_tensor(const Args& A, int b) {
   return __popcll(__ballot(before)) - 1;
 }
 
+// which piece of tensor k workgroup b has
+__device__ __forceinline__ int64_t piece_of(const Args& A, int k, int b) {
+  return b - A.first[k] + (k == 0 ? A.done : 0);
+}
+
 // four neighbours; fewer at a tensor's end
 template <typename GT> struct Grad4;
 template <> struct Grad4<float> {
@@ -153,7 +161,7 @@ __global__ __launch_bounds__(NT) void step32_kernel(Args A) {
   const Tensor& t = A.t[k];
   Scalars s;
   if (!scalars(A, k, s)) return;
-  const int64_t i0 = (int64_t)(blockIdx.x - A.first[k]) * SPAN32;
+  const int64_t i0 = piece_of(A, k, blockIdx.x) * SPAN32;
   float* mp = reinterpret_cast<float*>(t.m);
   float* vp = reinterpret_cast<float*>(t.v);
   auto update = [&](float& p, float g, float& m, float& v) {
@@ -255,7 +263,7 @@ __global__ __launch_bounds__(NT) void step8_kernel(Args A) {
   Scalars s;
   if (!scalars(A, k, s)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t i0 = (int64_t)(blockIdx.x - A.first[k]) * SPAN8 + wave * BLOCK;
+  const int64_t i0 = piece_of(A, k, blockIdx.x) * SPAN8 + wave * BLOCK;
   uint8_t* mc = reinterpret_cast<uint8_t*>(t.m);
   uint8_t* vc = reinterpret_cast<uint8_t*>(t.v);
   float4 p4[U];
@@ -387,20 +395,26 @@ hipError_t adamw_launch(const tp_adamw_desc& d, int n, const tp_adamw_tensor* t,
   a.inv_root_c2 = (float)(1.0 / sqrt(c2));
   const int64_t span = d.state_bits == 32 ? SPAN32 : SPAN8;
   int k = 0;
+  int64_t done = 0;  // pieces of tensor k
   while (k < n) {
     int64_t groups = 0;
     a.n = 0;
     a.place = k;
-    // a run of tensors; an empty one takes no workgroup (a place in the
-    // table keeps the numbering)
-    for (; k < n && a.n < TENSORS; ++k) {
+    a.done = done;
+    // a run of tensors, the last of which the next launch may go on with; an
+    // empty one takes no workgroup (a place in the table keeps the numbering)
+    while (k < n && a.n < TENSORS && groups < GROUPS) {
       const tp_adamw_tensor& x = t[k];
-      const int64_t pieces = (x.count + span - 1) / span;
-      if (groups + pieces > 0x7fffffff) break;
+      const int64_t left = (x.count + span - 1) / span - done;
+      const int64_t now = left < GROUPS - groups ? left : GROUPS - groups;
       a.first[a.n] = (int)groups;
       a.t[a.n++] = Tensor{x.param, (bf16_t*)x.param_bf16, x.grad, x.m, x.v, x.m_scale, x.v_scale,
                           x.count, x.weight_decay};
-      groups += pieces;
+      groups += now;
+      done += now;
+      if (now < left) break;
+      ++k;
+      done = 0;
     }
     if (groups == 0) continue;
     const bool bf = d.grad_dtype == TP_BF16;

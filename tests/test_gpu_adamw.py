@@ -310,3 +310,28 @@ def test_more_elements_than_32_bits_count():
     for i in at:
         assert abs(float(t["param"][i]) + 1e-2) < 1e-5
         assert int(t["m"][i]) == 0x7e and int(t["v"][i]) == 0x7e
+
+
+def test_more_elements_than_one_grid_has_threads_for():
+    # 8-bit states take 1024 elements a workgroup of 256 threads: from 2^34 elements on a launch
+    # would need 2^32 threads.  The first tensor ends behind that, the second begins there.
+    n = (1 << 34) + 70000
+    if torch.cuda.mem_get_info()[0] < n * 8.5:
+        pytest.skip("needs 146 GB of free device memory")
+    z = lambda k, d: torch.zeros(k, dtype=d, device="cuda")  # noqa: E731
+    ts = [dict(param=z(k, torch.float32), grad=z(k, torch.bfloat16), m=z(k, torch.uint8), v=z(k, torch.uint8),
+               m_scale=z(-(-k // 256), torch.float32), v_scale=z(-(-k // 256), torch.float32),
+               weight_decay=0.0) for k in (n, 5000)]
+    last = ((1 << 24) - 1) * 1024  # first element of the second launch
+    at = [0, (1 << 32) - 1, last - 1, last, last + 1023, (1 << 34) - 1, 1 << 34, n - 1]
+    ts[0]["grad"][torch.tensor(at, device="cuda")] = 1.0
+    ts[1]["grad"][4999] = 1.0
+    tp.tp_adamw_step(desc(8, torch.bfloat16, step=1, eps=1e-4), ts)
+    for t, places in zip(ts, (at, [4999])):
+        # (last + 1023 is 2^34 - 1)
+        assert sum(int((part != 0).sum()) for part in t["param"].split(1 << 30)) == len(set(places))
+        for i in places:
+            assert abs(float(t["param"][i]) + 1e-2) < 1e-5
+            assert int(t["m"][i]) == 0x7e and int(t["v"][i]) == 0x7e
+    del ts, t
+    torch.cuda.empty_cache()
