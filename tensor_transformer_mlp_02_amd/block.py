@@ -106,11 +106,15 @@ def _route(desc) -> tp_route_desc:
                score=TP_SCORE_SOFTMAX, renorm=0, dtype=0, scale=1.0)
 
 
+def _type(d) -> str:
+    return "bfloat16" if d.dtype == TP_BF16 else "float32"
+
+
 def _norm_sizes(d: tp_norm_desc):
     # (a negative size asks for nothing here: the library refuses it)
     n, h = d.N, d.H
     vec = h * _elt(d.dtype)
-    return n * vec, vec, d.gate_rows * vec, h * 4, d.gate_rows * h * 4, n * (8 if d.kind else 4)
+    return _type(d), n * vec, vec, d.gate_rows * vec, h * 4, d.gate_rows * h * 4, n * (8 if d.kind else 4)
 
 
 def tp_block_norm_fwd(desc, X, O, w_post, b_post, gate, w_pre, b_pre, Y, Hn, stat_post=None,
@@ -118,11 +122,11 @@ def tp_block_norm_fwd(desc, X, O, w_post, b_post, gate, w_pre, b_pre, Y, Hn, sta
     """Y = res_scale X + branch_scale gate norm(O), Hn = norm(Y).  ``desc``: N, H and, with their
     defaults, gate_rows 0, kind TP_NORM_RMS, dtype TP_BF16, eps 1e-5, res_scale 1, branch_scale 1."""
     d = _norm(desc)
-    rows, vec, gate_n, _, _, stat = _norm_sizes(d)
+    t, rows, vec, gate_n, _, _, stat = _norm_sizes(d)
     return _call("tp_block_norm_fwd", (
-        ctypes.addressof(d), (X, rows, "X"), (O, rows, "O"), (w_post, vec, "w_post"),
-        (b_post, vec, "b_post"), (gate, gate_n, "gate"), (w_pre, vec, "w_pre"),
-        (b_pre, vec, "b_pre"), (Y, rows, "Y"), (Hn, rows, "Hn"),
+        ctypes.addressof(d), (X, rows, "X", t), (O, rows, "O", t), (w_post, vec, "w_post", t),
+        (b_post, vec, "b_post", t), (gate, gate_n, "gate", t), (w_pre, vec, "w_pre", t),
+        (b_pre, vec, "b_pre", t), (Y, rows, "Y", t), (Hn, rows, "Hn", t),
         (stat_post, stat, "stat_post", "float32"), (stat_pre, stat, "stat_pre", "float32")), stream)
 
 
@@ -136,12 +140,12 @@ def tp_block_norm_bwd(desc, dY, dHn, Y, O, w_post, b_post, gate, w_pre, stat_pos
     """Gradients of tp_block_norm_fwd from its Y (X where O is None), O and statistics;
     accumulate=True adds into the fp32 gradients."""
     d = _norm(desc)
-    rows, vec, gate_n, out, gate_out, stat = _norm_sizes(d)
+    t, rows, vec, gate_n, out, gate_out, stat = _norm_sizes(d)
     return _call("tp_block_norm_bwd", (
-        ctypes.addressof(d), (dY, rows, "dY"), (dHn, rows, "dHn"), (Y, rows, "Y"), (O, rows, "O"),
-        (w_post, vec, "w_post"), (b_post, vec, "b_post"), (gate, gate_n, "gate"),
-        (w_pre, vec, "w_pre"), (stat_post, stat, "stat_post", "float32"),
-        (stat_pre, stat, "stat_pre", "float32"), (dX, rows, "dX"), (dO, rows, "dO"),
+        ctypes.addressof(d), (dY, rows, "dY", t), (dHn, rows, "dHn", t), (Y, rows, "Y", t), (O, rows, "O", t),
+        (w_post, vec, "w_post", t), (b_post, vec, "b_post", t), (gate, gate_n, "gate", t),
+        (w_pre, vec, "w_pre", t), (stat_post, stat, "stat_post", "float32"),
+        (stat_pre, stat, "stat_pre", "float32"), (dX, rows, "dX", t), (dO, rows, "dO", t),
         (dw_post, out, "dw_post", "float32"), (db_post, out, "db_post", "float32"),
         (dgate, gate_out, "dgate", "float32"), (dw_pre, out, "dw_pre", "float32"),
         (db_pre, out, "db_pre", "float32"), (workspace, int(ws_bytes), "workspace"),
@@ -152,9 +156,9 @@ def tp_moe_route_fwd(desc, logits, bias, topk_expert, topk_weight, stream=None) 
     """The K experts of each token and their weights.  ``desc``: N, E, K and, with their defaults,
     groups 1, groups_kept 1, group_best 1, score TP_SCORE_SOFTMAX, renorm 0, dtype TP_F32, scale 1."""
     d = _route(desc)
-    n, e, k = d.N, d.E, d.K
+    n, e, k, t = d.N, d.E, d.K, _type(d)
     return _call("tp_moe_route_fwd", (
-        ctypes.addressof(d), (logits, n * e * _elt(d.dtype), "logits"),
+        ctypes.addressof(d), (logits, n * e * _elt(d.dtype), "logits", t),
         (bias, e * 4, "bias", "float32"), (topk_expert, n * k * 4, "topk_expert", "int32"),
         (topk_weight, n * k * 4, "topk_weight", "float32")), stream)
 
@@ -163,13 +167,13 @@ def tp_moe_route_bwd(desc, logits, topk_expert, d_weight, slot_row, R: int, dlog
                      stream=None) -> int:
     """dlogits from the weights' gradient: d_weight [N,K] with slot_row None, else [R] by rows."""
     d = _route(desc)
-    n, e, k = d.N, d.E, d.K
+    n, e, k, t = d.N, d.E, d.K, _type(d)
     dw = n * k * 4 if slot_row is None else int(R) * 4
     whole = n * e * _elt(d.dtype)
     return _call("tp_moe_route_bwd", (
-        ctypes.addressof(d), (logits, whole, "logits"),
+        ctypes.addressof(d), (logits, whole, "logits", t),
         (topk_expert, n * k * 4, "topk_expert", "int32"), (d_weight, dw, "d_weight", "float32"),
-        (slot_row, n * k * 4, "slot_row", "int32"), int(R), (dlogits, whole, "dlogits")), stream)
+        (slot_row, n * k * 4, "slot_row", "int32"), int(R), (dlogits, whole, "dlogits", t)), stream)
 
 
 def tp_moe_route_tables_workspace(N: int, K: int, n_local: int) -> int:

@@ -310,3 +310,16 @@ def test_binding_refuses_host_tensors_and_wrong_types():
     table = tp.tp_adamw_tensors(ad(), [tensor()])
     with pytest.raises(ValueError):
         tp.tp_adamw_step(ad(state_bits=8), table)
+
+
+def test_tensors_of_another_type_are_refused():
+    torch = pytest.importorskip("torch")
+    wide, slim = torch.zeros(12, 64), torch.zeros(12, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="X must be a torch.bfloat16"):
+        tp.tp_block_norm_fwd(nd(), **{**FWD, "X": wide})
+    with pytest.raises(ValueError, match="dHn must be a torch.float32"):
+        tp.tp_block_norm_bwd(nd(dtype=tp.TP_F32), ws_bytes=1 << 20, **{**BWD, "dHn": slim})
+    with pytest.raises(ValueError, match="logits must be a torch.float32"):
+        tp.tp_moe_route_fwd(rd(dtype=tp.TP_F32), slim, None, addr(3), addr(4))
+    with pytest.raises(ValueError, match="dlogits must be a torch.bfloat16"):
+        tp.tp_moe_route_bwd(rd(dtype=tp.TP_BF16), addr(1), addr(2), addr(3), None, 0, wide)

@@ -178,6 +178,15 @@ def test_gate_rows(G, H):
     c.check_backward(c.backward())
 
 
+@pytest.mark.parametrize("G", [7, 20, 33])
+@pytest.mark.parametrize("H,dtype", [(16384, torch.bfloat16), (20000, torch.bfloat16), (8192, torch.float32)])
+def test_gate_rows_of_wide_rows(G, H, dtype):
+    # 20 tokens are 10 workers' work: gate rows for fewer, for more, for more than the tokens
+    c = Case(20, H, G=G, dtype=dtype, layer=True, bias=True, seed=G)
+    c.check_forward(c.forward())
+    c.check_backward(c.backward())
+
+
 PARTS = [dict(block=False), dict(post=False), dict(pre=False), dict(post=False, pre=False), dict()]
 
 
