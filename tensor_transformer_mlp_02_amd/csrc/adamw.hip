@@ -210,23 +210,43 @@ __global__ __launch_bounds__(NT) void step32_kernel(Args A) {
   }
 }
 
+// the largest over the wavefront, whole: within 16 lanes by moves between
+// them, then lane by lane
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_with(uint32_t x) {
+  return max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xf, 0xf, true));
+}
 __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) x = max(x, (uint32_t)__shfl_xor((int)x, d, 64));
-  return x;
+  x = max_with<0xB1>(x);   // lane ^ 1
+  x = max_with<0x4E>(x);   // lane ^ 2
+  x = max_with<0x141>(x);  // within 8: lane 7 - i
+  x = max_with<0x140>(x);  // within 16: lane 15 - i
+  auto row = [&](int i) { return (uint32_t)__builtin_amdgcn_readlane((int)x, 16 * i); };
+  return max(max(row(0), row(1)), max(row(2), row(3)));
 }
 
-// scale and its inverse of a block whose largest magnitude has these bits
-// (bits of non-negative floats order like the floats, NaN above all).  An
-// infinity makes the scale NaN, like a NaN: the block's state says so.
-__device__ __forceinline__ void block_scale(uint32_t bits, float& scale, float& inv) {
-  const float top = __uint_as_float(bits);
-  const bool none = top <= 0x1p-100f;
-  scale = none ? 0.f : bits >= 0x7f800000u ? __builtin_nanf("") : top / FMAX;
-  inv = top > 0x1p-100f ? FMAX / top : 0.f;
+// Scales and their inverses of a block whose largest magnitudes have these
+// bits (bits of non-negative floats order like the floats, NaN above all):
+// top / 448 and 448 / top, 0 where top is at most 2^-100.  An infinity makes
+// the scale NaN, like a NaN: the block's state says so.  One division serves
+// all four quotients, a lane for each.
+struct Scales {
+  float m, m_inv, v, v_inv;
+};
+__device__ __forceinline__ Scales block_scales(uint32_t m, uint32_t v, int lane) {
+  const float top = __uint_as_float(lane & 2 ? v : m);
+  const float q = (lane & 1 ? FMAX : top) / (lane & 1 ? top : FMAX);
+  auto at = [&](int i) { return __builtin_amdgcn_readlane(__float_as_int(q), i); };
+  constexpr uint32_t TINY = (127u - 100u) << 23, INFINITE = 0x7f800000u;
+  const int nan = 0x7fc00000;
+  auto usable = [&](uint32_t bits) { return bits > TINY && bits < INFINITE; };
+  return {__int_as_float(usable(m) ? at(0) : m < INFINITE ? 0 : nan),
+          __int_as_float(usable(m) ? at(1) : 0),
+          __int_as_float(usable(v) ? at(2) : v < INFINITE ? 0 : nan),
+          __int_as_float(usable(v) ? at(3) : 0)};
 }
 
-// t rounded to an E4M3 value, down or up by chance u in [0, 1).  The step
+// t rounded to an E4M3 value, down or up by a chance u = h / 2^16.  The step
 // between neighbouring values at |t| in [2^k, 2^(k+1)) is 2^(k-3), and 2^-9
 // below 2^-6.
 //   a plain value: floor(t + u) in steps, t on average
@@ -235,22 +255,23 @@ __device__ __forceinline__ void block_scale(uint32_t bits, float& scale, float& 
 //     on average would add the rounding's variance to v at every step); a
 //     positive one never becomes 0
 // The variance that this adds stays small: a state that moves by d steps of
-// its code is moved up or down with a chance of about d.
+// its code is moved up or down with a chance of about d.  u and its product
+// with 2 k + 1 are exact, so the multiply-adds round as the sums would.  (A
+// NaN becomes some value: its block's scale is NaN.)
 template <bool ROOT>
-__device__ __forceinline__ float round_e4m3(float t, float u, bool positive) {
-  const uint32_t e = max((__float_as_uint(t) >> 23) & 0xffu, 121u) - 3u;  // biased exponent of it
-  t = t * __uint_as_float((254u - e) << 23);
-  float k;
+__device__ __forceinline__ float round_e4m3(float t, float h, bool positive) {
+  const uint32_t power = max(__float_as_uint(t) & 0x7f800000u, (127u - 6u) << 23);  // 2^k
+  t = t * __uint_as_float(((254u + 3u) << 23) - power);
+  const float step = __uint_as_float(power - (3u << 23));
   if constexpr (ROOT) {
-    k = floorf(t);
+    float k = floorf(t);
     const float odd = 2.f * k + 1.f;
-    k += (t - k) * (t + k) + u * odd >= odd ? 1.f : 0.f;
-    if (positive) k = fmaxf(k, 1.f);
+    k += fmaf(h, odd * 0x1p-16f, (t - k) * (t + k)) >= odd ? 1.f : 0.f;
+    k = fmaxf(k, positive ? 1.f : 0.f);
+    return fminf(k * step, FMAX);
   } else {
-    k = floorf(t + u);
+    return __builtin_amdgcn_fmed3f(floorf(fmaf(h, 0x1p-16f, t)) * step, -FMAX, FMAX);
   }
-  k = k * __uint_as_float(e << 23);
-  return k > FMAX ? FMAX : k < -FMAX ? -FMAX : k;  // NaN stays NaN
 }
 
 // 8-bit states: a wavefront takes a block of 256, four neighbours a lane,
@@ -329,19 +350,17 @@ __global__ __launch_bounds__(NT) void step8_kernel(Args A) {
         vtop = max(vtop, __float_as_uint(r[j]) & 0x7fffffffu);
       }
     }
-    float msc, minv, vsc, vinv;
-    block_scale(wave_max(mtop), msc, minv);
-    block_scale(wave_max(vtop), vsc, vinv);
+    const Scales sc = block_scales(wave_max(mtop), wave_max(vtop), lane);
     if (lane == 0) {
-      t.ms[b0 / BLOCK] = msc;
-      t.vs[b0 / BLOCK] = vsc;
+      t.ms[b0 / BLOCK] = sc.m;
+      t.vs[b0 / BLOCK] = sc.v;
     }
     float km[4], kr[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t h = mix(((uint32_t)(i + j) ^ s.key) + (uint32_t)(i >> 32));
-      km[j] = round_e4m3<false>(m[j] * minv, (float)(h & 0xffffu) * 0x1p-16f, false);
-      kr[j] = round_e4m3<true>(r[j] * vinv, (float)(h >> 16) * 0x1p-16f, r[j] > 0.f);
+      km[j] = round_e4m3<false>(m[j] * sc.m_inv, (float)(h & 0xffffu), false);
+      kr[j] = round_e4m3<true>(r[j] * sc.v_inv, (float)(h >> 16), r[j] > 0.f);
     }
     // exact: the values are E4M3 already
     int wm = __builtin_amdgcn_cvt_pk_fp8_f32(km[0], km[1], 0, false);
