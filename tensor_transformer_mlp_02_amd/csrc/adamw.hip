@@ -21,9 +21,9 @@ namespace adamw {
 
 constexpr int NT = 256;
 constexpr int TENSORS = 44;        // of one launch: the arguments stay under 4 KiB
-// Elements of one workgroup's piece of a tensor.  fp32 states: 465 us at 4096
-// (88M elements), 479 at 2048, 488 at 1024; 8-bit: 470 us at 1024 (138M), 473
-// at 2048, 489 at 4096 (more registers, fewer wavefronts).
+// Elements of one workgroup's piece of a tensor.  fp32 states, 88M elements:
+// 471 us at 4096, 472 at 2048, 489 at 8192; 8-bit, 138M: 453 us at 1024, 449 at
+// 2048, 459 at 4096 (fewer wavefronts), and small tensors spread further.
 constexpr int SPAN32 = 4096, SPAN8 = 1024;
 // Workgroups of one launch: a grid holds fewer than 2^32 threads.
 constexpr int64_t GROUPS = ((int64_t)1 << 32) / NT - 1;
