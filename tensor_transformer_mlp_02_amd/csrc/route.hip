@@ -318,6 +318,13 @@ __device__ __forceinline__ int choose_wide(const FwdArgs& A, const float (&l)[V]
   return my_e;
 }
 
+// The same as a call: its registers are not the caller's
+template <int V, bool SIGMOID>
+__device__ __attribute__((noinline)) int choose_wide_apart(const FwdArgs& A, const float (&l)[V], float top,
+                                                           int lane, double* cs) {
+  return choose_wide<V, SIGMOID>(A, l, top, lane, cs);
+}
+
 // e^x by the hardware's 2^x: off by |x| 2^-23 relative at most (the rounded
 // argument), a unit in the last place more
 __device__ __forceinline__ float fast_exp(float x) {
@@ -335,13 +342,44 @@ template <bool SIGMOID>
 __device__ __forceinline__ float key_slack(float largest) {
   return SIGMOID ? 0x1p-20f : 0x1p-17f * largest;
 }
+// whether the order of two keys, `below` at most `key`, is not sure
+__device__ __forceinline__ bool too_close(uint32_t key, uint32_t below, float slack) {
+  const float m = from_key(key), n = from_key(below);
+  return below != 0 && !(m - n > slack + 0x1p-22f * fabsf(m));
+}
+
+// The first K + 1 experts of a token in the order of 64-bit sigmoid scores:
+// lane j of its lanes (from lane `base` on) holds the j-th by 32-bit keys, -1
+// where there is none, the order of the keys being sure but among neighbours.
+template <typename T>
+__device__ __forceinline__ int settle(const FwdArgs& A, const T* row, int e, int base, int lane) {
+  double c = -__builtin_huge_val();
+  if (e >= 0) {
+    float x;
+    if constexpr (sizeof(T) == 2) x = bf16_to_f32(row[e]); else x = row[e];
+    c = 1.0 / (1.0 + exp(-(double)fminf(x, LARGEST))) + (double)A.bias[e];
+  }
+  int rank = 0;
+  for (int j = 0; j <= A.K; ++j) {
+    const double o = __shfl(c, base + j, 64);
+    const int f = __shfl(e, base + j, 64);
+    rank += o > c || (o == c && f < e);
+  }
+  // the other lanes keep their places
+  const int to = e >= 0 ? base + rank : lane;
+  return __builtin_amdgcn_ds_permute(to * 4, e);
+}
 
 // One wavefront a token.  Choices are to be those of 64-bit arithmetic, made
 // in 32 bits: without a bias the experts' order is the logits' own, exact.
 // With one, the order of the first k + 1 keys is right if neighbours differ
 // by more than the slack, and the groups kept are if the worth of the last
-// one and of the first left out differ by twice that.  A token where they do
-// not (about one in a thousand at 256 experts) is done again in 64 bits.
+// one and of the first left out differ by twice that.  Where neighbours do not
+// (one token in a thousand at 256 experts), settle orders the k + 1 by their
+// sigmoids in 64 bits; where that is not enough (groups, the next after those,
+// softmax scores, whose sum takes every expert) the token is done again in 64
+// bits.  1024 tokens, top 8 of 256 in groups with a bias, some of them close:
+// 6.3 us so, 8.5 with every one done again.
 // Few tokens wait for one another's steps (8 tokens of 256 experts, top 8:
 // 5.2 us with the launch); many are bound by instruction issue: the k maxima
 // take about 25 vector instructions each at V = 4, the scores 15 for each of
@@ -439,9 +477,20 @@ __global__ __launch_bounds__(NT) void fwd_kernel(FwdArgs A) {
     if (A.bias) {
       // lane j's key against lane j + 1's
       const uint32_t below = (uint32_t)__shfl_down((int)my_key, 1, 64);
-      const float m = from_key(my_key), n = from_key(below);
-      const bool tight = lane < A.K && below != 0 && !(m - n > slack + 0x1p-22f * fabsf(m));
-      close = close || __ballot(tight) != 0;
+      const unsigned long long tight = __ballot(lane < A.K && too_close(my_key, below, slack));
+      if constexpr (SIGMOID) {
+        if (tight != 0 && !close) {
+          if ((tight >> (A.K - 1)) & 1) {  // is the first left out sure to be ahead of the next?
+            uint32_t head = key[0];
+#pragma unroll
+            for (int i = 1; i < V; ++i) head = max(head, key[i]);
+            close = too_close(key_of_lane(my_key, A.K), wave_max(head), slack);
+          }
+          if (!close) my_e = settle<T>(A, logits + t * A.E, my_e, 0, lane);
+        }
+      } else {
+        close = close || tight != 0;
+      }
     }
     if (lane >= A.K) my_e = -1;
     float my_s = my_e >= 0 ? scores[my_e] : 0.f;
@@ -467,11 +516,14 @@ __global__ __launch_bounds__(NT) void fwd_kernel(FwdArgs A) {
   }
 }
 
-// Many tokens: four to a wavefront, 16 lanes each, so that the moves within
-// 16 lanes serve four maxima at once.  V experts a lane, E <= 16 V, K <= 15,
-// groups of whole lanes only.  16384 tokens, top 2 of 64: 4.7 us; 8191, top 8
-// of 256 in groups: 17.1 us, 1449 vector instructions a wavefront (5.5 us of
-// issue at two wavefronts a SIMD, the rest dependent steps of the rounds).
+// Many tokens: several to a wavefront, L = 16 or 32 lanes each, so that the
+// moves within 16 lanes serve four maxima at once.  V experts a lane, E <= L V,
+// K <= 15, groups of whole lanes only.  32 lanes serve more than 256 experts
+// (at 256, 65536 tokens take 51 us with 16 lanes, 59 with 32).  16384 tokens,
+// top 2 of 64: 4.5 us; 8191, top 8 of 256 in groups: 14.3 us (two wavefronts a
+// SIMD, waiting for the dependent steps of the rounds).  The choice in 64 bits
+// is a call: inlined, its registers cost the rest (65536 tokens, top 8 of 256:
+// 49 us so, 59).
 template <typename X, typename F>
 __device__ __forceinline__ X row_all(X x, F&& f) {
   x = f(x, other<0>(x));
@@ -479,34 +531,75 @@ __device__ __forceinline__ X row_all(X x, F&& f) {
   x = f(x, other<2>(x));
   return f(x, other<3>(x));
 }
-// rank of this lane's group among the row's: groups of 2^LOG lanes
-template <int LOG, int N = 1>
-__device__ __forceinline__ int group_rank(float worth, int lane) {
+// this lane's value and the one 16 lanes on or back, the lower lane's first
+__device__ __forceinline__ void pair16(uint32_t x, uint32_t& lower, uint32_t& upper) {
+  const auto v = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  lower = v[0];
+  upper = v[1];
+}
+__device__ __forceinline__ void pair16(float x, float& lower, float& upper) {
+  uint32_t a, b;
+  pair16(__float_as_uint(x), a, b);
+  lower = __uint_as_float(a);
+  upper = __uint_as_float(b);
+}
+// over the lanes of a token
+template <int L, typename F>
+__device__ __forceinline__ float token_all(float x, F&& f) {
+  x = row_all(x, f);
+  if constexpr (L == 32) {
+    float a, b;
+    pair16(x, a, b);
+    x = f(a, b);
+  }
+  return x;
+}
+// rank of this lane's group among its token's: groups of 2^LOG lanes, compared
+// with those N groups on in 16 lanes, from N = 1 for its own, 0 for the others
+template <int LOG, int N>
+__device__ __forceinline__ int row_rank(float worth, int lane, float theirs, int from) {
   if constexpr ((N << LOG) >= 16) {
     return 0;
   } else {
-    constexpr int CTRL = 0x120 + (N << LOG);  // row_ror
-    const float o = dpp<CTRL>(worth);
-    const int from = __builtin_amdgcn_update_dpp(0, lane, CTRL, 0xf, 0xf, true);
-    return (o > worth || (o == worth && from < lane)) + group_rank<LOG, N + 1>(worth, lane);
+    float o = theirs;
+    int f = from;
+    if constexpr (N > 0) {
+      constexpr int CTRL = 0x120 + (N << LOG);  // row_ror
+      o = dpp<CTRL>(theirs);
+      f = __builtin_amdgcn_update_dpp(0, from, CTRL, 0xf, 0xf, true);
+    }
+    return (o > worth || (o == worth && f < lane)) + row_rank<LOG, N + 1>(worth, lane, theirs, from);
   }
 }
+template <int LOG, int L>
+__device__ __forceinline__ int group_rank(float worth, int lane) {
+  int rank = row_rank<LOG, 1>(worth, lane, worth, lane);
+  if constexpr (L == 32) {
+    float a, b;
+    pair16(worth, a, b);
+    rank += row_rank<LOG, 0>(worth, lane, lane & 16 ? a : b, lane ^ 16);
+  }
+  return rank;
+}
 
-template <typename T, int V, bool SIGMOID>
-__global__ __launch_bounds__(NT) void fwd_rows_kernel(FwdArgs A) {
-  constexpr int V64 = V < 4 ? 1 : V / 4;
-  constexpr int ROW = 16 * V + 16;  // scores, chosen
-  __shared__ alignas(16) float lds[WAVES * 4 * ROW + (V < 4 ? WAVES * 128 : 0)];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
+template <typename T, int V, bool SIGMOID, int L>
+// (four wavefronts a SIMD: 65536 tokens of 384 experts 72 us so, 90 with the
+// registers of three)
+__global__ __launch_bounds__(NT, L == 32 ? 4 : 1) void fwd_rows_kernel(FwdArgs A) {
+  constexpr int V64 = V * L < 64 ? 1 : V * L / 64, TOKENS = 64 / L;  // of a wavefront
+  constexpr int ROW = L * V + 16;  // scores, chosen
+  constexpr bool APART = V * L < 64;  // the 64-bit choice's shared memory
+  __shared__ alignas(16) float lds[WAVES * TOKENS * ROW + (APART ? WAVES * 128 : 0)];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & (L - 1), q = lane / L;
   const T* logits = reinterpret_cast<const T*>(A.logits);
   const float NEG = -__builtin_huge_valf();
-  float* scores = lds + (wave * 4 + q) * ROW;
-  int* chosen = reinterpret_cast<int*>(scores + 16 * V);
+  float* scores = lds + (wave * TOKENS + q) * ROW;
+  int* chosen = reinterpret_cast<int*>(scores + L * V);
   float bias[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) bias[i] = A.bias && r * V + i < A.E ? A.bias[r * V + i] : 0.f;
-  const int64_t stride = (int64_t)gridDim.x * WAVES * 4;
-  int64_t t = ((int64_t)blockIdx.x * WAVES + wave) * 4 + q;
+  const int64_t stride = (int64_t)gridDim.x * WAVES * TOKENS;
+  int64_t t = ((int64_t)blockIdx.x * WAVES + wave) * TOKENS + q;
   float l[V];
   load_row<T, V>(logits + t * A.E, A.E, r, t < A.N, l);
   for (; t - q < A.N; t += stride) {
@@ -523,14 +616,14 @@ __global__ __launch_bounds__(NT) void fwd_rows_kernel(FwdArgs A) {
       top = l[0];
 #pragma unroll
       for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
-      top = row_all(top, fmaxf_);
+      top = token_all<L>(top, fmaxf_);
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         s[i] = l[i] > LOWEST ? fast_exp(l[i] - top) : 0.f;
         sum += s[i];
       }
-      sum = row_all(sum, [](float a, float b) { return a + b; });
+      sum = token_all<L>(sum, [](float a, float b) { return a + b; });
       largest = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) s[i] *= largest;
@@ -558,14 +651,17 @@ __global__ __launch_bounds__(NT) void fwd_rows_kernel(FwdArgs A) {
       if (A.lanes_log2 > 0) merge_best<0>(b1, b2);
       if (A.lanes_log2 > 1) merge_best<1>(b1, b2);
       if (A.lanes_log2 > 2) merge_best<2>(b1, b2);
+      if constexpr (L == 32)
+        if (A.lanes_log2 > 3) merge_best<3>(b1, b2);
       const float worth = A.best == 2 && b2 > NEG ? b1 + b2 : b1;
-      const int rank = A.lanes_log2 == 0   ? group_rank<0>(worth, r)
-                       : A.lanes_log2 == 1 ? group_rank<1>(worth, r)
-                       : A.lanes_log2 == 2 ? group_rank<2>(worth, r)
-                                           : group_rank<3>(worth, r);
+      const int rank = A.lanes_log2 == 0   ? group_rank<0, L>(worth, r)
+                       : A.lanes_log2 == 1 ? group_rank<1, L>(worth, r)
+                       : A.lanes_log2 == 2 ? group_rank<2, L>(worth, r)
+                       : A.lanes_log2 == 3 ? group_rank<3, L>(worth, r)
+                                           : group_rank<4, L>(worth, r);
       kept = rank < A.kept;
-      const float last = -row_all(kept ? -worth : NEG, fmaxf_);
-      const float next = row_all(kept ? NEG : worth, fmaxf_);
+      const float last = -token_all<L>(kept ? -worth : NEG, fmaxf_);
+      const float next = token_all<L>(kept ? NEG : worth, fmaxf_);
       close = next > NEG && !(last - next > 2.f * slack + 0x1p-21f * (fabsf(last) + fabsf(next)));
     }
 #pragma unroll
@@ -581,8 +677,13 @@ __global__ __launch_bounds__(NT) void fwd_rows_kernel(FwdArgs A) {
       m = max_with<0x4E>(m);
       m = max_with<0x141>(m);
       m = max_with<0x140>(m);
-      // the lowest of the row's lanes that hold it, and there the lowest i
-      const uint32_t holders = (uint32_t)(__ballot(head == m) >> (lane & 48)) & 0xffffu;
+      if constexpr (L == 32) {
+        uint32_t a, b;
+        pair16(m, a, b);
+        m = max(a, b);
+      }
+      // the lowest of the token's lanes that hold it, and there the lowest i
+      const uint32_t holders = (uint32_t)(__ballot(head == m) >> (lane & (64 - L))) & (uint32_t)((1ull << L) - 1);
       bool mine = m != 0 && r == __ffs((int)holders) - 1;
       int at = 0;
 #pragma unroll
@@ -596,27 +697,41 @@ __global__ __launch_bounds__(NT) void fwd_rows_kernel(FwdArgs A) {
       my_key = r == j ? m : my_key;
     }
     wave_lds_sync();
-    int my_e = r < A.K && my_key != 0 ? chosen[r] : -1;
-    float my_s = my_e >= 0 ? scores[my_e] : 0.f;
+    int my_e = r < rounds && my_key != 0 ? chosen[r] : -1;
     if (A.bias) {
       const uint32_t below = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)my_key, 0x101, 0xf, 0xf, true);
-      const float m = from_key(my_key), n = from_key(below);
-      close = close || (r < A.K && below != 0 && !(m - n > slack + 0x1p-22f * fabsf(m)));
+      const unsigned long long tight = __ballot(r < A.K && too_close(my_key, below, slack));
+      if constexpr (SIGMOID) {
+        if (tight != 0) {
+          if ((tight >> (lane & (64 - L)) >> (A.K - 1)) & 1) {  // of this token
+            // is the first left out sure to be ahead of the next?
+            const uint32_t first_out = (uint32_t)__shfl((int)my_key, (lane & (64 - L)) + A.K, 64);
+#pragma unroll
+            for (int i = 0; i < V; ++i) close = close || too_close(first_out, key[i], slack);
+          }
+          // (tokens that were sure keep their order)
+          my_e = settle<T>(A, logits + t * A.E, my_e, lane & (64 - L), lane);
+        }
+      } else {
+        close = close || ((tight >> lane) & 1);
+      }
     }
+    if (r >= A.K) my_e = -1;
+    float my_s = my_e >= 0 ? scores[my_e] : 0.f;
     wave_lds_sync();
     const unsigned long long redo = __ballot(close);
     if (redo) {
       FwdArgs W = A;
       W.lanes_log2 = A.wide_log2;
-      double* cs = reinterpret_cast<double*>(lds + wave * 4 * ROW);
-      if constexpr (V < 4) cs = reinterpret_cast<double*>(lds + WAVES * 4 * ROW + wave * 128);
-      for (int k = 0; k < 4; ++k) {
-        if (!((redo >> (16 * k)) & 0xffff)) continue;
+      double* cs = reinterpret_cast<double*>(lds + wave * TOKENS * ROW);
+      if constexpr (APART) cs = reinterpret_cast<double*>(lds + WAVES * TOKENS * ROW + wave * 128);
+      for (int k = 0; k < TOKENS; ++k) {
+        if (!((redo >> (L * k)) & ((1ull << L) - 1))) continue;
         const int64_t tk = t - q + k;
         float w[V64];
         load_row<T, V64>(logits + tk * A.E, A.E, lane, tk < A.N, w);
-        const float tw = __shfl(top, 16 * k, 64);
-        const int e = __shfl(choose_wide<V64, SIGMOID>(W, w, tw, lane, cs), r, 64);
+        const float tw = __shfl(top, L * k, 64);
+        const int e = __shfl(choose_wide_apart<V64, SIGMOID>(W, w, tw, lane, cs), r, 64);
         if (q == k) {
           my_e = r < A.K ? e : -1;
           my_s = 0.f;
@@ -631,7 +746,7 @@ __global__ __launch_bounds__(NT) void fwd_rows_kernel(FwdArgs A) {
         wave_lds_sync();
       }
     }
-    if (A.renorm) my_s /= row_all(my_s, [](float a, float b) { return a + b; }) + 1e-20f;
+    if (A.renorm) my_s /= token_all<L>(my_s, [](float a, float b) { return a + b; }) + 1e-20f;
     if (r < A.K && t < A.N) {
       A.expert[t * A.K + r] = my_e;
       A.weight[t * A.K + r] = my_s * A.scale;
@@ -886,11 +1001,20 @@ __global__ __launch_bounds__(1024) void scan_kernel(TablesArgs A, int runs) {
   if (share == 15) A.ws[(int64_t)runs * width + e] = base;
 }
 
+// Shares in which a workgroup of place_kernel adds up the other runs' counts,
+// one thread for each share of an expert.  At most 16, which one thread adds
+// up in turn: 32768 pairs of one local expert 6.9 us so, 9.3 without a limit,
+// 7.5 and 8.7 with 8 and 4.
+__host__ __device__ __forceinline__ int shares_of(int run, int width) {
+  const int s = run / width;
+  return s < 1 ? 1 : s > 16 ? 16 : s;
+}
+
 // shared memory of place_kernel, in ints
 template <int RUN>
 static size_t place_lds(int n_local) {
   const size_t width = (size_t)n_local + 1;
-  const size_t shares = width < (size_t)RUN ? RUN / width : 1;
+  const size_t shares = shares_of(RUN, (int)width);
   return 2 * width + RUN + RUN / 64 * 2 + 2 * shares * width + ((size_t)RUN / 64 * n_local + 1) / 2;
 }
 
@@ -899,7 +1023,7 @@ __global__ __launch_bounds__(RUN) void place_kernel(TablesArgs A, int pairs, int
   constexpr int WV = RUN / 64;
   extern __shared__ int lds[];
   const int width = A.n_local + 1;
-  const int shares = max(1, RUN / width);
+  const int shares = shares_of(RUN, width);
   int* first = lds;            // [width] first row of each expert in this run
   int* total = first + width;  // [width] rows of each expert in all
   int* seen = total + width;   // [RUN] experts of this run's pairs
@@ -1106,11 +1230,12 @@ static void pick_rows(int dtype, int V, int score, F&& f) {
   dtype == TP_BF16 ? by_size(bf16_t{}) : by_size(0.f);
 }
 
-// Tokens from which four of them share a wavefront: then those wavefronts
+// Tokens from which several of them share a wavefront: then those wavefronts
 // fill the chip.  Forward, top 2 of 64: 2048 tokens 3.3 us so and 3.1 with a
-// wavefront each, 4096 3.3 and 3.6, 32768 6.4 and 12.5; top 8 of 256 in groups
-// (16 experts a lane): 4096 13.2 and 11.7, 8192 16.3 and 16.9, 32768 33 and 49.
-static int64_t rows_from(int E) { return E <= 128 ? 4096 : 7168; }
+// wavefront each, 4096 3.1 and 3.6, 32768 6.4 and 12.5; top 8 of 256 (16 experts
+// a lane): 6144 8.1 and 7.7, 7168 8.2 and 8.8, 12288 9.6 and 14.1; top 8 of 512
+// (32 lanes a token): 4096 8.0 and 10.3, 8192 11.1 and 17.4.
+static int64_t rows_from(int E) { return E <= 128 || E > 256 ? 4096 : 7168; }
 constexpr int64_t ROWS_GRID = 1024;
 // experts of a lane with 16 lanes a token
 static int rows_experts(int E) { return E <= 16 ? 1 : E <= 32 ? 2 : E <= 64 ? 4 : E <= 128 ? 8 : 16; }
@@ -1134,15 +1259,26 @@ hipError_t route_fwd_launch(const tp_route_desc& d, const void* logits, const fl
       if (per == V << b) return b;
     return -1;
   };
-  const int v16 = rows_experts(d.E);
-  if (d.N >= rows_from(d.E) && d.E <= 256 && d.K <= 15 && (d.groups == 1 || (log2_lanes(v16) >= 0 && log2_lanes(v16) <= 3))) {
-    const int64_t groups = (d.N + 4 * WAVES - 1) / (4 * WAVES);
+  const int L = d.E <= 256 ? 16 : 32;
+  const int v = L == 16 ? rows_experts(d.E) : 16;
+  const int64_t from = rows_from(d.E);
+  const int lanes = log2_lanes(v);
+  if (d.N >= from && d.E <= v * L && d.K <= 15 && (d.groups == 1 || (lanes >= 0 && lanes <= (L == 32 ? 4 : 3)))) {
+    const int tokens = WAVES * (64 / L);
+    const int64_t groups = (d.N + tokens - 1) / tokens;
     const dim3 grid((unsigned)(groups > ROWS_GRID ? ROWS_GRID : groups));
-    a.lanes_log2 = log2_lanes(v16);
-    a.wide_log2 = log2_lanes(v16 < 4 ? 1 : v16 / 4);
-    pick_rows(d.dtype, v16, d.score, [&](auto t, auto v, auto sig) {
-      hipLaunchKernelGGL((fwd_rows_kernel<decltype(t), decltype(v)::value, decltype(sig)::value>),
-                         grid, dim3(NT), 0, st, a);
+    a.lanes_log2 = lanes;
+    a.wide_log2 = log2_lanes(v * L < 64 ? 1 : v * L / 64);
+    pick_rows(d.dtype, v, d.score, [&](auto t, auto v, auto sig) {
+      constexpr int V = decltype(v)::value;
+      if constexpr (V == 16) {
+        if (L == 32) {
+          hipLaunchKernelGGL((fwd_rows_kernel<decltype(t), V, decltype(sig)::value, 32>), grid, dim3(NT), 0,
+                             st, a);
+          return;
+        }
+      }
+      hipLaunchKernelGGL((fwd_rows_kernel<decltype(t), V, decltype(sig)::value, 16>), grid, dim3(NT), 0, st, a);
     });
     return hipGetLastError();
   }

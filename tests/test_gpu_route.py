@@ -377,6 +377,37 @@ def test_many_tokens_with_equal_and_close_values(E, K, groups, kept, sigmoid):
             check_many(desc(N, E, K, groups, kept, 2, sigmoid), l, b)
 
 
+@pytest.mark.parametrize("E,K,groups,kept", [(257, 3, 1, 1), (300, 15, 1, 1), (384, 8, 24, 5), (400, 16, 1, 1), (512, 8, 2, 1),
+                                             (512, 6, 4, 2), (512, 8, 8, 3), (512, 15, 16, 6), (512, 12, 32, 4)])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_many_tokens_of_many_experts(E, K, groups, kept, sigmoid):
+    # 32 lanes a token, groups of 1 to 16 lanes
+    for k, (bias, masked, dtype) in enumerate([(True, True, F32), (False, True, BF16), (True, False, BF16)]):
+        d = desc(4097 + 5 * k, E, K, groups, kept, 2, sigmoid, True, dtype, scale=2.5)
+        l, b = inputs(d["N"], E, dtype, bias, masked, seed=E + k)
+        check_many(d, l, b)
+
+
+@pytest.mark.parametrize("E,K", [(64, 1), (64, 4), (64, 15), (128, 8), (256, 5), (256, 8), (256, 15), (512, 6), (512, 9),
+                                 (256, 32), (1000, 7)])
+@pytest.mark.parametrize("near", [2, 3, 4])
+def test_scores_in_close_clusters(E, K, near):
+    """Experts in clusters of `near` scores that 32 bits do not tell apart, far from the next cluster: the
+    choice ends between two clusters or inside one, with one, two or three more of it behind."""
+    g = torch.Generator(device="cuda").manual_seed(E + K + near)
+    clusters = -(-E // near)
+    bias = torch.randint(0, 16, (E,), generator=g, device="cuda").float() * 2.0 ** -26
+    for N in (60, 4096 + 3 if E <= 128 or E > 256 else 7168 + 3):
+        place = torch.rand(N, E, generator=g, device="cuda").argsort(1)      # which expert has which place
+        l = (place // near).float() * (4.0 / clusters) - 2.0
+        l = l + torch.randint(0, 3, (N, E), generator=g, device="cuda") * 2.0 ** -23
+        d = desc(N, E, K, sigmoid=True)
+        if N == 60:
+            check_forward(d, l, bias)
+        else:
+            check_many(d, l, bias)
+
+
 @pytest.mark.parametrize("N,K", [(40000, 2), (20000, 8), (16384, 2), (140000, 1), (9000, 32), (66000, 6)])
 @pytest.mark.parametrize("E,first,n_local", [(64, 0, 64), (64, 8, 1), (1024, 0, 1024), (256, 100, 70)])
 def test_tables_of_many_runs(N, K, E, first, n_local):
