@@ -1041,15 +1041,26 @@ __global__ __launch_bounds__(RUN) void place_kernel(TablesArgs A, int pairs, int
       sums[width + i] = A.ws[(int64_t)runs * width + i];
     }
   } else if (runs > 1) {
+    // counts on their way at a time (65528 pairs of 256 local experts 12.7 us
+    // so, 14.4 with eight, 18.3 with four)
+    constexpr int AT_ONCE = 16;
     for (int i = tid; i < width * shares; i += RUN) {
       const int share = i / width, col = i - share * width;
       int before = 0, all = 0;
-#pragma unroll 4
-      for (int r = share; r < runs; r += shares) {
-        const int v = A.ws[r * width + col];
-        all += v;
-        before += r < run ? v : 0;
-      }
+      int r = share;
+      auto batch = [&](auto whole) {
+        int v[AT_ONCE];
+#pragma unroll
+        for (int j = 0; j < AT_ONCE; ++j)
+          v[j] = whole || r + j * shares < runs ? A.ws[(r + j * shares) * width + col] : 0;
+#pragma unroll
+        for (int j = 0; j < AT_ONCE; ++j) {
+          all += v[j];
+          before += r + j * shares < run ? v[j] : 0;
+        }
+      };
+      for (; r + (AT_ONCE - 1) * shares < runs; r += AT_ONCE * shares) batch(std::true_type{});
+      if (r < runs) batch(std::false_type{});
       sums[i] = before;
       sums[shares * width + i] = all;
     }
