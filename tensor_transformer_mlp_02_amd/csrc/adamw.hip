@@ -200,13 +200,40 @@ __global__ __launch_bounds__(NT) void step32_kernel(Args A) {
     }
     return;
   }
-  for (int64_t i = i0 + threadIdx.x; i < t.count; i += NT) {
-    float p = t.p[i], m = mp[i], v = vp[i];
-    update(p, Grad4<GT>::one(t.g, i), m, v);
-    mp[i] = m;
-    vp[i] = v;
-    t.p[i] = p;
-    if (t.p16) t.p16[i] = f32_to_bf16(p);
+  // a tensor's last piece: up to three elements over, for the threads with
+  // least to do, and four neighbours a thread
+  const int64_t fours = t.count & ~(int64_t)3, over = fours + (NT - 1 - threadIdx.x);
+  const bool one = over < t.count;
+  float p1 = 0.f, g1 = 0.f, m1 = 0.f, v1 = 0.f;
+  if (one) {
+    p1 = t.p[over];
+    g1 = Grad4<GT>::one(t.g, over);
+    m1 = mp[over];
+    v1 = vp[over];
+  }
+#pragma unroll 1
+  for (int64_t i = i0 + threadIdx.x * 4; i < fours; i += NT * 4) {
+    float4 p = ld4(t.p + i), m = ld4(mp + i), v = ld4(vp + i);
+    Grad4<GT> g;
+    g.load(t.g, i);
+    float gg[4];
+    g.get(gg);
+    update(p.x, gg[0], m.x, v.x);
+    update(p.y, gg[1], m.y, v.y);
+    update(p.z, gg[2], m.z, v.z);
+    update(p.w, gg[3], m.w, v.w);
+    st4(mp + i, m);
+    st4(vp + i, v);
+    st4(t.p + i, p);
+    if (t.p16)
+      *reinterpret_cast<uint2*>(t.p16 + i) = make_uint2(pack_bf16x2(p.x, p.y), pack_bf16x2(p.z, p.w));
+  }
+  if (one) {
+    update(p1, g1, m1, v1);
+    mp[over] = m1;
+    vp[over] = v1;
+    t.p[over] = p1;
+    if (t.p16) t.p16[over] = f32_to_bf16(p1);
   }
 }
 
