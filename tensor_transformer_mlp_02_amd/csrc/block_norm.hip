@@ -105,6 +105,20 @@ __device__ __forceinline__ float wave_total(float x) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
 }
 
+// the same over each 8, 16 or 32 lanes
+template <int LANES>
+__device__ __forceinline__ float lanes_total(float x) {
+  x = dpp_add<0xB1, 0xf>(x);   // lane ^ 1
+  x = dpp_add<0x4E, 0xf>(x);   // lane ^ 2
+  x = dpp_add<0x141, 0xf>(x);  // within 8: lane 7 - i
+  if constexpr (LANES >= 16) x = dpp_add<0x140, 0xf>(x);  // within 16: lane 15 - i
+  if constexpr (LANES == 32) {
+    const auto v = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(v[0]) + __uint_as_float(v[1]);
+  }
+  return x;
+}
+
 template <int TPR>
 struct Rows {
   static constexpr int THREADS = TPR < 256 ? 256 : TPR;
@@ -117,7 +131,10 @@ struct Rows {
 template <int TPR, int K, int THREADS = Rows<TPR>::THREADS>
 __device__ __forceinline__ void row_sums(float (&v)[K], float* red, int& half) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = wave_total(v[k]);
+  for (int k = 0; k < K; ++k) {
+    if constexpr (TPR < 64) v[k] = lanes_total<TPR>(v[k]);
+    else v[k] = wave_total(v[k]);
+  }
   if constexpr (TPR > 64) {
     constexpr int W = TPR / 64;
     const int wave = threadIdx.x >> 6;
@@ -1094,14 +1111,19 @@ static hipError_t pick(int kind, int dtype, F&& f) {
 }  // namespace norm
 
 // f(TPR, P) of the threads a row and pieces a thread that hold `pieces`
-// pieces in registers; false: too wide for any.  WIDEST: threads of the
-// widest rows.  Forward, 2048 x 16384 bf16: 46 us with 512 threads, 82 with
-// 1024 (barriers of 16 wavefronts); backward, whose 512 threads would spill,
-// 393 and 123 us.
+// pieces in registers; false: too wide for any.  Narrow rows (a norm of each
+// head's channels) share a wavefront: 262144 x 64 bf16 24 us so, 114 with a
+// wavefront each, backward 39 and 148; 281330 x 96 42 and 129, 77 and 164.
+// WIDEST: threads of the widest rows.  Forward, 2048 x 16384 bf16: 46 us with
+// 512 threads, 82 with 1024 (barriers of 16 wavefronts); backward, whose 512
+// threads would spill, 393 and 123 us.
 template <int WIDEST, typename F>
 static bool pick_width(int64_t pieces, F&& f) {
   using std::integral_constant;
-  if (pieces <= 64) f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  if (pieces <= 8) f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+  else if (pieces <= 16) f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  else if (pieces <= 32) f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  else if (pieces <= 64) f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
   else if (pieces <= 128) f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
   else if (pieces <= 256) f(integral_constant<int, 128>{}, integral_constant<int, 2>{});
   else if (pieces <= 512) f(integral_constant<int, 256>{}, integral_constant<int, 2>{});

@@ -178,6 +178,17 @@ def test_gate_rows(G, H):
     c.check_backward(c.backward())
 
 
+@pytest.mark.parametrize("N", [1, 63, 65, 500, 40001])
+@pytest.mark.parametrize("H,dtype", [(24, torch.bfloat16), (64, torch.bfloat16), (72, torch.bfloat16), (128, torch.bfloat16),
+                                     (136, torch.bfloat16), (256, torch.bfloat16), (20, torch.float32), (128, torch.float32)])
+@pytest.mark.parametrize("G,bias,layer", [(0, False, False), (1, True, True), (13, False, True), (-1, True, False)])
+def test_narrow_rows(N, H, dtype, G, bias, layer):
+    # several rows a wavefront, more of them than the grid takes at once; G = -1: a gate a token
+    c = Case(N, H, G=N if G < 0 else G, dtype=dtype, layer=layer, bias=bias, seed=N + H)
+    c.check_forward(c.forward())
+    c.check_backward(c.backward(db=bias))
+
+
 @pytest.mark.parametrize("G", [7, 20, 33])
 @pytest.mark.parametrize("H,dtype", [(16384, torch.bfloat16), (20000, torch.bfloat16), (8192, torch.float32)])
 def test_gate_rows_of_wide_rows(G, H, dtype):
@@ -220,7 +231,7 @@ def test_several_turns_of_the_widest_rows(H, dtype, G, bias, layer):
     c.check_backward(c.backward(db=bias))
 
 
-@pytest.mark.parametrize("H", [256, 8192, 16384, 20000])
+@pytest.mark.parametrize("H", [64, 256, 8192, 16384, 20000])
 def test_stream_updated_in_place(H):
     c = Case(19, H, G=1)
     a, b = c.forward(), c.forward(in_place=True)
@@ -228,7 +239,7 @@ def test_stream_updated_in_place(H):
         assert torch.equal(x, y)
 
 
-@pytest.mark.parametrize("H,N", [(512, 700), (4096, 300), (20000, 20)])
+@pytest.mark.parametrize("H,N", [(64, 5000), (512, 700), (4096, 300), (20000, 20)])
 def test_accumulates_and_repeats_bitwise(H, N):
     for G in (1, 3, N):
         c = Case(N, H, G=G, layer=True, bias=True)
