@@ -1200,14 +1200,16 @@ __global__ __launch_bounds__(RUN) void place_kernel(TablesArgs A, int pairs, int
 }
 
 // Threads of a run, a pair each: one run where that is possible (one launch),
-// else the smallest runs whose counts place_kernel adds up itself (two).  32768
-// pairs of 8 local experts: 11.9 us for the routing with runs of 256 threads,
-// 12.5 with 512, 14.5 with 1024; 65528 pairs of 64: 25.5 with 512, 25.3 with
-// 1024, 32 with 256 (256 runs, a scan between).
-static int run_threads(int64_t N, int K) {
+// else the smallest runs whose counts place_kernel adds up itself (two), with
+// at most 24 counts a thread.  32768 pairs: of 8 local experts 7.1 us with runs
+// of 256 and 512 threads, 7.7 with 1024; of 64 (33 counts a thread, 8, 2) 8.8,
+// 8.3 and 9.6; of 256 (129, 32, 8) 14.4, 10.3 and 10.9.  8192 pairs of 32 (4
+// counts, 1) 7.5 and 8.0.
+static int run_threads(int64_t N, int K, int n_local) {
   if (N * K > 256 && (N + 1024 / K - 1) / (1024 / K) <= 1) return 1024;
   for (int run = 256; run < 1024; run *= 2)
-    if ((N + run / K - 1) / (run / K) <= FEW) return run;
+    if ((N + run / K - 1) / (run / K) <= FEW && N * K * (n_local + 1) <= 24 * (int64_t)run * run)
+      return run;
   return 1024;
 }
 
@@ -1326,7 +1328,7 @@ hipError_t route_bwd_launch(const tp_route_desc& d, const void* logits, const in
 }
 
 size_t route_tables_workspace(int64_t N, int K, int n_local) {
-  const int64_t tokens = route::run_threads(N, K) / K;
+  const int64_t tokens = route::run_threads(N, K, n_local) / K;
   const int64_t runs = (N + tokens - 1) / tokens;
   if (runs <= 1) return 16;  // not used; a caller need not tell sizes apart
   return (size_t)(runs + (runs > route::FEW ? 1 : 0)) * ((size_t)n_local + 1) * sizeof(int32_t);
@@ -1354,7 +1356,7 @@ static hipError_t tables_launch(const TablesArgs& a, hipStream_t st) {
 }
 
 hipError_t route_tables_launch(const TablesArgs& a, hipStream_t st) {
-  switch (route::run_threads(a.N, a.K)) {
+  switch (route::run_threads(a.N, a.K, a.n_local)) {
     case 256: return tables_launch<256>(a, st);
     case 512: return tables_launch<512>(a, st);
     default: return tables_launch<1024>(a, st);
