@@ -92,18 +92,37 @@ def _call(name: str, args: tuple, stream) -> int:
     return rc if rc == 0 else _check(rc)
 
 
-def _as(cls, desc, **defaults):
-    return desc if isinstance(desc, cls) else cls(**{**defaults, **desc})
+def _defaults(cls, **given):
+    """Every field of a descriptor in its order, 0 where nothing else is the default."""
+    return {name: given.get(name, 0) for name, _ in cls._fields_}
+
+
+_NORM = _defaults(tp_norm_desc, kind=TP_NORM_RMS, dtype=TP_BF16, eps=1e-5, res_scale=1.0,
+                  branch_scale=1.0)
+_ROUTE = _defaults(tp_route_desc, groups=1, groups_kept=1, group_best=1, score=TP_SCORE_SOFTMAX,
+                   scale=1.0)
+_ADAMW = _defaults(tp_adamw_desc, beta1=0.9, beta2=0.999, eps=1e-8, step=1, state_bits=32)
+
+
+def _as(cls, desc, defaults):
+    if isinstance(desc, cls):
+        return desc
+    fields = {**defaults, **desc}   # in the structure's order
+    if len(fields) != len(defaults):
+        raise TypeError(f"{cls.__name__} has no field {sorted(fields.keys() - defaults.keys())}")
+    return cls(*fields.values())
 
 
 def _norm(desc) -> tp_norm_desc:
-    return _as(tp_norm_desc, desc, gate_rows=0, kind=TP_NORM_RMS, dtype=TP_BF16, eps=1e-5,
-               res_scale=1.0, branch_scale=1.0)
+    return _as(tp_norm_desc, desc, _NORM)
 
 
 def _route(desc) -> tp_route_desc:
-    return _as(tp_route_desc, desc, groups=1, groups_kept=1, group_best=1,
-               score=TP_SCORE_SOFTMAX, renorm=0, dtype=0, scale=1.0)
+    return _as(tp_route_desc, desc, _ROUTE)
+
+
+def _adamw(desc) -> tp_adamw_desc:
+    return _as(tp_adamw_desc, desc, _ADAMW)
 
 
 def _type(d) -> str:
@@ -202,8 +221,7 @@ class AdamwTensors:
     they have to keep their memory (no resize) while the table is in use."""
 
     def __init__(self, desc, tensors):
-        d = _as(tp_adamw_desc, desc, beta1=0.9, beta2=0.999, eps=1e-8, step=1, grad_dtype=0,
-                state_bits=32, seed=0)
+        d = _adamw(desc)
         small = d.state_bits == 8
         self.formats = (d.grad_dtype, d.state_bits)
         self.n = len(tensors)
@@ -247,8 +265,7 @@ def tp_adamw_step(desc, tensors, dev_step=None, dev_lr=None, grad_scale=None,
     """One AdamW step over ``tensors`` (tp_adamw_tensors, or the list it takes).  ``desc``: lr and,
     with their defaults, beta1 0.9, beta2 0.999, eps 1e-8, step 1, grad_dtype TP_F32,
     state_bits 32, seed 0.  dev_step (int32), dev_lr, grad_scale (float32): device scalars."""
-    d = _as(tp_adamw_desc, desc, beta1=0.9, beta2=0.999, eps=1e-8, step=1, grad_dtype=0,
-            state_bits=32, seed=0)
+    d = _adamw(desc)
     t = tensors if isinstance(tensors, AdamwTensors) else AdamwTensors(d, tensors)
     if t.formats != (d.grad_dtype, d.state_bits):
         raise ValueError(f"the table is for (grad_dtype, state_bits) = {t.formats}")

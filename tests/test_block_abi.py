@@ -323,3 +323,15 @@ def test_tensors_of_another_type_are_refused():
         tp.tp_moe_route_fwd(rd(dtype=tp.TP_F32), slim, None, addr(3), addr(4))
     with pytest.raises(ValueError, match="dlogits must be a torch.bfloat16"):
         tp.tp_moe_route_bwd(rd(dtype=tp.TP_BF16), addr(1), addr(2), addr(3), None, 0, wide)
+
+
+def test_descriptors_take_their_fields_by_name():
+    for desc in (dict(E=8, N=2, K=1, scales=2.0), dict(N=2, K=1, E=8, group=2)):
+        with pytest.raises(TypeError, match="no field"):
+            tp.tp_moe_route_fwd(desc, addr(1), None, addr(3), addr(4))
+    with pytest.raises(TypeError, match="no field"):
+        tp.tp_adamw_step(dict(lr=1e-3, beta3=0.9), [])
+    from tensor_transformer_mlp_02_amd import block
+    d = block._norm(dict(H=64, N=3, eps=0.5))   # whatever their order
+    assert (d.N, d.H, d.eps, d.dtype, d.res_scale, d.gate_rows) == (3, 64, 0.5, tp.TP_BF16, 1.0, 0)
+    assert block._norm(d) is d
