@@ -753,7 +753,21 @@ __global__ __launch_bounds__(BwdRows<TPR>::THREADS) void bwd_kernel(NormBwdArgs 
   };
   float st[4];
   request(turns > 0 ? row_of(0) : N, dy, dh, yy, oo, st);
-  if constexpr (!MANY) load_gate(g_first);
+  // one gate row for all of a worker's tokens: b gate w_post (b gate without a
+  // norm), once (8192 x 4096 with biases 102 us without, 88 so)
+  float kw[MANY ? 1 : P][V];
+  if constexpr (!MANY) {
+    load_gate(g_first);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      float q[V], t[V];
+      unpack<T>(gate[p], q);
+      unpack<T>(w_post[p], t);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        kw[p][i] = A.b * (A.G > 0 ? q[i] : 1.f) * (A.w_post ? t[i] : in[p] ? 1.f : 0.f);
+    }
+  }
 
   for (uint32_t it = 0; it < turns; ++it) {
     const uint32_t n = row_of(it);
@@ -772,24 +786,27 @@ __global__ __launch_bounds__(BwdRows<TPR>::THREADS) void bwd_kernel(NormBwdArgs 
     for (int k = 0; k < SUMS_ROW; ++k) v[k] = 0.f;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      float g[V], x[V], y[V], o[V], kw[V], t[V];
+      float g[V], x[V], y[V], o[V], c[V], t[V];
       unpack<T>(dh[p], g);
       unpack<T>(w_pre[p], t);
       unpack<T>(yy[p], y);
       unpack<T>(oo[p], o);
       unpack<T>(dy[p], x);
-      unpack<T>(w_post[p], kw);
-      if (A.G > 0) {
+      if constexpr (MANY) {
         float q[V];
+        unpack<T>(w_post[p], c);
         unpack<T>(gate[p], q);
 #pragma unroll
-        for (int i = 0; i < V; ++i) kw[i] *= q[i];
+        for (int i = 0; i < V; ++i) c[i] *= q[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) c[i] = kw[p][i];
       }
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         // outside the row the weights are zeros: no term counts
         const float yh = (y[i] - my) * ry, oh = (o[i] - mo) * ro, pw = g[i] * t[i];
-        const float k = A.b * kw[i], f = x[i] + ry * pw;
+        const float k = MANY ? A.b * c[i] : c[i], f = x[i] + ry * pw;
         if constexpr (KEPT) kept[(p * V + i) * THREADS + tr] += g[i] * yh;
         else a_wpre[p][i] += g[i] * yh;
         if constexpr (BIAS) a_bpre[p][i] += g[i];
@@ -816,12 +833,11 @@ __global__ __launch_bounds__(BwdRows<TPR>::THREADS) void bwd_kernel(NormBwdArgs 
         t2 = (v[5] - ry * (m2 * v[7] + m1 * v[6])) * inv_h;
       }
     }
-    // From here the values are unpacked again: kept unpacked over the sums they
-    // would take twice the registers.  Without it 8192 x 4096 with biases takes
-    // 119 us for 102, with a gate a token besides 379 for 178, and 2048 x 16384
-    // 173 for 123; where the registers do hold them it costs (8192 x 4096
-    // without biases 91 us for 84).
-    if constexpr (V == 8 && BIAS != (TPR > CU_THREADS)) {
+    // From here the values are unpacked again where the registers do not hold
+    // them unpacked: 8192 x 4096 with biases and a gate a token 177 us so, 280
+    // without; 2048 x 16384 124 and 160.  Elsewhere it costs (381 x 6152 with
+    // biases 29.6 us so, 26.6 without).
+    if constexpr (V == 8 && ((MANY && BIAS) || TPR > CU_THREADS)) {
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         hold(dy[p]);
@@ -855,19 +871,20 @@ __global__ __launch_bounds__(BwdRows<TPR>::THREADS) void bwd_kernel(NormBwdArgs 
       const int64_t at = (int64_t)n * pieces + tr + p * TPR;
       if (A.O) {
         float q[V];
-        if (A.G > 0) {
+        if constexpr (MANY) {
           unpack<T>(gate[p], q);
+          if (A.w_post) {
+            unpack<T>(w_post[p], t);
+#pragma unroll
+            for (int i = 0; i < V; ++i) q[i] = ro * (A.b * q[i] * t[i] * D[i] - t2 - o[i] * t1);
+          } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) q[i] = A.b * q[i] * D[i];
+          }
         } else {
 #pragma unroll
-          for (int i = 0; i < V; ++i) q[i] = 1.f;
-        }
-        if (A.w_post) {
-          unpack<T>(w_post[p], t);
-#pragma unroll
-          for (int i = 0; i < V; ++i) q[i] = ro * (A.b * q[i] * t[i] * D[i] - t2 - o[i] * t1);
-        } else {
-#pragma unroll
-          for (int i = 0; i < V; ++i) q[i] = A.b * q[i] * D[i];
+          for (int i = 0; i < V; ++i)
+            q[i] = A.w_post ? ro * (kw[p][i] * D[i] - t2 - o[i] * t1) : kw[p][i] * D[i];
         }
         if (in[p] && live) store_piece<T>(A.dO, at, q);
 #pragma unroll
