@@ -145,11 +145,6 @@ __device__ __forceinline__ double wave_sum(double x) {
   x += other<5>(x);
   return x;
 }
-__device__ __forceinline__ int wave_sum(int x) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) x += __shfl_xor(x, d, 64);
-  return x;
-}
 
 struct FwdArgs {
   const void* logits;
