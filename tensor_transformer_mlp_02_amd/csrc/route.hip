@@ -205,8 +205,17 @@ __device__ __forceinline__ void merge_best(X& b1, X& b2) {
   b1 = fmax(b1, o1);
 }
 
-// What lane g's group of experts is worth: the sum of its `best` largest
-// choice scores c (-inf: none there).  `cs`: E values of shared memory.
+// What a group of experts is worth by its two largest choice scores (-inf: not
+// there): the larger one, or half the sum of both (a sum of two finite scores
+// may not be finite, and halving rounds nothing that counts).
+template <typename X>
+__device__ __forceinline__ X worth_of(X b1, X b2, int best) {
+  if (best == 1) return b1;
+  return (X)0.5 * b1 + (b2 > (X)-__builtin_huge_val() ? (X)0.5 * b2 : (X)0);
+}
+
+// What lane g's group of experts is worth (-inf: none there).  `cs`: E values
+// of shared memory.
 template <typename X, int V>
 __device__ __forceinline__ X group_worth(const X (&c)[V], const FwdArgs& A, int lane, X* cs) {
   const X NEG = (X)-__builtin_huge_val();
@@ -221,8 +230,7 @@ __device__ __forceinline__ X group_worth(const X (&c)[V], const FwdArgs& A, int 
     if (A.lanes_log2 > 1) merge_best<1>(b1, b2);
     if (A.lanes_log2 > 2) merge_best<2>(b1, b2);
     if (A.lanes_log2 > 3) merge_best<3>(b1, b2);
-    const X worth = A.best == 2 && b2 > NEG ? b1 + b2 : b1;
-    return __shfl(worth, (lane << A.lanes_log2) & 63, 64);
+    return __shfl(worth_of(b1, b2, A.best), (lane << A.lanes_log2) & 63, 64);
   }
 #pragma unroll
   for (int i = 0; i < V; ++i)
@@ -235,7 +243,7 @@ __device__ __forceinline__ X group_worth(const X (&c)[V], const FwdArgs& A, int 
       b1 = fmax(b1, x);
     }
   wave_lds_sync();
-  return A.best == 2 && b2 > NEG ? b1 + b2 : b1;
+  return worth_of(b1, b2, A.best);
 }
 
 // Which groups stay, one bit each: the `kept` worth most, the lower of equals
@@ -369,7 +377,7 @@ __device__ __forceinline__ int settle(const FwdArgs& A, const T* row, int e, int
 // in 32 bits: without a bias the experts' order is the logits' own, exact.
 // With one, the order of the first k + 1 keys is right if neighbours differ
 // by more than the slack, and the groups kept are if the worth of the last
-// one and of the first left out differ by twice that.  Where neighbours do not
+// one and of the first left out (a score, or half of two) do.  Where neighbours do not
 // (one token in a thousand at 256 experts), settle orders the k + 1 by their
 // sigmoids in 64 bits; where that is not enough (groups, the next after those,
 // softmax scores, whose sum takes every expert) the token is done again in 64
@@ -432,7 +440,7 @@ __global__ __launch_bounds__(NT) void fwd_kernel(FwdArgs A) {
       const bool mine = (keep >> lane) & 1;
       const float last = -wave_max(mine ? -worth : NEG);
       const float next = wave_max(lane < A.groups && !mine ? worth : NEG);
-      close = next > NEG && !(last - next > 2.f * slack + 0x1p-21f * (fabsf(last) + fabsf(next)));
+      close = next > NEG && !(last - next > slack + 0x1p-21f * (fabsf(last) + fabsf(next)));
 #pragma unroll
       for (int i = 0; i < V; ++i)
         key[i] = c[i] > NEG && in_kept<V>(keep, A, lane, i) ? to_key(A.bias ? c[i] : l[i]) : 0u;
@@ -648,7 +656,7 @@ __global__ __launch_bounds__(NT, L == 32 ? 4 : 1) void fwd_rows_kernel(FwdArgs A
       if (A.lanes_log2 > 2) merge_best<2>(b1, b2);
       if constexpr (L == 32)
         if (A.lanes_log2 > 3) merge_best<3>(b1, b2);
-      const float worth = A.best == 2 && b2 > NEG ? b1 + b2 : b1;
+      const float worth = worth_of(b1, b2, A.best);
       const int rank = A.lanes_log2 == 0   ? group_rank<0, L>(worth, r)
                        : A.lanes_log2 == 1 ? group_rank<1, L>(worth, r)
                        : A.lanes_log2 == 2 ? group_rank<2, L>(worth, r)
@@ -657,7 +665,7 @@ __global__ __launch_bounds__(NT, L == 32 ? 4 : 1) void fwd_rows_kernel(FwdArgs A
       kept = rank < A.kept;
       const float last = -token_all<L>(kept ? -worth : NEG, fmaxf_);
       const float next = token_all<L>(kept ? NEG : worth, fmaxf_);
-      close = next > NEG && !(last - next > 2.f * slack + 0x1p-21f * (fabsf(last) + fabsf(next)));
+      close = next > NEG && !(last - next > slack + 0x1p-21f * (fabsf(last) + fabsf(next)));
     }
 #pragma unroll
     for (int i = 0; i < V; ++i)
