@@ -213,11 +213,18 @@ __device__ __forceinline__ X worth_of(X b1, X b2, int best) {
   if (best == 1) return b1;
   return (X)0.5 * b1 + (b2 > (X)-__builtin_huge_val() ? (X)0.5 * b2 : (X)0);
 }
+// The magnitude of its terms, which the worth's rounding goes by: scores of
+// opposite signs cancel in the sum, not in its error.
+__device__ __forceinline__ float terms_of(float b1, float b2, int best) {
+  if (!(b1 > -__builtin_huge_valf())) return 0.f;
+  return best == 1 ? fabsf(b1) : worth_of(fabsf(b1), b2 > -__builtin_huge_valf() ? fabsf(b2) : b2, best);
+}
 
-// What lane g's group of experts is worth (-inf: none there).  `cs`: E values
-// of shared memory.
+// What lane g's group of experts is worth (-inf: none there), and where
+// `terms` is given their magnitude.  `cs`: E values of shared memory.
 template <typename X, int V>
-__device__ __forceinline__ X group_worth(const X (&c)[V], const FwdArgs& A, int lane, X* cs) {
+__device__ __forceinline__ X group_worth(const X (&c)[V], const FwdArgs& A, int lane, X* cs,
+                                         float* terms = nullptr) {
   const X NEG = (X)-__builtin_huge_val();
   X b1 = NEG, b2 = NEG;
   if (A.lanes_log2 >= 0) {
@@ -230,7 +237,9 @@ __device__ __forceinline__ X group_worth(const X (&c)[V], const FwdArgs& A, int 
     if (A.lanes_log2 > 1) merge_best<1>(b1, b2);
     if (A.lanes_log2 > 2) merge_best<2>(b1, b2);
     if (A.lanes_log2 > 3) merge_best<3>(b1, b2);
-    return __shfl(worth_of(b1, b2, A.best), (lane << A.lanes_log2) & 63, 64);
+    const int from = (lane << A.lanes_log2) & 63;
+    if (terms) *terms = __shfl(terms_of((float)b1, (float)b2, A.best), from, 64);
+    return __shfl(worth_of(b1, b2, A.best), from, 64);
   }
 #pragma unroll
   for (int i = 0; i < V; ++i)
@@ -243,6 +252,7 @@ __device__ __forceinline__ X group_worth(const X (&c)[V], const FwdArgs& A, int 
       b1 = fmax(b1, x);
     }
   wave_lds_sync();
+  if (terms) *terms = terms_of((float)b1, (float)b2, A.best);
   return worth_of(b1, b2, A.best);
 }
 
@@ -376,8 +386,8 @@ __device__ __forceinline__ int settle(const FwdArgs& A, const T* row, int e, int
 // One wavefront a token.  Choices are to be those of 64-bit arithmetic, made
 // in 32 bits: without a bias the experts' order is the logits' own, exact.
 // With one, the order of the first k + 1 keys is right if neighbours differ
-// by more than the slack, and the groups kept are if the worth of the last
-// one and of the first left out (a score, or half of two) do.  Where neighbours do not
+// by more than the slack, and the groups kept are if each is worth more than
+// every one left out by what both may be off.  Where neighbours do not
 // (one token in a thousand at 256 experts), settle orders the k + 1 by their
 // sigmoids in 64 bits; where that is not enough (groups, the next after those,
 // softmax scores, whose sum takes every expert) the token is done again in 64
@@ -387,6 +397,13 @@ __device__ __forceinline__ int settle(const FwdArgs& A, const T* row, int e, int
 // 5.2 us with the launch); many are bound by instruction issue: the k maxima
 // take about 25 vector instructions each at V = 4, the scores 15 for each of
 // a lane's experts.
+// How far a group's worth may be off: a score, or half of two, by a quarter of
+// the slack, and by 2^-24 of its terms' magnitude for the rounding of the terms
+// c and as much for that of their sum; all that twice to be on the safe side.
+__device__ __forceinline__ float worth_slack(float slack, float terms) {
+  return 0.5f * slack + 0x1p-22f * terms;
+}
+
 template <typename T, int V, bool SIGMOID>
 __global__ __launch_bounds__(NT) void fwd_kernel(FwdArgs A) {
   extern __shared__ double sh[];
@@ -435,12 +452,14 @@ __global__ __launch_bounds__(NT) void fwd_kernel(FwdArgs A) {
       float c[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) c[i] = l[i] > LOWEST ? s[i] + bias[i] : NEG;
-      const float worth = group_worth<float, V>(c, A, lane, scores);
+      float terms;
+      const float worth = group_worth<float, V>(c, A, lane, scores, &terms);
       const unsigned long long keep = keep_groups(worth, A, lane);
       const bool mine = (keep >> lane) & 1;
-      const float last = -wave_max(mine ? -worth : NEG);
-      const float next = wave_max(lane < A.groups && !mine ? worth : NEG);
-      close = next > NEG && !(last - next > slack + 0x1p-21f * (fabsf(last) + fabsf(next)));
+      const float off = worth_slack(slack, terms);
+      const float last = -wave_max(mine ? off - worth : NEG);
+      const float next = wave_max(lane < A.groups && !mine ? worth + off : NEG);
+      close = next > NEG && !(last > next);
 #pragma unroll
       for (int i = 0; i < V; ++i)
         key[i] = c[i] > NEG && in_kept<V>(keep, A, lane, i) ? to_key(A.bias ? c[i] : l[i]) : 0u;
@@ -587,8 +606,8 @@ __device__ __forceinline__ int group_rank(float worth, int lane) {
 
 template <typename T, int V, bool SIGMOID, int L>
 // (four wavefronts a SIMD: 65536 tokens of 384 experts 72 us so, 90 with the
-// registers of three)
-__global__ __launch_bounds__(NT, L == 32 ? 4 : 1) void fwd_rows_kernel(FwdArgs A) {
+// registers of three; of 256 experts in groups 48 and 58)
+__global__ __launch_bounds__(NT, V == 16 ? 4 : 1) void fwd_rows_kernel(FwdArgs A) {
   constexpr int V64 = V * L < 64 ? 1 : V * L / 64, TOKENS = 64 / L;  // of a wavefront
   constexpr int ROW = L * V + 16;  // scores, chosen
   constexpr bool APART = V * L < 64;  // the 64-bit choice's shared memory
@@ -663,9 +682,10 @@ __global__ __launch_bounds__(NT, L == 32 ? 4 : 1) void fwd_rows_kernel(FwdArgs A
                        : A.lanes_log2 == 3 ? group_rank<3, L>(worth, r)
                                            : group_rank<4, L>(worth, r);
       kept = rank < A.kept;
-      const float last = -token_all<L>(kept ? -worth : NEG, fmaxf_);
-      const float next = token_all<L>(kept ? NEG : worth, fmaxf_);
-      close = next > NEG && !(last - next > slack + 0x1p-21f * (fabsf(last) + fabsf(next)));
+      const float off = worth_slack(slack, terms_of(b1, b2, A.best));
+      const float last = -token_all<L>(kept ? off - worth : NEG, fmaxf_);
+      const float next = token_all<L>(kept ? NEG : worth + off, fmaxf_);
+      close = next > NEG && !(last > next);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i)
