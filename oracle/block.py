@@ -148,9 +148,11 @@ def route_fwd(logits, bias, K, groups=1, kept=1, best=1, sigmoid=False, renorm=F
 
 def route_bwd(logits, expert, d_weight, sigmoid=False, renorm=False, scale=1.0):
     """dlogits from the gradient of the weights [N,K] (0 for a slot without one)."""
-    s, _ = scores(logits, sigmoid)
+    s, there = scores(logits, sigmoid)
     N, E = s.shape
     out = np.zeros((N, E))
+    e = np.where(there, np.exp(-np.abs(np.where(there, np.asarray(logits, f64), 0.0))), 0.0)
+    slope = e / (1 + e) ** 2  # s (1 - s) of a sigmoid, without 1 - s
     for t in range(N):
         on = [j for j in range(expert.shape[1]) if 0 <= expert[t, j] < E]
         total = sum(s[t, expert[t, j]] for j in on) + 1e-20
@@ -159,7 +161,7 @@ def route_bwd(logits, expert, d_weight, sigmoid=False, renorm=False, scale=1.0):
         ds = np.zeros(E)
         for j in on:
             ds[expert[t, j]] += (up[j] - mean) / total if renorm else up[j]
-        out[t] = s[t] * (1 - s[t]) * ds if sigmoid else s[t] * (ds - (ds * s[t]).sum())
+        out[t] = slope[t] * ds if sigmoid else s[t] * (ds - (ds * s[t]).sum())
     return out
 
 

@@ -790,6 +790,17 @@ struct BwdArgs {
   float scale;
 };
 
+// A sigmoid and its derivative from e = exp(-|l|) <= 1: s (1 - s) is e / (1 + e)^2
+// on either side of 0, with nothing subtracted (1 - s has no bits left for a
+// large l).
+__device__ __forceinline__ float sigmoid_of(float l) {
+  return 1.f / (1.f + expf(-l));
+}
+__device__ __forceinline__ float sigmoid_slope(float l) {
+  const float e = expf(-fabsf(l)), d = 1.f + e;
+  return e / (d * d);
+}
+
 // t_j = scale dw_j; renorm: ds_j = (t_j - sum_i t_i s_i / S) / S with
 // S = sum s + 1e-20, else ds_j = t_j; then softmax: dl = s (ds - sum ds s),
 // sigmoid: dl = s (1 - s) ds.  One wavefront a token; slot j is lane j's.
@@ -815,10 +826,10 @@ __global__ __launch_bounds__(NT) void bwd_kernel(BwdArgs A) {
     if (!(le > LOWEST)) le = -__builtin_huge_valf();
     le = fminf(le, LARGEST);
     float se;
-    if constexpr (SIGMOID) {
+    if constexpr (SIGMOID) {  // s: the derivative
 #pragma unroll
-      for (int i = 0; i < V; ++i) s[i] = l[i] > LOWEST ? 1.f / (1.f + expf(-l[i])) : 0.f;
-      se = le > LOWEST ? 1.f / (1.f + expf(-le)) : 0.f;
+      for (int i = 0; i < V; ++i) s[i] = l[i] > LOWEST ? sigmoid_slope(l[i]) : 0.f;
+      se = le > LOWEST ? sigmoid_of(le) : 0.f;
     } else {
       float top = l[0], sum = 0.f;
 #pragma unroll
@@ -855,7 +866,7 @@ __global__ __launch_bounds__(NT) void bwd_kernel(BwdArgs A) {
     if constexpr (!SIGMOID) dot = wave_sum(d * se);
     T* out = reinterpret_cast<T*>(A.dlogits) + t * A.E;
 #pragma unroll
-    for (int i = 0; i < V; ++i) ds[i] = SIGMOID ? s[i] * (1.f - s[i]) * ds[i] : s[i] * (ds[i] - dot);
+    for (int i = 0; i < V; ++i) ds[i] = SIGMOID ? s[i] * ds[i] : s[i] * (ds[i] - dot);
     store_row<T, V>(out, A.E, lane, ds);
   }
 }
@@ -912,10 +923,10 @@ __global__ __launch_bounds__(NT) void bwd_rows_kernel(BwdArgs A) {
     }
     auto sum_ = [](float a, float b) { return a + b; };
     float se;
-    if constexpr (SIGMOID) {
+    if constexpr (SIGMOID) {  // s: the derivative
 #pragma unroll
-      for (int i = 0; i < V; ++i) s[i] = l[i] > LOWEST ? 1.f / (1.f + expf(-l[i])) : 0.f;
-      se = le > LOWEST ? 1.f / (1.f + expf(-le)) : 0.f;
+      for (int i = 0; i < V; ++i) s[i] = l[i] > LOWEST ? sigmoid_slope(l[i]) : 0.f;
+      se = le > LOWEST ? sigmoid_of(le) : 0.f;
     } else {
       float top = l[0], sum = 0.f;
 #pragma unroll
@@ -949,7 +960,7 @@ __global__ __launch_bounds__(NT) void bwd_rows_kernel(BwdArgs A) {
     for (int i = 0; i < V; ++i) ds[i] = mine[r * V + i];
     wave_lds_sync();
 #pragma unroll
-    for (int i = 0; i < V; ++i) ds[i] = SIGMOID ? s[i] * (1.f - s[i]) * ds[i] : s[i] * (ds[i] - dot);
+    for (int i = 0; i < V; ++i) ds[i] = SIGMOID ? s[i] * ds[i] : s[i] * (ds[i] - dot);
     if (live) store_row<T, V>(reinterpret_cast<T*>(A.dlogits) + t * A.E, A.E, r, ds);
   }
 }

@@ -1,0 +1,93 @@
+"""The logits' gradient where scores are near 0 or 1: against the derivative in a form that subtracts nothing
+from 1.
+
+With u = 2^-24 and every operation rounded once:
+  sigmoid   s (1 - s) = e / (1 + e)^2, e = exp(-|l|): e off by 4 u, the quotient by 10 u with the gradient's own two
+            products; a renormalised gradient adds the K scores of its sum and their quotients.  64 u + 4 K u, of
+            s (1 - s) times the terms of ds.
+  softmax   dl_e = s_e ((ds_e - c) - sum_i s_i (ds_i - c)), c the ds of the largest score m: its term is exactly 0.
+            The terms are s_e (|ds_e| + |c|) (e other than m) and s_e s_i (|ds_i| + |c|) (i other than m), each off
+            by gamma() of test_gpu_route.py: the exponentials' rounded arguments and the sums of E terms.
+  renormalised  ds_j = ((t_j - k) - sum_i w_i (t_i - k) + k 1e-20 / S) / S, k the t of the largest of the chosen,
+            in the same way."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+import tensor_transformer_mlp_02_amd as tp  # noqa: E402
+from oracle import block as ob  # noqa: E402
+from test_gpu_route import BF16, F32, HALF, INF, desc, gamma  # noqa: E402
+
+U = 2.0 ** -24
+
+
+def check(d, logits, expert, up, got):
+    """got [N,E] for the weights' gradient up [N,K]; expert in range, none twice."""
+    N, E, K = d["N"], d["E"], d["K"]
+    l, ex, t = logits.double().cpu().numpy(), expert.cpu().numpy(), up.double().cpu().numpy() * float(np.float32(d["scale"]))
+    sig, ren = bool(d["score"]), bool(d["renorm"])
+    s, there = ob.scores(l, sig)
+    want = ob.route_bwd(l, ex, up.double().cpu().numpy(), sig, ren, float(np.float32(d["scale"])))
+    ds, mds = np.zeros((N, E)), np.zeros((N, E))
+    for n in range(N):
+        v, tn = s[n, ex[n]], t[n]
+        if ren:
+            S = v.sum() + 1e-20
+            m = int(v.argmax())
+            k, w = tn[m], v / S
+            other = np.arange(K) != m
+            ds[n, ex[n]] = ((tn - k) - (w * (tn - k)).sum() + k * (1e-20 / S)) / S
+            mds[n, ex[n]] = ((np.abs(tn) + abs(k)) * other + (w * (np.abs(tn) + abs(k)) * other).sum()
+                             + abs(k) * 1e-20 / S) / S
+        else:
+            ds[n, ex[n]], mds[n, ex[n]] = tn, np.abs(tn)
+    if sig:
+        e = np.where(there, np.exp(-np.abs(np.where(there, l, 0.0))), 0.0)
+        mag, g = e / (1 + e) ** 2 * mds, (64 + 4 * K) * U
+    else:
+        m = np.where(there, l, -np.inf).argmax(1)[:, None]
+        rest = np.arange(E)[None] != m
+        # (c itself is off by its own terms)
+        each = mds + np.take_along_axis(mds, m, 1)
+        mag, g = s * (each * rest + (s * each * rest).sum(1, keepdims=True)), 2 * gamma(d, logits)
+    got = got.double().cpu().numpy()
+    tol = HALF[logits.dtype] * np.abs(want) + g * mag + 1e-37
+    over = np.abs(got - want) / tol
+    assert over.max() <= 1, (float(over.max()), np.unravel_index(over.argmax(), over.shape), got[over >= over.max()],
+                             want[over >= over.max()])
+
+
+def run(d, logits, expert, up):
+    out = torch.full((d["N"], d["E"]), float("nan"), dtype=logits.dtype, device="cuda")
+    tp.tp_moe_route_bwd(d, logits, expert, up, None, 0, out)
+    return out
+
+
+def sampled(d, logits, expert, up):
+    out = run(d, logits, expert, up)
+    N = d["N"]
+    pick = list(range(N)) if N < 100 else list(range(0, N, N // 60))
+    part = lambda x: x[pick].contiguous()  # noqa: E731
+    check({**d, "N": len(pick)}, part(logits), part(expert), part(up), part(out))
+
+
+# few tokens, and as many as share wavefronts; K of one lane's slots and of several lanes'
+SHAPES = [(40, 64, 1), (40, 64, 4), (33, 300, 6), (37, 1000, 32), (4101, 16, 1), (4101, 64, 2), (4101, 100, 16),
+          (7173, 256, 8)]
+
+
+def far_logits(N, E, K, dtype, lo, hi, renorm):
+    g = torch.Generator(device="cuda").manual_seed(N + E)
+    l = (torch.rand(N, E, generator=g, device="cuda") * (hi - lo) + lo).to(dtype)
+    e = l.float().topk(K, dim=1).indices.to(torch.int32)
+    sampled(desc(N, E, K, sigmoid=True, renorm=renorm, dtype=dtype, scale=1.5), l, e,
+            torch.randn(N, K, generator=g, device="cuda"))
+
+
+@pytest.mark.parametrize("N,E,K", SHAPES)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("lo,hi", [(10.0, 60.0), (-60.0, -10.0), (-60.0, 60.0)])
+def test_sigmoid_of_far_logits(N, E, K, dtype, lo, hi):
+    far_logits(N, E, K, dtype, lo, hi, False)
