@@ -161,7 +161,11 @@ def route_bwd(logits, expert, d_weight, sigmoid=False, renorm=False, scale=1.0):
         ds = np.zeros(E)
         for j in on:
             ds[expert[t, j]] += (up[j] - mean) / total if renorm else up[j]
-        out[t] = slope[t] * ds if sigmoid else s[t] * (ds - (ds * s[t]).sum())
+        if sigmoid:
+            out[t] = slope[t] * ds
+        else:  # ds - sum ds s, the largest score's ds taken out of both: nothing cancels where it is nearly 1
+            ds = ds - ds[s[t].argmax()]
+            out[t] = s[t] * (ds - (ds * s[t]).sum())
     return out
 
 

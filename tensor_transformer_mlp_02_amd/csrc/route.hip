@@ -802,8 +802,12 @@ __device__ __forceinline__ float sigmoid_slope(float l) {
 }
 
 // t_j = scale dw_j; renorm: ds_j = (t_j - sum_i t_i s_i / S) / S with
-// S = sum s + 1e-20, else ds_j = t_j; then softmax: dl = s (ds - sum ds s),
-// sigmoid: dl = s (1 - s) ds.  One wavefront a token; slot j is lane j's.
+// S = sum s + 1e-20, else ds_j = t_j; then sigmoid: dl = s (1 - s) ds, softmax:
+// dl = s (ds - sum ds s), formed as s ((ds - c) - sum (ds - c) s) with c the
+// largest score's ds: where that score is nearly 1 its own gradient is what
+// the others leave of it, and its term of the sum is exactly 0.  (c is 0 where
+// that expert is not among the chosen.)
+// One wavefront a token; slot j is lane j's.
 template <typename T, int V, bool SIGMOID>
 __global__ __launch_bounds__(NT) void bwd_kernel(BwdArgs A) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -815,7 +819,7 @@ __global__ __launch_bounds__(NT) void bwd_kernel(BwdArgs A) {
       e = A.expert[t * A.K + lane];
       r = A.slot_row ? (int64_t)A.slot_row[t * A.K + lane] : t * A.K + lane;
     }
-    float l[V], s[V];
+    float l[V], s[V], top = 0.f;
     load_row<T, V>(row, A.E, lane, true, l);
     if (e < 0 || e >= A.E) e = -1;
     float up = 0.f, le = -__builtin_huge_valf();
@@ -831,7 +835,8 @@ __global__ __launch_bounds__(NT) void bwd_kernel(BwdArgs A) {
       for (int i = 0; i < V; ++i) s[i] = l[i] > LOWEST ? sigmoid_slope(l[i]) : 0.f;
       se = le > LOWEST ? sigmoid_of(le) : 0.f;
     } else {
-      float top = l[0], sum = 0.f;
+      float sum = 0.f;
+      top = l[0];
 #pragma unroll
       for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
       top = wave_max(top);
@@ -856,14 +861,25 @@ __global__ __launch_bounds__(NT) void bwd_kernel(BwdArgs A) {
 #pragma unroll
     for (int i = 0; i < V; ++i) ds[i] = 0.f;
     // an expert that stands twice counts twice, in slot order
+    const unsigned long long lead = SIGMOID ? 0 : __ballot(e >= 0 && le == top);
+    const int e_top = lead ? __builtin_amdgcn_readlane(e, __ffsll(lead) - 1) : -1;
+    float c = 0.f;
     for (int j = 0; j < A.K; ++j) {
       const int ej = __builtin_amdgcn_readlane(e, j);
       const float dj = lane_value(d, j);
+      c += ej == e_top ? dj : 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) ds[i] += lane * V + i == ej ? dj : 0.f;
     }
     float dot = 0.f;
-    if constexpr (!SIGMOID) dot = wave_sum(d * se);
+    if constexpr (!SIGMOID) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        ds[i] -= c;
+        dot += ds[i] * s[i];
+      }
+      dot = wave_sum(dot);
+    }
     T* out = reinterpret_cast<T*>(A.dlogits) + t * A.E;
 #pragma unroll
     for (int i = 0; i < V; ++i) ds[i] = SIGMOID ? s[i] * ds[i] : s[i] * (ds[i] - dot);
@@ -903,7 +919,7 @@ __global__ __launch_bounds__(NT) void bwd_rows_kernel(BwdArgs A) {
       e = A.expert[t * A.K + r];
       at = A.slot_row ? (int64_t)A.slot_row[t * A.K + r] : t * A.K + r;
     }
-    float l[V], s[V];
+    float l[V], s[V], top = 0.f;
     load_row<T, V>(row, A.E, r, live, l);
     if (e < 0 || e >= A.E) e = -1;
     float up = 0.f, le = -__builtin_huge_valf();
@@ -928,7 +944,8 @@ __global__ __launch_bounds__(NT) void bwd_rows_kernel(BwdArgs A) {
       for (int i = 0; i < V; ++i) s[i] = l[i] > LOWEST ? sigmoid_slope(l[i]) : 0.f;
       se = le > LOWEST ? sigmoid_of(le) : 0.f;
     } else {
-      float top = l[0], sum = 0.f;
+      float sum = 0.f;
+      top = l[0];
 #pragma unroll
       for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
       top = row_all(top, [](float a, float b) { return fmaxf(a, b); });
@@ -953,12 +970,22 @@ __global__ __launch_bounds__(NT) void bwd_rows_kernel(BwdArgs A) {
     wave_lds_sync();
     if (e >= 0) mine[e] = all;
     wave_lds_sync();
-    float dot = 0.f;
-    if constexpr (!SIGMOID) dot = row_all(d * se, sum_);
     float ds[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) ds[i] = mine[r * V + i];
     wave_lds_sync();
+    float dot = 0.f;
+    if constexpr (!SIGMOID) {
+      const uint32_t lead = (uint32_t)(__ballot(e >= 0 && le == top) >> (lane & 48)) & 0xffffu;
+      const float first = __shfl(all, (lane & 48) + (lead ? __ffs((int)lead) - 1 : 0), 64);
+      const float c = lead ? first : 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        ds[i] -= c;
+        dot += ds[i] * s[i];
+      }
+      dot = row_all(dot, sum_);
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i) ds[i] = SIGMOID ? s[i] * ds[i] : s[i] * (ds[i] - dot);
     if (live) store_row<T, V>(reinterpret_cast<T*>(A.dlogits) + t * A.E, A.E, r, ds);

@@ -91,3 +91,20 @@ def far_logits(N, E, K, dtype, lo, hi, renorm):
 @pytest.mark.parametrize("lo,hi", [(10.0, 60.0), (-60.0, -10.0), (-60.0, 60.0)])
 def test_sigmoid_of_far_logits(N, E, K, dtype, lo, hi):
     far_logits(N, E, K, dtype, lo, hi, False)
+
+
+def one_far_ahead(N, E, K, dtype, renorm):
+    g = torch.Generator(device="cuda").manual_seed(N + E)
+    l = torch.randn(N, E, generator=g, device="cuda")
+    ahead = torch.randint(0, E, (N, 1), generator=g, device="cuda")
+    l.scatter_add_(1, ahead, torch.rand(N, 1, generator=g, device="cuda") * 40)
+    l[::5, ::3] = -INF                                   # (the one ahead may be out as well)
+    l = l.to(dtype)
+    e = l.float().topk(K, dim=1).indices.to(torch.int32)
+    sampled(desc(N, E, K, renorm=renorm, dtype=dtype, scale=1.5), l, e, torch.randn(N, K, generator=g, device="cuda"))
+
+
+@pytest.mark.parametrize("N,E,K", SHAPES)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_softmax_with_one_expert_far_ahead(N, E, K, dtype):
+    one_far_ahead(N, E, K, dtype, False)
