@@ -157,10 +157,13 @@ def route_bwd(logits, expert, d_weight, sigmoid=False, renorm=False, scale=1.0):
         on = [j for j in range(expert.shape[1]) if 0 <= expert[t, j] < E]
         total = sum(s[t, expert[t, j]] for j in on) + 1e-20
         up = {j: scale * float(d_weight[t, j]) for j in on}
-        mean = sum(up[j] * s[t, expert[t, j]] for j in on) / total
+        if renorm and on:  # up_j - sum_i up_i s_i / total, the largest score's up taken out of both
+            k = up[max(on, key=lambda j: s[t, expert[t, j]])]
+            mean = sum((up[j] - k) * s[t, expert[t, j]] for j in on) / total
+            up = {j: ((up[j] - k) - mean + k * (1e-20 / total)) / total for j in on}
         ds = np.zeros(E)
         for j in on:
-            ds[expert[t, j]] += (up[j] - mean) / total if renorm else up[j]
+            ds[expert[t, j]] += up[j]
         if sigmoid:
             out[t] = slope[t] * ds
         else:  # ds - sum ds s, the largest score's ds taken out of both: nothing cancels where it is nearly 1

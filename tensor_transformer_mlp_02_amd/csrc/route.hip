@@ -802,7 +802,10 @@ __device__ __forceinline__ float sigmoid_slope(float l) {
 }
 
 // t_j = scale dw_j; renorm: ds_j = (t_j - sum_i t_i s_i / S) / S with
-// S = sum s + 1e-20, else ds_j = t_j; then sigmoid: dl = s (1 - s) ds, softmax:
+// S = sum s + 1e-20, formed as ((t_j - k) - sum_i (t_i - k) s_i / S + k 1e-20 / S) / S
+// with k the t of the largest of the chosen scores (where it takes almost the
+// whole weight the gradients are small differences); else ds_j = t_j.
+// Then sigmoid: dl = s (1 - s) ds, softmax:
 // dl = s (ds - sum ds s), formed as s ((ds - c) - sum (ds - c) s) with c the
 // largest score's ds: where that score is nearly 1 its own gradient is what
 // the others leave of it, and its term of the sum is exactly 0.  (c is 0 where
@@ -854,7 +857,9 @@ __global__ __launch_bounds__(NT) void bwd_kernel(BwdArgs A) {
     float d = up;
     if (A.renorm) {
       const float S = wave_sum(se) + 1e-20f;
-      d = (up - wave_sum(up * se / S)) / S;
+      const unsigned long long on = __ballot(e >= 0 && se == wave_max(e >= 0 ? se : 0.f));
+      const float k = on ? lane_value(up, __ffsll(on) - 1) : 0.f;
+      d = ((up - k) - wave_sum((up - k) * se / S) + k * (1e-20f / S)) / S;
     }
     if (e < 0) d = 0.f;
     float ds[V];
@@ -963,7 +968,11 @@ __global__ __launch_bounds__(NT) void bwd_rows_kernel(BwdArgs A) {
     float d = up;
     if (A.renorm) {
       const float S = row_all(se, sum_) + 1e-20f;
-      d = (up - row_all(up * se / S, sum_)) / S;
+      const float most = row_all(e >= 0 ? se : 0.f, [](float a, float b) { return fmaxf(a, b); });
+      const uint32_t on = (uint32_t)(__ballot(e >= 0 && se == most) >> (lane & 48)) & 0xffffu;
+      const float first = __shfl(up, (lane & 48) + (on ? __ffs((int)on) - 1 : 0), 64);
+      const float k = on ? first : 0.f;
+      d = ((up - k) - row_all((up - k) * se / S, sum_) + k * (1e-20f / S)) / S;
     }
     if (e < 0) d = 0.f;
     const float all = slot_sum<0>(0.f, e, d, A.K);

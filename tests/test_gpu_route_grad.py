@@ -108,3 +108,29 @@ def one_far_ahead(N, E, K, dtype, renorm):
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_softmax_with_one_expert_far_ahead(N, E, K, dtype):
     one_far_ahead(N, E, K, dtype, False)
+
+
+@pytest.mark.parametrize("N,E,K", SHAPES)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_renormalised_weights_of_far_logits(N, E, K, dtype):
+    one_far_ahead(N, E, K, dtype, True)
+    for lo, hi in ((10.0, 60.0), (-60.0, -10.0), (-60.0, 60.0)):
+        far_logits(N, E, K, dtype, lo, hi, True)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("N", [40, 4101])
+def test_renormalised_weights_with_one_far_ahead(sigmoid, N):
+    """One of the chosen takes almost the whole weight: the gradients of the chosen are small differences."""
+    E, K = 64, 4
+    g = torch.Generator(device="cuda").manual_seed(N)
+    l = torch.randn(N, E, generator=g, device="cuda") - (12.0 if sigmoid else 0.0)
+    l.scatter_add_(1, torch.randint(0, E, (N, 1), generator=g, device="cuda"),
+                   8 + torch.rand(N, 1, generator=g, device="cuda") * 12)
+    e = l.topk(K, dim=1).indices.to(torch.int32)
+    sampled(desc(N, E, K, sigmoid=sigmoid, renorm=True, scale=2.5), l, e, torch.randn(N, K, generator=g, device="cuda"))
+    # a single weight that is always 1 has no gradient, but for the 1e-20 in its sum
+    one = e[:, :1].contiguous()
+    d = desc(N, E, 1, sigmoid=sigmoid, renorm=True)
+    sampled(d, l, one, torch.ones(N, 1, device="cuda"))
+    assert float(run(d, l, one, torch.ones(N, 1, device="cuda")).abs().max()) < 1e-12
