@@ -654,7 +654,9 @@ struct BwdRows {
   static constexpr int AT_ONCE = THREADS / TPR;
 };
 
-template <typename T, bool LAYER, bool BIAS, bool MANY, int TPR, int P>
+// AGAIN: after the row sums the values are unpacked from their pieces again,
+// so that they do not stay in registers meanwhile (see again_pays).
+template <typename T, bool LAYER, bool BIAS, bool MANY, bool AGAIN, int TPR, int P>
 __global__ __launch_bounds__(BwdRows<TPR>::THREADS) void bwd_kernel(NormBwdArgs A) {
   constexpr int V = Piece<T>::V, R = BwdRows<TPR>::AT_ONCE, THREADS = BwdRows<TPR>::THREADS;
   constexpr int SUMS_ROW = LAYER ? 8 : 3;
@@ -833,11 +835,7 @@ __global__ __launch_bounds__(BwdRows<TPR>::THREADS) void bwd_kernel(NormBwdArgs 
         t2 = (v[5] - ry * (m2 * v[7] + m1 * v[6])) * inv_h;
       }
     }
-    // From here the values are unpacked again where the registers do not hold
-    // them unpacked: 8192 x 4096 with biases and a gate a token 177 us so, 280
-    // without; 2048 x 16384 124 and 160.  Elsewhere it costs (381 x 6152 with
-    // biases 29.6 us so, 26.6 without).
-    if constexpr (V == 8 && ((MANY && BIAS) || TPR > CU_THREADS)) {
+    if constexpr (AGAIN) {
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         hold(dy[p]);
@@ -1177,6 +1175,20 @@ static bool two_sums_only(int dtype, int64_t H) {
   return dtype == TP_BF16 && H > norm::CU_THREADS * 2 * norm::Piece<bf16_t>::V;
 }
 
+// Whether the backward unpacks the values of bf16 rows again after the row
+// sums.  The widest rows: 2048 x 16384 124 us so, 160 without.  Eight sums of
+// two pieces a thread (biases, many gate rows): they leave too few registers
+// where a gate row is finished, which costs where its tokens are few.  8192 x
+// 4096, RMS: 168 us so and 233 without at a gate a token, 147 and 163 at two
+// tokens a gate row, 138 and 128 at four, 130 and 111 at eight, 182 and 132 at
+// 27.  Elsewhere it costs (65536 x 512 with biases and a gate a token, one
+// piece a thread, 157 us so, 132 without; 381 x 6152 with biases 29.6 and 26.6).
+constexpr int64_t AGAIN_BELOW = 4;  // tokens of a gate row
+template <typename T, int TPR, int P, bool BIAS, bool MANY>
+constexpr bool again_pays() {
+  return sizeof(T) == 2 && (TPR > norm::CU_THREADS || (BIAS && MANY && P == 2));
+}
+
 // workers of a call, and whether its rows fit the registers
 static int bwd_workers(int64_t N, int64_t G, int64_t pieces, bool* fits) {
   using namespace norm;
@@ -1216,16 +1228,20 @@ hipError_t norm_bwd_launch(int kind, int dtype, NormBwdArgs& a, hipStream_t st) 
         const size_t sums = 2 * (THREADS / 64) * (L ? 8 : 3) * sizeof(float);
         const size_t meet = R == 1 ? 0 : 2 * sizeof(float) * THREADS * P * Piece<T>::V;
         const size_t lds = sums > meet ? sums : meet;
+        auto launch = [&](auto b, auto m, auto again) {
+          hipLaunchKernelGGL((bwd_kernel<T, L, decltype(b)::value, decltype(m)::value, decltype(again)::value, TPR, P>),
+                             dim3(W), dim3(THREADS), lds, st, a);
+        };
+        constexpr std::true_type YES{};
+        constexpr std::false_type NO{};
         if constexpr (sizeof(T) == 4 || TPR <= CU_THREADS) {  // see two_sums_only
-          if (many && !bias)
-            hipLaunchKernelGGL((bwd_kernel<T, L, false, true, TPR, P>), dim3(W), dim3(THREADS), lds, st, a);
-          else if (many)
-            hipLaunchKernelGGL((bwd_kernel<T, L, true, true, TPR, P>), dim3(W), dim3(THREADS), lds, st, a);
-          else if (bias)
-            hipLaunchKernelGGL((bwd_kernel<T, L, true, false, TPR, P>), dim3(W), dim3(THREADS), lds, st, a);
+          constexpr std::bool_constant<again_pays<T, TPR, P, true, true>()> again{};
+          if (many && !bias) launch(NO, YES, NO);
+          else if (many && a.N < AGAIN_BELOW * a.G) launch(YES, YES, again);
+          else if (many) launch(YES, YES, NO);
+          else if (bias) launch(YES, NO, NO);
         }
-        if (!many && !bias)
-          hipLaunchKernelGGL((bwd_kernel<T, L, false, false, TPR, P>), dim3(W), dim3(THREADS), lds, st, a);
+        if (!many && !bias) launch(NO, NO, std::bool_constant<again_pays<T, TPR, P, false, false>()>{});
       });
       he = hipGetLastError();
     } else if (a.N > 0) {
