@@ -775,10 +775,12 @@ __global__ __launch_bounds__(BwdRows<TPR>::THREADS) void bwd_kernel(NormBwdArgs 
     const uint32_t n = row_of(it);
     const bool live = n < N;
     if (MANY && it % per_gate == 0) load_gate(gate_of(it));
-    // the next row's loads on their way, where registers are left for it (eight
-    // sums of two bf16 pieces leave none: 8192 x 4096 with biases and a gate a
-    // token 272 us so, 178 without; 65536 x 512, of one piece, 156 and 180)
-    constexpr bool AHEAD = TPR <= CU_THREADS && !(MANY && BIAS && V * P == 16);
+    // the next row's loads on their way, where registers are left for it.  The
+    // sums of many gate rows leave too few beside two bf16 pieces: 8192 x 4096
+    // with a gate a token 132 us so, 124 without, with biases 252 and 168; 4096 x
+    // 8192 140 and 131, 231 and 176.  (Of one piece, 65536 x 512: 122 us so;
+    // with biases 131 either way.)
+    constexpr bool AHEAD = TPR <= CU_THREADS && !(MANY && V * P == 16);
     uint4 dyn[P], dhn[P], yyn[P], oon[P];
     float stn[4];
     if constexpr (AHEAD) request(it + 1 < turns ? row_of(it + 1) : N, dyn, dhn, yyn, oon, stn);
