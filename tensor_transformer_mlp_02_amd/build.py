@@ -20,6 +20,7 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libtpmlp.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 BUILD_DIR = os.path.join(os.path.dirname(HERE), "_build")
 SOURCES = ["api.hip", "gemm_bf16.hip", "gemm_f32.hip", "partial_sum.hip", "moe.hip", "fp8.hip",
            "block_api.hip", "block_norm.hip", "route.hip", "adamw.hip"]
@@ -50,9 +51,11 @@ def build_marshal(verbose: bool = False) -> str:
     """_marshal.so: the binding's check of a call's tensors, against torch's C++ headers."""
     import importlib.util
     import sysconfig
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
-    out = os.path.join(HERE, "_marshal.so")
-    tmp = out + ".tmp"
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch is not installed")
+    torch_dir = os.path.dirname(spec.origin)
+    tmp = MARSHAL + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
            "-I" + sysconfig.get_path("include"), "-I" + os.path.join(torch_dir, "include"),
            "-I" + os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
@@ -61,8 +64,8 @@ def build_marshal(verbose: bool = False) -> str:
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
-    os.replace(tmp, out)
-    return out
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
 
 
 def build(verbose: bool = False, defines=(), out=None) -> str:
@@ -79,14 +82,18 @@ def build(verbose: bool = False, defines=(), out=None) -> str:
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         marshal = None if defines else ex.submit(build_marshal, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose, build_dir, defines), SOURCES))
-        if marshal:
-            marshal.result()
     tmp = out + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, out)
+    if marshal and marshal.exception() is not None:
+        # nothing in the library needs it, and the binding does without it; an
+        # older one may be for another torch
+        if os.path.exists(MARSHAL):
+            os.remove(MARSHAL)
+        print(f"{MARSHAL} is not built, calls marshal in Python: {marshal.exception()}", file=sys.stderr, flush=True)
     return out
 
 
