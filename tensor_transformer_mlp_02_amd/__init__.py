@@ -197,14 +197,17 @@ _compiled = None
 
 
 def _marshaller():
-    """The compiled part of the binding, False where it is not built (every
-    call then marshals in Python: the same checks, slower)."""
+    """The compiled part of the binding, False where it is not built for this
+    Python and torch (every call then marshals in Python: the same checks,
+    slower)."""
     global _compiled
     if _compiled is None:
         try:
-            c = _get_torch()._C
+            torch = _get_torch()
             from . import _marshal as module
-            module.setup(c._cuda_getDevice, c._cuda_getCurrentRawStream)
+            if torch.__version__.split("+")[0] != module.torch_version:
+                raise ImportError(f"_marshal is for torch {module.torch_version}")
+            module.setup(torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
             _compiled = module
         except (ImportError, AttributeError):
             _compiled = False

@@ -10,17 +10,20 @@ _build_<hash of the options>/libtpmlp.so (or --out); the binding loads such
 a library when TPMLP_LIBRARY names it.
 """
 import argparse
+import glob
 import hashlib
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libtpmlp.so")
-MARSHAL = os.path.join(HERE, "_marshal.so")
+# (the suffix names the Python that it is for)
+MARSHAL = os.path.join(HERE, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 BUILD_DIR = os.path.join(os.path.dirname(HERE), "_build")
 SOURCES = ["api.hip", "gemm_bf16.hip", "gemm_f32.hip", "partial_sum.hip", "moe.hip", "fp8.hip",
            "block_api.hip", "block_norm.hip", "route.hip", "adamw.hip"]
@@ -48,9 +51,8 @@ def _compile(src: str, verbose: bool, build_dir: str, defines) -> str:
 
 
 def build_marshal(verbose: bool = False) -> str:
-    """_marshal.so: the binding's check of a call's tensors, against torch's C++ headers."""
+    """_marshal: the binding's check of a call's tensors, against torch's C++ headers."""
     import importlib.util
-    import sysconfig
     spec = importlib.util.find_spec("torch")
     if spec is None:
         raise RuntimeError("torch is not installed")
@@ -88,11 +90,13 @@ def build(verbose: bool = False, defines=(), out=None) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, out)
+    if marshal:
+        # one that an earlier build left may be for another torch or Python
+        for old in glob.glob(os.path.join(HERE, "_marshal*.so")):
+            if old != MARSHAL or marshal.exception() is not None:
+                os.remove(old)
     if marshal and marshal.exception() is not None:
-        # nothing in the library needs it, and the binding does without it; an
-        # older one may be for another torch
-        if os.path.exists(MARSHAL):
-            os.remove(MARSHAL)
+        # nothing in the library needs it, and the binding does without it
         print(f"{MARSHAL} is not built, calls marshal in Python: {marshal.exception()}", file=sys.stderr, flush=True)
     return out
 

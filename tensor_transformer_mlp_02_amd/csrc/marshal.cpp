@@ -11,10 +11,12 @@
 //       the last, and whose result is an int; stream None: the current one
 //   setup(device, stream): torch's functions for the current device and for
 //       a device's current raw stream
+//   torch_version: the torch whose headers it was built with
 // The first two return None where an item does not pass, call also where no
 // item is a tensor (nothing shows that the GPU is in use): the binding's own
 // loop then does the work, or finds the item and words the error.
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include <cstdint>
 
@@ -200,4 +202,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__marshal(void) {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

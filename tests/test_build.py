@@ -67,3 +67,25 @@ def test_a_library_that_does_not_compile_is_an_error(tree, monkeypatch):
     monkeypatch.setattr(b, "_compile", fails)
     with pytest.raises(RuntimeError, match="hipcc failed"):
         b.build()
+
+
+def test_the_compiled_step_is_for_this_python(tree):
+    import sysconfig
+    path, _, _ = tree
+    (path / "_marshal.so").write_text("of an earlier build")
+    b.build()
+    assert marshals(path) == ["_marshal" + sysconfig.get_config_var("EXT_SUFFIX")]
+
+
+def test_a_compiled_step_for_another_torch_is_not_used(monkeypatch):
+    import types
+    torch = pytest.importorskip("torch")
+    import tensor_transformer_mlp_02_amd as tp
+    ran = []
+    fake = types.SimpleNamespace(torch_version="1.0.0", setup=lambda *a: ran.append(a))
+    monkeypatch.setattr(tp, "_marshal", fake, raising=False)
+    monkeypatch.setattr(tp, "_compiled", None)
+    assert tp._marshaller() is False and not ran
+    fake.torch_version = torch.__version__.split("+")[0]
+    monkeypatch.setattr(tp, "_compiled", None)
+    assert tp._marshaller() is fake and ran
