@@ -85,7 +85,7 @@ def _call(name: str, args: tuple, stream) -> int:
     if stream is not None:
         stream = _stream(stream)
     m = _marshaller()
-    rc = m.call(_entry[name], args, stream) if m else None
+    rc = m.call(name, _entry[name], args, stream) if m else None
     if rc is None:
         rc = getattr(L, name)(*[_sized([a])[0] if isinstance(a, tuple) else a for a in args],
                               _stream(stream))

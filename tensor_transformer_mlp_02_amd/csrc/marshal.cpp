@@ -5,10 +5,10 @@
 // done in one step, on the same items as the binding's own loop: tuples
 // (tensor | int | None, bytes | None, name[, type name]).
 //   addresses(items, device) -> the list of addresses
-//   call(function, args, stream) -> the function's int result; `args` is a
-//       tuple of items and of plain ints / None, `function` the address of an
-//       entry point whose arguments are all pointers or integers, a stream
-//       the last, and whose result is an int; stream None: the current one
+//   call(name, function, args, stream) -> the int result of the entry point
+//       `name` at the address `function`; `args` is a tuple of items and of
+//       plain ints / None, one for each of its arguments but the last, the
+//       stream; stream None: the current one
 //   setup(device, stream): torch's functions for the current device and for
 //       a device's current raw stream
 //   torch_version: the torch whose headers it was built with
@@ -19,6 +19,10 @@
 #include <torch/version.h>
 
 #include <cstdint>
+#include <type_traits>
+#include <utility>
+
+#include "../../include/tpmlp_block.h"
 
 namespace {
 
@@ -98,11 +102,43 @@ PyObject* addresses(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   return out;
 }
 
-// Every argument is a pointer or an integer of at most 64 bits and the C
-// calling convention of x86-64 passes each in a whole register or stack
-// slot, so one function type serves all entry points; slots past a
-// function's own arguments are not looked at.
+// An entry point is called as the function that its header declares: each slot
+// becomes an argument of the declared type, a pointer or an integer.
 constexpr int SLOTS = 24;
+template <typename A>
+A argument(uintptr_t v) {
+  if constexpr (std::is_pointer_v<A>) return reinterpret_cast<A>(v);
+  else return static_cast<A>(v);
+}
+template <typename F> struct Declared;
+template <typename... A>
+struct Declared<int(A...)> {
+  static_assert(sizeof...(A) <= SLOTS);
+  static constexpr int COUNT = sizeof...(A);
+  template <size_t... I>
+  static int spread(int (*f)(A...), const uintptr_t* v, std::index_sequence<I...>) {
+    return f(argument<A>(v[I])...);
+  }
+  static int call(uintptr_t f, const uintptr_t* v) {
+    return spread(reinterpret_cast<int (*)(A...)>(f), v, std::index_sequence_for<A...>{});
+  }
+};
+struct Entry {
+  const char* name;
+  int count;  // arguments
+  int (*call)(uintptr_t function, const uintptr_t* slots);
+};
+#define ENTRY(f) {#f, Declared<decltype(f)>::COUNT, &Declared<decltype(f)>::call}
+constexpr Entry entries[] = {ENTRY(tp_block_norm_fwd), ENTRY(tp_block_norm_bwd), ENTRY(tp_moe_route_fwd),
+                             ENTRY(tp_moe_route_bwd), ENTRY(tp_moe_route_tables), ENTRY(tp_adamw_step)};
+#undef ENTRY
+const Entry* entry_of(PyObject* name) {
+  if (PyUnicode_Check(name))
+    for (const Entry& e : entries)
+      if (PyUnicode_CompareWithASCIIString(name, e.name) == 0) return &e;
+  return nullptr;
+}
+
 PyObject* current_device = nullptr;
 PyObject* current_stream = nullptr;
 
@@ -120,20 +156,20 @@ PyObject* setup(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   Py_RETURN_NONE;
 }
 
-typedef int (*Entry)(uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t,
-                     uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t,
-                     uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t,
-                     uintptr_t, uintptr_t, uintptr_t);
-
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
-  if (nargs != 3 || !PyTuple_Check(args[1]) || PyTuple_GET_SIZE(args[1]) >= SLOTS || !current_device) {
-    PyErr_SetString(PyExc_TypeError, "call(function, tuple of at most 23, stream), after setup()");
+  if (nargs != 4 || !PyTuple_Check(args[2]) || !current_device) {
+    PyErr_SetString(PyExc_TypeError, "call(name, function, tuple, stream), after setup()");
     return nullptr;
   }
-  const uintptr_t fn = (uintptr_t)PyLong_AsUnsignedLongLong(args[0]);
+  const Entry* entry = entry_of(args[0]);
+  if (!entry) return PyErr_Format(PyExc_TypeError, "%R is no entry point", args[0]);
+  const uintptr_t fn = (uintptr_t)PyLong_AsUnsignedLongLong(args[1]);
   if (PyErr_Occurred()) return nullptr;
-  PyObject* list = args[1];
+  PyObject* list = args[2];
   const Py_ssize_t n = PyTuple_GET_SIZE(list);
+  if (n + 1 != entry->count)
+    return PyErr_Format(PyExc_TypeError, "%s takes %d arguments before the stream, got %zd", entry->name,
+                        entry->count - 1, n);
   long device = -1;
   PyObject* device_object = nullptr;
   uintptr_t v[SLOTS] = {0};
@@ -159,19 +195,17 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     if (!address_of(it, device, v[i])) return refused();
   }
   if (!device_object) return refused();
-  if (args[2] == Py_None) {
+  if (args[3] == Py_None) {
     Owned s{PyObject_CallOneArg(current_stream, device_object)};
     if (!s.p) return refused();
     v[n] = (uintptr_t)PyLong_AsUnsignedLongLong(s.p);
   } else {
-    v[n] = (uintptr_t)PyLong_AsUnsignedLongLong(args[2]);
+    v[n] = (uintptr_t)PyLong_AsUnsignedLongLong(args[3]);
   }
   if (PyErr_Occurred()) return refused();
   int rc;
   Py_BEGIN_ALLOW_THREADS  // a full queue makes a launch wait
-  rc = reinterpret_cast<Entry>(fn)(
-      v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], v[8], v[9], v[10], v[11], v[12], v[13], v[14],
-      v[15], v[16], v[17], v[18], v[19], v[20], v[21], v[22], v[23]);
+  rc = entry->call(fn, v);
   Py_END_ALLOW_THREADS
   return PyLong_FromLong(rc);
 }
@@ -194,7 +228,7 @@ PyCFunction method() {
 
 PyMethodDef methods[] = {
     {"addresses", method<addresses>(), METH_FASTCALL, "addresses(items, device)"},
-    {"call", method<call>(), METH_FASTCALL, "call(function, args, stream)"},
+    {"call", method<call>(), METH_FASTCALL, "call(name, function, args, stream)"},
     {"setup", method<setup>(), METH_FASTCALL, "setup(device function, stream function)"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,
