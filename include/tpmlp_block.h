@@ -61,7 +61,8 @@ typedef enum tp_norm_kind { TP_NORM_RMS = 0, TP_NORM_LAYER = 1 } tp_norm_kind;
 
 /* N tokens (0 .. 2^30), width H (a positive multiple of 8 for bf16, 4 for
  * fp32, at most 2^21), gate_rows 0 .. 2^30, kind a tp_norm_kind, dtype a
- * tp_dtype (activations, weights and gate alike), eps > 0, finite scales. */
+ * tp_dtype (activations, weights and gate alike), eps > 0, eps and scales
+ * finite. */
 typedef struct tp_norm_desc {
     int64_t N, H, gate_rows;
     int32_t kind, dtype;
@@ -124,7 +125,10 @@ int tp_block_norm_bwd(const tp_norm_desc *desc, const void *dY, const void *dHn,
  *   weight_j = scale s_j / (sum_i s_i + 1e-20)  (renorm 1, over the chosen)
  * The bias steers the choice alone (load balance); it is not in the
  * weights.  Equal values go to the lower expert (run).  Choices are decided
- * as by arithmetic in 64 bits; weights are fp32.
+ * as by arithmetic in 64 bits, for any finite bias; weights are fp32, from
+ * scores off by about 2^-22 relative and by 2^-23 more for each unit of
+ * l_max - l (softmax) or |l| (sigmoid): the exponent's rounding.  The gradient
+ * has scores of its own, without that growth for a sigmoid.
  * A logit that is NaN, -inf, or at most the lowest finite bf16 (-3.3895e38)
  * takes its expert out of the row: score 0, never chosen.  +inf counts as
  * the largest finite fp32.  Slots left over hold expert -1, weight 0.
@@ -232,7 +236,7 @@ int tp_moe_route_tables(int64_t N, int32_t K, int32_t first_expert, int32_t n_lo
 #define TP_ADAMW_BLOCK 256
 #define TP_ADAMW_MAX_TENSORS 65536
 typedef struct tp_adamw_desc {
-    double lr, beta1, beta2, eps; /* lr finite, 0 <= beta < 1, eps > 0 */
+    double lr, beta1, beta2, eps; /* lr finite in fp32, 0 <= beta < 1, 1e-30 <= eps <= 1e30 */
     int32_t step;                 /* >= 1 (unused with dev_step)       */
     int32_t grad_dtype;           /* a tp_dtype                        */
     int32_t state_bits;           /* 32 or 8                           */

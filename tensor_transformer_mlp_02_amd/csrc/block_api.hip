@@ -322,7 +322,7 @@ int tp_adamw_step(const tp_adamw_desc* desc, int32_t n, const tp_adamw_tensor* t
     return fail(TP_ERR_DTYPE, "unknown grad_dtype %d", d.grad_dtype);
   if (d.state_bits != 32 && d.state_bits != 8)
     return fail(TP_ERR_DTYPE, "state_bits must be 32 or 8");
-  if (!isfinite(d.lr)) return fail(TP_ERR_SHAPE, "lr must be finite");
+  if (!isfinite((float)d.lr)) return fail(TP_ERR_SHAPE, "lr must be finite in fp32");
   if (!(d.beta1 >= 0.0 && d.beta1 < 1.0) || !(d.beta2 >= 0.0 && d.beta2 < 1.0))
     return fail(TP_ERR_SHAPE, "beta1 and beta2 must be in [0, 1)");
   // eps keeps its meaning in fp32
