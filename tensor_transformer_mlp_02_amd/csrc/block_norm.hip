@@ -673,7 +673,8 @@ __global__ __launch_bounds__(BwdRows<TPR>::THREADS) void bwd_kernel(NormBwdArgs 
   uint4 w_post[P], w_pre[P], gate[P];
   uint4 dy[P], dh[P], yy[P], oo[P];
   // 16 wavefronts leave 128 registers a lane: there the two sums that every
-  // call may ask for are kept in shared memory, each thread's own
+  // call may ask for are kept in shared memory, each thread's own.  (bf16 rows
+  // still spill 18 registers with a LayerNorm and 27 with an RMS norm.)
   constexpr bool KEPT = TPR > CU_THREADS && !MANY && !BIAS;
   __shared__ float kept[KEPT ? 2 * P * V * THREADS : 1];
   float a_wpre[KEPT ? 1 : P][V], a_1[KEPT ? 1 : P][V], a_bpre[BIAS ? P : 1][V], a_0[BIAS ? P : 1][V];
@@ -1171,8 +1172,10 @@ hipError_t norm_fwd_launch(int kind, int dtype, const NormFwdArgs& a, hipStream_
 
 // 16 wavefronts a workgroup leave too few registers for bf16 rows with more
 // sums than two: those take the wide kernels (2048 x 16384: with biases 221 us
-// so, 502 with registers spilled; with a gate a token 326, 342; with both 319,
-// 762; fp32 rows do fit: 2048 x 8192 with both 213 us, 269 in the wide kernels)
+// so, 502 with registers spilled; with a gate a token 321, 342; with both 316,
+// 762).  fp32 rows hold half the values; with biases or many gate rows they
+// spill 11 to 66 registers and are faster all the same (2048 x 8192 with both
+// 215 us, 269 in the wide kernels).
 static bool two_sums_only(int dtype, int64_t H) {
   return dtype == TP_BF16 && H > norm::CU_THREADS * 2 * norm::Piece<bf16_t>::V;
 }

@@ -801,16 +801,15 @@ __device__ __forceinline__ float sigmoid_slope(float l) {
   return e / (d * d);
 }
 
-// t_j = scale dw_j; renorm: ds_j = (t_j - sum_i t_i s_i / S) / S with
-// S = sum s + 1e-20, formed as ((t_j - k) - sum_i (t_i - k) s_i / S + k 1e-20 / S) / S
-// with k the t of the largest of the chosen scores (where it takes almost the
-// whole weight the gradients are small differences); else ds_j = t_j.
-// Then sigmoid: dl = s (1 - s) ds, softmax:
-// dl = s (ds - sum ds s), formed as s ((ds - c) - sum (ds - c) s) with c the
-// largest score's ds: where that score is nearly 1 its own gradient is what
-// the others leave of it, and its term of the sum is exactly 0.  (c is 0 where
-// that expert is not among the chosen.)
-// One wavefront a token; slot j is lane j's.
+// t_j = scale dw_j; renorm: ds_j = (t_j - sum_i t_i w_i) / S with w = s / S and
+// S = sum s + 1e-20, else ds_j = t_j; then sigmoid: dl = s (1 - s) ds, softmax:
+// dl = s (ds - sum ds s).  Where one weight or score h is far above a half, its
+// own difference is what the others leave of it, and is formed from them:
+//   ds_h = (t_h (sum_{i not h} s_i + 1e-20) / S - sum_{i not h} t_i w_i) / S
+//   dl_h = s_h (ds_h sum_{i not h} s_i - sum_{i not h} ds_i s_i)
+// (a wavefront without such a token passes that by).  One wavefront a token;
+// slot j is lane j's.
+constexpr float ALMOST = 0.6f;  // only one can be above; below, 1 - s keeps its bits
 template <typename T, int V, bool SIGMOID>
 __global__ __launch_bounds__(NT) void bwd_kernel(BwdArgs A) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -822,7 +821,7 @@ __global__ __launch_bounds__(NT) void bwd_kernel(BwdArgs A) {
       e = A.expert[t * A.K + lane];
       r = A.slot_row ? (int64_t)A.slot_row[t * A.K + lane] : t * A.K + lane;
     }
-    float l[V], s[V], top = 0.f;
+    float l[V], s[V], inv = 0.f;  // inv: a softmax's largest score
     load_row<T, V>(row, A.E, lane, true, l);
     if (e < 0 || e >= A.E) e = -1;
     float up = 0.f, le = -__builtin_huge_valf();
@@ -838,8 +837,7 @@ __global__ __launch_bounds__(NT) void bwd_kernel(BwdArgs A) {
       for (int i = 0; i < V; ++i) s[i] = l[i] > LOWEST ? sigmoid_slope(l[i]) : 0.f;
       se = le > LOWEST ? sigmoid_of(le) : 0.f;
     } else {
-      float sum = 0.f;
-      top = l[0];
+      float top = l[0], sum = 0.f;
 #pragma unroll
       for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
       top = wave_max(top);
@@ -849,45 +847,51 @@ __global__ __launch_bounds__(NT) void bwd_kernel(BwdArgs A) {
         sum += s[i];
       }
       sum = wave_sum(sum);
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) s[i] *= inv;
       se = le > LOWEST ? expf(le - top) * inv : 0.f;
     }
     float d = up;
     if (A.renorm) {
-      const float S = wave_sum(se) + 1e-20f;
-      const unsigned long long on = __ballot(e >= 0 && se == wave_max(e >= 0 ? se : 0.f));
-      const float k = on ? lane_value(up, __ffsll(on) - 1) : 0.f;
-      d = ((up - k) - wave_sum((up - k) * se / S) + k * (1e-20f / S)) / S;
+      const float S = wave_sum(se) + 1e-20f, w = se / S;
+      d = up - wave_sum(up * w);
+      if (__ballot(w > ALMOST)) {
+        const float left = wave_sum(w > ALMOST ? 0.f : se) + 1e-20f;
+        const float others = wave_sum(w > ALMOST ? 0.f : up * w);
+        if (w > ALMOST) d = up * (left / S) - others;
+      }
+      d /= S;
     }
     if (e < 0) d = 0.f;
     float ds[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) ds[i] = 0.f;
     // an expert that stands twice counts twice, in slot order
-    const unsigned long long lead = SIGMOID ? 0 : __ballot(e >= 0 && le == top);
-    const int e_top = lead ? __builtin_amdgcn_readlane(e, __ffsll(lead) - 1) : -1;
-    float c = 0.f;
     for (int j = 0; j < A.K; ++j) {
       const int ej = __builtin_amdgcn_readlane(e, j);
       const float dj = lane_value(d, j);
-      c += ej == e_top ? dj : 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) ds[i] += lane * V + i == ej ? dj : 0.f;
     }
-    float dot = 0.f;
     if constexpr (!SIGMOID) {
+      const float dot = wave_sum(d * se);
+      if (__ballot(inv > ALMOST)) {
+        float rest = 0.f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        ds[i] -= c;
-        dot += ds[i] * s[i];
+        for (int i = 0; i < V; ++i) rest += s[i] > ALMOST ? 0.f : s[i];
+        rest = wave_sum(rest);
+        const float others = wave_sum(se > ALMOST ? 0.f : d * se);
+#pragma unroll
+        for (int i = 0; i < V; ++i) ds[i] = s[i] > ALMOST ? ds[i] * rest - others : ds[i] - dot;
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) ds[i] -= dot;
       }
-      dot = wave_sum(dot);
     }
     T* out = reinterpret_cast<T*>(A.dlogits) + t * A.E;
 #pragma unroll
-    for (int i = 0; i < V; ++i) ds[i] = SIGMOID ? s[i] * ds[i] : s[i] * (ds[i] - dot);
+    for (int i = 0; i < V; ++i) ds[i] *= s[i];
     store_row<T, V>(out, A.E, lane, ds);
   }
 }
@@ -924,7 +928,7 @@ __global__ __launch_bounds__(NT) void bwd_rows_kernel(BwdArgs A) {
       e = A.expert[t * A.K + r];
       at = A.slot_row ? (int64_t)A.slot_row[t * A.K + r] : t * A.K + r;
     }
-    float l[V], s[V], top = 0.f;
+    float l[V], s[V], inv = 0.f;
     load_row<T, V>(row, A.E, r, live, l);
     if (e < 0 || e >= A.E) e = -1;
     float up = 0.f, le = -__builtin_huge_valf();
@@ -949,8 +953,7 @@ __global__ __launch_bounds__(NT) void bwd_rows_kernel(BwdArgs A) {
       for (int i = 0; i < V; ++i) s[i] = l[i] > LOWEST ? sigmoid_slope(l[i]) : 0.f;
       se = le > LOWEST ? sigmoid_of(le) : 0.f;
     } else {
-      float sum = 0.f;
-      top = l[0];
+      float top = l[0], sum = 0.f;
 #pragma unroll
       for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
       top = row_all(top, [](float a, float b) { return fmaxf(a, b); });
@@ -960,19 +963,21 @@ __global__ __launch_bounds__(NT) void bwd_rows_kernel(BwdArgs A) {
         sum += s[i];
       }
       sum = row_all(sum, sum_);
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) s[i] *= inv;
       se = le > LOWEST ? expf(le - top) * inv : 0.f;
     }
     float d = up;
     if (A.renorm) {
-      const float S = row_all(se, sum_) + 1e-20f;
-      const float most = row_all(e >= 0 ? se : 0.f, [](float a, float b) { return fmaxf(a, b); });
-      const uint32_t on = (uint32_t)(__ballot(e >= 0 && se == most) >> (lane & 48)) & 0xffffu;
-      const float first = __shfl(up, (lane & 48) + (on ? __ffs((int)on) - 1 : 0), 64);
-      const float k = on ? first : 0.f;
-      d = ((up - k) - row_all((up - k) * se / S, sum_) + k * (1e-20f / S)) / S;
+      const float S = row_all(se, sum_) + 1e-20f, w = se / S;
+      d = up - row_all(up * w, sum_);
+      if (__ballot(w > ALMOST)) {
+        const float left = row_all(w > ALMOST ? 0.f : se, sum_) + 1e-20f;
+        const float others = row_all(w > ALMOST ? 0.f : up * w, sum_);
+        if (w > ALMOST) d = up * (left / S) - others;
+      }
+      d /= S;
     }
     if (e < 0) d = 0.f;
     const float all = slot_sum<0>(0.f, e, d, A.K);
@@ -983,20 +988,23 @@ __global__ __launch_bounds__(NT) void bwd_rows_kernel(BwdArgs A) {
 #pragma unroll
     for (int i = 0; i < V; ++i) ds[i] = mine[r * V + i];
     wave_lds_sync();
-    float dot = 0.f;
     if constexpr (!SIGMOID) {
-      const uint32_t lead = (uint32_t)(__ballot(e >= 0 && le == top) >> (lane & 48)) & 0xffffu;
-      const float first = __shfl(all, (lane & 48) + (lead ? __ffs((int)lead) - 1 : 0), 64);
-      const float c = lead ? first : 0.f;
+      const float dot = row_all(d * se, sum_);
+      if (__ballot(inv > ALMOST)) {
+        float rest = 0.f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        ds[i] -= c;
-        dot += ds[i] * s[i];
+        for (int i = 0; i < V; ++i) rest += s[i] > ALMOST ? 0.f : s[i];
+        rest = row_all(rest, sum_);
+        const float others = row_all(se > ALMOST ? 0.f : d * se, sum_);
+#pragma unroll
+        for (int i = 0; i < V; ++i) ds[i] = s[i] > ALMOST ? ds[i] * rest - others : ds[i] - dot;
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) ds[i] -= dot;
       }
-      dot = row_all(dot, sum_);
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) ds[i] = SIGMOID ? s[i] * ds[i] : s[i] * (ds[i] - dot);
+    for (int i = 0; i < V; ++i) ds[i] *= s[i];
     if (live) store_row<T, V>(reinterpret_cast<T*>(A.dlogits) + t * A.E, A.E, r, ds);
   }
 }

@@ -5,11 +5,11 @@ With u = 2^-24 and every operation rounded once:
   sigmoid   s (1 - s) = e / (1 + e)^2, e = exp(-|l|): e off by 4 u, the quotient by 10 u with the gradient's own two
             products; a renormalised gradient adds the K scores of its sum and their quotients.  64 u + 4 K u, of
             s (1 - s) times the terms of ds.
-  softmax   dl_e = s_e ((ds_e - c) - sum_i s_i (ds_i - c)), c the ds of the largest score m: its term is exactly 0.
-            The terms are s_e (|ds_e| + |c|) (e other than m) and s_e s_i (|ds_i| + |c|) (i other than m), each off
-            by gamma() of test_gpu_route.py: the exponentials' rounded arguments and the sums of E terms.
-  renormalised  ds_j = ((t_j - k) - sum_i w_i (t_i - k) + k 1e-20 / S) / S, k the t of the largest of the chosen,
-            in the same way."""
+  softmax   dl_e = s_e sum_i s_i (ds_e - ds_i).  With c the ds of the largest score m the terms are at most
+            s_e (|ds_e| + |c|) (e other than m) and s_e s_i (|ds_i| + |c|) (i other than m), each off by gamma()
+            of test_gpu_route.py: the exponentials' rounded arguments and the sums of E terms.
+  renormalised  ds_j = (sum_i w_i (t_j - t_i) + t_j 1e-20 / S) / S, in the same way with the largest of the
+            chosen."""
 import numpy as np
 import pytest
 
@@ -108,6 +108,24 @@ def one_far_ahead(N, E, K, dtype, renorm):
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_softmax_with_one_expert_far_ahead(N, E, K, dtype):
     one_far_ahead(N, E, K, dtype, False)
+
+
+@pytest.mark.parametrize("N,E", [(40, 64), (40, 1000), (4101, 128), (7173, 256)])
+@pytest.mark.parametrize("K", [1, 4])
+def test_softmax_of_nearly_equal_logits(N, E, K):
+    """Scores of about 1 / E: the experts that are not chosen get s_e sum_i ds_i s_i, far smaller than any ds.
+    Scores: e^x 4 u, a sum of at most 16 terms a lane over 64 lanes 22 u, quotient and product 2 u; twice in the
+    result (56 u), with the sum over K slots and the products 10 u more: 80 u of s_e (|ds_e| + sum_i |ds_i| s_i)."""
+    g = torch.Generator(device="cuda").manual_seed(N + E + K)
+    l = torch.randn(N, E, generator=g, device="cuda") * 0.01
+    e = l.topk(K, dim=1).indices.to(torch.int32)
+    up = torch.randn(N, K, generator=g, device="cuda")
+    got = run(desc(N, E, K, scale=1.5), l, e, up).double()
+    s = torch.softmax(l.double(), 1)
+    ds = torch.zeros_like(s).scatter_(1, e.long(), up.double() * 1.5)
+    want = s * (ds - (ds * s).sum(1, keepdim=True))
+    over = (got - want).abs() / (80 * U * s * (ds.abs() + (ds.abs() * s).sum(1, keepdim=True)))
+    assert float(over.max()) <= 1, float(over.max())
 
 
 @pytest.mark.parametrize("N,E,K", SHAPES)
