@@ -896,8 +896,8 @@ __global__ __launch_bounds__(NT) void bwd_kernel(BwdArgs A) {
   }
 }
 
-// Many tokens: four to a wavefront, as fwd_rows_kernel: 16384 x 64 fp32 4.4 us
-// (6.3 with one), 8191 x 256 bf16 top 8 5.8 (7.7).  The slots' gradients
+// Many tokens: four to a wavefront, as fwd_rows_kernel: 16384 x 64 fp32 4.0 us
+// (6.1 with one), 8192 x 256 bf16 top 8 5.8 (7.4).  The slots' gradients
 // meet the experts through shared memory: every slot of an expert writes the
 // same sum over the expert's slots, taken in slot order.  K <= 16.
 template <int J>
@@ -1388,8 +1388,13 @@ hipError_t route_bwd_launch(const tp_route_desc& d, const void* logits, const in
   using namespace route;
   if (d.N == 0) return hipSuccess;
   BwdArgs a{logits, expert, d_weight, slot_row, dlogits, d.N, R, d.E, d.K, d.renorm, d.scale};
-  // fp32, 256 experts: 8192 tokens 8.1 us so, 7.5 with a wavefront each
-  if (d.N >= rows_from(d.E) && d.E <= 256 && d.K <= 16 && (d.E <= 128 || d.dtype == TP_BF16)) {
+  // Where the experts are no whole lanes, single loads and stores cost more than
+  // shared wavefronts give, but for few bf16 experts.  8192 tokens, bf16: of 256
+  // 5.8 us so and 7.4 with a wavefront each, of 200 10.9 and 7.3, of 136 8.7 and
+  // 6.8, of 100 5.2 and 5.8; fp32: of 256 7.6 and 7.8, of 200 14.6 and 7.6, of
+  // 144 5.9 and 7.0, of 100 6.7 and 5.9.
+  const bool whole = d.E % rows_experts(d.E) == 0;
+  if (d.N >= rows_from(d.E) && d.E <= 256 && d.K <= 16 && (whole || (d.E <= 128 && d.dtype == TP_BF16))) {
     const int64_t groups = (d.N + 4 * WAVES - 1) / (4 * WAVES);
     const dim3 grid((unsigned)(groups > 2 * ROWS_GRID ? 2 * ROWS_GRID : groups));
     pick_rows(d.dtype, rows_experts(d.E), d.score, [&](auto t, auto v, auto sig) {
