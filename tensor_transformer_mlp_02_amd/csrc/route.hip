@@ -383,6 +383,13 @@ __device__ __forceinline__ int settle(const FwdArgs& A, const T* row, int e, int
   return __builtin_amdgcn_ds_permute(to * 4, e);
 }
 
+// How far a group's worth may be off: a score, or half of two, by a quarter of
+// the slack, and by 2^-24 of its terms' magnitude for the rounding of the terms
+// c and as much for that of their sum; all that twice to be on the safe side.
+__device__ __forceinline__ float worth_slack(float slack, float terms) {
+  return 0.5f * slack + 0x1p-22f * terms;
+}
+
 // One wavefront a token.  Choices are to be those of 64-bit arithmetic, made
 // in 32 bits: without a bias the experts' order is the logits' own, exact.
 // With one, the order of the first k + 1 keys is right if neighbours differ
@@ -397,13 +404,6 @@ __device__ __forceinline__ int settle(const FwdArgs& A, const T* row, int e, int
 // 5.2 us with the launch); many are bound by instruction issue: the k maxima
 // take about 25 vector instructions each at V = 4, the scores 15 for each of
 // a lane's experts.
-// How far a group's worth may be off: a score, or half of two, by a quarter of
-// the slack, and by 2^-24 of its terms' magnitude for the rounding of the terms
-// c and as much for that of their sum; all that twice to be on the safe side.
-__device__ __forceinline__ float worth_slack(float slack, float terms) {
-  return 0.5f * slack + 0x1p-22f * terms;
-}
-
 template <typename T, int V, bool SIGMOID>
 __global__ __launch_bounds__(NT) void fwd_kernel(FwdArgs A) {
   extern __shared__ double sh[];
