@@ -558,3 +558,8 @@ from .block import *  # noqa: E402,F401,F403  (the operators around the products
 from .block import __all__ as _block_all  # noqa: E402
 
 __all__ += _block_all
+
+from .fp8g import *  # noqa: E402,F401,F403  (FP8 with group scales)
+from .fp8g import __all__ as _fp8g_all  # noqa: E402
+
+__all__ += _fp8g_all

@@ -26,7 +26,8 @@ OUT = os.path.join(HERE, "libtpmlp.so")
 MARSHAL = os.path.join(HERE, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 BUILD_DIR = os.path.join(os.path.dirname(HERE), "_build")
 SOURCES = ["api.hip", "gemm_bf16.hip", "gemm_f32.hip", "partial_sum.hip", "moe.hip", "fp8.hip",
-           "block_api.hip", "block_norm.hip", "route.hip", "adamw.hip"]
+           "block_api.hip", "block_norm.hip", "route.hip", "adamw.hip", "fp8g_api.hip", "fp8g_quant.hip",
+           "fp8g_gemm.hip", "fp8g_gemm32.hip", "fp8g_glu.hip", "fp8g_few.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1,0 +1,145 @@
+// FP8 with group scales: what its kernels share, and their launchers.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "../../include/tpmlp_fp8g.h"
+#include "common.h"
+
+namespace tpmlp {
+
+constexpr int kGroup = TP_FP8G_GROUP;
+constexpr int64_t groups_of(int64_t n) { return (n + kGroup - 1) / kGroup; }
+constexpr int64_t padded(int64_t n) { return groups_of(n) * kGroup; }
+
+struct G8QuantArgs {
+  const void* x;        // [rows, ldx]; part p at column p * cols
+  uint8_t *q, *q_t;     // either may be NULL
+  void *s, *s_t;
+  int64_t rows, cols, ldx;
+  int parts;            // q has parts * padded(cols) columns, q_t and s_t one block a part
+};
+
+// A product's operands, or a gated block's (pair: B, B2 are the gate and the up
+// projection at the same k; otherwise B2 is part 1 of the k range).
+struct G8GemmArgs {
+  const uint8_t *A, *B, *B2;
+  const void *sA, *sB, *sB2;
+  int64_t M, lda;       // lda: bytes of a row of A
+  int N, K, parts;      // K: of one part, a multiple of 128; N: rows of B (F for the gated block)
+  int tiles_m, tiles_n;
+  void* C;              // EPI 0: [M,N]
+  int out_bf16, accumulate;
+  // gated block
+  void *Z, *H;          // Z [M,2N] bf16 (in for the backward), H [M,N] bf16
+  uint8_t *q, *q_t;
+  void *s, *s_t;
+  float* raw;           // few tokens: H [M,N], or [dG|dU] [M,2N], fp32
+  int gate;
+};
+
+hipError_t g8_quant_launch(int dtype, int fmt, int scale, int square, const G8QuantArgs& a, hipStream_t st);
+hipError_t g8_gemm_bf16_launch(int fmt_a, int fmt_b, int scale, int square, G8GemmArgs& a, hipStream_t st);
+hipError_t g8_gemm_f32_launch(int fmt_a, int fmt_b, int scale, int square, G8GemmArgs& a, hipStream_t st);
+hipError_t g8_glu_fwd_launch(int scale, G8GemmArgs& a, hipStream_t st);
+hipError_t g8_glu_bwd_launch(int fmt, int scale, G8GemmArgs& a, hipStream_t st);
+
+// The few-token kernels: which calls they take, and the calls
+bool g8_few(int64_t M);
+hipError_t g8_gemm_few_launch(int fmt_a, int fmt_b, int scale, int square, const G8GemmArgs& a, hipStream_t st);
+hipError_t g8_glu_fwd_few_launch(int scale, const G8GemmArgs& a, hipStream_t st);
+hipError_t g8_glu_bwd_few_launch(int fmt, int scale, const G8GemmArgs& a, hipStream_t st);
+
+namespace g8 {
+
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
+// Magnitudes are compared as bit patterns: those of non-negative floats
+// order like the floats, infinity and then every NaN above all of them.
+__device__ __forceinline__ uint32_t mag(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// A group's scale from its largest magnitude: what its values are multiplied
+// by (0: its codes are zeros) and what is stored.
+template <int FMT, int SC>
+struct GroupScale {
+  float inv;
+  uint32_t bits;  // of the fp32 scale, or the E8M0 byte
+  __device__ __forceinline__ explicit GroupScale(uint32_t top) {
+    constexpr float FMAX = FMT == 0 ? 448.0f : 57344.0f;  // 1.75 * 2^(8 or 15)
+    constexpr int EMAX = FMT == 0 ? 8 : 15;
+    const bool some = top > 0x0d800000u;  // 2^-100
+    const bool bad = top >= 0x7f800000u;
+    if constexpr (SC == TP_GROUP_F32) {
+      const float a = some && !bad ? __uint_as_float(top) : FMAX;
+      inv = some && !bad ? FMAX / a : 0.0f;
+      bits = bad ? 0x7fc00000u : __float_as_uint(a / FMAX);
+    } else {
+      const uint32_t e = (top >> 23) - EMAX + ((top & 0x7fffffu) > 0x600000u ? 1u : 0u);
+      inv = some && !bad ? __uint_as_float((254u - e) << 23) : 0.0f;
+      bits = bad ? 255u : some ? e : 127u;
+    }
+  }
+  __device__ __forceinline__ void store(void* s, int64_t i) const {
+    if constexpr (SC == TP_GROUP_F32) reinterpret_cast<uint32_t*>(s)[i] = bits;
+    else reinterpret_cast<uint8_t*>(s)[i] = (uint8_t)bits;
+  }
+};
+
+// Codes of four values; zeros where the group has no scale (a NaN times 0 is
+// no zero).
+template <int FMT>
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float inv) {
+  return inv > 0.0f ? fp8x4<FMT>(a, b, c, d, inv) : 0u;
+}
+
+__device__ __forceinline__ uint32_t xor_max(uint32_t v, int d) {
+  return max(v, (uint32_t)__shfl_xor((int)v, d, 64));
+}
+
+// Codes as bf16, which holds each of them exactly: the matrix cores add bf16
+// products in fp32, where FP8 products lose what lies 13 bits below the largest of 8 (a
+// product of 3584 codes then is off by 2e-5 of its size, by 1e-7 with
+// these).  `scale`: its exponent goes into the values (a power of two is
+// exact; NaN gives NaN).
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8g_t __attribute__((ext_vector_type(8)));
+template <int FMT>
+__device__ __forceinline__ bf16x8g_t widen(int lo, int hi, float scale) {
+  bf16x2_t v[4];
+  if constexpr (FMT == 0) {
+    v[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)lo, scale, false);
+    v[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)lo, scale, true);
+    v[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, scale, false);
+    v[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, scale, true);
+  } else {
+    v[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)lo, scale, false);
+    v[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)lo, scale, true);
+    v[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)hi, scale, false);
+    v[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)hi, scale, true);
+  }
+  return __builtin_bit_cast(bf16x8g_t, v);
+}
+// an E8M0 byte as the fp32 whose exponent it is (255: infinity, NaN above)
+__device__ __forceinline__ float e8m0_f32(uint32_t e) { return __uint_as_float(e << 23); }
+
+// The gate's activation, and its derivative beside it
+__device__ __forceinline__ float gate_act(int gate, float g) {
+  return gate == TP_GATE_SILU ? silu_f(g) : gelu_f(g);
+}
+__device__ __forceinline__ void gate_both(int gate, float g, float& act, float& slope) {
+  if (gate == TP_GATE_SILU) {
+    const float s = sigmoid_f(g);
+    act = g * s;
+    slope = s * (1.0f + g * (1.0f - s));
+  } else {
+    act = gelu_f(g);
+    slope = gelu_grad_f(g);
+  }
+}
+
+}  // namespace g8
+}  // namespace tpmlp

@@ -1,0 +1,486 @@
+// Products of 8-bit codes with group scales on the matrix cores (the
+// formulas: include/tpmlp_fp8g.h).  MFMA-bound.
+//
+// A workgroup makes a tile of (128 WM) x (16 FN WN) outputs with WM x WN
+// wavefronts, each 128 x 16 FN as 8 x FN blocks of
+// v_mfma_f32_16x16x128_f8f6f4: one instruction spans exactly one group of the
+// summed index, so its result is the group's exact sum, scaled and added in
+// fp32 (TP_GROUP_F32), or the instruction applies the scales itself and
+// accumulates (TP_GROUP_E8M0).
+//
+// Rows and columns are dealt to the blocks so that a lane's outputs lie
+// together: block i's row index a is row 8 a + i of the wavefront's 128,
+// block j's column index b is column FN b + j.  The instruction is issued with
+// the B codes first, which leaves a lane (p = lane % 16, q = lane / 16) with
+// row index p and column indices 4 q .. 4 q + 3: in all 8 neighbouring rows x 4 FN
+// neighbouring columns.  So outputs are stored without a turn through shared
+// memory, a lane's 8 row scales are neighbours, a group of 128 tokens is one
+// wavefront's (its largest magnitude a reduction over 16 lanes) and the codes
+// of a transposed output are 8 bytes a lane.
+//
+// Shared memory holds rows of 128 codes, the 16-byte chunk c of a row at
+// c ^ (the row's index a or b) % 8: the 8 lanes that are served together read 8
+// different chunks.
+#pragma once
+
+#include "fp8g.h"
+
+namespace tpmlp {
+namespace g8 {
+
+// How a group's products are added: by the FP8 instruction, or widened to bf16
+enum { SUM_FP8 = 0, SUM_F32 = 1 };
+enum { G_STORE = 0, G_GLU_FWD = 1, G_GLU_BWD = 2 };
+
+template <int FMT_A, int FMT_B, int OA, int OB>
+__device__ __forceinline__ f32x4_t mfma_scaled(i32x8_t b, i32x8_t a, f32x4_t c, int sb, int sa) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, FMT_B, FMT_A, OB, sb, OA, sa);
+}
+template <int FMT_A, int FMT_B>
+__device__ __forceinline__ f32x4_t mfma_plain(i32x8_t b, i32x8_t a, f32x4_t c) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, FMT_B, FMT_A, 0, 0, 0, 0);
+}
+
+struct Place {
+  int64_t m0;  // first row of the wavefront
+  int n0;      // first column of the workgroup's tile (of F, in the gated forward)
+  int wm, wn, p, q;
+};
+
+// acc[i][j][t]: row m0 + 8 p + i; column (4 q + t) FN + j of the wavefront's
+template <int WM, int WN, int FN>
+__device__ __forceinline__ void store_plain(const G8GemmArgs& a, const Place& at, f32x4_t (&acc)[8][FN]) {
+  const int n = at.n0 + at.wn * 16 * FN + at.q * 4 * FN;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t m = at.m0 + 8 * at.p + i;
+    if (m >= a.M) continue;
+#pragma unroll
+    for (int h = 0; h < FN; ++h) {  // 4 columns at a time (bf16: 8 where a lane has them)
+      float v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = acc[i][(4 * h + k) % FN][(4 * h + k) / FN];
+      const int64_t off = m * a.N + n + 4 * h;
+      if (n + 4 * h >= a.N) continue;
+      if (a.out_bf16) {
+        Store4<bf16_t>::store(a.C, off, v);
+      } else {
+        if (a.accumulate) {
+          float w[4];
+          Store4<float>::load(a.C, off, w);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] += w[k];
+        }
+        Store4<float>::store(a.C, off, v);
+      }
+    }
+  }
+}
+
+// The 8 codes that a lane has of one column (its 8 rows), from the column's
+// largest magnitude over the wavefront's 128 rows
+template <int FMT, int SC>
+__device__ __forceinline__ void store_column(uint8_t* q_t, void* s_t, const float v[8], int64_t pm, int64_t m,
+                                             int64_t col, int64_t cols, int64_t token_group, int p) {
+  uint32_t top = mag(v[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) top = max(top, mag(v[i]));
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) top = xor_max(top, d);
+  const GroupScale<FMT, SC> gs(top);
+  const u32x2_t o = {codes4<FMT>(v[0], v[1], v[2], v[3], gs.inv), codes4<FMT>(v[4], v[5], v[6], v[7], gs.inv)};
+  if (col < cols) {
+    *reinterpret_cast<u32x2_t*>(q_t + col * pm + m) = o;
+    if (p == 0) gs.store(s_t, token_group * cols + col);
+  }
+}
+
+// Gated forward: blocks j < FN/2 hold the gate, the others the up projection, of the
+// same columns f = (4 q + t) FN/2 + j: 8 neighbouring ones for FN = 4.  The
+// tile has 128 of them: one group.
+template <int WM, int WN, int FN, int SC>
+__device__ __forceinline__ void store_glu_fwd(const G8GemmArgs& a, const Place& at, f32x4_t (&acc)[8][FN],
+                                              uint32_t* red) {
+  static_assert(FN == 4 && WN == 4, "one group of 128 columns");
+  const int64_t F = a.N, pf = padded(F), pm = padded(a.M);
+  const int fl = at.wn * 32 + at.q * 8;
+  const int64_t f = at.n0 + fl;
+  const int64_t m = at.m0 + 8 * at.p;
+  uint32_t top[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float h[8];
+    if (a.Z && m + i < a.M && f < F) {
+      float g[8], u[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        g[k] = acc[i][k % 2][k / 2];
+        u[k] = acc[i][2 + k % 2][k / 2];
+      }
+      Vec8<bf16_t>::store(a.Z, (m + i) * 2 * F + f, g);
+      Vec8<bf16_t>::store(a.Z, (m + i) * 2 * F + F + f, u);
+    }
+    top[i] = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      h[k] = gate_act(a.gate, acc[i][k % 2][k / 2]) * acc[i][2 + k % 2][k / 2];
+      acc[i][k % 2][k / 2] = h[k];
+      top[i] = max(top[i], mag(h[k]));
+    }
+    if (a.H && m + i < a.M && f < F) Vec8<bf16_t>::store(a.H, (m + i) * F + f, h);
+  }
+  if (a.q) {
+    // the group's largest magnitude of each row: 4 lanes, then 4 wavefronts
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top[i] = xor_max(xor_max(top[i], 16), 32);
+    uint32_t* mine = red + (at.wm * WN + at.wn) * 128;
+    if (at.q == 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mine[8 * at.p + i] = top[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t w = 0;
+#pragma unroll
+      for (int c = 0; c < WN; ++c) w = max(w, red[(at.wm * WN + c) * 128 + 8 * at.p + i]);
+      const GroupScale<0, SC> gs(w);
+      if (m + i < a.M) {
+        const u32x2_t o = {codes4<0>(acc[i][0][0], acc[i][1][0], acc[i][0][1], acc[i][1][1], gs.inv),
+                           codes4<0>(acc[i][0][2], acc[i][1][2], acc[i][0][3], acc[i][1][3], gs.inv)};
+        *reinterpret_cast<u32x2_t*>(a.q + (m + i) * pf + f) = o;
+        if (fl == 0) gs.store(a.s, (int64_t)(at.n0 / kGroup) * a.M + m + i);
+      }
+    }
+  }
+  if (a.q_t && at.m0 < pm) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = acc[i][k % 2][k / 2];
+      store_column<0, SC>(a.q_t, a.s_t, v, pm, m, f + k, F, at.m0 / kGroup, at.p);
+    }
+  }
+}
+
+// Gated backward: acc is dH; a lane has 16 neighbouring columns of F, taken 8
+// at a time.  dG and dU are formed twice from the saved G and U: for the
+// groups' largest magnitudes, then for the codes (kept, they would take twice the
+// registers of dH).
+template <int WM, int WN, int FN, int FMT, int SC>
+__device__ __forceinline__ void store_glu_bwd(const G8GemmArgs& a, const Place& at, f32x4_t (&acc)[8][FN],
+                                              uint32_t* red) {
+  static_assert(FN == 4 && WN % 2 == 0, "two wavefronts a group of 128 columns");
+  const int64_t F = a.N, pf = padded(F), pm = padded(a.M), gf = pf / kGroup;
+  const int64_t f = at.n0 + at.wn * 64 + at.q * 16;
+  const int64_t m = at.m0 + 8 * at.p;
+  auto form = [&](int i, int hf, float dg[8], float du[8]) {
+    const int64_t c = f + 8 * hf;
+    if (m + i < a.M && c < F) {
+      float g[8], u[8];
+      Vec8<bf16_t>::load(a.Z, (m + i) * 2 * F + c, g);
+      Vec8<bf16_t>::load(a.Z, (m + i) * 2 * F + F + c, u);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float d = acc[i][k % 4][2 * hf + k / 4];
+        float act, slope;
+        gate_both(a.gate, g[k], act, slope);
+        dg[k] = d * u[k] * slope;
+        du[k] = d * act;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) dg[k] = du[k] = 0.0f;
+    }
+  };
+  uint32_t rg[8], ru[8], cg[2][8], cu[2][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    rg[i] = ru[i] = 0;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      float dg[8], du[8];
+      form(i, hf, dg, du);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t x = mag(dg[k]), y = mag(du[k]);
+        rg[i] = max(rg[i], x);
+        ru[i] = max(ru[i], y);
+        cg[hf][k] = i ? max(cg[hf][k], x) : x;
+        cu[hf][k] = i ? max(cu[hf][k], y) : y;
+      }
+    }
+  }
+  if (a.q) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      rg[i] = xor_max(xor_max(rg[i], 16), 32);
+      ru[i] = xor_max(xor_max(ru[i], 16), 32);
+    }
+    uint32_t* mine = red + (at.wm * WN + at.wn) * 256;
+    if (at.q == 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        mine[8 * at.p + i] = rg[i];
+        mine[128 + 8 * at.p + i] = ru[i];
+      }
+    }
+    __syncthreads();
+    const uint32_t* other = red + (at.wm * WN + (at.wn ^ 1)) * 256;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      rg[i] = max(rg[i], other[8 * at.p + i]);
+      ru[i] = max(ru[i], other[128 + 8 * at.p + i]);
+    }
+    if (at.q == 0 && (at.wn & 1) == 0 && f < F) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (m + i < a.M) {
+          const int64_t g = f / kGroup;
+          GroupScale<FMT, SC>(rg[i]).store(a.s, g * a.M + m + i);
+          GroupScale<FMT, SC>(ru[i]).store(a.s, (gf + g) * a.M + m + i);
+        }
+    }
+  }
+  const int64_t token_group = at.m0 / kGroup;
+  const bool turned = a.q_t && at.m0 < pm;
+#pragma unroll
+  for (int hf = 0; hf < 2; ++hf) {
+    float ig[8], iu[8];
+    if (a.q_t) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) {
+          cg[hf][k] = xor_max(cg[hf][k], d);
+          cu[hf][k] = xor_max(cu[hf][k], d);
+        }
+        const GroupScale<FMT, SC> sg(cg[hf][k]), su(cu[hf][k]);
+        ig[k] = sg.inv;
+        iu[k] = su.inv;
+        const int64_t c = f + 8 * hf + k;
+        if (turned && at.p == 0 && c < F) {
+          sg.store(a.s_t, token_group * F + c);
+          su.store(a.s_t, (pm / kGroup + token_group) * F + c);
+        }
+      }
+    }
+    uint32_t og[8][2], ou[8][2];  // codes of 8 columns: 8 rows in two words
+#pragma unroll
+    for (int i4 = 0; i4 < 2; ++i4) {
+      float dg[4][8], du[4][8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * i4 + i;
+        form(r, hf, dg[i], du[i]);
+        if (a.q && m + r < a.M && f + 8 * hf < pf) {
+          const GroupScale<FMT, SC> sg(rg[r]), su(ru[r]);
+          const u32x2_t x = {codes4<FMT>(dg[i][0], dg[i][1], dg[i][2], dg[i][3], sg.inv),
+                             codes4<FMT>(dg[i][4], dg[i][5], dg[i][6], dg[i][7], sg.inv)};
+          const u32x2_t y = {codes4<FMT>(du[i][0], du[i][1], du[i][2], du[i][3], su.inv),
+                             codes4<FMT>(du[i][4], du[i][5], du[i][6], du[i][7], su.inv)};
+          *reinterpret_cast<u32x2_t*>(a.q + (m + r) * 2 * pf + f + 8 * hf) = x;
+          *reinterpret_cast<u32x2_t*>(a.q + (m + r) * 2 * pf + pf + f + 8 * hf) = y;
+        }
+      }
+      if (a.q_t) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          og[k][i4] = codes4<FMT>(dg[0][k], dg[1][k], dg[2][k], dg[3][k], ig[k]);
+          ou[k][i4] = codes4<FMT>(du[0][k], du[1][k], du[2][k], du[3][k], iu[k]);
+        }
+      }
+    }
+    if (turned) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int64_t c = f + 8 * hf + k;
+        if (c < F) {
+          *reinterpret_cast<u32x2_t*>(a.q_t + c * pm + m) = (u32x2_t){og[k][0], og[k][1]};
+          *reinterpret_cast<u32x2_t*>(a.q_t + (F + c) * pm + m) = (u32x2_t){ou[k][0], ou[k][1]};
+        }
+      }
+    }
+  }
+}
+
+template <int WM, int WN, int FN, int SC, bool SQ, int FMT_A, int FMT_B, int SUM, int EPI>
+__global__ __launch_bounds__(64 * WM * WN, 1) void gemm(G8GemmArgs a) {
+  constexpr int BM = 128 * WM, BN = 16 * FN * WN, NT = 64 * WM * WN;
+  constexpr bool PAIR = EPI == G_GLU_FWD;
+  constexpr int COLS = PAIR ? BN / 2 : BN;  // columns of the output a tile has
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[(BM + BN) * 128];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  // tile: XCDs take contiguous runs, rastered in groups of 4 tile rows
+  const int tile = xcd_logical_block(blockIdx.x, gridDim.x);
+  const int group = tile / (4 * a.tiles_n), first = 4 * group;
+  const int gm = min(4, a.tiles_m - first), li = tile - group * 4 * a.tiles_n;
+  const int tm = first + li % gm, tn = li / gm;
+
+  Place at;
+  at.wm = wave / WN;
+  at.wn = wave % WN;
+  at.p = lane & 15;
+  at.q = lane >> 4;
+  const int64_t mt = (int64_t)tm * BM;
+  at.m0 = mt + at.wm * 128;
+  at.n0 = tn * COLS;
+
+  const int kt_part = a.K / kGroup, kt_all = kt_part * a.parts;
+  f32x4_t acc[8][FN];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
+
+  for (int kt = 0; kt < kt_all; ++kt) {
+    const int part = kt >= kt_part ? 1 : 0, kb = kt - part * kt_part;
+    // operand rows -> shared memory
+#pragma unroll
+    for (int c = tid; c < BM * 8; c += NT) {
+      const int r = c >> 3, ch = c & 7;
+      u32x4_t v = {0u, 0u, 0u, 0u};
+      if (mt + r < a.M) v = *reinterpret_cast<const u32x4_t*>(a.A + (mt + r) * a.lda + (int64_t)kt * 128 + ch * 16);
+      *reinterpret_cast<u32x4_t*>(lds + r * 128 + ((ch ^ ((r >> 3) & 7)) << 4)) = v;
+    }
+#pragma unroll
+    for (int c = tid; c < BN * 8; c += NT) {
+      const int r = c >> 3, ch = c & 7;
+      const int w = r / (16 * FN), b = (r % (16 * FN)) / FN, j = r % FN;
+      int n;
+      const uint8_t* src;
+      if constexpr (PAIR) {
+        n = at.n0 + w * 8 * FN + b * (FN / 2) + j % (FN / 2);
+        src = j < FN / 2 ? a.B : a.B2;
+      } else {
+        n = at.n0 + r;
+        src = part ? a.B2 : a.B;
+      }
+      u32x4_t v = {0u, 0u, 0u, 0u};
+      if (n < a.N) v = *reinterpret_cast<const u32x4_t*>(src + (int64_t)n * a.K + (int64_t)kb * 128 + ch * 16);
+      *reinterpret_cast<u32x4_t*>(lds + (BM + r) * 128 + ((ch ^ (b & 7)) << 4)) = v;
+    }
+    __syncthreads();
+    // scales: 8 rows, and the wavefront's columns
+    const int64_t mr = at.m0 + 8 * at.p;
+    i32x8_t fb[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const uint8_t* row = lds + (BM + at.wn * 16 * FN + at.p * FN + j) * 128;
+      const i32x4_t lo = *reinterpret_cast<const i32x4_t*>(row + (((2 * at.q) ^ (at.p & 7)) << 4));
+      const i32x4_t hi = *reinterpret_cast<const i32x4_t*>(row + (((2 * at.q + 1) ^ (at.p & 7)) << 4));
+      fb[j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    auto col_of = [&](int b, int j) -> int64_t {  // column of index b of block j
+      return PAIR ? at.n0 + at.wn * 8 * FN + b * (FN / 2) + j % (FN / 2) : at.n0 + at.wn * 16 * FN + b * FN + j;
+    };
+    auto sb_src = [&](int j) { return PAIR ? (j < FN / 2 ? a.sB : a.sB2) : (part ? a.sB2 : a.sB); };
+    // row i of the lane's 8
+    auto load_a = [&](int i) {
+      const uint8_t* row = lds + (at.wm * 128 + 8 * at.p + i) * 128;
+      const i32x4_t lo = *reinterpret_cast<const i32x4_t*>(row + (((2 * at.q) ^ (at.p & 7)) << 4));
+      const i32x4_t hi = *reinterpret_cast<const i32x4_t*>(row + (((2 * at.q + 1) ^ (at.p & 7)) << 4));
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    auto scale_a = [&](int i) { return (int64_t)kt * a.M + min(mr + i, a.M - 1); };
+    auto scale_b = [&](int b, int j) {
+      const int64_t n = min(col_of(b, j), (int64_t)a.N - 1);
+      return SQ ? n / kGroup * kt_part + kb : (int64_t)kb * a.N + n;
+    };
+    bf16x8g_t wb[SUM == SUM_F32 ? FN : 1][4];
+    if constexpr (SUM == SUM_F32) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        float s = 1.0f;
+        if constexpr (SC == TP_GROUP_E8M0) s = e8m0_f32(reinterpret_cast<const uint8_t*>(sb_src(j))[scale_b(at.p, j)]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) wb[j][c] = widen<FMT_B>(fb[j][2 * c], fb[j][2 * c + 1], s);
+      }
+    }
+    if constexpr (SC == TP_GROUP_F32) {
+      float sb[SQ ? 1 : 4][FN];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const float* s = reinterpret_cast<const float*>(sb_src(j));
+#pragma unroll
+        for (int t = 0; t < (SQ ? 1 : 4); ++t) sb[t][j] = s[scale_b(SQ ? 0 : 4 * at.q + t, j)];
+      }
+      static_for<0, 8>([&](auto I) {
+        constexpr int i = decltype(I)::value;
+        const i32x8_t fa = load_a(i);
+        const float sa = reinterpret_cast<const float*>(a.sA)[scale_a(i)];
+        f32x4_t p[FN];
+        if constexpr (SUM == SUM_F32) {
+#pragma unroll
+          for (int j = 0; j < FN; ++j) p[j] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const bf16x8g_t wa = widen<FMT_A>(fa[2 * c], fa[2 * c + 1], 1.0f);
+#pragma unroll
+            for (int j = 0; j < FN; ++j) p[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][c], wa, p[j], 0, 0, 0);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < FN; ++j) p[j] = mfma_plain<FMT_A, FMT_B>(fb[j], fa, (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f});
+        }
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) acc[i][j][t] = fmaf(p[j][t], sa * sb[SQ ? 0 : t][j], acc[i][j][t]);
+      });
+    } else if constexpr (SUM == SUM_F32) {
+      static_for<0, 8>([&](auto I) {
+        constexpr int i = decltype(I)::value;
+        const i32x8_t fa = load_a(i);
+        const float sa = e8m0_f32(reinterpret_cast<const uint8_t*>(a.sA)[scale_a(i)]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const bf16x8g_t wa = widen<FMT_A>(fa[2 * c], fa[2 * c + 1], sa);
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][c], wa, acc[i][j], 0, 0, 0);
+        }
+      });
+    } else {
+      uint32_t sbw = 0, saw[2] = {0, 0};
+#pragma unroll
+      for (int j = 0; j < FN; ++j) sbw |= (uint32_t)reinterpret_cast<const uint8_t*>(sb_src(j))[scale_b(at.p, j)] << (8 * j);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        saw[i >> 2] |= (uint32_t)reinterpret_cast<const uint8_t*>(a.sA)[scale_a(i)] << (8 * (i & 3));
+      static_for<0, 8>([&](auto I) {
+        constexpr int i = decltype(I)::value;
+        const i32x8_t fa = load_a(i);
+        static_for<0, FN>([&](auto J) {
+          constexpr int j = decltype(J)::value;
+          acc[i][j] = mfma_scaled<FMT_A, FMT_B, i & 3, j>(fb[j], fa, acc[i][j], (int)sbw, (int)saw[i >> 2]);
+        });
+      });
+    }
+    __syncthreads();
+  }
+
+  uint32_t* red = reinterpret_cast<uint32_t*>(lds);
+  if constexpr (EPI == G_GLU_FWD) store_glu_fwd<WM, WN, FN, SC>(a, at, acc, red);
+  else if constexpr (EPI == G_GLU_BWD) store_glu_bwd<WM, WN, FN, FMT_A, SC>(a, at, acc, red);
+  else store_plain<WM, WN, FN>(a, at, acc);
+}
+
+template <int WM, int WN, int FN, int SC, bool SQ, int FMT_A, int FMT_B, int SUM, int EPI>
+static hipError_t launch(G8GemmArgs& a, hipStream_t st) {
+  constexpr int BM = 128 * WM, BN = EPI == G_GLU_FWD ? 8 * FN * WN : 16 * FN * WN;
+  const int64_t tm = (a.M + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
+  if (tm * tn > 0x7fffffff) return hipErrorInvalidValue;
+  a.tiles_m = (int)tm;
+  a.tiles_n = (int)tn;
+  if (tm * tn == 0) return hipSuccess;
+  hipLaunchKernelGGL((gemm<WM, WN, FN, SC, SQ, FMT_A, FMT_B, SUM, EPI>), dim3((unsigned)(tm * tn)),
+                     dim3(64 * WM * WN), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace g8
+}  // namespace tpmlp

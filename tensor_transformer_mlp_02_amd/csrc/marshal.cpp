@@ -23,6 +23,7 @@
 #include <utility>
 
 #include "../../include/tpmlp_block.h"
+#include "../../include/tpmlp_fp8g.h"
 
 namespace {
 
@@ -130,7 +131,9 @@ struct Entry {
 };
 #define ENTRY(f) {#f, Declared<decltype(f)>::COUNT, &Declared<decltype(f)>::call}
 constexpr Entry entries[] = {ENTRY(tp_block_norm_fwd), ENTRY(tp_block_norm_bwd), ENTRY(tp_moe_route_fwd),
-                             ENTRY(tp_moe_route_bwd), ENTRY(tp_moe_route_tables), ENTRY(tp_adamw_step)};
+                             ENTRY(tp_moe_route_bwd), ENTRY(tp_moe_route_tables), ENTRY(tp_adamw_step),
+                             ENTRY(tp_fp8g_quantize), ENTRY(tp_fp8g_gemm), ENTRY(tp_fp8g_glu_fwd),
+                             ENTRY(tp_fp8g_glu_bwd)};
 #undef ENTRY
 const Entry* entry_of(PyObject* name) {
   if (PyUnicode_Check(name))
