@@ -211,7 +211,9 @@ __device__ __forceinline__ void store_glu_bwd(const G8GemmArgs& a, const Place& 
         cu[hf][k] = i ? max(cu[hf][k], y) : y;
       }
     }
+    __builtin_amdgcn_sched_barrier(0);  // (a few rows' loads at a time)
   }
+  asm volatile("" ::: "memory");  // the second forming loads G and U again
   if (a.q) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -291,6 +293,7 @@ __device__ __forceinline__ void store_glu_bwd(const G8GemmArgs& a, const Place& 
           ou[k][i4] = codes4<FMT>(du[0][k], du[1][k], du[2][k], du[3][k], iu[k]);
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
     if (turned) {
 #pragma unroll
@@ -305,12 +308,52 @@ __device__ __forceinline__ void store_glu_bwd(const G8GemmArgs& a, const Place& 
   }
 }
 
+// ---- operands: memory -> shared memory -> registers --------------------------
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+typedef __attribute__((address_space(3))) void lds_void_t;
+
+// a buffer of so many bytes: what is read behind its end is zeros
+__device__ __forceinline__ rsrc_t buffer_of(const void* p, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, bytes, 0x00020000);
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
+}
+
+// The 32 codes of a block's row that a lane has, waited for in the same
+// place; with them, a row's scale
+template <int OFF>
+__device__ __forceinline__ i32x8_t read_codes(uint32_t a0, uint32_t a1) {
+  i32x4_t lo, hi;
+  asm volatile("ds_read_b128 %0, %2 offset:%4\n\tds_read_b128 %1, %3 offset:%4\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(lo), "=&v"(hi) : "v"(a0), "v"(a1), "n"(OFF) : "memory");
+  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+template <int OFF, int SOFF>
+__device__ __forceinline__ i32x8_t read_codes_scale(uint32_t a0, uint32_t a1, uint32_t as, float& s) {
+  i32x4_t lo, hi;
+  asm volatile("ds_read_b128 %0, %3 offset:%6\n\tds_read_b128 %1, %4 offset:%6\n\tds_read_b32 %2, %5 offset:%7\n\t"
+               "s_waitcnt lgkmcnt(0)"
+               : "=&v"(lo), "=&v"(hi), "=&v"(s) : "v"(a0), "v"(a1), "v"(as), "n"(OFF), "n"(SOFF) : "memory");
+  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+struct __attribute__((packed)) Bytes8 { uint32_t v[2]; };
+
+// Two tile buffers in shared memory: while one is multiplied the other's
+// loads (straight into shared memory) are on their way.
 template <int WM, int WN, int FN, int SC, bool SQ, int FMT_A, int FMT_B, int SUM, int EPI>
-__global__ __launch_bounds__(64 * WM * WN, 1) void gemm(G8GemmArgs a) {
-  constexpr int BM = 128 * WM, BN = 16 * FN * WN, NT = 64 * WM * WN;
+__global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 ? 2 : 1) void gemm(G8GemmArgs a) {
+  constexpr int BM = 128 * WM, BN = 16 * FN * WN, NW = WM * WN;
   constexpr bool PAIR = EPI == G_GLU_FWD;
   constexpr int COLS = PAIR ? BN / 2 : BN;  // columns of the output a tile has
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[(BM + BN) * 128];
+  constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;  // 1 KiB loads of a wavefront (8 rows each)
+  constexpr bool SLDS = SC == TP_GROUP_F32;          // row scales by way of shared memory
+  constexpr int LOADS = LA + LB + (SLDS ? 1 : 0);
+  // [A 0 | A 1 | B 0 | B 1 | row scales 0 | 1]
+  constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, S_BYTES = SLDS ? BM * 4 : 0;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * (A_BYTES + B_BYTES + S_BYTES)];
+  constexpr int B_AT = 2 * A_BYTES, S_AT = B_AT + 2 * B_BYTES;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
@@ -330,137 +373,165 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm(G8GemmArgs a) {
   at.n0 = tn * COLS;
 
   const int kt_part = a.K / kGroup, kt_all = kt_part * a.parts;
+
+  // a wavefront's loads: lane l fills chunk l % 8 of row 8 block + l / 8.
+  // Rows past the last lie behind the buffer's end and read as zeros.  The
+  // offsets are formed at each load, from two registers an operand.
+  const int lda = (int)a.lda;
+  const int rows = (int)min((int64_t)BM, a.M - mt), cols = min(COLS, a.N - at.n0);
+  const rsrc_t ra = buffer_of(a.A + mt * a.lda, rows * lda);
+  const rsrc_t rb = buffer_of(a.B + (int64_t)at.n0 * a.K, cols * a.K);
+  const rsrc_t rb2 = buffer_of(a.B2 + (int64_t)at.n0 * a.K, cols * a.K);
+  // shared rows of B: of a wavefront's 16 FN, block j's row b is row FN b + j;
+  // gated forward: the gate's half of them, then the up projection's
+  constexpr int RB = PAIR ? FN / 2 : FN;
+  const int sr = (wave % (BM / 64)) * 64 + lane;
+  auto load_tile = [&](int kt, int buf) {
+    const int part = kt >= kt_part ? 1 : 0, kb = kt - part * kt_part;
+    int ln = lane;
+    asm volatile("" : "+v"(ln));  // (kept over the loop, each offset would be a register)
+    const int l8 = ln >> 3, ch = ln & 7;
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+      const int blk = wave * LA + i;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void_t*)(lds + buf * A_BYTES + blk * 1024), 16,
+                                               (blk * 8 + l8) * lda + ((ch ^ (blk & 7)) << 4), kt * 128, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < LB; ++i) {
+      const int r0 = (wave * LB + i) * 8, r = r0 + l8;
+      const bool second = PAIR ? (r0 / (8 * FN)) % 2 == 1 : part == 1;
+      const int n = PAIR ? r0 / (16 * FN) * (8 * FN) + r0 % (8 * FN) + l8 : r;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(second ? rb2 : rb, (lds_void_t*)(lds + B_AT + buf * B_BYTES + r0 * 128), 16,
+                                               n * a.K + ((ch ^ ((r / RB) & 7)) << 4), kb * 128, 0, 0);
+    }
+    if constexpr (SLDS) {
+      const rsrc_t rs = buffer_of(reinterpret_cast<const float*>(a.sA) + (int64_t)kt * a.M + mt, rows * 4);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rs, (lds_void_t*)(lds + S_AT + buf * S_BYTES + (wave % (BM / 64)) * 256), 4, sr * 4, 0, 0, 0);
+    }
+  };
+
+  // what a lane reads: chunks 2 q and 2 q + 1 of its rows
+  const uint32_t l0 = lds_address(lds);
+  const uint32_t c0 = ((2 * at.q) ^ (at.p & 7)) << 4, c1 = c0 ^ 16;
+  uint32_t pa = l0 + (at.wm * 128 + 8 * at.p) * 128, pb = l0 + B_AT + (at.wn * 16 * FN + at.p * RB) * 128;
+  uint32_t ps = l0 + S_AT + (at.wm * 128 + 8 * at.p) * 4;
+
+  // column of index b of block j, and its scale's place
+  auto col_of = [&](int b, int j) -> int64_t {
+    return PAIR ? at.n0 + at.wn * 8 * FN + b * RB + j % RB : at.n0 + at.wn * 16 * FN + b * FN + j;
+  };
+  const int64_t mr = at.m0 + 8 * at.p;
+  const bool whole = at.m0 + 128 <= a.M;  // every row of the wavefront is there
+
   f32x4_t acc[8][FN];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
 
+  load_tile(0, 0);
+  if (kt_all > 1) load_tile(1, 1);
   for (int kt = 0; kt < kt_all; ++kt) {
-    const int part = kt >= kt_part ? 1 : 0, kb = kt - part * kt_part;
-    // operand rows -> shared memory
-#pragma unroll
-    for (int c = tid; c < BM * 8; c += NT) {
-      const int r = c >> 3, ch = c & 7;
-      u32x4_t v = {0u, 0u, 0u, 0u};
-      if (mt + r < a.M) v = *reinterpret_cast<const u32x4_t*>(a.A + (mt + r) * a.lda + (int64_t)kt * 128 + ch * 16);
-      *reinterpret_cast<u32x4_t*>(lds + r * 128 + ((ch ^ ((r >> 3) & 7)) << 4)) = v;
-    }
-#pragma unroll
-    for (int c = tid; c < BN * 8; c += NT) {
-      const int r = c >> 3, ch = c & 7;
-      const int w = r / (16 * FN), b = (r % (16 * FN)) / FN, j = r % FN;
-      int n;
-      const uint8_t* src;
-      if constexpr (PAIR) {
-        n = at.n0 + w * 8 * FN + b * (FN / 2) + j % (FN / 2);
-        src = j < FN / 2 ? a.B : a.B2;
-      } else {
-        n = at.n0 + r;
-        src = part ? a.B2 : a.B;
-      }
-      u32x4_t v = {0u, 0u, 0u, 0u};
-      if (n < a.N) v = *reinterpret_cast<const u32x4_t*>(src + (int64_t)n * a.K + (int64_t)kb * 128 + ch * 16);
-      *reinterpret_cast<u32x4_t*>(lds + (BM + r) * 128 + ((ch ^ (b & 7)) << 4)) = v;
-    }
-    __syncthreads();
-    // scales: 8 rows, and the wavefront's columns
-    const int64_t mr = at.m0 + 8 * at.p;
-    i32x8_t fb[FN];
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const uint8_t* row = lds + (BM + at.wn * 16 * FN + at.p * FN + j) * 128;
-      const i32x4_t lo = *reinterpret_cast<const i32x4_t*>(row + (((2 * at.q) ^ (at.p & 7)) << 4));
-      const i32x4_t hi = *reinterpret_cast<const i32x4_t*>(row + (((2 * at.q + 1) ^ (at.p & 7)) << 4));
-      fb[j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    }
-    auto col_of = [&](int b, int j) -> int64_t {  // column of index b of block j
-      return PAIR ? at.n0 + at.wn * 8 * FN + b * (FN / 2) + j % (FN / 2) : at.n0 + at.wn * 16 * FN + b * FN + j;
-    };
+    const int part = kt >= kt_part ? 1 : 0, kb = kt - part * kt_part, buf = kt & 1;
     auto sb_src = [&](int j) { return PAIR ? (j < FN / 2 ? a.sB : a.sB2) : (part ? a.sB2 : a.sB); };
-    // row i of the lane's 8
-    auto load_a = [&](int i) {
-      const uint8_t* row = lds + (at.wm * 128 + 8 * at.p + i) * 128;
-      const i32x4_t lo = *reinterpret_cast<const i32x4_t*>(row + (((2 * at.q) ^ (at.p & 7)) << 4));
-      const i32x4_t hi = *reinterpret_cast<const i32x4_t*>(row + (((2 * at.q + 1) ^ (at.p & 7)) << 4));
-      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    };
-    auto scale_a = [&](int i) { return (int64_t)kt * a.M + min(mr + i, a.M - 1); };
     auto scale_b = [&](int b, int j) {
       const int64_t n = min(col_of(b, j), (int64_t)a.N - 1);
       return SQ ? n / kGroup * kt_part + kb : (int64_t)kb * a.N + n;
     };
-    bf16x8g_t wb[SUM == SUM_F32 ? FN : 1][4];
-    if constexpr (SUM == SUM_F32) {
+    // column scales (and E8M0 row scales) of this tile
+    constexpr int SBT = SC == TP_GROUP_F32 && !SQ ? 4 : 1;
+    float sb[SBT][FN];
+    uint32_t eb = 0, ea[2] = {0, 0};
+    if constexpr (SC == TP_GROUP_F32) {
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        float s = 1.0f;
-        if constexpr (SC == TP_GROUP_E8M0) s = e8m0_f32(reinterpret_cast<const uint8_t*>(sb_src(j))[scale_b(at.p, j)]);
+      for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) wb[j][c] = widen<FMT_B>(fb[j][2 * c], fb[j][2 * c + 1], s);
+        for (int t = 0; t < SBT; ++t)
+          sb[t][j] = reinterpret_cast<const float*>(sb_src(j))[scale_b(SQ ? 0 : 4 * at.q + t, j)];
+    } else {
+#pragma unroll
+      for (int j = 0; j < FN; ++j) eb |= (uint32_t)reinterpret_cast<const uint8_t*>(sb_src(j))[scale_b(SQ ? 0 : at.p, j)] << (8 * j);
+      const uint8_t* s = reinterpret_cast<const uint8_t*>(a.sA) + (int64_t)kt * a.M;
+      if (whole) {
+        const Bytes8 w = *reinterpret_cast<const Bytes8*>(s + mr);
+        ea[0] = w.v[0];
+        ea[1] = w.v[1];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ea[i >> 2] |= (uint32_t)s[min(mr + i, a.M - 1)] << (8 * (i & 3));
       }
     }
-    if constexpr (SC == TP_GROUP_F32) {
-      float sb[SQ ? 1 : 4][FN];
+    // this tile is there; the next one's loads may still be on their way
+    if (kt + 1 < kt_all) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+
+    const uint32_t a0 = pa + buf * A_BYTES + c0, a1 = pa + buf * A_BYTES + c1, as = ps + buf * S_BYTES;
+    const uint32_t b0 = pb + buf * B_BYTES + c0, b1 = pb + buf * B_BYTES + c1;
+    i32x8_t fb[FN];
+    bf16x8g_t wb[SUM == SUM_F32 ? FN : 1][4];
+    static_for<0, FN>([&](auto J) {
+      constexpr int j = decltype(J)::value;
+      fb[j] = read_codes<PAIR ? (j / RB) * 16 * RB * 128 + (j % RB) * 128 : j * 128>(b0, b1);
+      if constexpr (SUM == SUM_F32) {
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const float* s = reinterpret_cast<const float*>(sb_src(j));
-#pragma unroll
-        for (int t = 0; t < (SQ ? 1 : 4); ++t) sb[t][j] = s[scale_b(SQ ? 0 : 4 * at.q + t, j)];
+        for (int c = 0; c < 4; ++c)
+          wb[j][c] = widen<FMT_B>(fb[j][2 * c], fb[j][2 * c + 1], SC == TP_GROUP_F32 ? 1.0f : e8m0_f32((eb >> (8 * j)) & 255));
       }
-      static_for<0, 8>([&](auto I) {
-        constexpr int i = decltype(I)::value;
-        const i32x8_t fa = load_a(i);
-        const float sa = reinterpret_cast<const float*>(a.sA)[scale_a(i)];
+    });
+    static_for<0, 8>([&](auto I) {
+      constexpr int i = decltype(I)::value;
+      float sa = 1.0f;
+      i32x8_t fa;
+      if constexpr (SLDS) fa = read_codes_scale<i * 128, i * 4>(a0, a1, as, sa);
+      else fa = read_codes<i * 128>(a0, a1);
+      if constexpr (SUM == SUM_F32) {
+        if constexpr (SC == TP_GROUP_E8M0) sa = e8m0_f32((ea[i >> 2] >> (8 * (i & 3))) & 255);
         f32x4_t p[FN];
-        if constexpr (SUM == SUM_F32) {
 #pragma unroll
-          for (int j = 0; j < FN; ++j) p[j] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < FN; ++j) p[j] = SC == TP_GROUP_F32 ? (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f} : acc[i][j];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const bf16x8g_t wa = widen<FMT_A>(fa[2 * c], fa[2 * c + 1], 1.0f);
+        for (int c = 0; c < 4; ++c) {
+          const bf16x8g_t wa = widen<FMT_A>(fa[2 * c], fa[2 * c + 1], SC == TP_GROUP_F32 ? 1.0f : sa);
 #pragma unroll
-            for (int j = 0; j < FN; ++j) p[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][c], wa, p[j], 0, 0, 0);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < FN; ++j) p[j] = mfma_plain<FMT_A, FMT_B>(fb[j], fa, (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f});
+          for (int j = 0; j < FN; ++j) p[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][c], wa, p[j], 0, 0, 0);
         }
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          if constexpr (SC == TP_GROUP_F32) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) acc[i][j][t] = fmaf(p[j][t], sa * sb[SQ ? 0 : t][j], acc[i][j][t]);
+          } else {
+            acc[i][j] = p[j];
+          }
+        }
+      } else if constexpr (SC == TP_GROUP_F32) {
+        f32x4_t p[FN];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) p[j] = mfma_plain<FMT_A, FMT_B>(fb[j], fa, (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
           for (int t = 0; t < 4; ++t) acc[i][j][t] = fmaf(p[j][t], sa * sb[SQ ? 0 : t][j], acc[i][j][t]);
-      });
-    } else if constexpr (SUM == SUM_F32) {
-      static_for<0, 8>([&](auto I) {
-        constexpr int i = decltype(I)::value;
-        const i32x8_t fa = load_a(i);
-        const float sa = e8m0_f32(reinterpret_cast<const uint8_t*>(a.sA)[scale_a(i)]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const bf16x8g_t wa = widen<FMT_A>(fa[2 * c], fa[2 * c + 1], sa);
-#pragma unroll
-          for (int j = 0; j < FN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][c], wa, acc[i][j], 0, 0, 0);
-        }
-      });
-    } else {
-      uint32_t sbw = 0, saw[2] = {0, 0};
-#pragma unroll
-      for (int j = 0; j < FN; ++j) sbw |= (uint32_t)reinterpret_cast<const uint8_t*>(sb_src(j))[scale_b(at.p, j)] << (8 * j);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        saw[i >> 2] |= (uint32_t)reinterpret_cast<const uint8_t*>(a.sA)[scale_a(i)] << (8 * (i & 3));
-      static_for<0, 8>([&](auto I) {
-        constexpr int i = decltype(I)::value;
-        const i32x8_t fa = load_a(i);
+      } else {
         static_for<0, FN>([&](auto J) {
           constexpr int j = decltype(J)::value;
-          acc[i][j] = mfma_scaled<FMT_A, FMT_B, i & 3, j>(fb[j], fa, acc[i][j], (int)sbw, (int)saw[i >> 2]);
+          acc[i][j] = mfma_scaled<FMT_A, FMT_B, i & 3, j>(fb[j], fa, acc[i][j], (int)eb, (int)ea[i >> 2]);
         });
-      });
-    }
-    __syncthreads();
+      }
+      // (the reads of later rows moved up, or these sums put off past the
+      // barrier, would need registers of their own)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(acc[i][j]));
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    // every wavefront has read this tile: its buffer takes the one after next
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    if (kt + 2 < kt_all) load_tile(kt + 2, buf);
   }
 
   uint32_t* red = reinterpret_cast<uint32_t*>(lds);
