@@ -96,6 +96,16 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, f
   return inv > 0.0f ? fp8x4<FMT>(a, b, c, d, inv) : 0u;
 }
 
+// Two more of four codes: the low pair (the word is new) or the high one
+template <int FMT>
+__device__ __forceinline__ uint32_t codes2(float a, float b, float inv, uint32_t word, bool high) {
+  constexpr float VMAX = FMT == 0 ? 448.0f : 57344.0f;
+  a = inv > 0.0f ? fminf(fmaxf(a * inv, -VMAX), VMAX) : 0.0f;
+  b = inv > 0.0f ? fminf(fmaxf(b * inv, -VMAX), VMAX) : 0.0f;
+  if constexpr (FMT == 0) return high ? __builtin_amdgcn_cvt_pk_fp8_f32(a, b, (int)word, true) : __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  else return high ? __builtin_amdgcn_cvt_pk_bf8_f32(a, b, (int)word, true) : __builtin_amdgcn_cvt_pk_bf8_f32(a, b, 0, false);
+}
+
 __device__ __forceinline__ uint32_t xor_max(uint32_t v, int d) {
   return max(v, (uint32_t)__shfl_xor((int)v, d, 64));
 }
@@ -126,20 +136,24 @@ __device__ __forceinline__ bf16x8g_t widen(int lo, int hi, float scale) {
 // an E8M0 byte as the fp32 whose exponent it is (255: infinity, NaN above)
 __device__ __forceinline__ float e8m0_f32(uint32_t e) { return __uint_as_float(e << 23); }
 
-// The gate's activation, and its derivative beside it
-__device__ __forceinline__ float gate_act(int gate, float g) {
-  return gate == TP_GATE_SILU ? silu_f(g) : gelu_f(g);
-}
-__device__ __forceinline__ void gate_both(int gate, float g, float& act, float& slope) {
-  if (gate == TP_GATE_SILU) {
-    const float s = sigmoid_f(g);
-    act = g * s;
-    slope = s * (1.0f + g * (1.0f - s));
-  } else {
-    act = gelu_f(g);
-    slope = gelu_grad_f(g);
+// The gate's activation g sigmoid(z) and its derivative s + g s (1 - s) z':
+// SiLU has z = g, GeLU z = 2 c (g + k g^3), both g (z1 + z3 g^2): no branch.
+// (g^2 is held below infinity, which times SiLU's 0 would be NaN.)
+struct Gate {
+  float z1, z3;
+  __device__ __forceinline__ explicit Gate(int gate)
+      : z1(gate == TP_GATE_SILU ? 1.0f : 2.0f * TP_GELU_C), z3(gate == TP_GATE_SILU ? 0.0f : 2.0f * TP_GELU_C * TP_GELU_K) {}
+  __device__ __forceinline__ float act(float g) const {
+    const float g2 = fminf(g * g, 1e37f);
+    return g * sigmoid_rcp_f(g * fmaf(z3, g2, z1));
   }
-}
+  __device__ __forceinline__ void both(float g, float& act, float& slope) const {
+    const float g2 = fminf(g * g, 1e37f);
+    const float s = sigmoid_rcp_f(g * fmaf(z3, g2, z1));
+    act = g * s;
+    slope = fmaf(act * (1.0f - s), fmaf(3.0f * z3, g2, z1), s);
+  }
+};
 
 }  // namespace g8
 }  // namespace tpmlp

@@ -133,6 +133,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void gemm_few(G8GemmArgs a) {
   const int col = n0 + 4 * q;
   if (row >= M || col >= a.N) return;
   const int64_t off = row * a.N + col;
+  const Gate gate(a.gate);
   if constexpr (EPI == F_STORE) {
     if (a.out_bf16) {
       Store4<bf16_t>::store(a.C, off, v[0]);
@@ -152,7 +153,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void gemm_few(G8GemmArgs a) {
     }
     float h[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) h[t] = gate_act(a.gate, v[0][t]) * v[1][t];
+    for (int t = 0; t < 4; ++t) h[t] = gate.act(v[0][t]) * v[1][t];
     if (a.H) Store4<bf16_t>::store(a.H, off, h);
     if (a.raw) Store4<float>::store(a.raw, off, h);
   } else {
@@ -162,7 +163,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void gemm_few(G8GemmArgs a) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       float act, slope;
-      gate_both(a.gate, g[t], act, slope);
+      gate.both(g[t], act, slope);
       dg[t] = v[0][t] * u[t] * slope;
       du[t] = v[0][t] * act;
     }

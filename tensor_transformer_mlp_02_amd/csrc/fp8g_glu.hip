@@ -9,8 +9,10 @@ template <int SC, int FMT, int EPI>
 static hipError_t launch_glu(G8GemmArgs& a, hipStream_t st) {
   const int64_t cols = EPI == G_GLU_FWD ? 128 : 256;
   const int64_t big = ((a.M + 255) / 256) * ((a.N + cols - 1) / cols);
-  if (big >= 192) return launch<2, 4, 4, SC, true, FMT, 0, SUM_F32, EPI>(a, st);
-  return launch<1, 4, 4, SC, true, FMT, 0, SUM_F32, EPI>(a, st);
+  if (big >= 192) return launch<2, 4, 4, 2, SC, true, FMT, 0, SUM_F32, EPI>(a, st);
+  // one group of columns a workgroup
+  constexpr int FN = EPI == G_GLU_FWD ? 2 : 1;
+  return launch<1, 8, FN, 3, SC, true, FMT, 0, SUM_F32, EPI>(a, st);
 }
 
 }  // namespace g8

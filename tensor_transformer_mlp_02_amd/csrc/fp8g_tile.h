@@ -96,41 +96,47 @@ __device__ __forceinline__ void store_column(uint8_t* q_t, void* s_t, const floa
 }
 
 // Gated forward: blocks j < FN/2 hold the gate, the others the up projection, of the
-// same columns f = (4 q + t) FN/2 + j: 8 neighbouring ones for FN = 4.  The
-// tile has 128 of them: one group.
+// same columns f = (4 q + t) FN/2 + j: 2 FN neighbouring ones.  The tile has 128 of them: one
+// group.
 template <int WM, int WN, int FN, int SC>
 __device__ __forceinline__ void store_glu_fwd(const G8GemmArgs& a, const Place& at, f32x4_t (&acc)[8][FN],
                                               uint32_t* red) {
-  static_assert(FN == 4 && WN == 4, "one group of 128 columns");
+  constexpr int J = FN / 2, C = 2 * FN;
+  static_assert(8 * FN * WN == 128 && (C == 8 || C == 4), "one group of 128 columns");
   const int64_t F = a.N, pf = padded(F), pm = padded(a.M);
-  const int fl = at.wn * 32 + at.q * 8;
+  const int fl = at.wn * 8 * FN + at.q * C;
   const int64_t f = at.n0 + fl;
   const int64_t m = at.m0 + 8 * at.p;
+  const Gate gate(a.gate);
+  auto put = [&](void* to, int64_t off, const float* v) {
+    if constexpr (C == 8) Vec8<bf16_t>::store(to, off, v);
+    else Store4<bf16_t>::store(to, off, v);
+  };
   uint32_t top[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    float h[8];
+    float h[C];
     if (a.Z && m + i < a.M && f < F) {
-      float g[8], u[8];
+      float g[C], u[C];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        g[k] = acc[i][k % 2][k / 2];
-        u[k] = acc[i][2 + k % 2][k / 2];
+      for (int k = 0; k < C; ++k) {
+        g[k] = acc[i][k % J][k / J];
+        u[k] = acc[i][J + k % J][k / J];
       }
-      Vec8<bf16_t>::store(a.Z, (m + i) * 2 * F + f, g);
-      Vec8<bf16_t>::store(a.Z, (m + i) * 2 * F + F + f, u);
+      put(a.Z, (m + i) * 2 * F + f, g);
+      put(a.Z, (m + i) * 2 * F + F + f, u);
     }
     top[i] = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      h[k] = gate_act(a.gate, acc[i][k % 2][k / 2]) * acc[i][2 + k % 2][k / 2];
-      acc[i][k % 2][k / 2] = h[k];
+    for (int k = 0; k < C; ++k) {
+      h[k] = gate.act(acc[i][k % J][k / J]) * acc[i][J + k % J][k / J];
+      acc[i][k % J][k / J] = h[k];
       top[i] = max(top[i], mag(h[k]));
     }
-    if (a.H && m + i < a.M && f < F) Vec8<bf16_t>::store(a.H, (m + i) * F + f, h);
+    if (a.H && m + i < a.M && f < F) put(a.H, (m + i) * F + f, h);
   }
   if (a.q) {
-    // the group's largest magnitude of each row: 4 lanes, then 4 wavefronts
+    // the group's largest magnitude of each row: 4 lanes, then the wavefronts
 #pragma unroll
     for (int i = 0; i < 8; ++i) top[i] = xor_max(xor_max(top[i], 16), 32);
     uint32_t* mine = red + (at.wm * WN + at.wn) * 128;
@@ -146,162 +152,180 @@ __device__ __forceinline__ void store_glu_fwd(const G8GemmArgs& a, const Place& 
       for (int c = 0; c < WN; ++c) w = max(w, red[(at.wm * WN + c) * 128 + 8 * at.p + i]);
       const GroupScale<0, SC> gs(w);
       if (m + i < a.M) {
-        const u32x2_t o = {codes4<0>(acc[i][0][0], acc[i][1][0], acc[i][0][1], acc[i][1][1], gs.inv),
-                           codes4<0>(acc[i][0][2], acc[i][1][2], acc[i][0][3], acc[i][1][3], gs.inv)};
-        *reinterpret_cast<u32x2_t*>(a.q + (m + i) * pf + f) = o;
+#pragma unroll
+        for (int k = 0; k < C; k += 4)
+          *reinterpret_cast<uint32_t*>(a.q + (m + i) * pf + f + k) =
+              codes4<0>(acc[i][k % J][k / J], acc[i][(k + 1) % J][(k + 1) / J], acc[i][(k + 2) % J][(k + 2) / J],
+                        acc[i][(k + 3) % J][(k + 3) / J], gs.inv);
         if (fl == 0) gs.store(a.s, (int64_t)(at.n0 / kGroup) * a.M + m + i);
       }
     }
   }
   if (a.q_t && at.m0 < pm) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < C; ++k) {
       float v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = acc[i][k % 2][k / 2];
+      for (int i = 0; i < 8; ++i) v[i] = acc[i][k % J][k / J];
       store_column<0, SC>(a.q_t, a.s_t, v, pm, m, f + k, F, at.m0 / kGroup, at.p);
     }
   }
 }
 
-// Gated backward: acc is dH; a lane has 16 neighbouring columns of F, taken 8
-// at a time.  dG and dU are formed twice from the saved G and U: for the
-// groups' largest magnitudes, then for the codes (kept, they would take twice the
-// registers of dH).
+// Gated backward: acc is dH; a lane has 4 FN neighbouring columns of F, taken 8
+// (or all) at a time.  dG and dU are formed twice from the saved G and U: for
+// the groups' largest magnitudes, then for the codes (kept, they would take
+// twice the registers of dH).  The multipliers of rows and columns wait in
+// shared memory.  A tile has whole groups of 128 columns, WG wavefronts each.
 template <int WM, int WN, int FN, int FMT, int SC>
 __device__ __forceinline__ void store_glu_bwd(const G8GemmArgs& a, const Place& at, f32x4_t (&acc)[8][FN],
                                               uint32_t* red) {
-  static_assert(FN == 4 && WN % 2 == 0, "two wavefronts a group of 128 columns");
+  constexpr int WG = 128 / (16 * FN);          // wavefronts of a group of columns
+  constexpr int C = 4 * FN < 8 ? 4 * FN : 8;   // columns at a time
+  constexpr int NH = 4 * FN / C;
+  static_assert(WN % WG == 0 && NH >= 1);
+  // [dG|dU] of a row of a wavefront's 128; then [dG|dU] multipliers of its 16 FN columns
+  constexpr int ROWS = 2 * 128, COLSX = 2 * 16 * FN;
+  uint32_t* rows = red + (at.wm * WN + at.wn) * (ROWS + COLSX);
+  float* cols = reinterpret_cast<float*>(rows + ROWS);
   const int64_t F = a.N, pf = padded(F), pm = padded(a.M), gf = pf / kGroup;
-  const int64_t f = at.n0 + at.wn * 64 + at.q * 16;
+  const int64_t f = at.n0 + at.wn * 16 * FN + at.q * 4 * FN;
   const int64_t m = at.m0 + 8 * at.p;
-  auto form = [&](int i, int hf, float dg[8], float du[8]) {
-    const int64_t c = f + 8 * hf;
-    if (m + i < a.M && c < F) {
-      float g[8], u[8];
-      Vec8<bf16_t>::load(a.Z, (m + i) * 2 * F + c, g);
-      Vec8<bf16_t>::load(a.Z, (m + i) * 2 * F + F + c, u);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float d = acc[i][k % 4][2 * hf + k / 4];
-        float act, slope;
-        gate_both(a.gate, g[k], act, slope);
-        dg[k] = d * u[k] * slope;
-        du[k] = d * act;
-      }
+  const Gate gate(a.gate);
+  auto form = [&](int i, int hf, float* dg, float* du) {
+    // (past the last row or column: another's G and U, and zeros)
+    const int64_t c = f + C * hf, row = min(m + i, a.M - 1) * 2 * F + min(c, F - C);
+    const bool there = m + i < a.M && c < F;
+    float g[C], u[C];
+    if constexpr (C == 8) {
+      Vec8<bf16_t>::load(a.Z, row, g);
+      Vec8<bf16_t>::load(a.Z, row + F, u);
     } else {
+      Store4<bf16_t>::load(a.Z, row, g);
+      Store4<bf16_t>::load(a.Z, row + F, u);
+    }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) dg[k] = du[k] = 0.0f;
+    for (int k = 0; k < C; ++k) {
+      const float d = acc[i][(C * hf + k) % FN][(C * hf + k) / FN];
+      float act, slope;
+      gate.both(g[k], act, slope);
+      dg[k] = there ? d * u[k] * slope : 0.0f;
+      du[k] = there ? d * act : 0.0f;
     }
   };
-  uint32_t rg[8], ru[8], cg[2][8], cu[2][8];
+  const int64_t token_group = at.m0 / kGroup;
+  const bool turned = a.q_t && at.m0 < pm;
+  uint32_t rg[8], ru[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    rg[i] = ru[i] = 0;
+  for (int i = 0; i < 8; ++i) rg[i] = ru[i] = 0;
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      float dg[8], du[8];
+  for (int hf = 0; hf < NH; ++hf) {
+    uint32_t cg[C], cu[C];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float dg[C], du[C];
       form(i, hf, dg, du);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < C; ++k) {
         const uint32_t x = mag(dg[k]), y = mag(du[k]);
         rg[i] = max(rg[i], x);
         ru[i] = max(ru[i], y);
-        cg[hf][k] = i ? max(cg[hf][k], x) : x;
-        cu[hf][k] = i ? max(cu[hf][k], y) : y;
+        cg[k] = i ? max(cg[k], x) : x;
+        cu[k] = i ? max(cu[k], y) : y;
+      }
+      if (i & 1) {  // (a few rows' loads at a time)
+        asm volatile("" : "+v"(rg[i]), "+v"(ru[i])::"memory");
+#pragma unroll
+        for (int k = 0; k < C; ++k) asm volatile("" : "+v"(cg[k]), "+v"(cu[k]));
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
-    __builtin_amdgcn_sched_barrier(0);  // (a few rows' loads at a time)
-  }
-  asm volatile("" ::: "memory");  // the second forming loads G and U again
-  if (a.q) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      rg[i] = xor_max(xor_max(rg[i], 16), 32);
-      ru[i] = xor_max(xor_max(ru[i], 16), 32);
-    }
-    uint32_t* mine = red + (at.wm * WN + at.wn) * 256;
-    if (at.q == 0) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        mine[8 * at.p + i] = rg[i];
-        mine[128 + 8 * at.p + i] = ru[i];
-      }
-    }
-    __syncthreads();
-    const uint32_t* other = red + (at.wm * WN + (at.wn ^ 1)) * 256;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      rg[i] = max(rg[i], other[8 * at.p + i]);
-      ru[i] = max(ru[i], other[128 + 8 * at.p + i]);
-    }
-    if (at.q == 0 && (at.wn & 1) == 0 && f < F) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (m + i < a.M) {
-          const int64_t g = f / kGroup;
-          GroupScale<FMT, SC>(rg[i]).store(a.s, g * a.M + m + i);
-          GroupScale<FMT, SC>(ru[i]).store(a.s, (gf + g) * a.M + m + i);
-        }
-    }
-  }
-  const int64_t token_group = at.m0 / kGroup;
-  const bool turned = a.q_t && at.m0 < pm;
-#pragma unroll
-  for (int hf = 0; hf < 2; ++hf) {
-    float ig[8], iu[8];
     if (a.q_t) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < C; ++k) {
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1) {
-          cg[hf][k] = xor_max(cg[hf][k], d);
-          cu[hf][k] = xor_max(cu[hf][k], d);
+          cg[k] = xor_max(cg[k], d);
+          cu[k] = xor_max(cu[k], d);
         }
-        const GroupScale<FMT, SC> sg(cg[hf][k]), su(cu[hf][k]);
-        ig[k] = sg.inv;
-        iu[k] = su.inv;
-        const int64_t c = f + 8 * hf + k;
-        if (turned && at.p == 0 && c < F) {
-          sg.store(a.s_t, token_group * F + c);
-          su.store(a.s_t, (pm / kGroup + token_group) * F + c);
+        if (at.p == 0) {
+          const GroupScale<FMT, SC> sg(cg[k]), su(cu[k]);
+          cols[at.q * 4 * FN + C * hf + k] = sg.inv;
+          cols[16 * FN + at.q * 4 * FN + C * hf + k] = su.inv;
+          const int64_t c = f + C * hf + k;
+          if (turned && c < F) {
+            sg.store(a.s_t, token_group * F + c);
+            su.store(a.s_t, (pm / kGroup + token_group) * F + c);
+          }
         }
       }
     }
-    uint32_t og[8][2], ou[8][2];  // codes of 8 columns: 8 rows in two words
+  }
 #pragma unroll
-    for (int i4 = 0; i4 < 2; ++i4) {
-      float dg[4][8], du[4][8];
+  for (int i = 0; i < 8; ++i) {
+    rg[i] = xor_max(xor_max(rg[i], 16), 32);
+    ru[i] = xor_max(xor_max(ru[i], 16), 32);
+    if (at.q == 0) {
+      rows[8 * at.p + i] = rg[i];
+      rows[128 + 8 * at.p + i] = ru[i];
+    }
+  }
+  __syncthreads();
+  // a row's largest over the wavefronts of its group
+  const uint32_t* peers = red + (at.wm * WN + at.wn / WG * WG) * (ROWS + COLSX);
+  auto row_scale = [&](int which, int i) {
+    uint32_t w = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 4 * i4 + i;
+    for (int k = 0; k < WG; ++k) w = max(w, peers[k * (ROWS + COLSX) + which * 128 + 8 * at.p + i]);
+    return GroupScale<FMT, SC>(w);
+  };
+  if (a.q && at.q == 0 && at.wn % WG == 0 && f < F) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (m + i < a.M) {
+        const int64_t g = f / kGroup;
+        row_scale(0, i).store(a.s, g * a.M + m + i);
+        row_scale(1, i).store(a.s, (gf + g) * a.M + m + i);
+      }
+  }
+#pragma unroll
+  for (int hf = 0; hf < NH; ++hf) {
+    const int64_t c = f + C * hf;
+    uint32_t og[C][2], ou[C][2];  // codes of C columns: 8 rows in two words
+#pragma unroll
+    for (int i2 = 0; i2 < 4; ++i2) {
+      float dg[2][C], du[2][C];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = 2 * i2 + i;
         form(r, hf, dg[i], du[i]);
-        if (a.q && m + r < a.M && f + 8 * hf < pf) {
-          const GroupScale<FMT, SC> sg(rg[r]), su(ru[r]);
-          const u32x2_t x = {codes4<FMT>(dg[i][0], dg[i][1], dg[i][2], dg[i][3], sg.inv),
-                             codes4<FMT>(dg[i][4], dg[i][5], dg[i][6], dg[i][7], sg.inv)};
-          const u32x2_t y = {codes4<FMT>(du[i][0], du[i][1], du[i][2], du[i][3], su.inv),
-                             codes4<FMT>(du[i][4], du[i][5], du[i][6], du[i][7], su.inv)};
-          *reinterpret_cast<u32x2_t*>(a.q + (m + r) * 2 * pf + f + 8 * hf) = x;
-          *reinterpret_cast<u32x2_t*>(a.q + (m + r) * 2 * pf + pf + f + 8 * hf) = y;
+        if (a.q && m + r < a.M && c < pf) {
+          const float ig = row_scale(0, r).inv, iu = row_scale(1, r).inv;
+          uint8_t* o = a.q + (m + r) * 2 * pf + c;
+#pragma unroll
+          for (int k = 0; k < C; k += 4) {
+            *reinterpret_cast<uint32_t*>(o + k) = codes4<FMT>(dg[i][k], dg[i][k + 1], dg[i][k + 2], dg[i][k + 3], ig);
+            *reinterpret_cast<uint32_t*>(o + pf + k) = codes4<FMT>(du[i][k], du[i][k + 1], du[i][k + 2], du[i][k + 3], iu);
+          }
         }
       }
       if (a.q_t) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          og[k][i4] = codes4<FMT>(dg[0][k], dg[1][k], dg[2][k], dg[3][k], ig[k]);
-          ou[k][i4] = codes4<FMT>(du[0][k], du[1][k], du[2][k], du[3][k], iu[k]);
+        for (int k = 0; k < C; ++k) {
+          const float ig = cols[at.q * 4 * FN + C * hf + k], iu = cols[16 * FN + at.q * 4 * FN + C * hf + k];
+          og[k][i2 / 2] = codes2<FMT>(dg[0][k], dg[1][k], ig, og[k][i2 / 2], i2 & 1);
+          ou[k][i2 / 2] = codes2<FMT>(du[0][k], du[1][k], iu, ou[k][i2 / 2], i2 & 1);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
+      asm volatile("" ::: "memory");
     }
     if (turned) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int64_t c = f + 8 * hf + k;
-        if (c < F) {
-          *reinterpret_cast<u32x2_t*>(a.q_t + c * pm + m) = (u32x2_t){og[k][0], og[k][1]};
-          *reinterpret_cast<u32x2_t*>(a.q_t + (F + c) * pm + m) = (u32x2_t){ou[k][0], ou[k][1]};
+      for (int k = 0; k < C; ++k) {
+        if (c + k < F) {
+          *reinterpret_cast<u32x2_t*>(a.q_t + (c + k) * pm + m) = (u32x2_t){og[k][0], og[k][1]};
+          *reinterpret_cast<u32x2_t*>(a.q_t + (F + c + k) * pm + m) = (u32x2_t){ou[k][0], ou[k][1]};
         }
       }
     }
@@ -340,20 +364,20 @@ __device__ __forceinline__ i32x8_t read_codes_scale(uint32_t a0, uint32_t a1, ui
 
 struct __attribute__((packed)) Bytes8 { uint32_t v[2]; };
 
-// Two tile buffers in shared memory: while one is multiplied the other's
-// loads (straight into shared memory) are on their way.
-template <int WM, int WN, int FN, int SC, bool SQ, int FMT_A, int FMT_B, int SUM, int EPI>
-__global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 ? 2 : 1) void gemm(G8GemmArgs a) {
+// The operands' tiles pass through NS buffers in shared memory: while one is
+// multiplied, the next ones' loads (straight into shared memory) are on their way.
+template <int WM, int WN, int FN, int NS, int SC, bool SQ, int FMT_A, int FMT_B, int SUM, int EPI>
+__global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FN == 4 ? 2 : 1) void gemm(G8GemmArgs a) {
   constexpr int BM = 128 * WM, BN = 16 * FN * WN, NW = WM * WN;
   constexpr bool PAIR = EPI == G_GLU_FWD;
   constexpr int COLS = PAIR ? BN / 2 : BN;  // columns of the output a tile has
   constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;  // 1 KiB loads of a wavefront (8 rows each)
   constexpr bool SLDS = SC == TP_GROUP_F32;          // row scales by way of shared memory
   constexpr int LOADS = LA + LB + (SLDS ? 1 : 0);
-  // [A 0 | A 1 | B 0 | B 1 | row scales 0 | 1]
+  // [A .. | B .. | row scales ..], NS of each
   constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, S_BYTES = SLDS ? BM * 4 : 0;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * (A_BYTES + B_BYTES + S_BYTES)];
-  constexpr int B_AT = 2 * A_BYTES, S_AT = B_AT + 2 * B_BYTES;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * (A_BYTES + B_BYTES + S_BYTES)];
+  constexpr int B_AT = NS * A_BYTES, S_AT = B_AT + NS * B_BYTES;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
@@ -431,10 +455,12 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 ? 2 : 1) void gemm(G8Gem
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
 
-  load_tile(0, 0);
-  if (kt_all > 1) load_tile(1, 1);
+  static_for<0, NS>([&](auto T) {
+    if (decltype(T)::value < kt_all) load_tile(decltype(T)::value, decltype(T)::value);
+  });
+  int buf = 0;
   for (int kt = 0; kt < kt_all; ++kt) {
-    const int part = kt >= kt_part ? 1 : 0, kb = kt - part * kt_part, buf = kt & 1;
+    const int part = kt >= kt_part ? 1 : 0, kb = kt - part * kt_part;
     auto sb_src = [&](int j) { return PAIR ? (j < FN / 2 ? a.sB : a.sB2) : (part ? a.sB2 : a.sB); };
     auto scale_b = [&](int b, int j) {
       const int64_t n = min(col_of(b, j), (int64_t)a.N - 1);
@@ -463,8 +489,11 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 ? 2 : 1) void gemm(G8Gem
         for (int i = 0; i < 8; ++i) ea[i >> 2] |= (uint32_t)s[min(mr + i, a.M - 1)] << (8 * (i & 3));
       }
     }
-    // this tile is there; the next one's loads may still be on their way
-    if (kt + 1 < kt_all) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory");
+    // this tile is there; the next ones' loads may still be on their way
+    const int ahead = kt_all - 1 - kt;
+    if (ahead >= NS - 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS * (NS - 1)) : "memory");
+    else if (NS > 3 && ahead == 2) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS * 2) : "memory");
+    else if (NS > 2 && ahead == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory");
     else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
@@ -528,10 +557,11 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 ? 2 : 1) void gemm(G8Gem
       for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(acc[i][j]));
       __builtin_amdgcn_sched_barrier(0);
     });
-    // every wavefront has read this tile: its buffer takes the one after next
+    // every wavefront has read this tile: its buffer takes the one NS on
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
-    if (kt + 2 < kt_all) load_tile(kt + 2, buf);
+    if (kt + NS < kt_all) load_tile(kt + NS, buf);
+    buf = buf + 1 == NS ? 0 : buf + 1;
   }
 
   uint32_t* red = reinterpret_cast<uint32_t*>(lds);
@@ -540,7 +570,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 ? 2 : 1) void gemm(G8Gem
   else store_plain<WM, WN, FN>(a, at, acc);
 }
 
-template <int WM, int WN, int FN, int SC, bool SQ, int FMT_A, int FMT_B, int SUM, int EPI>
+template <int WM, int WN, int FN, int NS, int SC, bool SQ, int FMT_A, int FMT_B, int SUM, int EPI>
 static hipError_t launch(G8GemmArgs& a, hipStream_t st) {
   constexpr int BM = 128 * WM, BN = EPI == G_GLU_FWD ? 8 * FN * WN : 16 * FN * WN;
   const int64_t tm = (a.M + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
@@ -548,7 +578,7 @@ static hipError_t launch(G8GemmArgs& a, hipStream_t st) {
   a.tiles_m = (int)tm;
   a.tiles_n = (int)tn;
   if (tm * tn == 0) return hipSuccess;
-  hipLaunchKernelGGL((gemm<WM, WN, FN, SC, SQ, FMT_A, FMT_B, SUM, EPI>), dim3((unsigned)(tm * tn)),
+  hipLaunchKernelGGL((gemm<WM, WN, FN, NS, SC, SQ, FMT_A, FMT_B, SUM, EPI>), dim3((unsigned)(tm * tn)),
                      dim3(64 * WM * WN), 0, st, a);
   return hipGetLastError();
 }
