@@ -45,7 +45,7 @@ hipError_t g8_glu_fwd_launch(int scale, G8GemmArgs& a, hipStream_t st);
 hipError_t g8_glu_bwd_launch(int fmt, int scale, G8GemmArgs& a, hipStream_t st);
 
 // The few-token kernels: which calls they take, and the calls
-bool g8_few(int64_t M);
+bool g8_few(int64_t M, int64_t N, int64_t K);
 hipError_t g8_gemm_few_launch(int fmt_a, int fmt_b, int scale, int square, const G8GemmArgs& a, hipStream_t st);
 hipError_t g8_glu_fwd_few_launch(int scale, const G8GemmArgs& a, hipStream_t st);
 hipError_t g8_glu_bwd_few_launch(int fmt, int scale, const G8GemmArgs& a, hipStream_t st);

@@ -45,7 +45,7 @@ int check_glu(const tp_fp8g_glu_desc* d, bool backward) {
 
 // few tokens: the fp32 values between the product and their quantization
 size_t glu_workspace(const tp_fp8g_glu_desc& d, bool backward) {
-  const size_t need = g8_few(d.N) ? (size_t)d.N * (size_t)d.F * (backward ? 8 : 4) : 0;
+  const size_t need = g8_few(d.N, d.F, d.H) ? (size_t)d.N * (size_t)d.F * (backward ? 8 : 4) : 0;
   return need < 16 ? 16 : need;
 }
 
@@ -118,7 +118,7 @@ int tp_fp8g_gemm(const tp_fp8g_gemm_desc* desc, const void* A, const void* sA, c
   if (d.M == 0) return ok();
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   hipError_t he = timed(st, [&] {
-    if (g8_few(d.M)) return g8_gemm_few_launch(d.fmt_a, d.fmt_b, d.scale, d.square, a, st);
+    if (g8_few(d.M, d.N, d.K * d.parts)) return g8_gemm_few_launch(d.fmt_a, d.fmt_b, d.scale, d.square, a, st);
     return (a.out_bf16 ? g8_gemm_bf16_launch : g8_gemm_f32_launch)(d.fmt_a, d.fmt_b, d.scale, d.square, a, st);
   });
   if (he != hipSuccess) return hip_fail(he, "group-scaled product launch");
@@ -158,7 +158,7 @@ int tp_fp8g_glu_fwd(const tp_fp8g_glu_desc* desc, const void* X, const void* sX,
   a.Z = Z_save; a.H = H_act; a.gate = d.gate;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   hipError_t he = timed(st, [&] {
-    if (!g8_few(d.N)) {
+    if (!g8_few(d.N, d.F, d.H)) {
       a.q = (uint8_t*)Hq; a.q_t = (uint8_t*)Hq_t; a.s = sH; a.s_t = sH_t;
       return g8_glu_fwd_launch(d.scale, a, st);
     }
@@ -204,7 +204,7 @@ int tp_fp8g_glu_bwd(const tp_fp8g_glu_desc* desc, const void* dY, const void* sd
   a.Z = const_cast<void*>(Z_save); a.gate = d.gate;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   hipError_t he = timed(st, [&] {
-    if (!g8_few(d.N)) {
+    if (!g8_few(d.N, d.F, d.H)) {
       a.q = (uint8_t*)dZ; a.q_t = (uint8_t*)dZ_t; a.s = sdZ; a.s_t = sdZ_t;
       return g8_glu_bwd_launch(d.fmt, d.scale, a, st);
     }

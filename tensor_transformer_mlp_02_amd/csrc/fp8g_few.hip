@@ -11,11 +11,14 @@
 // fixed order.  Rows past the last are read as the last one and not stored.
 #include "fp8g.h"
 
+#ifndef G8_NW
+#define G8_NW 4
+#endif
 namespace tpmlp {
 namespace g8 {
 
 enum { F_STORE = 0, F_GLU_FWD = 1, F_GLU_BWD = 2 };
-constexpr int FEW_MAX = 64, FEW_WAVES = 4;
+constexpr int FEW_ROWS = 64;  // of A, at most, a workgroup
 
 __device__ __forceinline__ i32x8_t load_codes(const uint8_t* p) {
   const i32x4_t lo = *reinterpret_cast<const i32x4_t*>(p);
@@ -23,23 +26,24 @@ __device__ __forceinline__ i32x8_t load_codes(const uint8_t* p) {
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-template <int MT, int SC, bool SQ, int FMT_A, int FMT_B, int EPI>
-__global__ __launch_bounds__(64 * FEW_WAVES) void gemm_few(G8GemmArgs a) {
+template <int MT, int NW, int SC, bool SQ, int FMT_A, int FMT_B, int EPI>
+__global__ __launch_bounds__(64 * NW) void gemm_few(G8GemmArgs a) {
   constexpr int MATS = EPI == F_GLU_FWD ? 2 : 1;
   constexpr int U = MT <= 2 ? 4 : 2;  // groups on their way at a time
-  __shared__ f32x4_t red[FEW_WAVES][MATS][MT][64];
+  __shared__ f32x4_t red[NW][MATS][MT][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int p = lane & 15, q = lane >> 4;
   const int n0 = blockIdx.x * 16;
-  const int M = (int)a.M;
+  const int64_t m_first = (int64_t)blockIdx.y * FEW_ROWS;
+  const int64_t M = a.M;
   const int n = min(n0 + p, a.N - 1);
   const int kt_part = a.K / kGroup, kt_all = kt_part * a.parts;
   const uint8_t* xrow[MT];
-  int m[MT];
+  int64_t m[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
-    m[i] = min(16 * i + p, M - 1);
+    m[i] = min(m_first + 16 * i + p, M - 1);
     xrow[i] = a.A + m[i] * a.lda + 32 * q;
   }
   f32x4_t acc[MATS][MT];
@@ -48,13 +52,13 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void gemm_few(G8GemmArgs a) {
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[w][i] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
 
-  for (int k0 = wave; k0 < kt_all; k0 += FEW_WAVES * U) {
+  for (int k0 = wave; k0 < kt_all; k0 += NW * U) {
     i32x8_t fb[U][MATS], fa[U][MT];
     float sa[U][MT], sb[U][MATS][SQ ? 1 : 4];
     int ea[U][MT], eb[U][MATS];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int kt = min(k0 + u * FEW_WAVES, kt_all - 1);
+      const int kt = min(k0 + u * NW, kt_all - 1);
       const int part = kt >= kt_part ? 1 : 0, kb = kt - part * kt_part;
 #pragma unroll
       for (int w = 0; w < MATS; ++w) {
@@ -82,7 +86,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void gemm_few(G8GemmArgs a) {
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (k0 + u * FEW_WAVES >= kt_all) break;
+      if (k0 + u * NW >= kt_all) break;
       bf16x8g_t wb[MATS][4];
 #pragma unroll
       for (int w = 0; w < MATS; ++w)
@@ -125,11 +129,11 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void gemm_few(G8GemmArgs a) {
   for (int w = 0; w < MATS; ++w) {
     f32x4_t s = red[0][w][wave][lane];
 #pragma unroll
-    for (int c = 1; c < FEW_WAVES; ++c) s += red[c][w][wave][lane];
+    for (int c = 1; c < NW; ++c) s += red[c][w][wave][lane];
 #pragma unroll
     for (int t = 0; t < 4; ++t) v[w][t] = s[t];
   }
-  const int64_t row = 16 * wave + p;
+  const int64_t row = m_first + 16 * wave + p;
   const int col = n0 + 4 * q;
   if (row >= M || col >= a.N) return;
   const int64_t off = row * a.N + col;
@@ -172,14 +176,17 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void gemm_few(G8GemmArgs a) {
   }
 }
 
+template <int MT, int SC, bool SQ, int FMT_A, int FMT_B, int EPI>
+static hipError_t few_run(const G8GemmArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)((a.N + 15) / 16), (unsigned)((a.M + FEW_ROWS - 1) / FEW_ROWS));
+  hipLaunchKernelGGL((gemm_few<MT, G8_NW, SC, SQ, FMT_A, FMT_B, EPI>), grid, dim3(64 * G8_NW), 0, st, a);
+  return hipGetLastError();
+}
 template <int SC, bool SQ, int FMT_A, int FMT_B, int EPI>
 static hipError_t few(const G8GemmArgs& a, hipStream_t st) {
-  if (a.M == 0) return hipSuccess;
-  const dim3 grid((unsigned)((a.N + 15) / 16)), block(64 * FEW_WAVES);
-  if (a.M <= 16) hipLaunchKernelGGL((gemm_few<1, SC, SQ, FMT_A, FMT_B, EPI>), grid, block, 0, st, a);
-  else if (a.M <= 32) hipLaunchKernelGGL((gemm_few<2, SC, SQ, FMT_A, FMT_B, EPI>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((gemm_few<4, SC, SQ, FMT_A, FMT_B, EPI>), grid, block, 0, st, a);
-  return hipGetLastError();
+  if (a.M <= 16) return few_run<1, SC, SQ, FMT_A, FMT_B, EPI>(a, st);
+  if (a.M <= 32) return few_run<2, SC, SQ, FMT_A, FMT_B, EPI>(a, st);
+  return few_run<4, SC, SQ, FMT_A, FMT_B, EPI>(a, st);
 }
 
 template <int SC, bool SQ>
@@ -192,7 +199,10 @@ static hipError_t few_formats(int fa, int fb, const G8GemmArgs& a, hipStream_t s
 
 }  // namespace g8
 
-bool g8_few(int64_t M) { return M <= g8::FEW_MAX; }
+#ifndef G8_FEW
+#define G8_FEW (M <= 64)
+#endif
+bool g8_few(int64_t M, int64_t N, int64_t K) { return G8_FEW; }
 
 hipError_t g8_gemm_few_launch(int fmt_a, int fmt_b, int scale, int square, const G8GemmArgs& a, hipStream_t st) {
   using namespace g8;

@@ -8,7 +8,10 @@ namespace g8 {
 template <int SC, bool SQ, int FMT_A, int FMT_B>
 static hipError_t launch_plain(G8GemmArgs& a, hipStream_t st) {
   const int64_t big = ((a.M + 255) / 256) * ((a.N + 255) / 256);
-  if (big >= 192) return launch<2, 4, 4, 2, SC, SQ, FMT_A, FMT_B, SUM_FP8, G_STORE>(a, st);
+  // (fp32 scales for each column: no registers for them beside a large tile's sums)
+  if constexpr (SC == TP_GROUP_E8M0 || SQ) {
+    if (big >= 192) return launch<2, 4, 4, 2, SC, SQ, FMT_A, FMT_B, SUM_FP8, G_STORE>(a, st);
+  }
   return launch<1, 4, 2, 4, SC, SQ, FMT_A, FMT_B, SUM_FP8, G_STORE>(a, st);
 }
 template <int SC, bool SQ>

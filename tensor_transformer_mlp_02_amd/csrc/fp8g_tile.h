@@ -344,25 +344,40 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
 }
 
-// The 32 codes of a block's row that a lane has, waited for in the same
-// place; with them, a row's scale
-template <int OFF>
-__device__ __forceinline__ i32x8_t read_codes(uint32_t a0, uint32_t a1) {
+// The 32 codes of a block's row that a lane has, and the row's scale: asked
+// for, and later waited for.  In between nothing may touch the registers
+// (they have not arrived): what comes between is arithmetic on others.
+struct Row {
   i32x4_t lo, hi;
-  asm volatile("ds_read_b128 %0, %2 offset:%4\n\tds_read_b128 %1, %3 offset:%4\n\ts_waitcnt lgkmcnt(0)"
-               : "=&v"(lo), "=&v"(hi) : "v"(a0), "v"(a1), "n"(OFF) : "memory");
-  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-template <int OFF, int SOFF>
-__device__ __forceinline__ i32x8_t read_codes_scale(uint32_t a0, uint32_t a1, uint32_t as, float& s) {
-  i32x4_t lo, hi;
-  asm volatile("ds_read_b128 %0, %3 offset:%6\n\tds_read_b128 %1, %4 offset:%6\n\tds_read_b32 %2, %5 offset:%7\n\t"
-               "s_waitcnt lgkmcnt(0)"
-               : "=&v"(lo), "=&v"(hi), "=&v"(s) : "v"(a0), "v"(a1), "v"(as), "n"(OFF), "n"(SOFF) : "memory");
-  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-}
+  float s;
+  template <int OFF>
+  __device__ __forceinline__ void ask(uint32_t a0, uint32_t a1) {
+    asm volatile("ds_read_b128 %0, %2 offset:%4\n\tds_read_b128 %1, %3 offset:%4"
+                 : "=&v"(lo), "=&v"(hi) : "v"(a0), "v"(a1), "n"(OFF) : "memory");
+  }
+  template <int OFF, int SOFF>
+  __device__ __forceinline__ void ask(uint32_t a0, uint32_t a1, uint32_t as) {
+    asm volatile("ds_read_b128 %0, %3 offset:%6\n\tds_read_b128 %1, %4 offset:%6\n\tds_read_b32 %2, %5 offset:%7"
+                 : "=&v"(lo), "=&v"(hi), "=&v"(s) : "v"(a0), "v"(a1), "v"(as), "n"(OFF), "n"(SOFF) : "memory");
+  }
+  __device__ __forceinline__ void wait() { asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(lo), "+v"(hi)::"memory"); }
+  __device__ __forceinline__ void wait_scale() {
+    asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(lo), "+v"(hi), "+v"(s)::"memory");
+  }
+  __device__ __forceinline__ i32x8_t codes() const { return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7); }
+};
 
-struct __attribute__((packed)) Bytes8 { uint32_t v[2]; };
+// Scales that a wavefront shares, through the scalar cache: their loads do
+// not wait behind the operands' on their way to shared memory
+typedef __attribute__((address_space(4))) const float const_float_t;
+typedef __attribute__((address_space(4))) const uint32_t const_u32_t;
+__device__ __forceinline__ float scalar_f32(const void* p, int64_t i) {
+  return ((const_float_t*)(uintptr_t)p)[i];
+}
+__device__ __forceinline__ uint32_t scalar_byte(const void* p, int64_t i) {
+  const uintptr_t at = (uintptr_t)p + (uintptr_t)i;
+  return (((const_u32_t*)(at & ~(uintptr_t)3))[0] >> (8 * (at & 3))) & 255u;
+}
 
 // The operands' tiles pass through NS buffers in shared memory: while one is
 // multiplied, the next ones' loads (straight into shared memory) are on their way.
@@ -438,16 +453,61 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FN == 4 ? 2 : 1) void
 
   // what a lane reads: chunks 2 q and 2 q + 1 of its rows
   const uint32_t l0 = lds_address(lds);
-  const uint32_t c0 = ((2 * at.q) ^ (at.p & 7)) << 4, c1 = c0 ^ 16;
-  uint32_t pa = l0 + (at.wm * 128 + 8 * at.p) * 128, pb = l0 + B_AT + (at.wn * 16 * FN + at.p * RB) * 128;
-  uint32_t ps = l0 + S_AT + (at.wm * 128 + 8 * at.p) * 4;
+  const uint32_t c0 = ((2 * at.q) ^ (at.p & 7)) << 4;
+  const uint32_t pa = l0 + (at.wm * 128 + 8 * at.p) * 128 + c0, pb = l0 + B_AT + (at.wn * 16 * FN + at.p * RB) * 128 + c0;
+  const uint32_t ps = l0 + S_AT + (at.wm * 128 + 8 * at.p) * 4;
 
-  // column of index b of block j, and its scale's place
-  auto col_of = [&](int b, int j) -> int64_t {
-    return PAIR ? at.n0 + at.wn * 8 * FN + b * RB + j % RB : at.n0 + at.wn * 16 * FN + b * FN + j;
+  // Scales of a tile: of its columns, and E8M0 ones of its rows.  Those of a
+  // lane are neighbours, behind one offset from a base that a wavefront
+  // shares; past the last row or column they read as zeros.
+  constexpr int SBT = SC == TP_GROUP_F32 && !SQ ? 4 : 1;
+  struct Scales {
+    float b[SC == TP_GROUP_F32 ? SBT : 1][SC == TP_GROUP_F32 ? FN : 1];
+    uint32_t eb, ea[2];
   };
-  const int64_t mr = at.m0 + 8 * at.p;
-  const bool whole = at.m0 + 128 <= a.M;  // every row of the wavefront is there
+  const int nw = PAIR ? at.n0 + at.wn * 8 * FN : at.n0 + at.wn * 16 * FN;  // the wavefront's first column
+  const int rows_w = (int)max((int64_t)0, min((int64_t)128, a.M - at.m0)), cols_w = max(0, min(16 * FN, a.N - nw));
+  const int64_t square = (int64_t)(min(nw, a.N - 1) / kGroup) * kt_part;
+  auto load_scales = [&](int kt, Scales& s) {
+    const int part = kt >= kt_part ? 1 : 0, kb = kt - part * kt_part;
+    auto from = [&](int j) { return PAIR ? (j < FN / 2 ? a.sB : a.sB2) : (part ? a.sB2 : a.sB); };
+    if constexpr (SC == TP_GROUP_F32) {
+      if constexpr (SQ) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) s.b[0][j] = scalar_f32(from(j), square + kb);
+      } else {
+        const rsrc_t rs = buffer_of(reinterpret_cast<const float*>(from(0)) + (int64_t)kb * a.N + nw, cols_w * 4);
+#pragma unroll
+        for (int k = 0; k < 4 * FN; k += 4) {  // column FN t + j of the lane's 4 FN
+          const u32x4_t w = __builtin_amdgcn_raw_buffer_load_b128(rs, (at.q * 4 * FN + k) * 4, 0, 0);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s.b[(k + c) / FN][(k + c) % FN] = __uint_as_float(w[c]);
+        }
+      }
+    } else {
+      s.eb = 0;
+      if constexpr (SQ) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) s.eb |= scalar_byte(from(j), square + kb) << (8 * j);
+      } else {
+        const rsrc_t rs = buffer_of(reinterpret_cast<const uint8_t*>(from(0)) + (int64_t)kb * a.N + nw, cols_w);
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          s.eb |= (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rs, at.p * FN + j, 0, 0) << (8 * j);
+      }
+      const rsrc_t rs = buffer_of(reinterpret_cast<const uint8_t*>(a.sA) + (int64_t)kt * a.M + at.m0, rows_w);
+      s.ea[0] = s.ea[1] = 0;
+      if (rows_w == 128) {
+        const u32x2_t w = __builtin_amdgcn_raw_buffer_load_b64(rs, 8 * at.p, 0, 0);
+        s.ea[0] = w[0];
+        s.ea[1] = w[1];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          s.ea[i >> 2] |= (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rs, 8 * at.p + i, 0, 0) << (8 * (i & 3));
+      }
+    }
+  };
 
   f32x4_t acc[8][FN];
 #pragma unroll
@@ -455,114 +515,138 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FN == 4 ? 2 : 1) void
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
 
+  Scales sc, sc_next;
+  load_scales(0, sc_next);
   static_for<0, NS>([&](auto T) {
     if (decltype(T)::value < kt_all) load_tile(decltype(T)::value, decltype(T)::value);
   });
-  int buf = 0;
-  for (int kt = 0; kt < kt_all; ++kt) {
-    const int part = kt >= kt_part ? 1 : 0, kb = kt - part * kt_part;
-    auto sb_src = [&](int j) { return PAIR ? (j < FN / 2 ? a.sB : a.sB2) : (part ? a.sB2 : a.sB); };
-    auto scale_b = [&](int b, int j) {
-      const int64_t n = min(col_of(b, j), (int64_t)a.N - 1);
-      return SQ ? n / kGroup * kt_part + kb : (int64_t)kb * a.N + n;
-    };
-    // column scales (and E8M0 row scales) of this tile
-    constexpr int SBT = SC == TP_GROUP_F32 && !SQ ? 4 : 1;
-    float sb[SBT][FN];
-    uint32_t eb = 0, ea[2] = {0, 0};
-    if constexpr (SC == TP_GROUP_F32) {
-#pragma unroll
-      for (int j = 0; j < FN; ++j)
-#pragma unroll
-        for (int t = 0; t < SBT; ++t)
-          sb[t][j] = reinterpret_cast<const float*>(sb_src(j))[scale_b(SQ ? 0 : 4 * at.q + t, j)];
-    } else {
-#pragma unroll
-      for (int j = 0; j < FN; ++j) eb |= (uint32_t)reinterpret_cast<const uint8_t*>(sb_src(j))[scale_b(SQ ? 0 : at.p, j)] << (8 * j);
-      const uint8_t* s = reinterpret_cast<const uint8_t*>(a.sA) + (int64_t)kt * a.M;
-      if (whole) {
-        const Bytes8 w = *reinterpret_cast<const Bytes8*>(s + mr);
-        ea[0] = w.v[0];
-        ea[1] = w.v[1];
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ea[i >> 2] |= (uint32_t)s[min(mr + i, a.M - 1)] << (8 * (i & 3));
-      }
-    }
-    // this tile is there; the next ones' loads may still be on their way
-    const int ahead = kt_all - 1 - kt;
-    if (ahead >= NS - 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS * (NS - 1)) : "memory");
-    else if (NS > 3 && ahead == 2) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS * 2) : "memory");
-    else if (NS > 2 && ahead == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory");
+  // waits until at most `tiles` of the newest tiles' loads are on their way
+  auto wait_tiles = [&](int tiles) {
+    if (NS > 3 && tiles >= 3) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS * 3) : "memory");
+    else if (NS > 2 && tiles == 2) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS * 2) : "memory");
+    else if (tiles == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory");
     else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+  };
+  wait_tiles(min(kt_all, NS) - 1);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 
-    const uint32_t a0 = pa + buf * A_BYTES + c0, a1 = pa + buf * A_BYTES + c1, as = ps + buf * S_BYTES;
-    const uint32_t b0 = pb + buf * B_BYTES + c0, b1 = pb + buf * B_BYTES + c1;
-    i32x8_t fb[FN];
-    bf16x8g_t wb[SUM == SUM_F32 ? FN : 1][4];
-    static_for<0, FN>([&](auto J) {
-      constexpr int j = decltype(J)::value;
-      fb[j] = read_codes<PAIR ? (j / RB) * 16 * RB * 128 + (j % RB) * 128 : j * 128>(b0, b1);
-      if constexpr (SUM == SUM_F32) {
+  Row ra0, ra1;  // the rows of two steps in turn
+  i32x8_t fb[SUM == SUM_FP8 ? FN : 1];
+  bf16x8g_t wb[SUM == SUM_F32 ? FN : 1][4];
+  auto offset_b = [](int j) constexpr { return PAIR ? (j / RB) * 16 * RB * 128 + (j % RB) * 128 : j * 128; };
+  auto widen_b = [&](auto J, const Row& r, const Scales& s) {
+    constexpr int j = decltype(J)::value;
+    const i32x8_t f = r.codes();
+    if constexpr (SUM == SUM_FP8) {
+      fb[j] = f;
+    } else {
+      const float e = SC == TP_GROUP_F32 ? 1.0f : e8m0_f32((s.eb >> (8 * j)) & 255);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          wb[j][c] = widen<FMT_B>(fb[j][2 * c], fb[j][2 * c + 1], SC == TP_GROUP_F32 ? 1.0f : e8m0_f32((eb >> (8 * j)) & 255));
-      }
+      for (int c = 0; c < 4; ++c) wb[j][c] = widen<FMT_B>(f[2 * c], f[2 * c + 1], e);
+    }
+  };
+  auto ask_a = [&](auto I, Row& r, int buf) {
+    constexpr int i = decltype(I)::value;
+    const uint32_t a0 = pa + buf * A_BYTES;
+    if constexpr (SLDS) r.template ask<i * 128, i * 4>(a0, a0 ^ 16, ps + buf * S_BYTES);
+    else r.template ask<i * 128>(a0, a0 ^ 16);
+  };
+  auto wait_a = [&](Row& r) {
+    if constexpr (SLDS) r.wait_scale();
+    else r.wait();
+  };
+  auto load_b = [&](int buf, const Scales& s) {  // the wavefront's columns of a tile
+    const uint32_t b0 = pb + buf * B_BYTES;
+    static_for<0, FN>([&](auto J) {
+      Row r;
+      r.template ask<offset_b(decltype(J)::value)>(b0, b0 ^ 16);
+      r.wait();
+      widen_b(J, r, s);
     });
+  };
+
+  f32x4_t p[FN];
+  float sa = 0.0f;
+  auto add_group = [&](auto I, auto J) {
+    constexpr int i = decltype(I)::value, j = decltype(J)::value;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) acc[i][j][t] = fmaf(p[j][t], sa * sc.b[SQ ? 0 : t][j], acc[i][j][t]);
+    asm volatile("" : "+v"(acc[i][j]));  // (put off past the barrier, it would hold its registers)
+  };
+
+  int buf = 0;
+  sc = sc_next;
+  load_b(0, sc);
+  ask_a(std::integral_constant<int, 0>{}, ra0, 0);
+  for (int kt = 0; kt < kt_all; ++kt) {
+    const bool more = kt + 1 < kt_all;
+    const int buf_next = buf + 1 == NS ? 0 : buf + 1;
+    load_scales(more ? kt + 1 : kt, sc_next);
     static_for<0, 8>([&](auto I) {
       constexpr int i = decltype(I)::value;
-      float sa = 1.0f;
-      i32x8_t fa;
-      if constexpr (SLDS) fa = read_codes_scale<i * 128, i * 4>(a0, a1, as, sa);
-      else fa = read_codes<i * 128>(a0, a1);
+      Row& r = i & 1 ? ra1 : ra0;
+      Row& next = i & 1 ? ra0 : ra1;
+      wait_a(r);
+      if constexpr (i < 7) {
+        ask_a(std::integral_constant<int, (i + 1) & 7>{}, next, buf);
+      } else {
+        // the tile is read; the next one is there for every wavefront after
+        // this, and the buffer takes the one NS on
+        wait_tiles(max(0, min(kt_all - 2 - kt, NS - 2)));
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        // (behind the last tile: rows that nothing uses, so that every path asks)
+        ask_a(std::integral_constant<int, 0>{}, next, buf_next);
+        if (kt + NS < kt_all) load_tile(kt + NS, buf);
+      }
+      const i32x8_t fa = r.codes();
+      // fp32 scales: a step's group sums are scaled and added during the next
+      // step, when the instructions that make them have ended
       if constexpr (SUM == SUM_F32) {
-        if constexpr (SC == TP_GROUP_E8M0) sa = e8m0_f32((ea[i >> 2] >> (8 * (i & 3))) & 255);
-        f32x4_t p[FN];
-#pragma unroll
-        for (int j = 0; j < FN; ++j) p[j] = SC == TP_GROUP_F32 ? (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f} : acc[i][j];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const bf16x8g_t wa = widen<FMT_A>(fa[2 * c], fa[2 * c + 1], SC == TP_GROUP_F32 ? 1.0f : sa);
-#pragma unroll
-          for (int j = 0; j < FN; ++j) p[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][c], wa, p[j], 0, 0, 0);
-        }
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          if constexpr (SC == TP_GROUP_F32) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t) acc[i][j][t] = fmaf(p[j][t], sa * sb[SQ ? 0 : t][j], acc[i][j][t]);
-          } else {
-            acc[i][j] = p[j];
-          }
-        }
-      } else if constexpr (SC == TP_GROUP_F32) {
-        f32x4_t p[FN];
-#pragma unroll
-        for (int j = 0; j < FN; ++j) p[j] = mfma_plain<FMT_A, FMT_B>(fb[j], fa, (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f});
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-          for (int t = 0; t < 4; ++t) acc[i][j][t] = fmaf(p[j][t], sa * sb[SQ ? 0 : t][j], acc[i][j][t]);
+        float e = 1.0f;
+        if constexpr (SC == TP_GROUP_E8M0) e = e8m0_f32((sc.ea[i >> 2] >> (8 * (i & 3))) & 255);
+        static_for<0, 4>([&](auto Cc) {
+          constexpr int c = decltype(Cc)::value;
+          const bf16x8g_t wa = widen<FMT_A>(fa[2 * c], fa[2 * c + 1], e);
+          static_for<0, FN>([&](auto J) {
+            constexpr int j = decltype(J)::value;
+            if constexpr (SC == TP_GROUP_E8M0) {
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][c], wa, acc[i][j], 0, 0, 0);
+            } else {
+              if constexpr (c == 0 && i > 0) add_group(std::integral_constant<int, i - 1>{}, J);
+              p[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][c], wa, c ? p[j] : (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+            }
+          });
+          __builtin_amdgcn_sched_barrier(0);
+        });
       } else {
         static_for<0, FN>([&](auto J) {
           constexpr int j = decltype(J)::value;
-          acc[i][j] = mfma_scaled<FMT_A, FMT_B, i & 3, j>(fb[j], fa, acc[i][j], (int)eb, (int)ea[i >> 2]);
+          if constexpr (SC == TP_GROUP_F32) {
+            if constexpr (i > 0) add_group(std::integral_constant<int, i - 1>{}, J);
+            p[j] = mfma_plain<FMT_A, FMT_B>(fb[j], fa, (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f});
+          } else {
+            acc[i][j] = mfma_scaled<FMT_A, FMT_B, i & 3, j>(fb[j], fa, acc[i][j], (int)sc.eb, (int)sc.ea[i >> 2]);
+          }
         });
       }
-      // (the reads of later rows moved up, or these sums put off past the
-      // barrier, would need registers of their own)
+      if constexpr (SLDS) sa = r.s;
+      if constexpr (SC == TP_GROUP_E8M0) {
 #pragma unroll
-      for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(acc[i][j]));
+        for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(acc[i][j]));
+      }
       __builtin_amdgcn_sched_barrier(0);
     });
-    // every wavefront has read this tile: its buffer takes the one NS on
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    if (kt + NS < kt_all) load_tile(kt + NS, buf);
-    buf = buf + 1 == NS ? 0 : buf + 1;
+    if constexpr (SC == TP_GROUP_F32) {
+      static_for<0, FN>([&](auto J) { add_group(std::integral_constant<int, 7>{}, J); });
+    }
+    sc = sc_next;
+    load_b(buf_next, sc);
+    buf = buf_next;
   }
+  wait_a(ra0);
+  __syncthreads();
 
   uint32_t* red = reinterpret_cast<uint32_t*>(lds);
   if constexpr (EPI == G_GLU_FWD) store_glu_fwd<WM, WN, FN, SC>(a, at, acc, red);
