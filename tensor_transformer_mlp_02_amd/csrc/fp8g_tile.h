@@ -8,15 +8,13 @@
 // fp32 (TP_GROUP_F32), or the instruction applies the scales itself and
 // accumulates (TP_GROUP_E8M0).
 //
-// Rows and columns are dealt to the blocks so that a lane's outputs lie
-// together: block i's row index a is row 8 a + i of the wavefront's 128,
-// block j's column index b is column FN b + j.  The instruction is issued with
-// the B codes first, which leaves a lane (p = lane % 16, q = lane / 16) with
-// row index p and column indices 4 q .. 4 q + 3: in all 8 neighbouring rows x 4 FN
-// neighbouring columns.  So outputs are stored without a turn through shared
-// memory, a lane's 8 row scales are neighbours, a group of 128 tokens is one
-// wavefront's (its largest magnitude a reduction over 16 lanes) and the codes
-// of a transposed output are 8 bytes a lane.
+// Block i's row index a is row 8 a + i of the wavefront's 128, block j's column
+// index b is column 16 j + b.  The instruction is issued with the B codes first, which
+// leaves a lane (p = lane % 16, q = lane / 16) with row index p and column indices
+// 4 q .. 4 q + 3: in all 8 neighbouring rows x 4 neighbouring columns of each block j.  So
+// outputs are stored without a turn through shared memory, a lane's 8 row scales are neighbours,
+// a group of 128 tokens is one wavefront's (its largest magnitude a reduction
+// over 16 lanes) and the codes of a transposed output are 8 bytes a lane.
 //
 // Shared memory holds rows of 128 codes, the 16-byte chunk c of a row at
 // c ^ (the row's index a or b) % 8: the 8 lanes that are served together read 8
@@ -41,27 +39,32 @@ __device__ __forceinline__ f32x4_t mfma_plain(i32x8_t b, i32x8_t a, f32x4_t c) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, FMT_B, FMT_A, 0, 0, 0, 0);
 }
 
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+typedef __attribute__((address_space(3))) void lds_void_t;
+
+// a buffer of so many bytes: what is read behind its end is zeros
+__device__ __forceinline__ rsrc_t buffer_of(const void* p, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, bytes, 0x00020000);
+}
 struct Place {
   int64_t m0;  // first row of the wavefront
   int n0;      // first column of the workgroup's tile (of F, in the gated forward)
   int wm, wn, p, q;
 };
 
-// acc[i][j][t]: row m0 + 8 p + i; column (4 q + t) FN + j of the wavefront's
+// acc[i][j][t]: row m0 + 8 p + i; column 16 j + 4 q + t of the wavefront's
 template <int WM, int WN, int FN>
 __device__ __forceinline__ void store_plain(const G8GemmArgs& a, const Place& at, f32x4_t (&acc)[8][FN]) {
-  const int n = at.n0 + at.wn * 16 * FN + at.q * 4 * FN;
+  const int n = at.n0 + at.wn * 16 * FN + at.q * 4;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t m = at.m0 + 8 * at.p + i;
     if (m >= a.M) continue;
 #pragma unroll
-    for (int h = 0; h < FN; ++h) {  // 4 columns at a time (bf16: 8 where a lane has them)
-      float v[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = acc[i][(4 * h + k) % FN][(4 * h + k) / FN];
-      const int64_t off = m * a.N + n + 4 * h;
-      if (n + 4 * h >= a.N) continue;
+    for (int j = 0; j < FN; ++j) {
+      if (n + 16 * j >= a.N) continue;
+      float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+      const int64_t off = m * a.N + n + 16 * j;
       if (a.out_bf16) {
         Store4<bf16_t>::store(a.C, off, v);
       } else {
@@ -77,14 +80,11 @@ __device__ __forceinline__ void store_plain(const G8GemmArgs& a, const Place& at
   }
 }
 
-// The 8 codes that a lane has of one column (its 8 rows), from the column's
-// largest magnitude over the wavefront's 128 rows
+// The 8 codes that a lane has of one column (its 8 rows; `top` the largest
+// magnitude among them), by the largest over the wavefront's 128 rows
 template <int FMT, int SC>
-__device__ __forceinline__ void store_column(uint8_t* q_t, void* s_t, const float v[8], int64_t pm, int64_t m,
-                                             int64_t col, int64_t cols, int64_t token_group, int p) {
-  uint32_t top = mag(v[0]);
-#pragma unroll
-  for (int i = 1; i < 8; ++i) top = max(top, mag(v[i]));
+__device__ __forceinline__ void store_column(uint8_t* q_t, void* s_t, const float v[8], uint32_t top, int64_t pm,
+                                             int64_t m, int64_t col, int64_t cols, int64_t token_group, int p) {
 #pragma unroll
   for (int d = 1; d < 16; d <<= 1) top = xor_max(top, d);
   const GroupScale<FMT, SC> gs(top);
@@ -96,44 +96,39 @@ __device__ __forceinline__ void store_column(uint8_t* q_t, void* s_t, const floa
 }
 
 // Gated forward: blocks j < FN/2 hold the gate, the others the up projection, of the
-// same columns f = (4 q + t) FN/2 + j: 2 FN neighbouring ones.  The tile has 128 of them: one
-// group.
+// same columns 16 (j mod FN/2) + 4 q + t.  The tile has 128 of them: one group.
 template <int WM, int WN, int FN, int SC>
 __device__ __forceinline__ void store_glu_fwd(const G8GemmArgs& a, const Place& at, f32x4_t (&acc)[8][FN],
                                               uint32_t* red) {
-  constexpr int J = FN / 2, C = 2 * FN;
-  static_assert(8 * FN * WN == 128 && (C == 8 || C == 4), "one group of 128 columns");
+  constexpr int J = FN / 2;
+  static_assert(8 * FN * WN == 128, "one group of 128 columns");
   const int64_t F = a.N, pf = padded(F), pm = padded(a.M);
-  const int fl = at.wn * 8 * FN + at.q * C;
-  const int64_t f = at.n0 + fl;
+  const int64_t f = at.n0 + at.wn * 8 * FN + at.q * 4;
   const int64_t m = at.m0 + 8 * at.p;
   const Gate gate(a.gate);
-  auto put = [&](void* to, int64_t off, const float* v) {
-    if constexpr (C == 8) Vec8<bf16_t>::store(to, off, v);
-    else Store4<bf16_t>::store(to, off, v);
-  };
   uint32_t top[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    float h[C];
-    if (a.Z && m + i < a.M && f < F) {
-      float g[C], u[C];
-#pragma unroll
-      for (int k = 0; k < C; ++k) {
-        g[k] = acc[i][k % J][k / J];
-        u[k] = acc[i][J + k % J][k / J];
-      }
-      put(a.Z, (m + i) * 2 * F + f, g);
-      put(a.Z, (m + i) * 2 * F + F + f, u);
-    }
     top[i] = 0;
 #pragma unroll
-    for (int k = 0; k < C; ++k) {
-      h[k] = gate.act(acc[i][k % J][k / J]) * acc[i][J + k % J][k / J];
-      acc[i][k % J][k / J] = h[k];
-      top[i] = max(top[i], mag(h[k]));
+    for (int j = 0; j < J; ++j) {
+      const int64_t c = f + 16 * j;
+      const bool there = m + i < a.M && c < F;
+      float g[4], u[4], h[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        g[t] = acc[i][j][t];
+        u[t] = acc[i][J + j][t];
+        h[t] = gate.act(g[t]) * u[t];
+        acc[i][j][t] = h[t];
+        top[i] = max(top[i], mag(h[t]));
+      }
+      if (a.Z && there) {
+        Store4<bf16_t>::store(a.Z, (m + i) * 2 * F + c, g);
+        Store4<bf16_t>::store(a.Z, (m + i) * 2 * F + F + c, u);
+      }
+      if (a.H && there) Store4<bf16_t>::store(a.H, (m + i) * F + c, h);
     }
-    if (a.H && m + i < a.M && f < F) put(a.H, (m + i) * F + f, h);
   }
   if (a.q) {
     // the group's largest magnitude of each row: 4 lanes, then the wavefronts
@@ -153,193 +148,162 @@ __device__ __forceinline__ void store_glu_fwd(const G8GemmArgs& a, const Place& 
       const GroupScale<0, SC> gs(w);
       if (m + i < a.M) {
 #pragma unroll
-        for (int k = 0; k < C; k += 4)
-          *reinterpret_cast<uint32_t*>(a.q + (m + i) * pf + f + k) =
-              codes4<0>(acc[i][k % J][k / J], acc[i][(k + 1) % J][(k + 1) / J], acc[i][(k + 2) % J][(k + 2) / J],
-                        acc[i][(k + 3) % J][(k + 3) / J], gs.inv);
-        if (fl == 0) gs.store(a.s, (int64_t)(at.n0 / kGroup) * a.M + m + i);
+        for (int j = 0; j < J; ++j)
+          *reinterpret_cast<uint32_t*>(a.q + (m + i) * pf + f + 16 * j) =
+              codes4<0>(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3], gs.inv);
+        if (at.wn == 0 && at.q == 0) gs.store(a.s, (int64_t)(at.n0 / kGroup) * a.M + m + i);
       }
     }
   }
   if (a.q_t && at.m0 < pm) {
 #pragma unroll
-    for (int k = 0; k < C; ++k) {
-      float v[8];
+    for (int j = 0; j < J; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = acc[i][k % J][k / J];
-      store_column<0, SC>(a.q_t, a.s_t, v, pm, m, f + k, F, at.m0 / kGroup, at.p);
-    }
+      for (int t = 0; t < 4; ++t) {
+        float v[8];
+        uint32_t col = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[i] = acc[i][j][t];
+          col = max(col, mag(v[i]));
+        }
+        store_column<0, SC>(a.q_t, a.s_t, v, col, pm, m, f + 16 * j + t, F, at.m0 / kGroup, at.p);
+      }
   }
 }
 
-// Gated backward: acc is dH; a lane has 4 FN neighbouring columns of F, taken 8
-// (or all) at a time.  dG and dU are formed twice from the saved G and U: for
-// the groups' largest magnitudes, then for the codes (kept, they would take
-// twice the registers of dH).  The multipliers of rows and columns wait in
-// shared memory.  A tile has whole groups of 128 columns, WG wavefronts each.
+// Gated backward: acc is dH; a lane has 4 neighbouring columns of F of each of FN
+// blocks, taken block by block: dG and dU are formed from the saved G and U, and a column's codes
+// can be made at once.  A row's wait for the largest of its group: of 4
+// blocks the first two's dU waits in shared memory meanwhile, so that dG, dU and the
+// dH that is left fit the registers.  A tile has whole groups of 128 columns, WG wavefronts each.
+// Rows and columns past the last read as zeros and are not stored.
+template <int WM, int WN, int FN>
+constexpr int glu_bwd_shared() {  // bytes
+  return WM * WN * (2 * 128 * 4 + (FN == 4 ? 64 * 64 * 4 : 0));
+}
 template <int WM, int WN, int FN, int FMT, int SC>
 __device__ __forceinline__ void store_glu_bwd(const G8GemmArgs& a, const Place& at, f32x4_t (&acc)[8][FN],
-                                              uint32_t* red) {
+                                              uint8_t* shared) {
   constexpr int WG = 128 / (16 * FN);          // wavefronts of a group of columns
-  constexpr int C = 4 * FN < 8 ? 4 * FN : 8;   // columns at a time
-  constexpr int NH = 4 * FN / C;
-  static_assert(WN % WG == 0 && NH >= 1);
-  // [dG|dU] of a row of a wavefront's 128; then [dG|dU] multipliers of its 16 FN columns
-  constexpr int ROWS = 2 * 128, COLSX = 2 * 16 * FN;
-  uint32_t* rows = red + (at.wm * WN + at.wn) * (ROWS + COLSX);
-  float* cols = reinterpret_cast<float*>(rows + ROWS);
-  const int64_t F = a.N, pf = padded(F), pm = padded(a.M), gf = pf / kGroup;
-  const int64_t f = at.n0 + at.wn * 16 * FN + at.q * 4 * FN;
+  constexpr int C = 4, NH = FN, PARKED = FN == 4 ? 2 : 0;
+  static_assert(WN % WG == 0 && (FN == 1 || FN == 4));
+  const int wave = at.wm * WN + at.wn, lane = at.q * 16 + at.p;
+  uint32_t* red = reinterpret_cast<uint32_t*>(shared);  // [dG|dU] of each wavefront's 128 rows
+  f32x4_t* wait = reinterpret_cast<f32x4_t*>(shared + WM * WN * 1024) + (wave * 16) * 64 + lane;
+  const int F = a.N, pf = (int)padded(F), gf = pf / kGroup;
+  const int64_t pm = padded(a.M);
+  const int f = at.n0 + at.wn * 16 * FN + at.q * 4;
   const int64_t m = at.m0 + 8 * at.p;
+  const int rows = (int)max((int64_t)0, min((int64_t)128, a.M - at.m0));
+  const rsrc_t rz = buffer_of(reinterpret_cast<const bf16_t*>(a.Z) + at.m0 * 2 * F, rows * F * 4);
+  const rsrc_t rq = buffer_of(a.q + at.m0 * 2 * pf, a.q ? rows * pf * 2 : 0);
   const Gate gate(a.gate);
-  auto form = [&](int i, int hf, float* dg, float* du) {
-    // (past the last row or column: another's G and U, and zeros)
-    const int64_t c = f + C * hf, row = min(m + i, a.M - 1) * 2 * F + min(c, F - C);
-    const bool there = m + i < a.M && c < F;
-    float g[C], u[C];
-    if constexpr (C == 8) {
-      Vec8<bf16_t>::load(a.Z, row, g);
-      Vec8<bf16_t>::load(a.Z, row + F, u);
-    } else {
-      Store4<bf16_t>::load(a.Z, row, g);
-      Store4<bf16_t>::load(a.Z, row + F, u);
-    }
-#pragma unroll
-    for (int k = 0; k < C; ++k) {
-      const float d = acc[i][(C * hf + k) % FN][(C * hf + k) / FN];
-      float act, slope;
-      gate.both(g[k], act, slope);
-      dg[k] = there ? d * u[k] * slope : 0.0f;
-      du[k] = there ? d * act : 0.0f;
-    }
-  };
   const int64_t token_group = at.m0 / kGroup;
   const bool turned = a.q_t && at.m0 < pm;
+  float dg[NH][8][C], du[NH][8][C];
   uint32_t rg[8], ru[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) rg[i] = ru[i] = 0;
+  static_for<0, NH>([&](auto Hc) {
+    constexpr int hf = decltype(Hc)::value;
+    const int c = f + 16 * hf;
+    uint32_t cg[C] = {0, 0, 0, 0}, cu[C] = {0, 0, 0, 0};
+    static_for<0, 2>([&](auto Ic) {  // four rows' loads at a time
+      constexpr int i0 = 4 * decltype(Ic)::value;
+      u32x2_t zg[4], zu[4];
 #pragma unroll
-  for (int hf = 0; hf < NH; ++hf) {
-    uint32_t cg[C], cu[C];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float dg[C], du[C];
-      form(i, hf, dg, du);
-#pragma unroll
-      for (int k = 0; k < C; ++k) {
-        const uint32_t x = mag(dg[k]), y = mag(du[k]);
-        rg[i] = max(rg[i], x);
-        ru[i] = max(ru[i], y);
-        cg[k] = i ? max(cg[k], x) : x;
-        cu[k] = i ? max(cu[k], y) : y;
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t off = c < F ? (uint32_t)((8 * at.p + i0 + i) * 2 * F + c) * 2u : 0x80000000u;
+        zg[i] = __builtin_amdgcn_raw_buffer_load_b64(rz, off, 0, 0);
+        zu[i] = __builtin_amdgcn_raw_buffer_load_b64(rz, off, 2 * F, 0);
       }
-      if (i & 1) {  // (a few rows' loads at a time)
-        asm volatile("" : "+v"(rg[i]), "+v"(ru[i])::"memory");
 #pragma unroll
-        for (int k = 0; k < C; ++k) asm volatile("" : "+v"(cg[k]), "+v"(cu[k]));
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
-    if (a.q_t) {
+      for (int i = 0; i < 4; ++i) {
 #pragma unroll
-      for (int k = 0; k < C; ++k) {
-#pragma unroll
-        for (int d = 1; d < 16; d <<= 1) {
-          cg[k] = xor_max(cg[k], d);
-          cu[k] = xor_max(cu[k], d);
-        }
-        if (at.p == 0) {
-          const GroupScale<FMT, SC> sg(cg[k]), su(cu[k]);
-          cols[at.q * 4 * FN + C * hf + k] = sg.inv;
-          cols[16 * FN + at.q * 4 * FN + C * hf + k] = su.inv;
-          const int64_t c = f + C * hf + k;
-          if (turned && c < F) {
-            sg.store(a.s_t, token_group * F + c);
-            su.store(a.s_t, (pm / kGroup + token_group) * F + c);
-          }
+        for (int k = 0; k < C; ++k) {
+          const float g = __uint_as_float(k & 1 ? zg[i][k / 2] & 0xffff0000u : zg[i][k / 2] << 16);
+          const float u = __uint_as_float(k & 1 ? zu[i][k / 2] & 0xffff0000u : zu[i][k / 2] << 16);
+          const float d = acc[i0 + i][hf][k];
+          float act, slope;
+          gate.both(g, act, slope);
+          dg[hf][i0 + i][k] = d * u * slope;
+          du[hf][i0 + i][k] = d * act;
+          // (both maxima here and not put off: the magnitudes kept would take as many registers again)
+          const uint32_t x = mag(dg[hf][i0 + i][k]), y = mag(du[hf][i0 + i][k]);
+          rg[i0 + i] = max(rg[i0 + i], x);
+          ru[i0 + i] = max(ru[i0 + i], y);
+          cg[k] = max(cg[k], x);
+          cu[k] = max(cu[k], y);
         }
       }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) asm volatile("" : "+v"(cg[k]), "+v"(cu[k]), "+v"(rg[i0 + k]), "+v"(ru[i0 + k]));
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    if (turned) {
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        float v[8], w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[i] = dg[hf][i][k];
+          w[i] = du[hf][i][k];
+        }
+        store_column<FMT, SC>(a.q_t, a.s_t, v, cg[k], pm, m, c + k, F, token_group, at.p);
+        store_column<FMT, SC>(a.q_t + F * pm, reinterpret_cast<uint8_t*>(a.s_t) + F * (pm / kGroup) * (SC == TP_GROUP_F32 ? 4 : 1),
+                              w, cu[k], pm, m, c + k, F, token_group, at.p);
+      }
     }
-  }
+    if constexpr (hf < PARKED) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) wait[(8 * hf + i) * 64] = (f32x4_t){du[hf][i][0], du[hf][i][1], du[hf][i][2], du[hf][i][3]};
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  });
+  if (!a.q) return;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     rg[i] = xor_max(xor_max(rg[i], 16), 32);
     ru[i] = xor_max(xor_max(ru[i], 16), 32);
     if (at.q == 0) {
-      rows[8 * at.p + i] = rg[i];
-      rows[128 + 8 * at.p + i] = ru[i];
+      red[wave * 256 + 8 * at.p + i] = rg[i];
+      red[wave * 256 + 128 + 8 * at.p + i] = ru[i];
     }
   }
   __syncthreads();
   // a row's largest over the wavefronts of its group
-  const uint32_t* peers = red + (at.wm * WN + at.wn / WG * WG) * (ROWS + COLSX);
-  auto row_scale = [&](int which, int i) {
-    uint32_t w = 0;
+  const uint32_t* peers = red + (at.wm * WN + at.wn / WG * WG) * 256 + 8 * at.p;
+  static_for<0, 8>([&](auto Ic) {
+    constexpr int i = decltype(Ic)::value;
+    uint32_t tg = 0, tu = 0;
 #pragma unroll
-    for (int k = 0; k < WG; ++k) w = max(w, peers[k * (ROWS + COLSX) + which * 128 + 8 * at.p + i]);
-    return GroupScale<FMT, SC>(w);
-  };
-  if (a.q && at.q == 0 && at.wn % WG == 0 && f < F) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (m + i < a.M) {
-        const int64_t g = f / kGroup;
-        row_scale(0, i).store(a.s, g * a.M + m + i);
-        row_scale(1, i).store(a.s, (gf + g) * a.M + m + i);
-      }
-  }
-#pragma unroll
-  for (int hf = 0; hf < NH; ++hf) {
-    const int64_t c = f + C * hf;
-    uint32_t og[C][2], ou[C][2];  // codes of C columns: 8 rows in two words
-#pragma unroll
-    for (int i2 = 0; i2 < 4; ++i2) {
-      float dg[2][C], du[2][C];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = 2 * i2 + i;
-        form(r, hf, dg[i], du[i]);
-        if (a.q && m + r < a.M && c < pf) {
-          const float ig = row_scale(0, r).inv, iu = row_scale(1, r).inv;
-          uint8_t* o = a.q + (m + r) * 2 * pf + c;
-#pragma unroll
-          for (int k = 0; k < C; k += 4) {
-            *reinterpret_cast<uint32_t*>(o + k) = codes4<FMT>(dg[i][k], dg[i][k + 1], dg[i][k + 2], dg[i][k + 3], ig);
-            *reinterpret_cast<uint32_t*>(o + pf + k) = codes4<FMT>(du[i][k], du[i][k + 1], du[i][k + 2], du[i][k + 3], iu);
-          }
-        }
-      }
-      if (a.q_t) {
-#pragma unroll
-        for (int k = 0; k < C; ++k) {
-          const float ig = cols[at.q * 4 * FN + C * hf + k], iu = cols[16 * FN + at.q * 4 * FN + C * hf + k];
-          og[k][i2 / 2] = codes2<FMT>(dg[0][k], dg[1][k], ig, og[k][i2 / 2], i2 & 1);
-          ou[k][i2 / 2] = codes2<FMT>(du[0][k], du[1][k], iu, ou[k][i2 / 2], i2 & 1);
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      asm volatile("" ::: "memory");
+    for (int k = 0; k < WG; ++k) {
+      tg = max(tg, peers[k * 256 + i]);
+      tu = max(tu, peers[k * 256 + 128 + i]);
     }
-    if (turned) {
-#pragma unroll
-      for (int k = 0; k < C; ++k) {
-        if (c + k < F) {
-          *reinterpret_cast<u32x2_t*>(a.q_t + (c + k) * pm + m) = (u32x2_t){og[k][0], og[k][1]};
-          *reinterpret_cast<u32x2_t*>(a.q_t + (F + c + k) * pm + m) = (u32x2_t){ou[k][0], ou[k][1]};
-        }
-      }
+    const GroupScale<FMT, SC> sg(tg), su(tu);
+    if (at.q == 0 && at.wn % WG == 0 && f < F && m + i < a.M) {
+      sg.store(a.s, (int64_t)(f / kGroup) * a.M + m + i);
+      su.store(a.s, (int64_t)(gf + f / kGroup) * a.M + m + i);
     }
-  }
+    static_for<0, NH>([&](auto Hc) {
+      constexpr int hf = decltype(Hc)::value;
+      const int c = f + 16 * hf;
+      const uint32_t off = c < pf ? (uint32_t)((8 * at.p + i) * 2 * pf + c) : 0x80000000u;
+      if constexpr (hf < PARKED) {
+        const f32x4_t w = wait[(8 * hf + i) * 64];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) du[hf][i][k] = w[k];
+      }
+      const float *x = dg[hf][i], *y = du[hf][i];
+      __builtin_amdgcn_raw_buffer_store_b32(codes4<FMT>(x[0], x[1], x[2], x[3], sg.inv), rq, off, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b32(codes4<FMT>(y[0], y[1], y[2], y[3], su.inv), rq, off, pf, 0);
+    });
+  });
 }
 
 // ---- operands: memory -> shared memory -> registers --------------------------
-typedef __amdgpu_buffer_rsrc_t rsrc_t;
-typedef __attribute__((address_space(3))) void lds_void_t;
-
-// a buffer of so many bytes: what is read behind its end is zeros
-__device__ __forceinline__ rsrc_t buffer_of(const void* p, int bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, bytes, 0x00020000);
-}
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
 }
@@ -391,7 +355,9 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FN == 4 ? 2 : 1) void
   constexpr int LOADS = LA + LB + (SLDS ? 1 : 0);
   // [A .. | B .. | row scales ..], NS of each
   constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, S_BYTES = SLDS ? BM * 4 : 0;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * (A_BYTES + B_BYTES + S_BYTES)];
+  constexpr int TILES = NS * (A_BYTES + B_BYTES + S_BYTES), LAST = EPI == G_GLU_BWD ? glu_bwd_shared<WM, WN, FN>() : 0;
+  constexpr int SHARED = TILES > LAST ? TILES : LAST;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[SHARED];
   constexpr int B_AT = NS * A_BYTES, S_AT = B_AT + NS * B_BYTES;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -421,9 +387,6 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FN == 4 ? 2 : 1) void
   const rsrc_t ra = buffer_of(a.A + mt * a.lda, rows * lda);
   const rsrc_t rb = buffer_of(a.B + (int64_t)at.n0 * a.K, cols * a.K);
   const rsrc_t rb2 = buffer_of(a.B2 + (int64_t)at.n0 * a.K, cols * a.K);
-  // shared rows of B: of a wavefront's 16 FN, block j's row b is row FN b + j;
-  // gated forward: the gate's half of them, then the up projection's
-  constexpr int RB = PAIR ? FN / 2 : FN;
   const int sr = (wave % (BM / 64)) * 64 + lane;
   auto load_tile = [&](int kt, int buf) {
     const int part = kt >= kt_part ? 1 : 0, kb = kt - part * kt_part;
@@ -438,11 +401,12 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FN == 4 ? 2 : 1) void
     }
 #pragma unroll
     for (int i = 0; i < LB; ++i) {
-      const int r0 = (wave * LB + i) * 8, r = r0 + l8;
+      // (gated forward: of a wavefront's rows the first half is the gate's)
+      const int r0 = (wave * LB + i) * 8;
       const bool second = PAIR ? (r0 / (8 * FN)) % 2 == 1 : part == 1;
-      const int n = PAIR ? r0 / (16 * FN) * (8 * FN) + r0 % (8 * FN) + l8 : r;
+      const int n = PAIR ? r0 / (16 * FN) * (8 * FN) + r0 % (8 * FN) + l8 : r0 + l8;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(second ? rb2 : rb, (lds_void_t*)(lds + B_AT + buf * B_BYTES + r0 * 128), 16,
-                                               n * a.K + ((ch ^ ((r / RB) & 7)) << 4), kb * 128, 0, 0);
+                                               n * a.K + ((ch ^ l8) << 4), kb * 128, 0, 0);
     }
     if constexpr (SLDS) {
       const rsrc_t rs = buffer_of(reinterpret_cast<const float*>(a.sA) + (int64_t)kt * a.M + mt, rows * 4);
@@ -454,7 +418,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FN == 4 ? 2 : 1) void
   // what a lane reads: chunks 2 q and 2 q + 1 of its rows
   const uint32_t l0 = lds_address(lds);
   const uint32_t c0 = ((2 * at.q) ^ (at.p & 7)) << 4;
-  const uint32_t pa = l0 + (at.wm * 128 + 8 * at.p) * 128 + c0, pb = l0 + B_AT + (at.wn * 16 * FN + at.p * RB) * 128 + c0;
+  const uint32_t pa = l0 + (at.wm * 128 + 8 * at.p) * 128 + c0, pb = l0 + B_AT + (at.wn * 16 * FN + at.p) * 128 + c0;
   const uint32_t ps = l0 + S_AT + (at.wm * 128 + 8 * at.p) * 4;
 
   // Scales of a tile: of its columns, and E8M0 ones of its rows.  Those of a
@@ -478,10 +442,10 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FN == 4 ? 2 : 1) void
       } else {
         const rsrc_t rs = buffer_of(reinterpret_cast<const float*>(from(0)) + (int64_t)kb * a.N + nw, cols_w * 4);
 #pragma unroll
-        for (int k = 0; k < 4 * FN; k += 4) {  // column FN t + j of the lane's 4 FN
-          const u32x4_t w = __builtin_amdgcn_raw_buffer_load_b128(rs, (at.q * 4 * FN + k) * 4, 0, 0);
+        for (int j = 0; j < FN; ++j) {
+          const u32x4_t w = __builtin_amdgcn_raw_buffer_load_b128(rs, (16 * j + 4 * at.q) * 4, 0, 0);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) s.b[(k + c) / FN][(k + c) % FN] = __uint_as_float(w[c]);
+          for (int t = 0; t < 4; ++t) s.b[t][j] = __uint_as_float(w[t]);
         }
       }
     } else {
@@ -493,7 +457,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FN == 4 ? 2 : 1) void
         const rsrc_t rs = buffer_of(reinterpret_cast<const uint8_t*>(from(0)) + (int64_t)kb * a.N + nw, cols_w);
 #pragma unroll
         for (int j = 0; j < FN; ++j)
-          s.eb |= (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rs, at.p * FN + j, 0, 0) << (8 * j);
+          s.eb |= (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rs, 16 * j + at.p, 0, 0) << (8 * j);
       }
       const rsrc_t rs = buffer_of(reinterpret_cast<const uint8_t*>(a.sA) + (int64_t)kt * a.M + at.m0, rows_w);
       s.ea[0] = s.ea[1] = 0;
@@ -534,7 +498,6 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FN == 4 ? 2 : 1) void
   Row ra0, ra1;  // the rows of two steps in turn
   i32x8_t fb[SUM == SUM_FP8 ? FN : 1];
   bf16x8g_t wb[SUM == SUM_F32 ? FN : 1][4];
-  auto offset_b = [](int j) constexpr { return PAIR ? (j / RB) * 16 * RB * 128 + (j % RB) * 128 : j * 128; };
   auto widen_b = [&](auto J, const Row& r, const Scales& s) {
     constexpr int j = decltype(J)::value;
     const i32x8_t f = r.codes();
@@ -560,7 +523,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FN == 4 ? 2 : 1) void
     const uint32_t b0 = pb + buf * B_BYTES;
     static_for<0, FN>([&](auto J) {
       Row r;
-      r.template ask<offset_b(decltype(J)::value)>(b0, b0 ^ 16);
+      r.template ask<decltype(J)::value * 2048>(b0, b0 ^ 16);
       r.wait();
       widen_b(J, r, s);
     });
@@ -650,7 +613,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FN == 4 ? 2 : 1) void
 
   uint32_t* red = reinterpret_cast<uint32_t*>(lds);
   if constexpr (EPI == G_GLU_FWD) store_glu_fwd<WM, WN, FN, SC>(a, at, acc, red);
-  else if constexpr (EPI == G_GLU_BWD) store_glu_bwd<WM, WN, FN, FMT_A, SC>(a, at, acc, red);
+  else if constexpr (EPI == G_GLU_BWD) store_glu_bwd<WM, WN, FN, FMT_A, SC>(a, at, acc, lds);
   else store_plain<WM, WN, FN>(a, at, acc);
 }
 
