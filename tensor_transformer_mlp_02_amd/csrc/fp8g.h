@@ -5,6 +5,7 @@
 
 #include "../../include/tpmlp_fp8g.h"
 #include "common.h"
+#include "fp8g_plan.h"
 
 namespace tpmlp {
 
@@ -34,18 +35,18 @@ struct G8GemmArgs {
   void *Z, *H;          // Z [M,2N] bf16 (in for the backward), H [M,N] bf16
   uint8_t *q, *q_t;
   void *s, *s_t;
-  float* raw;           // few tokens: H [M,N], or [dG|dU] [M,2N], fp32
+  float* raw;           // fp32 values for a quantization of their own: H [M,N], or [dG|dU] [M,2N]
   int gate;
 };
 
 hipError_t g8_quant_launch(int dtype, int fmt, int scale, int square, const G8QuantArgs& a, hipStream_t st);
-hipError_t g8_gemm_bf16_launch(int fmt_a, int fmt_b, int scale, int square, G8GemmArgs& a, hipStream_t st);
-hipError_t g8_gemm_f32_launch(int fmt_a, int fmt_b, int scale, int square, G8GemmArgs& a, hipStream_t st);
-hipError_t g8_glu_fwd_launch(int scale, G8GemmArgs& a, hipStream_t st);
-hipError_t g8_glu_bwd_launch(int fmt, int scale, G8GemmArgs& a, hipStream_t st);
-
-// The few-token kernels: which calls they take, and the calls
-bool g8_few(int64_t M, int64_t N, int64_t K);
+// bf16 and fp32 results; large: 256 x 256 tiles, else 64 x 128
+hipError_t g8_gemm_bf16_launch(bool large, int fmt_a, int fmt_b, int scale, int square, G8GemmArgs& a, hipStream_t st);
+hipError_t g8_gemm_f32_launch(bool large, int fmt_a, int fmt_b, int scale, int square, G8GemmArgs& a, hipStream_t st);
+// G8_SMALL leaves the values in a.raw, the others make the codes
+hipError_t g8_glu_fwd_launch(G8Form form, int scale, G8GemmArgs& a, hipStream_t st);
+hipError_t g8_glu_bwd_launch(G8Form form, int fmt, int scale, G8GemmArgs& a, hipStream_t st);
+// G8_FEW (the gated block's values are left in a.raw)
 hipError_t g8_gemm_few_launch(int fmt_a, int fmt_b, int scale, int square, const G8GemmArgs& a, hipStream_t st);
 hipError_t g8_glu_fwd_few_launch(int scale, const G8GemmArgs& a, hipStream_t st);
 hipError_t g8_glu_bwd_few_launch(int fmt, int scale, const G8GemmArgs& a, hipStream_t st);

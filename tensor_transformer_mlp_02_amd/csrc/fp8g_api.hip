@@ -43,9 +43,16 @@ int check_glu(const tp_fp8g_glu_desc* d, bool backward) {
   return TP_OK;
 }
 
-// few tokens: the fp32 values between the product and their quantization
+G8Form glu_form(const tp_fp8g_glu_desc& d, bool backward) {
+  return g8_plan_glu(d.N, d.F, groups_of(d.H), backward);
+}
+
+// the fp32 values between the product and their quantization, where that is a
+// launch of its own
 size_t glu_workspace(const tp_fp8g_glu_desc& d, bool backward) {
-  const size_t need = g8_few(d.N, d.F, d.H) ? (size_t)d.N * (size_t)d.F * (backward ? 8 : 4) : 0;
+  const G8Form form = glu_form(d, backward);
+  const bool raw = form == G8_FEW || form == G8_SMALL;
+  const size_t need = raw ? (size_t)d.N * (size_t)d.F * (backward ? 8 : 4) : 0;
   return need < 16 ? 16 : need;
 }
 
@@ -118,8 +125,10 @@ int tp_fp8g_gemm(const tp_fp8g_gemm_desc* desc, const void* A, const void* sA, c
   if (d.M == 0) return ok();
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   hipError_t he = timed(st, [&] {
-    if (g8_few(d.M, d.N, d.K * d.parts)) return g8_gemm_few_launch(d.fmt_a, d.fmt_b, d.scale, d.square, a, st);
-    return (a.out_bf16 ? g8_gemm_bf16_launch : g8_gemm_f32_launch)(d.fmt_a, d.fmt_b, d.scale, d.square, a, st);
+    const bool f32 = !a.out_bf16, large = d.scale == TP_GROUP_E8M0 || d.square;
+    const G8Form form = g8_plan_gemm(d.M, d.N, d.K / kGroup * d.parts, f32, large);
+    if (form == G8_FEW) return g8_gemm_few_launch(d.fmt_a, d.fmt_b, d.scale, d.square, a, st);
+    return (f32 ? g8_gemm_f32_launch : g8_gemm_bf16_launch)(form == G8_LARGE, d.fmt_a, d.fmt_b, d.scale, d.square, a, st);
   });
   if (he != hipSuccess) return hip_fail(he, "group-scaled product launch");
   return ok();
@@ -158,12 +167,13 @@ int tp_fp8g_glu_fwd(const tp_fp8g_glu_desc* desc, const void* X, const void* sX,
   a.Z = Z_save; a.H = H_act; a.gate = d.gate;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   hipError_t he = timed(st, [&] {
-    if (!g8_few(d.N, d.F, d.H)) {
+    const G8Form form = glu_form(d, false);
+    if (form == G8_LARGE || form == G8_GROUP) {
       a.q = (uint8_t*)Hq; a.q_t = (uint8_t*)Hq_t; a.s = sH; a.s_t = sH_t;
-      return g8_glu_fwd_launch(d.scale, a, st);
+      return g8_glu_fwd_launch(form, d.scale, a, st);
     }
     if (Hq || Hq_t) a.raw = (float*)workspace;
-    hipError_t r = g8_glu_fwd_few_launch(d.scale, a, st);
+    hipError_t r = form == G8_FEW ? g8_glu_fwd_few_launch(d.scale, a, st) : g8_glu_fwd_launch(form, d.scale, a, st);
     if (r != hipSuccess || !a.raw) return r;
     const G8QuantArgs c{workspace, (uint8_t*)Hq, (uint8_t*)Hq_t, sH, sH_t, d.N, d.F, d.F, 1};
     return g8_quant_launch(TP_F32, TP_FP8_E4M3, d.scale, 0, c, st);
@@ -204,12 +214,13 @@ int tp_fp8g_glu_bwd(const tp_fp8g_glu_desc* desc, const void* dY, const void* sd
   a.Z = const_cast<void*>(Z_save); a.gate = d.gate;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   hipError_t he = timed(st, [&] {
-    if (!g8_few(d.N, d.F, d.H)) {
+    const G8Form form = glu_form(d, true);
+    if (form == G8_LARGE || form == G8_GROUP) {
       a.q = (uint8_t*)dZ; a.q_t = (uint8_t*)dZ_t; a.s = sdZ; a.s_t = sdZ_t;
-      return g8_glu_bwd_launch(d.fmt, d.scale, a, st);
+      return g8_glu_bwd_launch(form, d.fmt, d.scale, a, st);
     }
     a.raw = (float*)workspace;
-    hipError_t r = g8_glu_bwd_few_launch(d.fmt, d.scale, a, st);
+    hipError_t r = form == G8_FEW ? g8_glu_bwd_few_launch(d.fmt, d.scale, a, st) : g8_glu_bwd_launch(form, d.fmt, d.scale, a, st);
     if (r != hipSuccess) return r;
     const G8QuantArgs c{workspace, (uint8_t*)dZ, (uint8_t*)dZ_t, sdZ, sdZ_t, d.N, d.F, 2 * d.F, 2};
     return g8_quant_launch(TP_F32, d.fmt, d.scale, 0, c, st);

@@ -1,24 +1,23 @@
-// Products of 8-bit codes with group scales for few tokens (up to 64), as
-// single-token serving makes them.  Bound by the weights' bytes: each is read
-// once, straight into registers, by the wavefront that multiplies it.
+// Products of 8-bit codes with group scales for few rows, or few outputs
+// behind a long sum.  A generated token's product is bound by the weights'
+// bytes: each is read once, straight into registers, by the wavefront that multiplies it.
 //
-// A workgroup has 16 rows of the weight (the gated forward: of both), and its
-// four wavefronts deal the groups of the summed index among themselves:
-// wavefront w takes groups w, w + 4, ...  Block: codes widened to bf16, v_mfma_f32_16x16x32_bf16 with the
-// weights first; lane (p = lane % 16, q = lane / 16) gives row p's codes 32 q .. + 31
-// of the group (32 bytes: a row's 128 are one cache line) and receives token p,
-// weight rows 4 q .. 4 q + 3.  The wavefronts' sums are joined in shared memory in a
-// fixed order.  Rows past the last are read as the last one and not stored.
+// A workgroup has up to 64 rows of A and 16 or 32 of the weight (the gated
+// forward: 16 of both), and its four wavefronts deal the groups of the summed index among
+// themselves: wavefront w takes groups w, w + 4, ...  Codes are widened to bf16
+// for v_mfma_f32_16x16x32_bf16 with the weights first; lane (p = lane % 16, q = lane / 16)
+// gives row p's codes 32 q .. + 31 of the group (32 bytes: a row's 128 are one cache line) and
+// receives token p, weight rows 4 q .. 4 q + 3.  The wavefronts' sums are joined
+// in shared memory in a fixed order.  Rows past the last are read as the last one and not
+// stored.  1 x 8192 x 3584: 6.6 us (4.4 TB/s of weights).
 #include "fp8g.h"
 
-#ifndef G8_NW
-#define G8_NW 4
-#endif
 namespace tpmlp {
 namespace g8 {
 
 enum { F_STORE = 0, F_GLU_FWD = 1, F_GLU_BWD = 2 };
 constexpr int FEW_ROWS = 64;  // of A, at most, a workgroup
+constexpr int FEW_WAVES = 4;
 
 __device__ __forceinline__ i32x8_t load_codes(const uint8_t* p) {
   const i32x4_t lo = *reinterpret_cast<const i32x4_t*>(p);
@@ -26,18 +25,22 @@ __device__ __forceinline__ i32x8_t load_codes(const uint8_t* p) {
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-template <int MT, int NW, int SC, bool SQ, int FMT_A, int FMT_B, int EPI>
+template <int MT, int NB, int NW, int SC, bool SQ, int FMT_A, int FMT_B, int EPI>
 __global__ __launch_bounds__(64 * NW) void gemm_few(G8GemmArgs a) {
-  constexpr int MATS = EPI == F_GLU_FWD ? 2 : 1;
+  // blocks of 16 weight rows: the gate's and the up projection's, or NB neighbours
+  constexpr int MATS = EPI == F_GLU_FWD ? 2 : NB;
+  static_assert(EPI != F_GLU_FWD || NB == 1);
   constexpr int U = MT <= 2 ? 4 : 2;  // groups on their way at a time
   __shared__ f32x4_t red[NW][MATS][MT][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int p = lane & 15, q = lane >> 4;
-  const int n0 = blockIdx.x * 16;
+  const int n0 = blockIdx.x * 16 * NB;
   const int64_t m_first = (int64_t)blockIdx.y * FEW_ROWS;
   const int64_t M = a.M;
-  const int n = min(n0 + p, a.N - 1);
+  int n[MATS];
+#pragma unroll
+  for (int w = 0; w < MATS; ++w) n[w] = min(n0 + (EPI == F_GLU_FWD ? 0 : 16 * w) + p, a.N - 1);
   const int kt_part = a.K / kGroup, kt_all = kt_part * a.parts;
   const uint8_t* xrow[MT];
   int64_t m[MT];
@@ -62,8 +65,8 @@ __global__ __launch_bounds__(64 * NW) void gemm_few(G8GemmArgs a) {
       const int part = kt >= kt_part ? 1 : 0, kb = kt - part * kt_part;
 #pragma unroll
       for (int w = 0; w < MATS; ++w) {
-        const bool second = MATS == 2 ? w == 1 : part == 1;
-        fb[u][w] = load_codes((second ? a.B2 : a.B) + (int64_t)n * a.K + kb * 128 + 32 * q);
+        const bool second = EPI == F_GLU_FWD ? w == 1 : part == 1;
+        fb[u][w] = load_codes((second ? a.B2 : a.B) + (int64_t)n[w] * a.K + kb * 128 + 32 * q);
         const void* s = second ? a.sB2 : a.sB;
         if constexpr (SC == TP_GROUP_F32) {
           const float* f = reinterpret_cast<const float*>(s);
@@ -71,10 +74,10 @@ __global__ __launch_bounds__(64 * NW) void gemm_few(G8GemmArgs a) {
             sb[u][w][0] = f[(int64_t)(n0 / kGroup) * kt_part + kb];
           } else {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) sb[u][w][t] = f[(int64_t)kb * a.N + min(n0 + 4 * q + t, a.N - 1)];
+            for (int t = 0; t < 4; ++t) sb[u][w][t] = f[(int64_t)kb * a.N + min(n0 + 16 * w + 4 * q + t, a.N - 1)];
           }
         } else {
-          eb[u][w] = reinterpret_cast<const uint8_t*>(s)[SQ ? (int64_t)(n0 / kGroup) * kt_part + kb : (int64_t)kb * a.N + n];
+          eb[u][w] = reinterpret_cast<const uint8_t*>(s)[SQ ? (int64_t)(n0 / kGroup) * kt_part + kb : (int64_t)kb * a.N + n[w]];
         }
       }
 #pragma unroll
@@ -139,16 +142,20 @@ __global__ __launch_bounds__(64 * NW) void gemm_few(G8GemmArgs a) {
   const int64_t off = row * a.N + col;
   const Gate gate(a.gate);
   if constexpr (EPI == F_STORE) {
-    if (a.out_bf16) {
-      Store4<bf16_t>::store(a.C, off, v[0]);
-    } else {
-      if (a.accumulate) {
-        float w[4];
-        Store4<float>::load(a.C, off, w);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) v[0][t] += w[t];
+    for (int w = 0; w < MATS; ++w) {
+      if (col + 16 * w >= a.N) break;
+      if (a.out_bf16) {
+        Store4<bf16_t>::store(a.C, off + 16 * w, v[w]);
+      } else {
+        if (a.accumulate) {
+          float c[4];
+          Store4<float>::load(a.C, off + 16 * w, c);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) v[w][t] += c[t];
+        }
+        Store4<float>::store(a.C, off + 16 * w, v[w]);
       }
-      Store4<float>::store(a.C, off, v[0]);
     }
   } else if constexpr (EPI == F_GLU_FWD) {
     if (a.Z) {
@@ -161,32 +168,40 @@ __global__ __launch_bounds__(64 * NW) void gemm_few(G8GemmArgs a) {
     if (a.H) Store4<bf16_t>::store(a.H, off, h);
     if (a.raw) Store4<float>::store(a.raw, off, h);
   } else {
-    float g[4], u[4], dg[4], du[4];
-    Store4<bf16_t>::load(a.Z, row * 2 * a.N + col, g);
-    Store4<bf16_t>::load(a.Z, row * 2 * a.N + a.N + col, u);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      float act, slope;
-      gate.both(g[t], act, slope);
-      dg[t] = v[0][t] * u[t] * slope;
-      du[t] = v[0][t] * act;
+    for (int w = 0; w < MATS; ++w) {
+      const int c = col + 16 * w;
+      if (c >= a.N) break;
+      float g[4], u[4], dg[4], du[4];
+      Store4<bf16_t>::load(a.Z, row * 2 * a.N + c, g);
+      Store4<bf16_t>::load(a.Z, row * 2 * a.N + a.N + c, u);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        float act, slope;
+        gate.both(g[t], act, slope);
+        dg[t] = v[w][t] * u[t] * slope;
+        du[t] = v[w][t] * act;
+      }
+      Store4<float>::store(a.raw, row * 2 * a.N + c, dg);
+      Store4<float>::store(a.raw, row * 2 * a.N + a.N + c, du);
     }
-    Store4<float>::store(a.raw, row * 2 * a.N + col, dg);
-    Store4<float>::store(a.raw, row * 2 * a.N + a.N + col, du);
   }
 }
 
-template <int MT, int SC, bool SQ, int FMT_A, int FMT_B, int EPI>
+template <int MT, int NB, int SC, bool SQ, int FMT_A, int FMT_B, int EPI>
 static hipError_t few_run(const G8GemmArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)((a.N + 15) / 16), (unsigned)((a.M + FEW_ROWS - 1) / FEW_ROWS));
-  hipLaunchKernelGGL((gemm_few<MT, G8_NW, SC, SQ, FMT_A, FMT_B, EPI>), grid, dim3(64 * G8_NW), 0, st, a);
+  const dim3 grid((unsigned)((a.N + 16 * NB - 1) / (16 * NB)), (unsigned)((a.M + FEW_ROWS - 1) / FEW_ROWS));
+  hipLaunchKernelGGL((gemm_few<MT, NB, FEW_WAVES, SC, SQ, FMT_A, FMT_B, EPI>), grid, dim3(64 * FEW_WAVES), 0, st, a);
   return hipGetLastError();
 }
 template <int SC, bool SQ, int FMT_A, int FMT_B, int EPI>
 static hipError_t few(const G8GemmArgs& a, hipStream_t st) {
-  if (a.M <= 16) return few_run<1, SC, SQ, FMT_A, FMT_B, EPI>(a, st);
-  if (a.M <= 32) return few_run<2, SC, SQ, FMT_A, FMT_B, EPI>(a, st);
-  return few_run<4, SC, SQ, FMT_A, FMT_B, EPI>(a, st);
+  if (a.M <= 16) return few_run<1, 1, SC, SQ, FMT_A, FMT_B, EPI>(a, st);
+  if (a.M <= 32) return few_run<2, 1, SC, SQ, FMT_A, FMT_B, EPI>(a, st);
+  if constexpr (EPI != F_GLU_FWD) {  // (its workgroups have 32 weight rows at any rate)
+    if (g8_wide(a.M, a.N)) return few_run<4, 2, SC, SQ, FMT_A, FMT_B, EPI>(a, st);
+  }
+  return few_run<4, 1, SC, SQ, FMT_A, FMT_B, EPI>(a, st);
 }
 
 template <int SC, bool SQ>
@@ -198,11 +213,6 @@ static hipError_t few_formats(int fa, int fb, const G8GemmArgs& a, hipStream_t s
 }
 
 }  // namespace g8
-
-#ifndef G8_FEW
-#define G8_FEW (M <= 64)
-#endif
-bool g8_few(int64_t M, int64_t N, int64_t K) { return G8_FEW; }
 
 hipError_t g8_gemm_few_launch(int fmt_a, int fmt_b, int scale, int square, const G8GemmArgs& a, hipStream_t st) {
   using namespace g8;

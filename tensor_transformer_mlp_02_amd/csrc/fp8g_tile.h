@@ -1,20 +1,20 @@
 // Products of 8-bit codes with group scales on the matrix cores (the
 // formulas: include/tpmlp_fp8g.h).  MFMA-bound.
 //
-// A workgroup makes a tile of (128 WM) x (16 FN WN) outputs with WM x WN
-// wavefronts, each 128 x 16 FN as 8 x FN blocks of
+// A workgroup makes a tile of (16 FM WM) x (16 FN WN) outputs with WM x WN
+// wavefronts, each 16 FM x 16 FN as FM x FN blocks of
 // v_mfma_f32_16x16x128_f8f6f4: one instruction spans exactly one group of the
 // summed index, so its result is the group's exact sum, scaled and added in
 // fp32 (TP_GROUP_F32), or the instruction applies the scales itself and
 // accumulates (TP_GROUP_E8M0).
 //
-// Block i's row index a is row 8 a + i of the wavefront's 128, block j's column
+// Block i's row index a is row FM a + i of the wavefront's, block j's column
 // index b is column 16 j + b.  The instruction is issued with the B codes first, which
 // leaves a lane (p = lane % 16, q = lane / 16) with row index p and column indices
-// 4 q .. 4 q + 3: in all 8 neighbouring rows x 4 neighbouring columns of each block j.  So
-// outputs are stored without a turn through shared memory, a lane's 8 row scales are neighbours,
-// a group of 128 tokens is one wavefront's (its largest magnitude a reduction
-// over 16 lanes) and the codes of a transposed output are 8 bytes a lane.
+// 4 q .. 4 q + 3: in all FM neighbouring rows x 4 neighbouring columns of each block j.  So
+// outputs are stored without a turn through shared memory, a lane's row scales are neighbours,
+// and with FM = 8 a group of 128 tokens is one wavefront's (its largest magnitude a
+// reduction over 16 lanes) and the codes of a transposed output are 8 bytes a lane.
 //
 // Shared memory holds rows of 128 codes, the 16-byte chunk c of a row at
 // c ^ (the row's index a or b) % 8: the 8 lanes that are served together read 8
@@ -28,7 +28,8 @@ namespace g8 {
 
 // How a group's products are added: by the FP8 instruction, or widened to bf16
 enum { SUM_FP8 = 0, SUM_F32 = 1 };
-enum { G_STORE = 0, G_GLU_FWD = 1, G_GLU_BWD = 2 };
+// G_RAW_*: the gated block's fp32 values, for a quantization of their own
+enum { G_STORE = 0, G_GLU_FWD = 1, G_GLU_BWD = 2, G_RAW_FWD = 3, G_RAW_BWD = 4 };
 
 template <int FMT_A, int FMT_B, int OA, int OB>
 __device__ __forceinline__ f32x4_t mfma_scaled(i32x8_t b, i32x8_t a, f32x4_t c, int sb, int sa) {
@@ -52,13 +53,13 @@ struct Place {
   int wm, wn, p, q;
 };
 
-// acc[i][j][t]: row m0 + 8 p + i; column 16 j + 4 q + t of the wavefront's
-template <int WM, int WN, int FN>
-__device__ __forceinline__ void store_plain(const G8GemmArgs& a, const Place& at, f32x4_t (&acc)[8][FN]) {
+// acc[i][j][t]: row m0 + FM p + i; column 16 j + 4 q + t of the wavefront's
+template <int WM, int WN, int FM, int FN>
+__device__ __forceinline__ void store_plain(const G8GemmArgs& a, const Place& at, f32x4_t (&acc)[FM][FN]) {
   const int n = at.n0 + at.wn * 16 * FN + at.q * 4;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t m = at.m0 + 8 * at.p + i;
+  for (int i = 0; i < FM; ++i) {
+    const int64_t m = at.m0 + FM * at.p + i;
     if (m >= a.M) continue;
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
@@ -76,6 +77,64 @@ __device__ __forceinline__ void store_plain(const G8GemmArgs& a, const Place& at
         }
         Store4<float>::store(a.C, off, v);
       }
+    }
+  }
+}
+
+// The gated block's values in fp32 (a.raw): their groups span tiles
+template <int WM, int WN, int FM, int FN>
+__device__ __forceinline__ void store_raw_fwd(const G8GemmArgs& a, const Place& at, f32x4_t (&acc)[FM][FN]) {
+  constexpr int J = FN / 2;
+  const int64_t F = a.N, f = at.n0 + at.wn * 8 * FN + at.q * 4;
+  const Gate gate(a.gate);
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int64_t m = at.m0 + FM * at.p + i;
+    if (m >= a.M) continue;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int64_t c = f + 16 * j;
+      if (c >= F) continue;
+      float g[4], u[4], h[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        g[t] = acc[i][j][t];
+        u[t] = acc[i][J + j][t];
+        h[t] = gate.act(g[t]) * u[t];
+      }
+      if (a.Z) {
+        Store4<bf16_t>::store(a.Z, m * 2 * F + c, g);
+        Store4<bf16_t>::store(a.Z, m * 2 * F + F + c, u);
+      }
+      if (a.H) Store4<bf16_t>::store(a.H, m * F + c, h);
+      if (a.raw) Store4<float>::store(a.raw, m * F + c, h);
+    }
+  }
+}
+template <int WM, int WN, int FM, int FN>
+__device__ __forceinline__ void store_raw_bwd(const G8GemmArgs& a, const Place& at, f32x4_t (&acc)[FM][FN]) {
+  const int64_t F = a.N, f = at.n0 + at.wn * 16 * FN + at.q * 4;
+  const Gate gate(a.gate);
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int64_t m = at.m0 + FM * at.p + i;
+    if (m >= a.M) continue;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const int64_t c = f + 16 * j;
+      if (c >= F) continue;
+      float g[4], u[4], dg[4], du[4];
+      Store4<bf16_t>::load(a.Z, m * 2 * F + c, g);
+      Store4<bf16_t>::load(a.Z, m * 2 * F + F + c, u);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        float act, slope;
+        gate.both(g[t], act, slope);
+        dg[t] = acc[i][j][t] * u[t] * slope;
+        du[t] = acc[i][j][t] * act;
+      }
+      Store4<float>::store(a.raw, m * 2 * F + c, dg);
+      Store4<float>::store(a.raw, m * 2 * F + F + c, du);
     }
   }
 }
@@ -328,6 +387,8 @@ struct Row {
   __device__ __forceinline__ void wait_scale() {
     asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(lo), "+v"(hi), "+v"(s)::"memory");
   }
+  __device__ __forceinline__ void arrived() { asm volatile("" : "+v"(lo), "+v"(hi)); }  // after a wait
+  __device__ __forceinline__ void arrived_scale() { asm volatile("" : "+v"(lo), "+v"(hi), "+v"(s)); }
   __device__ __forceinline__ i32x8_t codes() const { return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7); }
 };
 
@@ -345,10 +406,12 @@ __device__ __forceinline__ uint32_t scalar_byte(const void* p, int64_t i) {
 
 // The operands' tiles pass through NS buffers in shared memory: while one is
 // multiplied, the next ones' loads (straight into shared memory) are on their way.
-template <int WM, int WN, int FN, int NS, int SC, bool SQ, int FMT_A, int FMT_B, int SUM, int EPI>
-__global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FN == 4 ? 2 : 1) void gemm(G8GemmArgs a) {
-  constexpr int BM = 128 * WM, BN = 16 * FN * WN, NW = WM * WN;
-  constexpr bool PAIR = EPI == G_GLU_FWD;
+template <int WM, int WN, int FM, int FN, int NS, int SC, bool SQ, int FMT_A, int FMT_B, int SUM, int EPI>
+__global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM == 4 ? 2 : 1) void gemm(G8GemmArgs a) {
+  constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN, NW = WM * WN;
+  constexpr bool PAIR = EPI == G_GLU_FWD || EPI == G_RAW_FWD;
+  static_assert(FM == 8 || (FM == 4 && EPI != G_GLU_FWD && EPI != G_GLU_BWD));
+  static_assert(BM % 64 == 0 && BM % (8 * WM * WN) == 0 && BN % (8 * WM * WN) == 0);
   constexpr int COLS = PAIR ? BN / 2 : BN;  // columns of the output a tile has
   constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;  // 1 KiB loads of a wavefront (8 rows each)
   constexpr bool SLDS = SC == TP_GROUP_F32;          // row scales by way of shared memory
@@ -374,7 +437,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FN == 4 ? 2 : 1) void
   at.p = lane & 15;
   at.q = lane >> 4;
   const int64_t mt = (int64_t)tm * BM;
-  at.m0 = mt + at.wm * 128;
+  at.m0 = mt + at.wm * 16 * FM;
   at.n0 = tn * COLS;
 
   const int kt_part = a.K / kGroup, kt_all = kt_part * a.parts;
@@ -397,7 +460,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FN == 4 ? 2 : 1) void
     for (int i = 0; i < LA; ++i) {
       const int blk = wave * LA + i;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void_t*)(lds + buf * A_BYTES + blk * 1024), 16,
-                                               (blk * 8 + l8) * lda + ((ch ^ (blk & 7)) << 4), kt * 128, 0, 0);
+                                               (blk * 8 + l8) * lda + ((ch ^ (((blk * 8 + l8) / FM) & 7)) << 4), kt * 128, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < LB; ++i) {
@@ -418,8 +481,8 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FN == 4 ? 2 : 1) void
   // what a lane reads: chunks 2 q and 2 q + 1 of its rows
   const uint32_t l0 = lds_address(lds);
   const uint32_t c0 = ((2 * at.q) ^ (at.p & 7)) << 4;
-  const uint32_t pa = l0 + (at.wm * 128 + 8 * at.p) * 128 + c0, pb = l0 + B_AT + (at.wn * 16 * FN + at.p) * 128 + c0;
-  const uint32_t ps = l0 + S_AT + (at.wm * 128 + 8 * at.p) * 4;
+  const uint32_t pa = l0 + (at.wm * 16 * FM + FM * at.p) * 128 + c0, pb = l0 + B_AT + (at.wn * 16 * FN + at.p) * 128 + c0;
+  const uint32_t ps = l0 + S_AT + (at.wm * 16 * FM + FM * at.p) * 4;
 
   // Scales of a tile: of its columns, and E8M0 ones of its rows.  Those of a
   // lane are neighbours, behind one offset from a base that a wavefront
@@ -430,7 +493,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FN == 4 ? 2 : 1) void
     uint32_t eb, ea[2];
   };
   const int nw = PAIR ? at.n0 + at.wn * 8 * FN : at.n0 + at.wn * 16 * FN;  // the wavefront's first column
-  const int rows_w = (int)max((int64_t)0, min((int64_t)128, a.M - at.m0)), cols_w = max(0, min(16 * FN, a.N - nw));
+  const int rows_w = (int)max((int64_t)0, min((int64_t)(16 * FM), a.M - at.m0)), cols_w = max(0, min(16 * FN, a.N - nw));
   const int64_t square = (int64_t)(min(nw, a.N - 1) / kGroup) * kt_part;
   auto load_scales = [&](int kt, Scales& s) {
     const int part = kt >= kt_part ? 1 : 0, kb = kt - part * kt_part;
@@ -461,21 +524,25 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FN == 4 ? 2 : 1) void
       }
       const rsrc_t rs = buffer_of(reinterpret_cast<const uint8_t*>(a.sA) + (int64_t)kt * a.M + at.m0, rows_w);
       s.ea[0] = s.ea[1] = 0;
-      if (rows_w == 128) {
-        const u32x2_t w = __builtin_amdgcn_raw_buffer_load_b64(rs, 8 * at.p, 0, 0);
-        s.ea[0] = w[0];
-        s.ea[1] = w[1];
+      if (rows_w == 16 * FM) {
+        if constexpr (FM == 8) {
+          const u32x2_t w = __builtin_amdgcn_raw_buffer_load_b64(rs, 8 * at.p, 0, 0);
+          s.ea[0] = w[0];
+          s.ea[1] = w[1];
+        } else {
+          s.ea[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, 4 * at.p, 0, 0);
+        }
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          s.ea[i >> 2] |= (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rs, 8 * at.p + i, 0, 0) << (8 * (i & 3));
+        for (int i = 0; i < FM; ++i)
+          s.ea[i >> 2] |= (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rs, FM * at.p + i, 0, 0) << (8 * (i & 3));
       }
     }
   };
 
-  f32x4_t acc[8][FN];
+  f32x4_t acc[FM][FN];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
 
@@ -538,94 +605,183 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FN == 4 ? 2 : 1) void
     asm volatile("" : "+v"(acc[i][j]));  // (put off past the barrier, it would hold its registers)
   };
 
-  int buf = 0;
-  sc = sc_next;
-  load_b(0, sc);
-  ask_a(std::integral_constant<int, 0>{}, ra0, 0);
-  for (int kt = 0; kt < kt_all; ++kt) {
-    const bool more = kt + 1 < kt_all;
-    const int buf_next = buf + 1 == NS ? 0 : buf + 1;
-    load_scales(more ? kt + 1 : kt, sc_next);
-    static_for<0, 8>([&](auto I) {
-      constexpr int i = decltype(I)::value;
-      Row& r = i & 1 ? ra1 : ra0;
-      Row& next = i & 1 ? ra0 : ra1;
-      wait_a(r);
-      if constexpr (i < 7) {
-        ask_a(std::integral_constant<int, (i + 1) & 7>{}, next, buf);
-      } else {
-        // the tile is read; the next one is there for every wavefront after
-        // this, and the buffer takes the one NS on
-        wait_tiles(max(0, min(kt_all - 2 - kt, NS - 2)));
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        // (behind the last tile: rows that nothing uses, so that every path asks)
-        ask_a(std::integral_constant<int, 0>{}, next, buf_next);
-        if (kt + NS < kt_all) load_tile(kt + NS, buf);
-      }
-      const i32x8_t fa = r.codes();
-      // fp32 scales: a step's group sums are scaled and added during the next
-      // step, when the instructions that make them have ended
-      if constexpr (SUM == SUM_F32) {
-        float e = 1.0f;
-        if constexpr (SC == TP_GROUP_E8M0) e = e8m0_f32((sc.ea[i >> 2] >> (8 * (i & 3))) & 255);
-        static_for<0, 4>([&](auto Cc) {
-          constexpr int c = decltype(Cc)::value;
-          const bf16x8g_t wa = widen<FMT_A>(fa[2 * c], fa[2 * c + 1], e);
+  if constexpr (FM == 4) {
+    // A small tile: there are registers for all that a wavefront reads of it
+    // and of the next, asked for together a tile ahead (one at a time, their
+    // latencies were most of a tile's time)
+    struct Set {
+      Row a[FM], b[FN];
+    };
+    Set even, odd;
+    auto ask_set = [&](Set& t, int buf) {
+      const uint32_t b0 = pb + buf * B_BYTES;
+      static_for<0, FN>([&](auto J) { t.b[J].template ask<decltype(J)::value * 2048>(b0, b0 ^ 16); });
+      static_for<0, FM>([&](auto I) { ask_a(I, t.a[I], buf); });
+    };
+    auto wait_set = [&](Set& t) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      static_for<0, FN>([&](auto J) { t.b[J].arrived(); });
+      static_for<0, FM>([&](auto I) {
+        if constexpr (SLDS) t.a[I].arrived_scale();
+        else t.a[I].arrived();
+      });
+    };
+    auto one_tile = [&](Set& t, Set& next, int kt, int buf, int buf_next) {
+      sc = sc_next;
+      load_scales(min(kt + 1, kt_all - 1), sc_next);
+      // this tile is read, and the next one there, for every wavefront
+      wait_tiles(max(0, min(kt_all - 2 - kt, NS - 2)));
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      ask_set(next, buf_next);  // (behind the last tile: what nothing uses)
+      if (kt + NS < kt_all) load_tile(kt + NS, buf);
+      static_for<0, FN>([&](auto J) { widen_b(J, t.b[J], sc); });
+      static_for<0, FM>([&](auto I) {
+        constexpr int i = decltype(I)::value;
+        const i32x8_t fa = t.a[i].codes();
+        if constexpr (SUM == SUM_F32) {
+          float e = 1.0f;
+          if constexpr (SC == TP_GROUP_E8M0) e = e8m0_f32((sc.ea[i >> 2] >> (8 * (i & 3))) & 255);
+          f32x4_t g[FN];
+          static_for<0, 4>([&](auto Cc) {
+            constexpr int c = decltype(Cc)::value;
+            const bf16x8g_t wa = widen<FMT_A>(fa[2 * c], fa[2 * c + 1], e);
+            static_for<0, FN>([&](auto J) {
+              constexpr int j = decltype(J)::value;
+              if constexpr (SC == TP_GROUP_E8M0) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][c], wa, acc[i][j], 0, 0, 0);
+              else g[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][c], wa, c ? g[j] : (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+            });
+          });
+          if constexpr (SC == TP_GROUP_F32) {
+            static_for<0, FN>([&](auto J) {
+              constexpr int j = decltype(J)::value;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) acc[i][j][k] = fmaf(g[j][k], t.a[i].s * sc.b[SQ ? 0 : k][j], acc[i][j][k]);
+            });
+          }
+        } else {
           static_for<0, FN>([&](auto J) {
             constexpr int j = decltype(J)::value;
-            if constexpr (SC == TP_GROUP_E8M0) {
-              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][c], wa, acc[i][j], 0, 0, 0);
+            if constexpr (SC == TP_GROUP_F32) {
+              const f32x4_t g = mfma_plain<FMT_A, FMT_B>(fb[j], fa, (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+              for (int k = 0; k < 4; ++k) acc[i][j][k] = fmaf(g[k], t.a[i].s * sc.b[SQ ? 0 : k][j], acc[i][j][k]);
             } else {
-              if constexpr (c == 0 && i > 0) add_group(std::integral_constant<int, i - 1>{}, J);
-              p[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][c], wa, c ? p[j] : (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+              acc[i][j] = mfma_scaled<FMT_A, FMT_B, i & 3, j>(fb[j], fa, acc[i][j], (int)sc.eb, (int)sc.ea[i >> 2]);
             }
           });
-          __builtin_amdgcn_sched_barrier(0);
-        });
-      } else {
-        static_for<0, FN>([&](auto J) {
-          constexpr int j = decltype(J)::value;
-          if constexpr (SC == TP_GROUP_F32) {
-            if constexpr (i > 0) add_group(std::integral_constant<int, i - 1>{}, J);
-            p[j] = mfma_plain<FMT_A, FMT_B>(fb[j], fa, (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f});
-          } else {
-            acc[i][j] = mfma_scaled<FMT_A, FMT_B, i & 3, j>(fb[j], fa, acc[i][j], (int)sc.eb, (int)sc.ea[i >> 2]);
-          }
-        });
-      }
-      if constexpr (SLDS) sa = r.s;
-      if constexpr (SC == TP_GROUP_E8M0) {
+        }
+      });
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(acc[i][j]));
-      }
       __builtin_amdgcn_sched_barrier(0);
-    });
-    if constexpr (SC == TP_GROUP_F32) {
-      static_for<0, FN>([&](auto J) { add_group(std::integral_constant<int, 7>{}, J); });
+      wait_set(next);  // (here: on their way round the loop they might be moved)
+    };
+    auto after = [](int buf) { return buf + 1 == NS ? 0 : buf + 1; };
+    ask_set(even, 0);
+    wait_set(even);
+    int buf = 0, kt = 0;
+    for (; kt + 1 < kt_all; kt += 2) {
+      one_tile(even, odd, kt, buf, after(buf));
+      buf = after(buf);
+      one_tile(odd, even, kt + 1, buf, after(buf));
+      buf = after(buf);
     }
+    if (kt < kt_all) one_tile(even, odd, kt, buf, after(buf));
+  } else {
+    int buf = 0;
     sc = sc_next;
-    load_b(buf_next, sc);
-    buf = buf_next;
+    load_b(0, sc);
+    ask_a(std::integral_constant<int, 0>{}, ra0, 0);
+    for (int kt = 0; kt < kt_all; ++kt) {
+      const bool more = kt + 1 < kt_all;
+      const int buf_next = buf + 1 == NS ? 0 : buf + 1;
+      load_scales(more ? kt + 1 : kt, sc_next);
+      static_for<0, FM>([&](auto I) {
+        constexpr int i = decltype(I)::value;
+        Row& r = i & 1 ? ra1 : ra0;
+        Row& next = i & 1 ? ra0 : ra1;
+        wait_a(r);
+        if constexpr (i < FM - 1) {
+          ask_a(std::integral_constant<int, (i + 1) % FM>{}, next, buf);
+        } else {
+          // the tile is read; the next one is there for every wavefront after
+          // this, and the buffer takes the one NS on
+          wait_tiles(max(0, min(kt_all - 2 - kt, NS - 2)));
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+          // (behind the last tile: rows that nothing uses, so that every path asks)
+          ask_a(std::integral_constant<int, 0>{}, next, buf_next);
+          if (kt + NS < kt_all) load_tile(kt + NS, buf);
+        }
+        const i32x8_t fa = r.codes();
+        // fp32 scales: a step's group sums are scaled and added during the next
+        // step, when the instructions that make them have ended
+        if constexpr (SUM == SUM_F32) {
+          float e = 1.0f;
+          if constexpr (SC == TP_GROUP_E8M0) e = e8m0_f32((sc.ea[i >> 2] >> (8 * (i & 3))) & 255);
+          static_for<0, 4>([&](auto Cc) {
+            constexpr int c = decltype(Cc)::value;
+            const bf16x8g_t wa = widen<FMT_A>(fa[2 * c], fa[2 * c + 1], e);
+            static_for<0, FN>([&](auto J) {
+              constexpr int j = decltype(J)::value;
+              if constexpr (SC == TP_GROUP_E8M0) {
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][c], wa, acc[i][j], 0, 0, 0);
+              } else {
+                if constexpr (c == 0 && i > 0) add_group(std::integral_constant<int, i - 1>{}, J);
+                p[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][c], wa, c ? p[j] : (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+              }
+            });
+            __builtin_amdgcn_sched_barrier(0);
+          });
+        } else {
+          static_for<0, FN>([&](auto J) {
+            constexpr int j = decltype(J)::value;
+            if constexpr (SC == TP_GROUP_F32) {
+              if constexpr (i > 0) add_group(std::integral_constant<int, i - 1>{}, J);
+              p[j] = mfma_plain<FMT_A, FMT_B>(fb[j], fa, (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f});
+            } else {
+              acc[i][j] = mfma_scaled<FMT_A, FMT_B, i & 3, j>(fb[j], fa, acc[i][j], (int)sc.eb, (int)sc.ea[i >> 2]);
+            }
+          });
+        }
+        if constexpr (SLDS) sa = r.s;
+        if constexpr (SC == TP_GROUP_E8M0) {
+  #pragma unroll
+          for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(acc[i][j]));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      if constexpr (SC == TP_GROUP_F32) {
+        static_for<0, FN>([&](auto J) { add_group(std::integral_constant<int, FM - 1>{}, J); });
+      }
+      sc = sc_next;
+      load_b(buf_next, sc);
+      buf = buf_next;
+    }
+    wait_a(ra0);
   }
-  wait_a(ra0);
   __syncthreads();
 
   uint32_t* red = reinterpret_cast<uint32_t*>(lds);
   if constexpr (EPI == G_GLU_FWD) store_glu_fwd<WM, WN, FN, SC>(a, at, acc, red);
   else if constexpr (EPI == G_GLU_BWD) store_glu_bwd<WM, WN, FN, FMT_A, SC>(a, at, acc, lds);
-  else store_plain<WM, WN, FN>(a, at, acc);
+  else if constexpr (EPI == G_RAW_FWD) store_raw_fwd<WM, WN, FM, FN>(a, at, acc);
+  else if constexpr (EPI == G_RAW_BWD) store_raw_bwd<WM, WN, FM, FN>(a, at, acc);
+  else store_plain<WM, WN, FM, FN>(a, at, acc);
 }
 
-template <int WM, int WN, int FN, int NS, int SC, bool SQ, int FMT_A, int FMT_B, int SUM, int EPI>
+template <int WM, int WN, int FM, int FN, int NS, int SC, bool SQ, int FMT_A, int FMT_B, int SUM, int EPI>
 static hipError_t launch(G8GemmArgs& a, hipStream_t st) {
-  constexpr int BM = 128 * WM, BN = EPI == G_GLU_FWD ? 8 * FN * WN : 16 * FN * WN;
+  constexpr int BM = 16 * FM * WM, BN = EPI == G_GLU_FWD || EPI == G_RAW_FWD ? 8 * FN * WN : 16 * FN * WN;
   const int64_t tm = (a.M + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
   if (tm * tn > 0x7fffffff) return hipErrorInvalidValue;
   a.tiles_m = (int)tm;
   a.tiles_n = (int)tn;
   if (tm * tn == 0) return hipSuccess;
-  hipLaunchKernelGGL((gemm<WM, WN, FN, NS, SC, SQ, FMT_A, FMT_B, SUM, EPI>), dim3((unsigned)(tm * tn)),
+  hipLaunchKernelGGL((gemm<WM, WN, FM, FN, NS, SC, SQ, FMT_A, FMT_B, SUM, EPI>), dim3((unsigned)(tm * tn)),
                      dim3(64 * WM * WN), 0, st, a);
   return hipGetLastError();
 }
