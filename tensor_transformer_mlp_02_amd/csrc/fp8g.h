@@ -90,23 +90,39 @@ struct GroupScale {
   }
 };
 
-// Codes of four values; zeros where the group has no scale (a NaN times 0 is
+// The same without the clamp, for values of the group that `inv` is of: none
+// of them times inv lies more than two roundings above the largest code.
+template <int FMT>
+__device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
+  int w;
+  if constexpr (FMT == 0) {
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+  } else {
+    w = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, 0, false);
+    w = __builtin_amdgcn_cvt_pk_bf8_f32(c, d, w, true);
+  }
+  return (uint32_t)w;
+}
+
+// Codes of four values of a group; zeros where the group has no scale (a NaN times 0 is
 // no zero).
 template <int FMT>
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float inv) {
-  return inv > 0.0f ? fp8x4<FMT>(a, b, c, d, inv) : 0u;
+  return inv > 0.0f ? pack4<FMT>(a * inv, b * inv, c * inv, d * inv) : 0u;
 }
 
-// Two more of four codes: the low pair (the word is new) or the high one
-template <int FMT>
-__device__ __forceinline__ uint32_t codes2(float a, float b, float inv, uint32_t word, bool high) {
-  constexpr float VMAX = FMT == 0 ? 448.0f : 57344.0f;
-  a = inv > 0.0f ? fminf(fmaxf(a * inv, -VMAX), VMAX) : 0.0f;
-  b = inv > 0.0f ? fminf(fmaxf(b * inv, -VMAX), VMAX) : 0.0f;
-  if constexpr (FMT == 0) return high ? __builtin_amdgcn_cvt_pk_fp8_f32(a, b, (int)word, true) : __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-  else return high ? __builtin_amdgcn_cvt_pk_bf8_f32(a, b, (int)word, true) : __builtin_amdgcn_cvt_pk_bf8_f32(a, b, 0, false);
+// the largest over the 16 lanes of a row, in all of them
+template <typename F>
+__device__ __forceinline__ uint32_t over16(uint32_t v, F most) {
+  v = most(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xb1, 0xf, 0xf, true));   // lanes 1 0 3 2
+  v = most(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4e, 0xf, 0xf, true));   // 2 3 0 1
+  v = most(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xf, 0xf, true));  // mirrored in 8
+  return most(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xf, 0xf, true));  // and in 16
 }
-
+__device__ __forceinline__ uint32_t top_of_16(uint32_t v) {
+  return over16(v, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
 __device__ __forceinline__ uint32_t xor_max(uint32_t v, int d) {
   return max(v, (uint32_t)__shfl_xor((int)v, d, 64));
 }

@@ -46,9 +46,9 @@ inline double g8_small_ns(int64_t tiles, int64_t kt, double first, double one, d
 // whether there is a LARGE kernel
 inline G8Form g8_plan_gemm(int64_t M, int64_t N, int64_t kt, bool f32, bool large) {
   if (M <= 64) return G8_FEW;
-  const double few = 5000 + g8_few_ns(M, N, kt, 0.64, 1.06, 2000, 2900);
+  const double few = 4000 + g8_few_ns(M, N, kt, 0.64, 1.06, 2000, 1800);
   const double small = f32 ? g8_small_ns(g8_over(M, 64) * g8_over(N, 128), kt, 4000, 850, 0, 1350)
-                           : g8_small_ns(g8_over(M, 64) * g8_over(N, 128), kt, 3000, 700, 0, 880);
+                           : g8_small_ns(g8_over(M, 64) * g8_over(N, 128), kt, 2500, 700, 0, 880);
   const double whole = 4000 + kt * (f32 ? 3300.0 : 2250.0) * g8_over(g8_over(M, 256) * g8_over(N, 256), 256);
   if (large && whole < std::min(few, small)) return G8_LARGE;
   return few < small ? G8_FEW : G8_SMALL;

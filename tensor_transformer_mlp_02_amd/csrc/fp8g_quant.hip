@@ -50,12 +50,6 @@ __device__ __forceinline__ uint32_t top8(const float f[8]) {
   return m;
 }
 
-__device__ __forceinline__ uint32_t top_of_16(uint32_t m) {
-#pragma unroll
-  for (int d = 1; d < 16; d <<= 1) m = xor_max(m, d);
-  return m;
-}
-
 // rows form: a workgroup takes 16 rows x QG groups a turn (the scales of the
 // 16 rows lie together)
 constexpr int QG = 4;
@@ -90,63 +84,99 @@ __global__ __launch_bounds__(QNT) void quant_rows(G8QuantArgs a) {
   }
 }
 
-// tile form
+// tile form.  A lane's 8 neighbouring values of a row, as loaded: bf16 ones
+// are compared two at a time, as 15-bit magnitudes.
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a), __builtin_bit_cast(u16x2_t, b)));
+}
+template <typename T> struct Eight;
+template <> struct Eight<bf16_t> {
+  static constexpr int W = 4;  // words of magnitudes
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const bf16_t* x, int64_t off, int64_t left) {
+    u32x4_t v = {0u, 0u, 0u, 0u};
+    if (left > 0) v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(x + off));
+    *reinterpret_cast<u32x4_t*>(w) = v;
+  }
+  __device__ __forceinline__ float value(int k) const {
+    return __uint_as_float(k & 1 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
+  }
+  __device__ __forceinline__ uint32_t mags(int i) const { return w[i] & 0x7fff7fffu; }
+  static __device__ __forceinline__ uint32_t most(uint32_t a, uint32_t b) { return max_u16x2(a, b); }
+  // fp32 magnitude of a word's value, and of the larger of its two
+  static __device__ __forceinline__ uint32_t one(const uint32_t* m, int k) { return k & 1 ? m[k / 2] & 0xffff0000u : m[k / 2] << 16; }
+  static __device__ __forceinline__ uint32_t whole(uint32_t m) { return max(m & 0xffff0000u, m << 16); }
+};
+template <> struct Eight<float> {
+  static constexpr int W = 8;
+  float f[8];
+  __device__ __forceinline__ void load(const float* x, int64_t off, int64_t left) { load8_part(x + off, left > 8 ? 8 : (int)left, f); }
+  __device__ __forceinline__ float value(int k) const { return f[k]; }
+  __device__ __forceinline__ uint32_t mags(int i) const { return mag(f[i]); }
+  static __device__ __forceinline__ uint32_t most(uint32_t a, uint32_t b) { return max(a, b); }
+  static __device__ __forceinline__ uint32_t one(const uint32_t* m, int k) { return m[k]; }
+  static __device__ __forceinline__ uint32_t whole(uint32_t m) { return m; }
+};
+
 constexpr int T_PITCH = 132;  // bytes of a staged row of codes
 template <typename T, int FMT, int SC, bool SQ>
-__global__ __launch_bounds__(QNT) void quant_tile(G8QuantArgs a) {
+__global__ __launch_bounds__(QNT, 4) void quant_tile(G8QuantArgs a) {
+  typedef Eight<T> E;
   __shared__ __attribute__((aligned(16))) uint8_t stage[kGroup * T_PITCH];
-  __shared__ uint32_t red[QNT / 64][kGroup];
+  __shared__ uint32_t red[QNT / 64][16 * E::W];
+  __shared__ float inverse[kGroup];
   const T* x = reinterpret_cast<const T*>(a.x);
   const int64_t gc = groups_of(a.cols), gr = groups_of(a.rows);
   const int64_t pc = gc * kGroup, pr = gr * kGroup, ldq = pc * a.parts;
   const int64_t turns = gc * gr * a.parts;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int r16 = tid >> 4, c8 = (tid & 15) * 8;
+  const int r16 = tid >> 4, l16 = tid & 15, c8 = l16 * 8;
   for (int64_t t = blockIdx.x; t < turns; t += gridDim.x) {
     const int64_t part = t / (gc * gr), v = t - part * gc * gr;
     const int64_t tr = v / gc, tc = v % gc;
     const int64_t r0 = tr * kGroup, c = tc * kGroup + c8;
-    float f[8][8];
+    E e[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int64_t r = r0 + 16 * u + r16;
-      load_row8<T>(x, r * a.ldx + part * a.cols + c, r < a.rows ? a.cols - c : 0, f[u]);
+      e[u].load(x, r * a.ldx + part * a.cols + c, r < a.rows ? a.cols - c : 0);
     }
-    float col_inv[8];
     float sq_inv = 0.0f;
     if (SQ || a.q_t) {
-      // largest magnitude of each column (squares: of all)
-      uint32_t m[8];
+      // largest magnitude of each column over the rows of a thread, a
+      // wavefront, the workgroup
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        m[k] = mag(f[0][k]);
+      for (int i = 0; i < E::W; ++i) {
+        uint32_t m = e[0].mags(i);
 #pragma unroll
-        for (int u = 1; u < 8; ++u) m[k] = max(m[k], mag(f[u][k]));
-        m[k] = xor_max(xor_max(m[k], 16), 32);
-      }
-      if (lane < 16) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) red[wave][c8 + k] = m[k];
+        for (int u = 1; u < 8; ++u) m = E::most(m, e[u].mags(i));
+        m = E::most(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+        m = E::most(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+        if (lane < 16) red[wave][l16 * E::W + i] = m;
       }
       __syncthreads();
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        m[k] = max(max(red[0][c8 + k], red[1][c8 + k]), max(red[2][c8 + k], red[3][c8 + k]));
       if constexpr (SQ) {
-        uint32_t w = m[0];
+        uint32_t w = 0;
 #pragma unroll
-        for (int k = 1; k < 8; ++k) w = max(w, m[k]);
-        const GroupScale<FMT, SC> gs(top_of_16(w));
+        for (int i = 0; i < E::W; ++i) {
+          const int at = l16 * E::W + i;
+          w = E::most(w, E::most(E::most(red[0][at], red[1][at]), E::most(red[2][at], red[3][at])));
+        }
+        const GroupScale<FMT, SC> gs(top_of_16(E::whole(w)));
         sq_inv = gs.inv;
         if (tid == 0 && a.q) gs.store(a.s, (part * gr + tr) * gc + tc);
         if (tid == 0 && a.q_t) gs.store(a.s_t, (part * gc + tc) * gr + tr);
       } else {
+        if (tid < kGroup) {  // a column each
+          uint32_t m[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const GroupScale<FMT, SC> gs(m[k]);
-          col_inv[k] = gs.inv;
-          if (tid < 16 && c + k < a.cols) gs.store(a.s_t, (part * gr + tr) * a.cols + c + k);
+          for (int k = 0; k < 4; ++k) m[k] = E::one(red[k] + tid / 8 * E::W, tid % 8);
+          const GroupScale<FMT, SC> gs(max(max(m[0], m[1]), max(m[2], m[3])));
+          inverse[tid] = gs.inv;
+          if (tc * kGroup + tid < a.cols) gs.store(a.s_t, (part * gr + tr) * a.cols + tc * kGroup + tid);
         }
+        __syncthreads();
       }
     }
     if (a.q) {
@@ -155,32 +185,41 @@ __global__ __launch_bounds__(QNT) void quant_tile(G8QuantArgs a) {
         const int64_t r = r0 + 16 * u + r16;
         float inv = sq_inv;
         if constexpr (!SQ) {
-          const GroupScale<FMT, SC> gs(top_of_16(top8(f[u])));
+          uint32_t m = e[u].mags(0);
+#pragma unroll
+          for (int i = 1; i < E::W; ++i) m = E::most(m, e[u].mags(i));
+          const GroupScale<FMT, SC> gs(top_of_16(E::whole(m)));
           inv = gs.inv;
-          if (c8 == 0 && r < a.rows) gs.store(a.s, (part * gc + tc) * a.rows + r);
+          if (l16 == 0 && r < a.rows) gs.store(a.s, (part * gc + tc) * a.rows + r);
         }
         if (r < a.rows) {
-          const u32x2_t o = {codes4<FMT>(f[u][0], f[u][1], f[u][2], f[u][3], inv),
-                             codes4<FMT>(f[u][4], f[u][5], f[u][6], f[u][7], inv)};
+          const u32x2_t o = {codes4<FMT>(e[u].value(0), e[u].value(1), e[u].value(2), e[u].value(3), inv),
+                             codes4<FMT>(e[u].value(4), e[u].value(5), e[u].value(6), e[u].value(7), inv)};
           *reinterpret_cast<u32x2_t*>(a.q + r * ldq + part * pc + c) = o;
         }
       }
     }
     if (a.q_t) {
+      float ci[8];
+      bool plain = true;  // (a column without a scale: zeros, whatever it holds)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        ci[k] = SQ ? sq_inv : inverse[c8 + k];
+        plain = plain && ci[k] > 0.0f;
+      }
+      plain = __all(plain);
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         uint32_t* d = reinterpret_cast<uint32_t*>(stage + (16 * u + r16) * T_PITCH + c8);
+        float y[8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if constexpr (SQ) {
-            d[h] = codes4<FMT>(f[u][4 * h], f[u][4 * h + 1], f[u][4 * h + 2], f[u][4 * h + 3], sq_inv);
-          } else {
-            float y[4];
+        for (int k = 0; k < 8; ++k) y[k] = e[u].value(k) * ci[k];
+        if (!plain) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) y[k] = col_inv[4 * h + k] > 0.0f ? f[u][4 * h + k] * col_inv[4 * h + k] : 0.0f;
-            d[h] = fp8x4<FMT>(y[0], y[1], y[2], y[3], 1.0f);
-          }
+          for (int k = 0; k < 8; ++k) y[k] = ci[k] > 0.0f ? y[k] : 0.0f;
         }
+        d[0] = pack4<FMT>(y[0], y[1], y[2], y[3]);
+        d[1] = pack4<FMT>(y[4], y[5], y[6], y[7]);
       }
       __syncthreads();
       // thread: columns 4 q .. 4 q + 3, rows 16 g .. 16 g + 15
@@ -204,10 +243,8 @@ __global__ __launch_bounds__(QNT) void quant_tile(G8QuantArgs a) {
           *reinterpret_cast<u32x4_t*>(a.q_t + (part * a.cols + col) * pr + r0 + 16 * g) = o;
         }
       }
-      __syncthreads();  // the stage and the sums are rewritten by the next turn
-    } else if constexpr (SQ) {
-      __syncthreads();
     }
+    __syncthreads();  // the stage and the sums are rewritten by the next turn
   }
 }
 

@@ -144,9 +144,7 @@ __device__ __forceinline__ void store_raw_bwd(const G8GemmArgs& a, const Place& 
 template <int FMT, int SC>
 __device__ __forceinline__ void store_column(uint8_t* q_t, void* s_t, const float v[8], uint32_t top, int64_t pm,
                                              int64_t m, int64_t col, int64_t cols, int64_t token_group, int p) {
-#pragma unroll
-  for (int d = 1; d < 16; d <<= 1) top = xor_max(top, d);
-  const GroupScale<FMT, SC> gs(top);
+  const GroupScale<FMT, SC> gs(top_of_16(top));
   const u32x2_t o = {codes4<FMT>(v[0], v[1], v[2], v[3], gs.inv), codes4<FMT>(v[4], v[5], v[6], v[7], gs.inv)};
   if (col < cols) {
     *reinterpret_cast<u32x2_t*>(q_t + col * pm + m) = o;
