@@ -53,32 +53,46 @@ struct Place {
   int wm, wn, p, q;
 };
 
+// Outputs go through buffers that end with the last row; a column past the
+// last takes an offset behind every end.  So no output needs a branch.
+constexpr uint32_t OUTSIDE = 0x80000000u;
+__device__ __forceinline__ u32x2_t bf16x4(f32x4_t v) {
+  return (u32x2_t){pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+}
+
 // acc[i][j][t]: row m0 + FM p + i; column 16 j + 4 q + t of the wavefront's
 template <int WM, int WN, int FM, int FN>
 __device__ __forceinline__ void store_plain(const G8GemmArgs& a, const Place& at, f32x4_t (&acc)[FM][FN]) {
-  const int n = at.n0 + at.wn * 16 * FN + at.q * 4;
+  const int n = at.n0 + at.wn * 16 * FN + at.q * 4, size = a.out_bf16 ? 2 : 4;
+  const int rows = (int)max((int64_t)0, min((int64_t)(16 * FM), a.M - at.m0));
+  const rsrc_t rc = buffer_of(reinterpret_cast<uint8_t*>(a.C) + at.m0 * a.N * size, rows * a.N * size);
+  auto offset = [&](int i, int j) {
+    return n + 16 * j < a.N ? (uint32_t)((FM * at.p + i) * a.N + n + 16 * j) * size : OUTSIDE;
+  };
+  static_for<0, FM / 2>([&](auto Ic) {  // two rows' loads at a time
+    constexpr int i0 = 2 * decltype(Ic)::value;
+    if (a.accumulate) {
+      f32x4_t c[2][FN];
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int64_t m = at.m0 + FM * at.p + i;
-    if (m >= a.M) continue;
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      if (n + 16 * j >= a.N) continue;
-      float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-      const int64_t off = m * a.N + n + 16 * j;
-      if (a.out_bf16) {
-        Store4<bf16_t>::store(a.C, off, v);
-      } else {
-        if (a.accumulate) {
-          float w[4];
-          Store4<float>::load(a.C, off, w);
+        for (int j = 0; j < FN; ++j)
+          c[i][j] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rc, offset(i0 + i, j), 0, 0));
 #pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] += w[k];
-        }
-        Store4<float>::store(a.C, off, v);
-      }
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) acc[i0 + i][j][t] += c[i][j][t];
     }
-  }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        if (a.out_bf16) __builtin_amdgcn_raw_buffer_store_b64(bf16x4(acc[i0 + i][j]), rc, offset(i0 + i, j), 0, 0);
+        else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[i0 + i][j]), rc, offset(i0 + i, j), 0, 0);
+      }
+  });
 }
 
 // The gated block's values in fp32 (a.raw): their groups span tiles
@@ -159,9 +173,13 @@ __device__ __forceinline__ void store_glu_fwd(const G8GemmArgs& a, const Place& 
                                               uint32_t* red) {
   constexpr int J = FN / 2;
   static_assert(8 * FN * WN == 128, "one group of 128 columns");
-  const int64_t F = a.N, pf = padded(F), pm = padded(a.M);
-  const int64_t f = at.n0 + at.wn * 8 * FN + at.q * 4;
-  const int64_t m = at.m0 + 8 * at.p;
+  const int F = a.N, pf = (int)padded(F);
+  const int64_t pm = padded(a.M), m = at.m0 + 8 * at.p;
+  const int f = at.n0 + at.wn * 8 * FN + at.q * 4;
+  const int rows = (int)max((int64_t)0, min((int64_t)128, a.M - at.m0));
+  const rsrc_t rz = buffer_of(reinterpret_cast<bf16_t*>(a.Z) + at.m0 * 2 * F, a.Z ? rows * F * 4 : 0);
+  const rsrc_t rh = buffer_of(reinterpret_cast<bf16_t*>(a.H) + at.m0 * F, a.H ? rows * F * 2 : 0);
+  const rsrc_t rq = buffer_of(a.q + at.m0 * pf, a.q ? rows * pf : 0);
   const Gate gate(a.gate);
   uint32_t top[8];
 #pragma unroll
@@ -169,22 +187,20 @@ __device__ __forceinline__ void store_glu_fwd(const G8GemmArgs& a, const Place& 
     top[i] = 0;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int64_t c = f + 16 * j;
-      const bool there = m + i < a.M && c < F;
-      float g[4], u[4], h[4];
+      const int c = f + 16 * j;
+      const f32x4_t g = acc[i][j], u = acc[i][J + j];
+      if (a.Z) {
+        const uint32_t off = c < F ? (uint32_t)((8 * at.p + i) * 2 * F + c) * 2u : OUTSIDE;
+        __builtin_amdgcn_raw_buffer_store_b64(bf16x4(g), rz, off, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b64(bf16x4(u), rz, off, 2 * F, 0);
+      }
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        g[t] = acc[i][j][t];
-        u[t] = acc[i][J + j][t];
-        h[t] = gate.act(g[t]) * u[t];
-        acc[i][j][t] = h[t];
-        top[i] = max(top[i], mag(h[t]));
+        acc[i][j][t] = gate.act(g[t]) * u[t];
+        top[i] = max(top[i], mag(acc[i][j][t]));
       }
-      if (a.Z && there) {
-        Store4<bf16_t>::store(a.Z, (m + i) * 2 * F + c, g);
-        Store4<bf16_t>::store(a.Z, (m + i) * 2 * F + F + c, u);
-      }
-      if (a.H && there) Store4<bf16_t>::store(a.H, (m + i) * F + c, h);
+      if (a.H)
+        __builtin_amdgcn_raw_buffer_store_b64(bf16x4(acc[i][j]), rh, c < F ? (uint32_t)((8 * at.p + i) * F + c) * 2u : OUTSIDE, 0, 0);
     }
   }
   if (a.q) {
@@ -203,13 +219,11 @@ __device__ __forceinline__ void store_glu_fwd(const G8GemmArgs& a, const Place& 
 #pragma unroll
       for (int c = 0; c < WN; ++c) w = max(w, red[(at.wm * WN + c) * 128 + 8 * at.p + i]);
       const GroupScale<0, SC> gs(w);
-      if (m + i < a.M) {
 #pragma unroll
-        for (int j = 0; j < J; ++j)
-          *reinterpret_cast<uint32_t*>(a.q + (m + i) * pf + f + 16 * j) =
-              codes4<0>(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3], gs.inv);
-        if (at.wn == 0 && at.q == 0) gs.store(a.s, (int64_t)(at.n0 / kGroup) * a.M + m + i);
-      }
+      for (int j = 0; j < J; ++j)
+        __builtin_amdgcn_raw_buffer_store_b32(codes4<0>(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3], gs.inv), rq,
+                                              (uint32_t)((8 * at.p + i) * pf + f + 16 * j), 0, 0);
+      if (at.wn == 0 && at.q == 0 && m + i < a.M) gs.store(a.s, (int64_t)(at.n0 / kGroup) * a.M + m + i);
     }
   }
   if (a.q_t && at.m0 < pm) {
@@ -271,7 +285,7 @@ __device__ __forceinline__ void store_glu_bwd(const G8GemmArgs& a, const Place& 
       u32x2_t zg[4], zu[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t off = c < F ? (uint32_t)((8 * at.p + i0 + i) * 2 * F + c) * 2u : 0x80000000u;
+        const uint32_t off = c < F ? (uint32_t)((8 * at.p + i0 + i) * 2 * F + c) * 2u : OUTSIDE;
         zg[i] = __builtin_amdgcn_raw_buffer_load_b64(rz, off, 0, 0);
         zu[i] = __builtin_amdgcn_raw_buffer_load_b64(rz, off, 2 * F, 0);
       }
@@ -347,7 +361,7 @@ __device__ __forceinline__ void store_glu_bwd(const G8GemmArgs& a, const Place& 
     static_for<0, NH>([&](auto Hc) {
       constexpr int hf = decltype(Hc)::value;
       const int c = f + 16 * hf;
-      const uint32_t off = c < pf ? (uint32_t)((8 * at.p + i) * 2 * pf + c) : 0x80000000u;
+      const uint32_t off = c < pf ? (uint32_t)((8 * at.p + i) * 2 * pf + c) : OUTSIDE;
       if constexpr (hf < PARKED) {
         const f32x4_t w = wait[(8 * hf + i) * 64];
 #pragma unroll
