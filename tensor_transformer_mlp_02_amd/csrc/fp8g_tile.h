@@ -18,7 +18,7 @@
 //
 // Shared memory holds rows of 128 codes, the 16-byte chunk c of a row at
 // c ^ (the row's index a or b) % 8: the 8 lanes that are served together read 8
-// different chunks.
+// different chunks.  Row scales lie by step: that of row FM a + i at 16 i + a.
 #pragma once
 
 #include "fp8g.h"
@@ -462,7 +462,8 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
   const rsrc_t ra = buffer_of(a.A + mt * a.lda, rows * lda);
   const rsrc_t rb = buffer_of(a.B + (int64_t)at.n0 * a.K, cols * a.K);
   const rsrc_t rb2 = buffer_of(a.B2 + (int64_t)at.n0 * a.K, cols * a.K);
-  const int sr = (wave % (BM / 64)) * 64 + lane;
+  const int slot = (wave % (BM / 64)) * 64 + lane;
+  const int sr = slot / (16 * FM) * (16 * FM) + slot % 16 * FM + slot % (16 * FM) / 16;
   auto load_tile = [&](int kt, int buf) {
     const int part = kt >= kt_part ? 1 : 0, kb = kt - part * kt_part;
     int ln = lane;
@@ -470,9 +471,9 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
     const int l8 = ln >> 3, ch = ln & 7;
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
-      const int blk = wave * LA + i;
+      const int blk = wave * LA + i, r = blk * 8 + l8;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void_t*)(lds + buf * A_BYTES + blk * 1024), 16,
-                                               (blk * 8 + l8) * lda + ((ch ^ (((blk * 8 + l8) / FM) & 7)) << 4), kt * 128, 0, 0);
+                                               r * lda + ((ch ^ ((r / FM) & 7)) << 4), kt * 128, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < LB; ++i) {
@@ -494,7 +495,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
   const uint32_t l0 = lds_address(lds);
   const uint32_t c0 = ((2 * at.q) ^ (at.p & 7)) << 4;
   const uint32_t pa = l0 + (at.wm * 16 * FM + FM * at.p) * 128 + c0, pb = l0 + B_AT + (at.wn * 16 * FN + at.p) * 128 + c0;
-  const uint32_t ps = l0 + S_AT + (at.wm * 16 * FM + FM * at.p) * 4;
+  const uint32_t ps = l0 + S_AT + (at.wm * 16 * FM + at.p) * 4;
 
   // Scales of a tile: of its columns, and E8M0 ones of its rows.  Those of a
   // lane are neighbours, behind one offset from a base that a wavefront
@@ -503,6 +504,15 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
   struct Scales {
     float b[SC == TP_GROUP_F32 ? SBT : 1][SC == TP_GROUP_F32 ? FN : 1];
     uint32_t eb, ea[2];
+    uint32_t byte[SC == TP_GROUP_E8M0 && !SQ ? FN : 1];  // eb's, as loaded
+    // (joined when they are used: here they are still on their way)
+    __device__ __forceinline__ void join() {
+      if constexpr (SC == TP_GROUP_E8M0 && !SQ) {
+        eb = 0;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) eb |= byte[j] << (8 * j);
+      }
+    }
   };
   const int nw = PAIR ? at.n0 + at.wn * 8 * FN : at.n0 + at.wn * 16 * FN;  // the wavefront's first column
   const int rows_w = (int)max((int64_t)0, min((int64_t)(16 * FM), a.M - at.m0)), cols_w = max(0, min(16 * FN, a.N - nw));
@@ -531,8 +541,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
       } else {
         const rsrc_t rs = buffer_of(reinterpret_cast<const uint8_t*>(from(0)) + (int64_t)kb * a.N + nw, cols_w);
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
-          s.eb |= (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rs, 16 * j + at.p, 0, 0) << (8 * j);
+        for (int j = 0; j < FN; ++j) s.byte[j] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rs, 16 * j + at.p, 0, 0);
       }
       const rsrc_t rs = buffer_of(reinterpret_cast<const uint8_t*>(a.sA) + (int64_t)kt * a.M + at.m0, rows_w);
       s.ea[0] = s.ea[1] = 0;
@@ -591,7 +600,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
   auto ask_a = [&](auto I, Row& r, int buf) {
     constexpr int i = decltype(I)::value;
     const uint32_t a0 = pa + buf * A_BYTES;
-    if constexpr (SLDS) r.template ask<i * 128, i * 4>(a0, a0 ^ 16, ps + buf * S_BYTES);
+    if constexpr (SLDS) r.template ask<i * 128, i * 64>(a0, a0 ^ 16, ps + buf * S_BYTES);
     else r.template ask<i * 128>(a0, a0 ^ 16);
   };
   auto wait_a = [&](Row& r) {
@@ -640,6 +649,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
     };
     auto one_tile = [&](Set& t, Set& next, int kt, int buf, int buf_next) {
       sc = sc_next;
+      sc.join();
       load_scales(min(kt + 1, kt_all - 1), sc_next);
       // this tile is read, and the next one there, for every wavefront
       wait_tiles(max(0, min(kt_all - 2 - kt, NS - 2)));
@@ -705,6 +715,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
   } else {
     int buf = 0;
     sc = sc_next;
+    sc.join();
     load_b(0, sc);
     ask_a(std::integral_constant<int, 0>{}, ra0, 0);
     for (int kt = 0; kt < kt_all; ++kt) {
@@ -770,6 +781,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
         static_for<0, FN>([&](auto J) { add_group(std::integral_constant<int, FM - 1>{}, J); });
       }
       sc = sc_next;
+      sc.join();
       load_b(buf_next, sc);
       buf = buf_next;
     }
