@@ -607,14 +607,15 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
     if constexpr (SLDS) r.wait_scale();
     else r.wait();
   };
-  auto load_b = [&](int buf, const Scales& s) {  // the wavefront's columns of a tile
+  Row cb[FN];  // the wavefront's columns of a tile, on their way
+  auto ask_b = [&](int buf) {
     const uint32_t b0 = pb + buf * B_BYTES;
-    static_for<0, FN>([&](auto J) {
-      Row r;
-      r.template ask<decltype(J)::value * 2048>(b0, b0 ^ 16);
-      r.wait();
-      widen_b(J, r, s);
-    });
+    static_for<0, FN>([&](auto J) { cb[J].template ask<decltype(J)::value * 2048>(b0, b0 ^ 16); });
+  };
+  auto take_b = [&](const Scales& s) {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    static_for<0, FN>([&](auto J) { cb[J].arrived(); });
+    static_for<0, FN>([&](auto J) { widen_b(J, cb[J], s); });
   };
 
   f32x4_t p[FN];
@@ -716,7 +717,8 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
     int buf = 0;
     sc = sc_next;
     sc.join();
-    load_b(0, sc);
+    ask_b(0);
+    take_b(sc);
     ask_a(std::integral_constant<int, 0>{}, ra0, 0);
     for (int kt = 0; kt < kt_all; ++kt) {
       const bool more = kt + 1 < kt_all;
@@ -777,12 +779,15 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
         }
         __builtin_amdgcn_sched_barrier(0);
       });
+      // (widened, the columns leave no room for the next ones before here; FP8 ones
+      // would, but asked for beside the step's rows they took 3 % longer)
+      ask_b(buf_next);
       if constexpr (SC == TP_GROUP_F32) {
         static_for<0, FN>([&](auto J) { add_group(std::integral_constant<int, FM - 1>{}, J); });
       }
       sc = sc_next;
       sc.join();
-      load_b(buf_next, sc);
+      take_b(sc);
       buf = buf_next;
     }
     wait_a(ra0);
