@@ -35,8 +35,10 @@ __global__ __launch_bounds__(64 * NW) void gemm_few(G8GemmArgs a) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int p = lane & 15, q = lane >> 4;
-  const int n0 = blockIdx.x * 16 * NB;
-  const int64_t m_first = (int64_t)blockIdx.y * FEW_ROWS;
+  // (blocks of columns first: those that run together read the same rows of A)
+  const int blocks_n = (a.N + 16 * NB - 1) / (16 * NB);
+  const int n0 = (int)(blockIdx.x % blocks_n) * 16 * NB;
+  const int64_t m_first = (int64_t)(blockIdx.x / blocks_n) * FEW_ROWS;
   const int64_t M = a.M;
   int n[MATS];
 #pragma unroll
@@ -190,8 +192,10 @@ __global__ __launch_bounds__(64 * NW) void gemm_few(G8GemmArgs a) {
 
 template <int MT, int NB, int SC, bool SQ, int FMT_A, int FMT_B, int EPI>
 static hipError_t few_run(const G8GemmArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)((a.N + 16 * NB - 1) / (16 * NB)), (unsigned)((a.M + FEW_ROWS - 1) / FEW_ROWS));
-  hipLaunchKernelGGL((gemm_few<MT, NB, FEW_WAVES, SC, SQ, FMT_A, FMT_B, EPI>), grid, dim3(64 * FEW_WAVES), 0, st, a);
+  const int64_t blocks = g8_over(a.N, 16 * NB) * g8_over(a.M, FEW_ROWS);
+  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((gemm_few<MT, NB, FEW_WAVES, SC, SQ, FMT_A, FMT_B, EPI>), dim3((unsigned)blocks), dim3(64 * FEW_WAVES), 0,
+                     st, a);
   return hipGetLastError();
 }
 template <int SC, bool SQ, int FMT_A, int FMT_B, int EPI>

@@ -759,7 +759,9 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
                 p[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][c], wa, c ? p[j] : (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
               }
             });
-            __builtin_amdgcn_sched_barrier(0);
+            
+            if constexpr (c % 2) __builtin_amdgcn_sched_barrier(0);  // (two widenings at a time hold fewer registers)
+
           });
         } else {
           static_for<0, FN>([&](auto J) {

@@ -102,3 +102,10 @@ def few_bits_error(A, B):
     largest (2^-13 of it; a product may be twice the power of two that goes by, so 2^-12), and
     8 of them, against their sum of magnitudes: 2^-9."""
     return 2.0 ** -9 * (A.abs() @ B.abs().t()) + sum_error(A, B)
+
+
+# Sizes at which each of the kernels is taken (tests/test_fp8g_plan.py holds them to that): ragged in every dimension
+GEMM_FORMS = [(300, 1000, 640, "f32", "FEW"), (65, 2056, 1152, "bf16", "FEW"), (1030, 1000, 384, "bf16", "SMALL"),
+              (2000, 2040, 1152, "f32", "SMALL"), (2100, 2056, 384, "bf16", "LARGE"), (4100, 2056, 640, "f32", "LARGE")]
+FWD_FORMS = [(300, 2056, 1416, "FEW"), (500, 264, 1416, "SMALL"), (2000, 520, 1032, "GROUP"), (4100, 136, 1416, "LARGE")]
+BWD_FORMS = [(500, 264, 1416, "FEW"), (1000, 1032, 1416, "SMALL"), (2000, 520, 1032, "GROUP"), (6000, 1032, 2056, "LARGE")]

@@ -1,0 +1,66 @@
+"""The shared-memory reads that the tile kernels of FP8 with group scales ask for ahead of their use: in the assembly
+that hipcc writes for them, nothing touches a read's registers before the wait for it (CPU).  The compiler takes such
+a read's registers as written at once; a copy or a spill of one that is still on its way would be wrong."""
+import os
+import re
+import subprocess
+
+import pytest
+
+from tensor_transformer_mlp_02_amd import build as b
+
+REG = re.compile(r"\bv\[(\d+):(\d+)\]|\bv(\d+)\b")
+
+
+def registers(text):
+    out = set()
+    for m in REG.finditer(text):
+        out |= set(range(int(m.group(1)), int(m.group(2)) + 1)) if m.group(1) else {int(m.group(3))}
+    return out
+
+
+def touched_in_flight(lines):
+    """(reads seen, offending lines) of a listing; reads count where they stand in inline assembly."""
+    on_the_way, inline, reads, bad = set(), False, 0, []
+    for n, line in enumerate(lines, 1):
+        if "#ASMSTART" in line:
+            inline = True
+        if "#ASMEND" in line:
+            inline = False
+        text = line.split(";")[0].strip()
+        if re.match(r"^[^.\s]\S*:$", text):      # the next kernel
+            on_the_way = set()
+        if not text or text.startswith(".") or text.endswith(":"):
+            continue
+        op, _, rest = text.partition(" ")
+        if op.startswith("ds_read") and inline:
+            to, _, address = rest.partition(",")
+            if registers(to) & on_the_way or registers(address) & on_the_way:
+                bad.append((n, text))
+            on_the_way |= registers(to)
+            reads += 1
+        elif op == "s_waitcnt" and "lgkmcnt(0)" in text:
+            on_the_way = set()
+        elif registers(text) & on_the_way:
+            bad.append((n, text))
+    return reads, bad
+
+
+def test_the_check_sees_a_copy():
+    ask = ["k:", ";;#ASMSTART", "ds_read_b128 v[4:7], v1 offset:16", ";;#ASMEND"]
+    wait = [";;#ASMSTART", "s_waitcnt lgkmcnt(0)", ";;#ASMEND", "v_mov_b32 v9, v5"]
+    assert touched_in_flight(ask + ["v_add_u32 v8, v2, v3"] + wait) == (1, [])
+    assert touched_in_flight(ask + ["v_mov_b32 v9, v5"] + wait)[1] == [(5, "v_mov_b32 v9, v5")]
+    assert touched_in_flight(ask + ["scratch_store_dwordx4 off, v[4:7], off"] + wait)[1]
+    assert touched_in_flight(ask + [";;#ASMSTART", "ds_read_b32 v4, v2", ";;#ASMEND"] + wait)[1]
+
+
+@pytest.mark.skipif(not os.path.exists(b.HIPCC), reason="hipcc not available")
+@pytest.mark.parametrize("source", ["fp8g_gemm.hip", "fp8g_gemm32.hip", "fp8g_glu.hip"])
+def test_nothing_touches_a_read_on_its_way(source, tmp_path):
+    out = tmp_path / "listing.s"
+    flags = [f for f in b.FLAGS if f != "-Wall"]
+    subprocess.run([b.HIPCC, *flags, "--cuda-device-only", "-S", os.path.join(b.CSRC, source), "-o", str(out)], check=True,
+                   capture_output=True)
+    reads, bad = touched_in_flight(out.read_text().splitlines())
+    assert reads > 300 and not bad, bad[:5]

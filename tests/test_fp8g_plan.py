@@ -1,0 +1,49 @@
+"""Which kernel a product with group scales takes (CPU): the sizes of the GPU tests reach each of them, and small
+changes of the sizes do not leave the range of the kernels."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+import fp8g_ref as ref
+from tensor_transformer_mlp_02_amd import build as b
+
+NAMES = ["FEW", "SMALL", "GROUP", "LARGE"]
+
+
+@pytest.fixture(scope="module")
+def plan(tmp_path_factory):
+    if shutil.which("g++") is None:
+        pytest.skip("no host compiler")
+    d = tmp_path_factory.mktemp("plan")
+    (d / "plan.cpp").write_text("""
+#include <cstdio>
+#include <cstdlib>
+#include "fp8g_plan.h"
+using namespace tpmlp;
+int main(int, char** v) {  // kind M N kt flag, ...
+  const long M = atol(v[2]), N = atol(v[3]), kt = atol(v[4]), flag = atol(v[5]);
+  printf("%d", v[1][0] == 'g' ? g8_plan_gemm(M, N, kt, flag, true) : g8_plan_glu(M, N, kt, flag));
+}
+""")
+    exe = str(d / "plan")
+    subprocess.run(["g++", "-std=c++17", "-I", b.CSRC, str(d / "plan.cpp"), "-o", exe], check=True)
+    return lambda *a: NAMES[int(subprocess.run([exe, *map(str, a)], capture_output=True, text=True, check=True).stdout)]
+
+
+@pytest.mark.parametrize("M,N,K,out,form", ref.GEMM_FORMS)
+def test_gemm_forms(plan, M, N, K, out, form):
+    assert plan("gemm", M, N, K // 128, int(out == "f32")) == form
+
+
+@pytest.mark.parametrize("back,sizes", [(0, s) for s in ref.FWD_FORMS] + [(1, s) for s in ref.BWD_FORMS])
+def test_gated_forms(plan, back, sizes):
+    N, H, F, form = sizes
+    assert plan("glu", N, F, ref.up(H), back) == form
+
+
+def test_every_kernel_is_reached():
+    assert {s[-1] for s in ref.GEMM_FORMS} == {"FEW", "SMALL", "LARGE"}
+    for forms in (ref.FWD_FORMS, ref.BWD_FORMS):
+        assert {s[-1] for s in forms} == set(NAMES)
