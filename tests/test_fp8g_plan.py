@@ -24,7 +24,7 @@ def plan(tmp_path_factory):
 using namespace tpmlp;
 int main(int, char** v) {  // kind M N kt flag, ...
   const long M = atol(v[2]), N = atol(v[3]), kt = atol(v[4]), flag = atol(v[5]);
-  printf("%d", v[1][0] == 'g' ? g8_plan_gemm(M, N, kt, flag, true) : g8_plan_glu(M, N, kt, flag));
+  printf("%d", v[1][1] == 'e' ? g8_plan_gemm(M, N, kt, flag, true) : g8_plan_glu(M, N, kt, flag));
 }
 """)
     exe = str(d / "plan")
