@@ -90,8 +90,8 @@ struct GroupScale {
   }
 };
 
-// The same without the clamp, for values of the group that `inv` is of: none
-// of them times inv lies more than two roundings above the largest code.
+// Values of the group that `inv` is of need no clamp: none of them times inv
+// lies more than two roundings above the largest code.
 template <int FMT>
 __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
   int w;

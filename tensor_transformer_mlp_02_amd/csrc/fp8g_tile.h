@@ -2,11 +2,16 @@
 // formulas: include/tpmlp_fp8g.h).  MFMA-bound.
 //
 // A workgroup makes a tile of (16 FM WM) x (16 FN WN) outputs with WM x WN
-// wavefronts, each 16 FM x 16 FN as FM x FN blocks of
-// v_mfma_f32_16x16x128_f8f6f4: one instruction spans exactly one group of the
-// summed index, so its result is the group's exact sum, scaled and added in
-// fp32 (TP_GROUP_F32), or the instruction applies the scales itself and
-// accumulates (TP_GROUP_E8M0).
+// wavefronts, each 16 FM x 16 FN as FM x FN blocks.  A k-tile is one group of 128.
+//   SUM_FP8  v_mfma_f32_16x16x128_f8f6f4 makes a block's sum over the group in one
+//            instruction: scaled and added in fp32 a step later (TP_GROUP_F32), or the
+//            instruction applies the scales itself and accumulates (TP_GROUP_E8M0).
+//   SUM_F32  codes are widened to bf16 (E8M0 scales go into the exponents) for four
+//            v_mfma_f32_16x16x32_bf16, whose sums are fp32's.
+// 4096 x 8192 x 3584: SUM_FP8 136 us (1.77 PFLOP/s; among others 123 to 129), SUM_F32 212.
+// The matrix cores are busy 35 to 45 % of the time: SUM_FP8 waits for shared memory (8 codes are
+// read for each 16 that a tile of 256 x 256 multiplies), SUM_F32 for the widening and the sums
+// beside its instructions.
 //
 // Block i's row index a is row FM a + i of the wavefront's, block j's column
 // index b is column 16 j + b.  The instruction is issued with the B codes first, which
@@ -56,7 +61,9 @@ struct Place {
 };
 
 // Outputs go through buffers that end with the last row; a column past the
-// last takes an offset behind every end.  So no output needs a branch.
+// last takes an offset behind every end.  So no output needs a branch.  (Both halves of
+// [G|U] have a buffer: a scalar offset is taken off the size before the comparison,
+// and a wavefront without rows has none to take it from.)
 constexpr uint32_t OUTSIDE = 0x80000000u;
 __device__ __forceinline__ u32x2_t bf16x4(f32x4_t v) {
   return (u32x2_t){pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
@@ -180,6 +187,7 @@ __device__ __forceinline__ void store_glu_fwd(const G8GemmArgs& a, const Place& 
   const int f = at.n0 + at.wn * 8 * FN + at.q * 4;
   const int rows = (int)max((int64_t)0, min((int64_t)128, a.M - at.m0));
   const rsrc_t rz = buffer_of(reinterpret_cast<bf16_t*>(a.Z) + at.m0 * 2 * F, a.Z ? rows * F * 4 : 0);
+  const rsrc_t rz2 = buffer_of(reinterpret_cast<bf16_t*>(a.Z) + (at.m0 * 2 + 1) * F, a.Z && rows ? (rows * 2 - 1) * F * 2 : 0);
   const rsrc_t rh = buffer_of(reinterpret_cast<bf16_t*>(a.H) + at.m0 * F, a.H ? rows * F * 2 : 0);
   const rsrc_t rq = buffer_of(a.q + at.m0 * pf, a.q ? rows * pf : 0);
   const Gate gate(a.gate);
@@ -194,7 +202,7 @@ __device__ __forceinline__ void store_glu_fwd(const G8GemmArgs& a, const Place& 
       if (a.Z) {
         const uint32_t off = c < F ? (uint32_t)((8 * at.p + i) * 2 * F + c) * 2u : OUTSIDE;
         __builtin_amdgcn_raw_buffer_store_b64(bf16x4(g), rz, off, 0, 0);
-        __builtin_amdgcn_raw_buffer_store_b64(bf16x4(u), rz, off, 2 * F, 0);
+        __builtin_amdgcn_raw_buffer_store_b64(bf16x4(u), rz2, off, 0, 0);
       }
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
@@ -270,7 +278,9 @@ __device__ __forceinline__ void store_glu_bwd(const G8GemmArgs& a, const Place& 
   const int64_t m = at.m0 + 8 * at.p;
   const int rows = (int)max((int64_t)0, min((int64_t)128, a.M - at.m0));
   const rsrc_t rz = buffer_of(reinterpret_cast<const bf16_t*>(a.Z) + at.m0 * 2 * F, rows * F * 4);
+  const rsrc_t rz2 = buffer_of(reinterpret_cast<const bf16_t*>(a.Z) + (at.m0 * 2 + 1) * F, rows ? (rows * 2 - 1) * F * 2 : 0);
   const rsrc_t rq = buffer_of(a.q + at.m0 * 2 * pf, a.q ? rows * pf * 2 : 0);
+  const rsrc_t rq2 = buffer_of(a.q + (at.m0 * 2 + 1) * pf, a.q && rows ? (rows * 2 - 1) * pf : 0);
   const Gate gate(a.gate);
   const int64_t token_group = at.m0 / kGroup;
   const bool turned = a.q_t && at.m0 < pm;
@@ -289,7 +299,7 @@ __device__ __forceinline__ void store_glu_bwd(const G8GemmArgs& a, const Place& 
       for (int i = 0; i < 4; ++i) {
         const uint32_t off = c < F ? (uint32_t)((8 * at.p + i0 + i) * 2 * F + c) * 2u : OUTSIDE;
         zg[i] = __builtin_amdgcn_raw_buffer_load_b64(rz, off, 0, 0);
-        zu[i] = __builtin_amdgcn_raw_buffer_load_b64(rz, off, 2 * F, 0);
+        zu[i] = __builtin_amdgcn_raw_buffer_load_b64(rz2, off, 0, 0);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -371,7 +381,7 @@ __device__ __forceinline__ void store_glu_bwd(const G8GemmArgs& a, const Place& 
       }
       const float *x = dg[hf][i], *y = du[hf][i];
       __builtin_amdgcn_raw_buffer_store_b32(codes4<FMT>(x[0], x[1], x[2], x[3], sg.inv), rq, off, 0, 0);
-      __builtin_amdgcn_raw_buffer_store_b32(codes4<FMT>(y[0], y[1], y[2], y[3], su.inv), rq, off, pf, 0);
+      __builtin_amdgcn_raw_buffer_store_b32(codes4<FMT>(y[0], y[1], y[2], y[3], su.inv), rq2, off, 0, 0);
     });
   });
 }
@@ -424,6 +434,7 @@ template <int WM, int WN, int FM, int FN, int NS, int SC, bool SQ, int FMT_A, in
 __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM == 4 ? 2 : 1) void gemm(G8GemmArgs a) {
   constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN, NW = WM * WN;
   constexpr bool PAIR = EPI == G_GLU_FWD || EPI == G_RAW_FWD;
+  static_assert(NS == 2 || NS == 3);
   static_assert(FM == 8 || (FM == 4 && EPI != G_GLU_FWD && EPI != G_GLU_BWD));
   static_assert(BM % 64 == 0 && BM % (8 * WM * WN) == 0 && BN % (8 * WM * WN) == 0);
   constexpr int COLS = PAIR ? BN / 2 : BN;  // columns of the output a tile has
@@ -576,8 +587,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
   });
   // waits until at most `tiles` of the newest tiles' loads are on their way
   auto wait_tiles = [&](int tiles) {
-    if (NS > 3 && tiles >= 3) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS * 3) : "memory");
-    else if (NS > 2 && tiles == 2) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS * 2) : "memory");
+    if (NS > 2 && tiles == 2) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS * 2) : "memory");
     else if (tiles == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory");
     else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   };
@@ -761,9 +771,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
                 p[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][c], wa, c ? p[j] : (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
               }
             });
-            
             if constexpr (c % 2) __builtin_amdgcn_sched_barrier(0);  // (two widenings at a time hold fewer registers)
-
           });
         } else {
           static_for<0, FN>([&](auto J) {
@@ -778,7 +786,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
         }
         if constexpr (SLDS) sa = r.s;
         if constexpr (SC == TP_GROUP_E8M0) {
-  #pragma unroll
+#pragma unroll
           for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(acc[i][j]));
         }
         __builtin_amdgcn_sched_barrier(0);

@@ -131,6 +131,58 @@ def test_nan_beside_the_last_row(N, H, F, form):
     assert torch.equal(s_t.isnan(), bad)
 
 
+def with_rows_behind(rows, behind, cols, dtype):
+    """A tensor of `rows` rows, and the rows behind it, filled with a pattern."""
+    whole = torch.full((rows + behind, cols * torch.empty((), dtype=dtype).element_size()), 0xA5, dtype=torch.uint8, device=DEV)
+    return whole[:rows].view(dtype), whole[rows:]
+
+
+@pytest.mark.parametrize("M,N,K,out,form", ref.GEMM_FORMS)
+def test_gemm_leaves_the_rows_behind(M, N, K, out, form):
+    """A whole tile of rows behind the last one stays as it was."""
+    A, sA, a = quantized(tokens(1, M, K))
+    B, sB, b = quantized(tokens(2, N, K), False, True)
+    dtype = torch.bfloat16 if out == "bf16" else torch.float32
+    C, behind = with_rows_behind(M, 320, N, dtype)
+    product(A, sA, B, sB, M, N, K, dtype, C, square=1)
+    check_product(C, a, b, dtype)
+    assert bool((behind == 0xA5).all())
+
+
+@pytest.mark.parametrize("N,H,F,form", ref.FWD_FORMS)
+def test_glu_fwd_leaves_the_rows_behind(N, H, F, form):
+    X, Wg, Wu = glu_inputs(N, H, F, False, 3)
+    full = glu_fwd(N, H, F, 0, False, X, Wg, Wu)
+    outs = {k: with_rows_behind(N, 320, c, t) for k, c, t in
+            (("Z", 2 * F, torch.bfloat16), ("H", F, torch.bfloat16), ("Hq", ref.up(F) * G, torch.uint8))}
+    sH, d = torch.empty_like(full["sH"]), dict(N=N, H=H, F=F)
+    n = tp.tp_fp8g_glu_fwd_workspace(d)
+    tp.tp_fp8g_glu_fwd(d, X[0], X[1], Wg[0], Wg[1], Wu[0], Wu[1], outs["Z"][0], outs["H"][0], outs["Hq"][0], sH, None, None,
+                       torch.empty(n, dtype=torch.uint8, device=DEV), n)
+    assert torch.equal(sH, full["sH"])
+    for k, (got, behind) in outs.items():
+        assert torch.equal(got, full[k]) and bool((behind == 0xA5).all())
+
+
+@pytest.mark.parametrize("N,H,F,form", ref.BWD_FORMS)
+def test_glu_bwd_leaves_the_rows_behind(N, H, F, form):
+    """And takes nothing from them: the rows behind Z are NaN (bytes 0xFF)."""
+    dY, B = quantized(tokens(1, N, H)), quantized(tokens(2, F, H, 0.1), False, True)
+    z = tokens(3, N, 2 * F).to(torch.bfloat16).to(DEV)
+    full = glu_bwd(N, H, F, 0, False, 0, dY, B, z)
+    Z, behind_z = with_rows_behind(N, 320, 2 * F, torch.bfloat16)
+    Z.copy_(z)
+    behind_z.fill_(0xFF)
+    q, behind = with_rows_behind(N, 320, 2 * ref.up(F) * G, torch.uint8)
+    s, q_t, s_t = (torch.empty_like(t) for t in full[1:])
+    d = dict(N=N, H=H, F=F)
+    n = tp.tp_fp8g_glu_bwd_workspace(d)
+    tp.tp_fp8g_glu_bwd(d, dY[0], dY[1], B[0], B[1], Z, q, s, q_t, s_t, torch.empty(n, dtype=torch.uint8, device=DEV), n)
+    for got, want in zip((q, s, q_t, s_t), full):
+        assert torch.equal(got, want)
+    assert bool((behind == 0xA5).all())
+
+
 @pytest.mark.parametrize("M,N,K", [(3, 264, 384), (300, 1000, 640), (2100, 2056, 384)])
 @pytest.mark.parametrize("square", [False, True])
 def test_byte_scales_anywhere(M, N, K, square):
