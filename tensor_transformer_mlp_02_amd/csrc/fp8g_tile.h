@@ -467,35 +467,34 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
 
   const int kt_part = a.K / kGroup, kt_all = kt_part * a.parts;
 
-  // a wavefront's loads: lane l fills chunk l % 8 of row 8 block + l / 8.
-  // Rows past the last lie behind the buffer's end and read as zeros.  The
-  // offsets are formed at each load, from two registers an operand.
+  // a wavefront's loads, 8 rows each: lane l fills chunk l % 8 of row l / 8.  Each has a
+  // buffer of its own, which begins at its first row's group: so the offsets are a
+  // lane's alone (formed at each load they took the vector unit as long as a seventh of the
+  // tile), and rows past the last lie behind its end and read as zeros.
   const int lda = (int)a.lda;
   const int rows = (int)min((int64_t)BM, a.M - mt), cols = min(COLS, a.N - at.n0);
-  const rsrc_t ra = buffer_of(a.A + mt * a.lda, rows * lda);
-  const rsrc_t rb = buffer_of(a.B + (int64_t)at.n0 * a.K, cols * a.K);
-  const rsrc_t rb2 = buffer_of(a.B2 + (int64_t)at.n0 * a.K, cols * a.K);
+  const uint8_t* const from_a = a.A + mt * a.lda;
+  const int l8 = lane >> 3, ch = lane & 7;
+  const uint32_t va = l8 * lda, vb = l8 * a.K + ((ch ^ l8) << 4);
   const int slot = (wave % (BM / 64)) * 64 + lane;
   const int sr = slot / (16 * FM) * (16 * FM) + slot % 16 * FM + slot % (16 * FM) / 16;
   auto load_tile = [&](int kt, int buf) {
     const int part = kt >= kt_part ? 1 : 0, kb = kt - part * kt_part;
-    int ln = lane;
-    asm volatile("" : "+v"(ln));  // (kept over the loop, each offset would be a register)
-    const int l8 = ln >> 3, ch = ln & 7;
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
-      const int blk = wave * LA + i, r = blk * 8 + l8;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void_t*)(lds + buf * A_BYTES + blk * 1024), 16,
-                                               r * lda + ((ch ^ ((r / FM) & 7)) << 4), kt * 128, 0, 0);
+      const int r0 = (wave * LA + i) * 8;
+      const rsrc_t ra = buffer_of(from_a + r0 * lda + kt * 128, max(0, (rows - r0) * lda - kt * 128));
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void_t*)(lds + buf * A_BYTES + r0 * 128), 16,
+                                               va + ((ch ^ ((r0 / FM + l8 / FM) & 7)) << 4), 0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < LB; ++i) {
       // (gated forward: of a wavefront's rows the first half is the gate's)
       const int r0 = (wave * LB + i) * 8;
       const bool second = PAIR ? (r0 / (8 * FN)) % 2 == 1 : part == 1;
-      const int n = PAIR ? r0 / (16 * FN) * (8 * FN) + r0 % (8 * FN) + l8 : r0 + l8;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(second ? rb2 : rb, (lds_void_t*)(lds + B_AT + buf * B_BYTES + r0 * 128), 16,
-                                               n * a.K + ((ch ^ l8) << 4), kb * 128, 0, 0);
+      const int n = PAIR ? r0 / (16 * FN) * (8 * FN) + r0 % (8 * FN) : r0;
+      const rsrc_t rb = buffer_of((second ? a.B2 : a.B) + (int64_t)(at.n0 + n) * a.K + kb * 128, max(0, (cols - n) * a.K - kb * 128));
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void_t*)(lds + B_AT + buf * B_BYTES + r0 * 128), 16, vb, 0, 0, 0);
     }
     if constexpr (SLDS) {
       const rsrc_t rs = buffer_of(reinterpret_cast<const float*>(a.sA) + (int64_t)kt * a.M + mt, rows * 4);
