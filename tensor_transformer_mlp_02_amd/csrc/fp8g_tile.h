@@ -38,9 +38,9 @@ enum { SUM_FP8 = 0, SUM_F32 = 1 };
 // G_RAW_*: the gated block's fp32 values, for a quantization of their own
 enum { G_STORE = 0, G_GLU_FWD = 1, G_GLU_BWD = 2, G_RAW_FWD = 3, G_RAW_BWD = 4 };
 
-template <int FMT_A, int FMT_B, int OA, int OB>
+template <int FMT_A, int FMT_B, int OB>  // OB: sb's byte; sa's is the first
 __device__ __forceinline__ f32x4_t mfma_scaled(i32x8_t b, i32x8_t a, f32x4_t c, int sb, int sa) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, FMT_B, FMT_A, OB, sb, OA, sa);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, FMT_B, FMT_A, OB, sb, 0, sa);
 }
 template <int FMT_A, int FMT_B>
 __device__ __forceinline__ f32x4_t mfma_plain(i32x8_t b, i32x8_t a, f32x4_t c) {
@@ -407,7 +407,6 @@ struct Row {
     asm volatile("ds_read_b128 %0, %3 offset:%6\n\tds_read_b128 %1, %4 offset:%6\n\tds_read_b32 %2, %5 offset:%7"
                  : "=&v"(lo), "=&v"(hi), "=&v"(s) : "v"(a0), "v"(a1), "v"(as), "n"(OFF), "n"(SOFF) : "memory");
   }
-  __device__ __forceinline__ void wait() { asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(lo), "+v"(hi)::"memory"); }
   __device__ __forceinline__ void wait_scale() {
     asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(lo), "+v"(hi), "+v"(s)::"memory");
   }
@@ -439,14 +438,17 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
   static_assert(BM % 64 == 0 && BM % (8 * WM * WN) == 0 && BN % (8 * WM * WN) == 0);
   constexpr int COLS = PAIR ? BN / 2 : BN;  // columns of the output a tile has
   constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;  // 1 KiB loads of a wavefront (8 rows each)
-  constexpr bool SLDS = SC == TP_GROUP_F32;          // row scales by way of shared memory
-  constexpr int LOADS = LA + LB + (SLDS ? 1 : 0);
-  // [A .. | B .. | row scales ..], NS of each
-  constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, S_BYTES = SLDS ? BM * 4 : 0;
-  constexpr int TILES = NS * (A_BYTES + B_BYTES + S_BYTES), LAST = EPI == G_GLU_BWD ? glu_bwd_shared<WM, WN, FN>() : 0;
+  // Scales of rows, and E8M0 ones of columns, go by way of shared memory, a word each: a load
+  // into registers is waited for together with all loads into shared memory before it.
+  constexpr bool BLDS = SC == TP_GROUP_E8M0 && !SQ;
+  constexpr bool LATE = SC == TP_GROUP_F32;  // a step's products before the loads of a tile ahead
+  constexpr int LOADS = LA + LB + 1 + (BLDS ? 1 : 0);
+  // [A .. | B .. | row scales .. | column scales ..], NS of each
+  constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, S_BYTES = BM * 4, SB_BYTES = BLDS ? BN * 4 : 0;
+  constexpr int TILES = NS * (A_BYTES + B_BYTES + S_BYTES + SB_BYTES), LAST = EPI == G_GLU_BWD ? glu_bwd_shared<WM, WN, FN>() : 0;
   constexpr int SHARED = TILES > LAST ? TILES : LAST;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[SHARED];
-  constexpr int B_AT = NS * A_BYTES, S_AT = B_AT + NS * B_BYTES;
+  constexpr int B_AT = NS * A_BYTES, S_AT = B_AT + NS * B_BYTES, SB_AT = S_AT + NS * S_BYTES;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
@@ -496,10 +498,15 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
       const rsrc_t rb = buffer_of((second ? a.B2 : a.B) + (int64_t)(at.n0 + n) * a.K + kb * 128, max(0, (cols - n) * a.K - kb * 128));
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void_t*)(lds + B_AT + buf * B_BYTES + r0 * 128), 16, vb, 0, 0, 0);
     }
-    if constexpr (SLDS) {
-      const rsrc_t rs = buffer_of(reinterpret_cast<const float*>(a.sA) + (int64_t)kt * a.M + mt, rows * 4);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rs, (lds_void_t*)(lds + S_AT + buf * S_BYTES + (wave % (BM / 64)) * 256), 4, sr * 4, 0, 0, 0);
+    constexpr int W = SC == TP_GROUP_F32 ? 4 : 1;  // (bytes arrive as words)
+    const rsrc_t rs = buffer_of(reinterpret_cast<const uint8_t*>(a.sA) + ((int64_t)kt * a.M + mt) * W, rows * W);
+    lds_void_t* const to = (lds_void_t*)(lds + S_AT + buf * S_BYTES + (wave % (BM / 64)) * 256);
+    if constexpr (W == 4) __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, to, 4, sr * 4, 0, 0, 0);
+    else __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, to, 1, sr, 0, 0, 0);
+    if constexpr (BLDS) {
+      const int n = (wave % (BN / 64)) * 64;
+      const rsrc_t rsb = buffer_of(reinterpret_cast<const uint8_t*>(part ? a.sB2 : a.sB) + (int64_t)kb * a.N + at.n0, cols);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_void_t*)(lds + SB_AT + buf * SB_BYTES + n * 4), 1, n + lane, 0, 0, 0);
     }
   };
 
@@ -507,68 +514,35 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
   const uint32_t l0 = lds_address(lds);
   const uint32_t c0 = (at.q ^ (at.p & 7)) << 4;
   const uint32_t pa = l0 + (at.wm * 16 * FM + FM * at.p) * 128 + c0, pb = l0 + B_AT + (at.wn * 16 * FN + at.p) * 128 + c0;
-  const uint32_t ps = l0 + S_AT + (at.wm * 16 * FM + at.p) * 4;
+  const uint32_t ps = l0 + S_AT + (at.wm * 16 * FM + at.p) * 4, psb = l0 + SB_AT + (at.wn * 16 * FN + at.p) * 4;
 
-  // Scales of a tile: of its columns, and E8M0 ones of its rows.  Those of a
-  // lane are neighbours, behind one offset from a base that a wavefront
-  // shares; past the last row or column they read as zeros.
+  // Scales of a tile's columns: shared ones by way of the scalar cache, fp32 ones of each
+  // column (a lane's are neighbours) straight into registers; past the last column they read as zeros
   constexpr int SBT = SC == TP_GROUP_F32 && !SQ ? 4 : 1;
   struct Scales {
     float b[SC == TP_GROUP_F32 ? SBT : 1][SC == TP_GROUP_F32 ? FN : 1];
-    uint32_t eb, ea[2];
-    uint32_t byte[SC == TP_GROUP_E8M0 && !SQ ? FN : 1];  // eb's, as loaded
-    // (joined when they are used: here they are still on their way)
-    __device__ __forceinline__ void join() {
-      if constexpr (SC == TP_GROUP_E8M0 && !SQ) {
-        eb = 0;
-#pragma unroll
-        for (int j = 0; j < FN; ++j) eb |= byte[j] << (8 * j);
-      }
-    }
+    uint32_t eb;  // byte j: block j's
   };
   const int nw = PAIR ? at.n0 + at.wn * 8 * FN : at.n0 + at.wn * 16 * FN;  // the wavefront's first column
-  const int rows_w = (int)max((int64_t)0, min((int64_t)(16 * FM), a.M - at.m0)), cols_w = max(0, min(16 * FN, a.N - nw));
   const int64_t square = (int64_t)(min(nw, a.N - 1) / kGroup) * kt_part;
   auto load_scales = [&](int kt, Scales& s) {
     const int part = kt >= kt_part ? 1 : 0, kb = kt - part * kt_part;
     auto from = [&](int j) { return PAIR ? (j < FN / 2 ? a.sB : a.sB2) : (part ? a.sB2 : a.sB); };
-    if constexpr (SC == TP_GROUP_F32) {
-      if constexpr (SQ) {
-#pragma unroll
-        for (int j = 0; j < FN; ++j) s.b[0][j] = scalar_f32(from(j), square + kb);
-      } else {
-        const rsrc_t rs = buffer_of(reinterpret_cast<const float*>(from(0)) + (int64_t)kb * a.N + nw, cols_w * 4);
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          const u32x4_t w = __builtin_amdgcn_raw_buffer_load_b128(rs, (16 * j + 4 * at.q) * 4, 0, 0);
-#pragma unroll
-          for (int t = 0; t < 4; ++t) s.b[t][j] = __uint_as_float(w[t]);
-        }
-      }
-    } else {
+    if constexpr (SQ) {
       s.eb = 0;
-      if constexpr (SQ) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j) s.eb |= scalar_byte(from(j), square + kb) << (8 * j);
-      } else {
-        const rsrc_t rs = buffer_of(reinterpret_cast<const uint8_t*>(from(0)) + (int64_t)kb * a.N + nw, cols_w);
-#pragma unroll
-        for (int j = 0; j < FN; ++j) s.byte[j] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rs, 16 * j + at.p, 0, 0);
+      for (int j = 0; j < FN; ++j) {
+        if constexpr (SC == TP_GROUP_F32) s.b[0][j] = scalar_f32(from(j), square + kb);
+        else s.eb |= scalar_byte(from(j), square + kb) << (8 * j);
       }
-      const rsrc_t rs = buffer_of(reinterpret_cast<const uint8_t*>(a.sA) + (int64_t)kt * a.M + at.m0, rows_w);
-      s.ea[0] = s.ea[1] = 0;
-      if (rows_w == 16 * FM) {
-        if constexpr (FM == 8) {
-          const u32x2_t w = __builtin_amdgcn_raw_buffer_load_b64(rs, 8 * at.p, 0, 0);
-          s.ea[0] = w[0];
-          s.ea[1] = w[1];
-        } else {
-          s.ea[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, 4 * at.p, 0, 0);
-        }
-      } else {
+    } else if constexpr (SC == TP_GROUP_F32) {
+      const int cols_w = max(0, min(16 * FN, a.N - nw));
+      const rsrc_t rs = buffer_of(reinterpret_cast<const float*>(from(0)) + (int64_t)kb * a.N + nw, cols_w * 4);
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
-          s.ea[i >> 2] |= (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rs, FM * at.p + i, 0, 0) << (8 * (i & 3));
+      for (int j = 0; j < FN; ++j) {
+        const u32x4_t w = __builtin_amdgcn_raw_buffer_load_b128(rs, (16 * j + 4 * at.q) * 4, 0, 0);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) s.b[t][j] = __uint_as_float(w[t]);
       }
     }
   };
@@ -597,13 +571,14 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
   Row ra0, ra1;  // the rows of two steps in turn
   i32x8_t fb[SUM == SUM_FP8 ? FN : 1];
   bf16x8g_t wb[SUM == SUM_F32 ? FN : 1][4];
+  auto byte_of = [](const Row& r) { return __float_as_uint(r.s); };  // a scale's, which arrived as a word
   auto widen_b = [&](auto J, const Row& r, const Scales& s) {
     constexpr int j = decltype(J)::value;
     const i32x8_t f = r.codes();
     if constexpr (SUM == SUM_FP8) {
       fb[j] = f;
     } else {
-      const float e = SC == TP_GROUP_F32 ? 1.0f : e8m0_f32((s.eb >> (8 * j)) & 255);
+      const float e = SC == TP_GROUP_F32 ? 1.0f : e8m0_f32(BLDS ? byte_of(r) : (s.eb >> (8 * j)) & 255);
 #pragma unroll
       for (int c = 0; c < 4; ++c) wb[j][c] = widen<FMT_B>(f[2 * c], f[2 * c + 1], e);
     }
@@ -611,23 +586,31 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
   auto ask_a = [&](auto I, Row& r, int buf) {
     constexpr int i = decltype(I)::value;
     const uint32_t a0 = pa + buf * A_BYTES;
-    if constexpr (SLDS) r.template ask<i * 128, i * 64>(a0, a0 ^ 64, ps + buf * S_BYTES);
-    else r.template ask<i * 128>(a0, a0 ^ 64);
+    r.template ask<i * 128, i * 64>(a0, a0 ^ 64, ps + buf * S_BYTES);
   };
-  auto wait_a = [&](Row& r) {
-    if constexpr (SLDS) r.wait_scale();
-    else r.wait();
+  auto ask_columns = [&](Row (&b)[FN], int buf) {
+    const uint32_t b0 = pb + buf * B_BYTES;
+    static_for<0, FN>([&](auto J) {
+      constexpr int j = decltype(J)::value;
+      if constexpr (BLDS) b[j].template ask<j * 2048, j * 64>(b0, b0 ^ 64, psb + buf * SB_BYTES);
+      else b[j].template ask<j * 2048>(b0, b0 ^ 64);
+    });
+  };
+  // (all reads have been waited for)
+  auto take_columns = [&](Row (&b)[FN], Scales& s) {
+    if constexpr (BLDS) s.eb = 0;
+    static_for<0, FN>([&](auto J) {
+      constexpr int j = decltype(J)::value;
+      if constexpr (BLDS) {
+        b[j].arrived_scale();
+        s.eb |= byte_of(b[j]) << (8 * j);
+      } else {
+        b[j].arrived();
+      }
+    });
+    static_for<0, FN>([&](auto J) { widen_b(J, b[J], s); });
   };
   Row cb[FN];  // the wavefront's columns of a tile, on their way
-  auto ask_b = [&](int buf) {
-    const uint32_t b0 = pb + buf * B_BYTES;
-    static_for<0, FN>([&](auto J) { cb[J].template ask<decltype(J)::value * 2048>(b0, b0 ^ 64); });
-  };
-  auto take_b = [&](const Scales& s) {
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    static_for<0, FN>([&](auto J) { cb[J].arrived(); });
-    static_for<0, FN>([&](auto J) { widen_b(J, cb[J], s); });
-  };
 
   f32x4_t p[FN];
   float sa = 0.0f;
@@ -647,21 +630,19 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
     };
     Set even, odd;
     auto ask_set = [&](Set& t, int buf) {
-      const uint32_t b0 = pb + buf * B_BYTES;
-      static_for<0, FN>([&](auto J) { t.b[J].template ask<decltype(J)::value * 2048>(b0, b0 ^ 64); });
+      ask_columns(t.b, buf);
       static_for<0, FM>([&](auto I) { ask_a(I, t.a[I], buf); });
     };
     auto wait_set = [&](Set& t) {
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      static_for<0, FN>([&](auto J) { t.b[J].arrived(); });
-      static_for<0, FM>([&](auto I) {
-        if constexpr (SLDS) t.a[I].arrived_scale();
-        else t.a[I].arrived();
+      static_for<0, FN>([&](auto J) {
+        if constexpr (BLDS) t.b[J].arrived_scale();
+        else t.b[J].arrived();
       });
+      static_for<0, FM>([&](auto I) { t.a[I].arrived_scale(); });
     };
     auto one_tile = [&](Set& t, Set& next, int kt, int buf, int buf_next) {
       sc = sc_next;
-      sc.join();
       load_scales(min(kt + 1, kt_all - 1), sc_next);
       // this tile is read, and the next one there, for every wavefront
       wait_tiles(max(0, min(kt_all - 2 - kt, NS - 2)));
@@ -669,13 +650,13 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
       asm volatile("" ::: "memory");
       ask_set(next, buf_next);  // (behind the last tile: what nothing uses)
       if (kt + NS < kt_all) load_tile(kt + NS, buf);
-      static_for<0, FN>([&](auto J) { widen_b(J, t.b[J], sc); });
+      take_columns(t.b, sc);
       static_for<0, FM>([&](auto I) {
         constexpr int i = decltype(I)::value;
         const i32x8_t fa = t.a[i].codes();
         if constexpr (SUM == SUM_F32) {
           float e = 1.0f;
-          if constexpr (SC == TP_GROUP_E8M0) e = e8m0_f32((sc.ea[i >> 2] >> (8 * (i & 3))) & 255);
+          if constexpr (SC == TP_GROUP_E8M0) e = e8m0_f32(byte_of(t.a[i]));
           f32x4_t g[FN];
           static_for<0, 4>([&](auto Cc) {
             constexpr int c = decltype(Cc)::value;
@@ -701,7 +682,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
 #pragma unroll
               for (int k = 0; k < 4; ++k) acc[i][j][k] = fmaf(g[k], t.a[i].s * sc.b[SQ ? 0 : k][j], acc[i][j][k]);
             } else {
-              acc[i][j] = mfma_scaled<FMT_A, FMT_B, i & 3, j>(fb[j], fa, acc[i][j], (int)sc.eb, (int)sc.ea[i >> 2]);
+              acc[i][j] = mfma_scaled<FMT_A, FMT_B, j>(fb[j], fa, acc[i][j], (int)sc.eb, (int)byte_of(t.a[i]));
             }
           });
         }
@@ -727,9 +708,9 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
   } else {
     int buf = 0;
     sc = sc_next;
-    sc.join();
-    ask_b(0);
-    take_b(sc);
+    ask_columns(cb, 0);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    take_columns(cb, sc);
     ask_a(std::integral_constant<int, 0>{}, ra0, 0);
     for (int kt = 0; kt < kt_all; ++kt) {
       const bool more = kt + 1 < kt_all;
@@ -739,7 +720,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
         constexpr int i = decltype(I)::value;
         Row& r = i & 1 ? ra1 : ra0;
         Row& next = i & 1 ? ra0 : ra1;
-        wait_a(r);
+        r.wait_scale();
         if constexpr (i < FM - 1) {
           ask_a(std::integral_constant<int, (i + 1) % FM>{}, next, buf);
         } else {
@@ -750,14 +731,14 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
           asm volatile("" ::: "memory");
           // (behind the last tile: rows that nothing uses, so that every path asks)
           ask_a(std::integral_constant<int, 0>{}, next, buf_next);
-          if (kt + NS < kt_all) load_tile(kt + NS, buf);
+          if (!LATE && kt + NS < kt_all) load_tile(kt + NS, buf);
         }
         const i32x8_t fa = r.codes();
         // fp32 scales: a step's group sums are scaled and added during the next
         // step, when the instructions that make them have ended
         if constexpr (SUM == SUM_F32) {
           float e = 1.0f;
-          if constexpr (SC == TP_GROUP_E8M0) e = e8m0_f32((sc.ea[i >> 2] >> (8 * (i & 3))) & 255);
+          if constexpr (SC == TP_GROUP_E8M0) e = e8m0_f32(byte_of(r));
           static_for<0, 4>([&](auto Cc) {
             constexpr int c = decltype(Cc)::value;
             const bf16x8g_t wa = widen<FMT_A>(fa[2 * c], fa[2 * c + 1], e);
@@ -779,11 +760,17 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
               if constexpr (i > 0) add_group(std::integral_constant<int, i - 1>{}, J);
               p[j] = mfma_plain<FMT_A, FMT_B>(fb[j], fa, (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f});
             } else {
-              acc[i][j] = mfma_scaled<FMT_A, FMT_B, i & 3, j>(fb[j], fa, acc[i][j], (int)sc.eb, (int)sc.ea[i >> 2]);
+              acc[i][j] = mfma_scaled<FMT_A, FMT_B, j>(fb[j], fa, acc[i][j], (int)sc.eb, (int)byte_of(r));
             }
           });
         }
-        if constexpr (SLDS) sa = r.s;
+        // (the matrix cores are at work meanwhile: before the step's products the gated forward
+        // took 417 us, so 406; with E8M0 scales the weight gradient 267, so 275)
+        if constexpr (i == FM - 1 && LATE) {
+          __builtin_amdgcn_sched_barrier(0);
+          if (kt + NS < kt_all) load_tile(kt + NS, buf);
+        }
+        if constexpr (SC == TP_GROUP_F32) sa = r.s;
         if constexpr (SC == TP_GROUP_E8M0) {
 #pragma unroll
           for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(acc[i][j]));
@@ -792,16 +779,16 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
       });
       // (widened, the columns leave no room for the next ones before here; FP8 ones
       // would, but asked for beside the step's rows they took 3 % longer)
-      ask_b(buf_next);
+      ask_columns(cb, buf_next);
       if constexpr (SC == TP_GROUP_F32) {
         static_for<0, FN>([&](auto J) { add_group(std::integral_constant<int, FM - 1>{}, J); });
       }
       sc = sc_next;
-      sc.join();
-      take_b(sc);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      take_columns(cb, sc);
       buf = buf_next;
     }
-    wait_a(ra0);
+    ra0.wait_scale();
   }
   __syncthreads();
 

@@ -19,31 +19,75 @@ def registers(text):
     return out
 
 
-def touched_in_flight(lines):
-    """(reads seen, offending lines) of a listing; reads count where they stand in inline assembly."""
-    on_the_way, inline, reads, bad = set(), False, 0, []
+def kernels(lines):
+    """Each kernel's basic blocks: label -> ([(line, op, operands, in inline assembly)], labels that may follow)."""
+    inline, blocks, label = False, {}, None
     for n, line in enumerate(lines, 1):
         if "#ASMSTART" in line:
             inline = True
         if "#ASMEND" in line:
             inline = False
         text = line.split(";")[0].strip()
-        if re.match(r"^[^.\s]\S*:$", text):      # the next kernel
-            on_the_way = set()
-        if not text or text.startswith(".") or text.endswith(":"):
+        start = re.match(r"^([^\s]+):$", text)
+        if start:
+            if not text.startswith("."):         # the next kernel
+                if blocks:
+                    yield blocks
+                blocks = {}
+            elif label is not None and blocks and not blocks[label][2]:
+                blocks[label][1].append(start.group(1))
+            label = start.group(1)
+            blocks[label] = ([], [], [])         # the last: whether it has ended
+            continue
+        if label is None or not text or text.startswith("."):
             continue
         op, _, rest = text.partition(" ")
-        if op.startswith("ds_read") and inline:
-            to, _, address = rest.partition(",")
-            if registers(to) & on_the_way or registers(address) & on_the_way:
-                bad.append((n, text))
-            on_the_way |= registers(to)
-            reads += 1
-        elif op == "s_waitcnt" and "lgkmcnt(0)" in text:
-            on_the_way = set()
-        elif registers(text) & on_the_way:
-            bad.append((n, text))
-    return reads, bad
+        if op in ("s_branch", "s_endpgm") or op.startswith("s_cbranch"):
+            if op != "s_endpgm":
+                blocks[label][1].append(rest.strip())
+            if op.startswith("s_cbranch"):       # what follows is a block of its own
+                follow = f"{label}+{n}"
+                blocks[label][1].append(follow)
+                blocks[label][2].append(n)
+                label = follow
+                blocks[label] = ([], [], [])
+            else:
+                blocks[label][2].append(n)
+            continue
+        if not blocks[label][2]:
+            blocks[label][0].append((n, op, rest, inline))
+    if blocks:
+        yield blocks
+
+
+def touched_in_flight(lines):
+    """(reads seen, offending lines) of a listing, along every path; reads count where they stand in inline assembly."""
+    reads, bad = set(), set()
+    for blocks in kernels(lines):
+        before = {next(iter(blocks)): frozenset()}
+        todo = list(before)
+        while todo:
+            label = todo.pop()
+            on_the_way = set(before[label])
+            for n, op, rest, inline in blocks[label][0]:
+                if op.startswith("ds_read") and inline:
+                    to, _, address = rest.partition(",")
+                    if registers(to) & on_the_way or registers(address) & on_the_way:
+                        bad.add((n, f"{op} {rest}"))
+                    on_the_way |= registers(to)
+                    reads.add(n)
+                elif op == "s_waitcnt" and "lgkmcnt(0)" in rest:
+                    on_the_way = set()
+                elif registers(rest) & on_the_way:
+                    bad.add((n, f"{op} {rest}"))
+            for follow in blocks[label][1]:
+                if follow not in blocks:
+                    continue
+                seen = before.get(follow)
+                if seen is None or not on_the_way <= seen:
+                    before[follow] = frozenset(on_the_way | (seen or frozenset()))
+                    todo.append(follow)
+    return len(reads), sorted(bad)
 
 
 def test_the_check_sees_a_copy():
@@ -53,6 +97,11 @@ def test_the_check_sees_a_copy():
     assert touched_in_flight(ask + ["v_mov_b32 v9, v5"] + wait)[1] == [(5, "v_mov_b32 v9, v5")]
     assert touched_in_flight(ask + ["scratch_store_dwordx4 off, v[4:7], off"] + wait)[1]
     assert touched_in_flight(ask + [";;#ASMSTART", "ds_read_b32 v4, v2", ";;#ASMEND"] + wait)[1]
+    # along a branch, and round a loop
+    assert touched_in_flight(ask + ["s_branch .L2", ".L1:", "v_mov_b32 v9, v5", "s_endpgm", ".L2:"] + wait) == (1, [])
+    assert touched_in_flight(ask + ["s_cbranch_scc1 .L2"] + wait + ["s_endpgm", ".L2:", "v_mov_b32 v9, v5"])[1]
+    assert touched_in_flight(["k:", ".L1:", "v_mov_b32 v9, v5", *ask[1:], "s_cbranch_scc1 .L1", "s_endpgm"])[1]
+    assert touched_in_flight(["k:", ".L1:", "v_mov_b32 v9, v5", *ask[1:], *wait, "s_cbranch_scc1 .L1", "s_endpgm"]) == (1, [])
 
 
 @pytest.mark.skipif(not os.path.exists(b.HIPCC), reason="hipcc not available")
