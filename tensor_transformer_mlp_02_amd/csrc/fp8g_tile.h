@@ -441,7 +441,6 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
   // Scales of rows, and E8M0 ones of columns, go by way of shared memory, a word each: a load
   // into registers is waited for together with all loads into shared memory before it.
   constexpr bool BLDS = SC == TP_GROUP_E8M0 && !SQ;
-  constexpr bool LATE = SC == TP_GROUP_F32;  // a step's products before the loads of a tile ahead
   constexpr int LOADS = LA + LB + 1 + (BLDS ? 1 : 0);
   // [A .. | B .. | row scales .. | column scales ..], NS of each
   constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, S_BYTES = BM * 4, SB_BYTES = BLDS ? BN * 4 : 0;
@@ -731,7 +730,6 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
           asm volatile("" ::: "memory");
           // (behind the last tile: rows that nothing uses, so that every path asks)
           ask_a(std::integral_constant<int, 0>{}, next, buf_next);
-          if (!LATE && kt + NS < kt_all) load_tile(kt + NS, buf);
         }
         const i32x8_t fa = r.codes();
         // fp32 scales: a step's group sums are scaled and added during the next
@@ -765,8 +763,8 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
           });
         }
         // (the matrix cores are at work meanwhile: before the step's products the gated forward
-        // took 417 us, so 406; with E8M0 scales the weight gradient 267, so 275)
-        if constexpr (i == FM - 1 && LATE) {
+        // took 417 us, so 406; the weight gradient 234, so 227)
+        if constexpr (i == FM - 1) {
           __builtin_amdgcn_sched_barrier(0);
           if (kt + NS < kt_all) load_tile(kt + NS, buf);
         }
