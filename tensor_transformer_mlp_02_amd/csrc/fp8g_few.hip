@@ -9,7 +9,7 @@
 // gives row p's codes 32 q .. + 31 of the group (32 bytes: a row's 128 are one cache line) and
 // receives token p, weight rows 4 q .. 4 q + 3.  The wavefronts' sums are joined
 // in shared memory in a fixed order.  Rows past the last are read as the last one and not
-// stored.  1 x 8192 x 3584: 6.6 us (4.4 TB/s of weights).
+// stored.  1 x 8192 x 3584: 6.9 us (4.3 TB/s of weights).
 #include "fp8g.h"
 
 namespace tpmlp {

@@ -1,5 +1,6 @@
 // The product with bf16 results: its rounding is some 100 times what the FP8
-// instruction loses in a group's sum, so that instruction adds the products.
+// instruction loses in a group's sum, so that instruction adds the products
+// (4096 x 8192 x 3584: 119 us, and 206 with fp32 sums).
 #include "fp8g_tile.h"
 
 namespace tpmlp {

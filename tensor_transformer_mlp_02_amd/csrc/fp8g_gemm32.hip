@@ -1,4 +1,5 @@
 // The product with fp32 results: codes widened to bf16, fp32 sums.
+// 8192 x 3584 x 4096 with E8M0 scales, added into C: 226 us, of them 34 for C.
 #include "fp8g_tile.h"
 
 namespace tpmlp {

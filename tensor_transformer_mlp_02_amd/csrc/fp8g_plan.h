@@ -9,10 +9,10 @@
 //          made in the tile, no second launch
 //   LARGE  tiles of 256 x 256
 //
-// 4096 x 8192 x 3584 (bf16 results): FEW 613 us, SMALL 195, LARGE 127; 512 x 2048 x
+// 4096 x 8192 x 3584 (bf16 results): FEW 613 us, SMALL 195, LARGE 119; 512 x 2048 x
 // 4096: 26, 24, 62; 129 x 264 x 7040: 18, 37, 94.  The gated forward, 8192 -> 3584: 64 tokens
 // 38, 64, GROUP 130, 202; 512 tokens 166, 94, 135, 215; 1024 tokens 319, 171, 137, 217; 4096
-// tokens LARGE 430.
+// tokens LARGE 404.
 #pragma once
 
 #include <stdint.h>

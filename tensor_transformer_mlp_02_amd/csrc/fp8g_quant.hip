@@ -8,7 +8,8 @@
 //    transpose is made.  The same 16 lanes have a row; a column's largest
 //    magnitude goes through the wavefront and shared memory.  Transposed codes are
 //    staged as bytes and turned 4 x 4 in registers, so that a column's 128
-//    codes are written by 8 neighbouring threads, 16 bytes each.
+//    codes are written by 8 neighbouring threads, 16 bytes each.  4096 x 8192 bf16 both
+//    ways 29.4 us (4.6 TB/s), 8192 x 3584 fp32 in squares both ways 36 (4.9).
 #include "fp8g.h"
 
 namespace tpmlp {

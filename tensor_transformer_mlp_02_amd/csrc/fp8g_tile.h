@@ -8,10 +8,9 @@
 //            instruction applies the scales itself and accumulates (TP_GROUP_E8M0).
 //   SUM_F32  codes are widened to bf16 (E8M0 scales go into the exponents) for four
 //            v_mfma_f32_16x16x32_bf16, whose sums are fp32's.
-// 4096 x 8192 x 3584: SUM_FP8 136 us (1.77 PFLOP/s; among others 123 to 129), SUM_F32 212.
-// The matrix cores are busy 35 to 45 % of the time: SUM_FP8 waits for shared memory (8 codes are
-// read for each 16 that a tile of 256 x 256 multiplies), SUM_F32 for the widening and the sums
-// beside its instructions.
+// 4096 x 8192 x 3584: SUM_FP8 119 us (2.0 PFLOP/s; 132 under sustained load), SUM_F32 206.
+// The matrix cores are busy 42 % of the time; the rest is waiting at the barrier and for the
+// columns of each k-tile, and the widening beside SUM_F32's instructions.
 //
 // Block i's row index a is row FM a + i of the wavefront's, block j's column
 // index b is column 16 j + b.  The instruction is issued with the B codes first, which
@@ -25,7 +24,7 @@
 // c ^ (the row's index a or b) % 8: the 8 lanes that are served together read 8
 // different chunks.  A lane takes chunks q and q + 4 (the order of the summed index is free,
 // as long as A and B agree; 2 q and 2 q + 1 met half as many bank conflicts again, and
-// 4096 x 8192 x 3584 took 140 us instead of 136.5).  Row scales lie by step: that of row FM a + i at 16 i + a.
+// 4096 x 8192 x 3584 took 140 us instead of 136.5 then; with none left it is no faster).  Row scales lie by step: that of row FM a + i at 16 i + a.
 #pragma once
 
 #include "fp8g.h"
@@ -470,8 +469,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
 
   // a wavefront's loads, 8 rows each: lane l fills chunk l % 8 of row l / 8.  Each has a
   // buffer of its own, which begins at its first row's group: so the offsets are a
-  // lane's alone (formed at each load they took the vector unit as long as a seventh of the
-  // tile), and rows past the last lie behind its end and read as zeros.
+  // lane's alone (formed at each load, 4096 x 8192 x 3584 took 137 us, so 131), and rows past the last lie behind its end and read as zeros.
   const int lda = (int)a.lda;
   const int rows = (int)min((int64_t)BM, a.M - mt), cols = min(COLS, a.N - at.n0);
   const uint8_t* const from_a = a.A + mt * a.lda;
