@@ -10,8 +10,8 @@
 //   LARGE  tiles of 256 x 256
 //
 // 4096 x 8192 x 3584 (bf16 results): FEW 613 us, SMALL 195, LARGE 119; 512 x 2048 x
-// 4096: 26, 24, 62; 129 x 264 x 7040: 18, 37, 94.  The gated forward, 8192 -> 3584: 64 tokens
-// 38, 64, GROUP 130, 202; 512 tokens 166, 94, 135, 215; 1024 tokens 319, 171, 137, 217; 4096
+// 4096: 26, 22, 59; 129 x 264 x 7040: 18, 37, 94.  The gated forward, 8192 -> 3584: 64 tokens
+// 37, 64, GROUP 130, 193; 512 tokens 166, 87, 135, 194; 1024 tokens 319, 171, 132, 200; 4096
 // tokens LARGE 404.
 #pragma once
 
@@ -30,10 +30,11 @@ inline int64_t g8_over(int64_t n, int64_t d) { return (n + d - 1) / d; }
 // 1024 x 256 x 4096, 256 workgroups of 16 columns: 12 against 16)
 inline bool g8_wide(int64_t M, int64_t N) { return M > 32 && g8_over(M, 64) * g8_over(N, 16) > 320; }
 
-// kt: groups of the summed index, every part's
-inline double g8_few_ns(int64_t M, int64_t N, int64_t kt, double wide_unit, double unit, double turn, double wide_turn) {
+// kt: groups of the summed index, every part's; ends: what a workgroup's start and end take, in
+// groups (2100 x 2056 x 384: FEW 17.6 us, SMALL 10.6)
+inline double g8_few_ns(int64_t M, int64_t N, int64_t kt, int64_t ends, double wide_unit, double unit, double turn, double wide_turn) {
   const bool wide = g8_wide(M, N);
-  const double units = (double)g8_over(M, 64) * g8_over(N, 16) * kt, turns = (double)g8_over(kt, 8);
+  const double units = (double)g8_over(M, 64) * g8_over(N, 16) * (kt + ends), turns = (double)g8_over(kt, 8);
   return std::max(units * (wide ? wide_unit : unit), turns * (wide ? wide_turn : turn));
 }
 
@@ -46,10 +47,11 @@ inline double g8_small_ns(int64_t tiles, int64_t kt, double first, double one, d
 // whether there is a LARGE kernel
 inline G8Form g8_plan_gemm(int64_t M, int64_t N, int64_t kt, bool f32, bool large) {
   if (M <= 64) return G8_FEW;
-  const double few = 4000 + g8_few_ns(M, N, kt, 0.64, 1.06, 2000, 1800);
-  const double small = f32 ? g8_small_ns(g8_over(M, 64) * g8_over(N, 128), kt, 4000, 850, 0, 1350)
-                           : g8_small_ns(g8_over(M, 64) * g8_over(N, 128), kt, 2500, 700, 0, 880);
-  const double whole = 4000 + kt * (f32 ? 3300.0 : 2250.0) * g8_over(g8_over(M, 256) * g8_over(N, 256), 256);
+  const double few = 4000 + g8_few_ns(M, N, kt, 2, 0.64, 1.06, 2000, 1800);
+  const double small = f32 ? g8_small_ns(g8_over(M, 64) * g8_over(N, 128), kt, 4000, 850, 1200, 1350)
+                           : g8_small_ns(g8_over(M, 64) * g8_over(N, 128), kt, 2500, 700, 1000, 880);
+  // (a tile's first loads and its store count: 4096 x 2048 x 512 19 us by LARGE, 14 by SMALL; 8192 x 8192 x 256 62 and 71)
+  const double whole = 3000 + (f32 ? 13000 + kt * 2900.0 : 8000 + kt * 1700.0) * g8_over(g8_over(M, 256) * g8_over(N, 256), 256);
   if (large && whole < std::min(few, small)) return G8_LARGE;
   return few < small ? G8_FEW : G8_SMALL;
 }
@@ -57,7 +59,7 @@ inline G8Form g8_plan_gemm(int64_t M, int64_t N, int64_t kt, bool f32, bool larg
 inline G8Form g8_plan_glu(int64_t N, int64_t F, int64_t kt, bool backward) {
   if (N <= 64) return G8_FEW;
   const int64_t fb = backward ? 128 : 64;  // columns of F a SMALL tile has
-  const double few = backward ? 14000 + g8_few_ns(N, F, kt, 0.95, 1.12, 2000, 2900) : 13000 + g8_few_ns(N, F, kt, 1.45, 1.45, 2300, 2300);
+  const double few = backward ? 14000 + g8_few_ns(N, F, kt, 0, 0.95, 1.12, 2000, 2900) : 13000 + g8_few_ns(N, F, kt, 0, 1.45, 1.45, 2300, 2300);
   const double small = backward ? g8_small_ns(g8_over(N, 64) * g8_over(F, fb), kt, 15000, 870, 16000, 1350)
                                 : g8_small_ns(g8_over(N, 64) * g8_over(F, fb), kt, 13000, 800, 6000, 1200);
   const double group = (backward ? 13500 + kt * 1400.0 : 11000 + kt * 1930.0) * g8_over(g8_over(N, 128) * g8_over(F, 128), 256);

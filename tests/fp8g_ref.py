@@ -106,6 +106,7 @@ def few_bits_error(A, B):
 
 # Sizes at which each of the kernels is taken (tests/test_fp8g_plan.py holds them to that): ragged in every dimension
 GEMM_FORMS = [(300, 1000, 640, "f32", "FEW"), (65, 2056, 1152, "bf16", "FEW"), (1030, 1000, 384, "bf16", "SMALL"),
-              (2000, 2040, 1152, "f32", "SMALL"), (2100, 2056, 384, "bf16", "LARGE"), (4100, 2056, 640, "f32", "LARGE")]
+              (2000, 2040, 1152, "f32", "SMALL"), (2100, 2056, 384, "bf16", "SMALL"), (4100, 2056, 640, "f32", "SMALL"),
+              (4000, 4000, 640, "bf16", "LARGE"), (4000, 3976, 640, "f32", "LARGE")]
 FWD_FORMS = [(300, 2056, 1416, "FEW"), (500, 264, 1416, "SMALL"), (2000, 520, 1032, "GROUP"), (4100, 136, 1416, "LARGE")]
 BWD_FORMS = [(500, 264, 1416, "FEW"), (1000, 1032, 1416, "SMALL"), (2000, 520, 1032, "GROUP"), (6000, 1032, 2056, "LARGE")]
