@@ -22,7 +22,9 @@
  *   TP_GROUP_F32    s = fp32(a / fmax), codes of fp32(x * fp32(fmax / a))
  *   TP_GROUP_E8M0   s = the least power of two with a / s <= fmax, one byte,
  *                   2^(byte - 127): a quarter of the scales' bytes, and
- *                   nothing is rounded in applying it
+ *                   nothing is rounded in applying it.  An operand's bytes have
+ *                   to be among 12 .. 247 with E4M3 codes, 12 .. 240 with E5M2
+ *                   ones, as those made here are, or 255 (NaN)
  * A group with a <= 2^-100 has zero codes and s = 1.  A group that holds a
  * NaN or an infinity has s = NaN (byte 255) and zero codes: what is computed from it
  * is NaN.

@@ -150,8 +150,13 @@ __device__ __forceinline__ bf16x8g_t widen(int lo, int hi, float scale) {
   }
   return __builtin_bit_cast(bf16x8g_t, v);
 }
-// an E8M0 byte as the fp32 whose exponent it is (255: infinity, NaN above)
-__device__ __forceinline__ float e8m0_f32(uint32_t e) { return __uint_as_float(e << 23); }
+// An E8M0 byte as the scale of a widening: half of what it stands for, since a code times it may
+// round to 2^128, which bf16 does not hold (a group whose largest value is FLT_MAX has the code 256 and
+// the scale 2^120).  Halves of the smallest values that a group has, 2^-131 and more, are
+// multiples of bf16's smallest.  So sums are a quarter of the product's: E8M0_SUMS makes them whole,
+// exactly.  (Byte 255: infinity, of which the widening makes NaN.)
+__device__ __forceinline__ float e8m0_half(uint32_t e) { return 0.5f * __uint_as_float(e << 23); }
+constexpr float E8M0_SUMS = 4.0f;
 
 // The gate's activation g sigmoid(z) and its derivative s + g s (1 - s) z':
 // SiLU has z = g, GeLU z = 2 c (g + k g^3), both g (z1 + z3 g^2): no branch.

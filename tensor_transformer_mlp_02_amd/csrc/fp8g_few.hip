@@ -97,7 +97,7 @@ __global__ __launch_bounds__(64 * NW) void gemm_few(G8GemmArgs a) {
       for (int w = 0; w < MATS; ++w)
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          wb[w][c] = widen<FMT_B>(fb[u][w][2 * c], fb[u][w][2 * c + 1], SC == TP_GROUP_F32 ? 1.0f : e8m0_f32(eb[u][w]));
+          wb[w][c] = widen<FMT_B>(fb[u][w][2 * c], fb[u][w][2 * c + 1], SC == TP_GROUP_F32 ? 1.0f : e8m0_half(eb[u][w]));
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         f32x4_t r[MATS];
@@ -105,7 +105,7 @@ __global__ __launch_bounds__(64 * NW) void gemm_few(G8GemmArgs a) {
         for (int w = 0; w < MATS; ++w) r[w] = SC == TP_GROUP_F32 ? (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f} : acc[w][i];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const bf16x8g_t wa = widen<FMT_A>(fa[u][i][2 * c], fa[u][i][2 * c + 1], SC == TP_GROUP_F32 ? 1.0f : e8m0_f32(ea[u][i]));
+          const bf16x8g_t wa = widen<FMT_A>(fa[u][i][2 * c], fa[u][i][2 * c + 1], SC == TP_GROUP_F32 ? 1.0f : e8m0_half(ea[u][i]));
 #pragma unroll
           for (int w = 0; w < MATS; ++w) r[w] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[w][c], wa, r[w], 0, 0, 0);
         }
@@ -136,7 +136,7 @@ __global__ __launch_bounds__(64 * NW) void gemm_few(G8GemmArgs a) {
 #pragma unroll
     for (int c = 1; c < NW; ++c) s += red[c][w][wave][lane];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) v[w][t] = s[t];
+    for (int t = 0; t < 4; ++t) v[w][t] = SC == TP_GROUP_E8M0 ? s[t] * E8M0_SUMS : s[t];
   }
   const int64_t row = m_first + 16 * wave + p;
   const int col = n0 + 4 * q;

@@ -575,7 +575,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
     if constexpr (SUM == SUM_FP8) {
       fb[j] = f;
     } else {
-      const float e = SC == TP_GROUP_F32 ? 1.0f : e8m0_f32(BLDS ? byte_of(r) : (s.eb >> (8 * j)) & 255);
+      const float e = SC == TP_GROUP_F32 ? 1.0f : e8m0_half(BLDS ? byte_of(r) : (s.eb >> (8 * j)) & 255);
 #pragma unroll
       for (int c = 0; c < 4; ++c) wb[j][c] = widen<FMT_B>(f[2 * c], f[2 * c + 1], e);
     }
@@ -653,7 +653,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
         const i32x8_t fa = t.a[i].codes();
         if constexpr (SUM == SUM_F32) {
           float e = 1.0f;
-          if constexpr (SC == TP_GROUP_E8M0) e = e8m0_f32(byte_of(t.a[i]));
+          if constexpr (SC == TP_GROUP_E8M0) e = e8m0_half(byte_of(t.a[i]));
           f32x4_t g[FN];
           static_for<0, 4>([&](auto Cc) {
             constexpr int c = decltype(Cc)::value;
@@ -734,7 +734,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
         // step, when the instructions that make them have ended
         if constexpr (SUM == SUM_F32) {
           float e = 1.0f;
-          if constexpr (SC == TP_GROUP_E8M0) e = e8m0_f32(byte_of(r));
+          if constexpr (SC == TP_GROUP_E8M0) e = e8m0_half(byte_of(r));
           static_for<0, 4>([&](auto Cc) {
             constexpr int c = decltype(Cc)::value;
             const bf16x8g_t wa = widen<FMT_A>(fa[2 * c], fa[2 * c + 1], e);
@@ -788,6 +788,12 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
   }
   __syncthreads();
 
+  if constexpr (SUM == SUM_F32 && SC == TP_GROUP_E8M0) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] *= E8M0_SUMS;
+  }
   uint32_t* red = reinterpret_cast<uint32_t*>(lds);
   if constexpr (EPI == G_GLU_FWD) store_glu_fwd<WM, WN, FN, SC>(a, at, acc, red);
   else if constexpr (EPI == G_GLU_BWD) store_glu_bwd<WM, WN, FN, FMT_A, SC>(a, at, acc, lds);

@@ -1,0 +1,86 @@
+"""GPU: FP8 with group scales at the ends of its ranges, against the formulas in 64 bits: power-of-two scales beside
+fp32's largest and smallest values."""
+import pytest
+import torch
+
+import fp8g_ref as ref
+import tensor_transformer_mlp_02_amd as tp
+from test_gpu_fp8g import (BF16, DEV, G, check_codes, glu_bwd, glu_bwd_reference, glu_fwd,
+                           glu_reference, product, quantized, tokens)
+
+pytestmark = pytest.mark.gpu
+FLT_MAX = 3.4028234663852886e38
+# a few rows; then each of the kernels (fp8g_ref.GEMM_FORMS)
+SIZES = [(8, 264, 256, "f32"), (8, 264, 256, "bf16")] + [s[:4] for s in ref.GEMM_FORMS]
+
+
+# --- power-of-two scales ------------------------------------------------------
+def check_far(got, a, b, out):
+    """As check_product, with what fp32 and bf16 cannot hold below their smallest normal numbers: a product and its
+    addition are each off by at most fp32's smallest step 2^-149, of a quarter of them (the widened scales are
+    halves) 4 times that, 2 K of them; a bf16 result by half its smallest step, 2^-134."""
+    want = a @ b.t()
+    small = 8 * a.shape[1] * 2.0 ** -149
+    if out == "bf16":
+        bound = BF16 * want.abs() * 1.01 + ref.few_bits_error(a, b) + small + 2.0 ** -134
+    else:
+        bound = ref.sum_error(a, b) + small
+    err = (got.double().cpu() - want).abs()
+    assert bool((err <= bound).all()), float((err / bound).max())
+
+
+@pytest.mark.parametrize("M,N,K,out", SIZES)
+@pytest.mark.parametrize("far", ["A", "B"])
+def test_largest_values(M, N, K, out, far):
+    """FLT_MAX has the code 256 and the scale 2^120: 2^128, whose products with small numbers are ordinary ones."""
+    a, b = tokens(1, M, K) * 2.0 ** -70, tokens(2, N, K) * 2.0 ** -70
+    t = a if far == "A" else b
+    t[3, 1], t[5, G + 2], t[-1] = FLT_MAX, -FLT_MAX, FLT_MAX
+    A, sA, a = quantized(a, True)
+    B, sB, b = quantized(b, True)
+    assert float((a if far == "A" else b).abs().max()) == 2.0 ** 128
+    dtype = torch.bfloat16 if out == "bf16" else torch.float32
+    check_far(product(A, sA, B, sB, M, N, K, dtype, scale=1), a, b, out)
+
+
+@pytest.mark.parametrize("M,N,K,out", SIZES)
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_smallest_codes(M, N, K, out, fmt):
+    """The smallest code of the smallest scale that a group has, against a large number: exact."""
+    byte, code = (19, 2.0 ** -9) if fmt == 0 else (12, 2.0 ** -16)
+    A, sA = torch.ones(M, K, dtype=torch.uint8, device=DEV), torch.full((K // G, M), byte, dtype=torch.uint8, device=DEV)
+    B, sB = torch.full((N, K), 0x38, dtype=torch.uint8, device=DEV), torch.full((K // G, N), 127 + 100, dtype=torch.uint8, device=DEV)
+    dtype = torch.bfloat16 if out == "bf16" else torch.float32
+    got = product(A, sA, B, sB, M, N, K, dtype, scale=1, fmt_a=fmt).double()
+    want = torch.tensor(K * code * 2.0 ** (byte - 127 + 100), dtype=torch.float64)
+    assert bool((got == want.to(dtype).double().item()).all()), (float(got[0, 0]), float(want))
+
+
+@pytest.mark.parametrize("N,H,F", [(9, 264, 392)] + [s[:3] for s in ref.FWD_FORMS])
+def test_largest_values_glu_fwd(N, H, F):
+    x = tokens(N, N, H)
+    x[3, 1], x[-1, 2] = FLT_MAX, -FLT_MAX
+    X = quantized(x, True)
+    Wg, Wu = (quantized(tokens(N + k, F, H, 0.3 / H ** 0.5) * 2.0 ** -90, True, True) for k in (1, 2))
+    o = glu_fwd(N, H, F, 0, True, X, Wg, Wu)
+    g, u, h, eg, eu, eh = glu_reference(0, X, Wg, Wu)
+    z = o["Z"].double().cpu()
+    for got, want, e in ((z[:, :F], g, eg), (z[:, F:], u, eu), (o["H"].double().cpu(), h, eh)):
+        assert bool(((got - want).abs() <= BF16 * 1.01 * want.abs() + 2 * e + 1e-38).all())
+    check_codes(o["Hq"], o["sH"], h, eh, True)
+    check_codes(o["Hq_t"], o["sH_t"], h.t().contiguous(), eh.t().contiguous(), True)
+
+
+@pytest.mark.parametrize("N,H,F", [(9, 264, 392)] + [s[:3] for s in ref.BWD_FORMS])
+def test_largest_values_glu_bwd(N, H, F):
+    dy = tokens(N + 1, N, H) * 2.0 ** 60
+    dy[3, 1], dy[-1, 2] = FLT_MAX, -FLT_MAX
+    dY = quantized(dy, True)
+    B = quantized(tokens(N + 2, F, H, 0.05) * 2.0 ** -90, True, True)
+    Z = (tokens(N + 3, N, 2 * F) * 0.5).to(torch.bfloat16).to(DEV)
+    q, s, q_t, s_t = glu_bwd(N, H, F, 0, True, 0, dY, B, Z)
+    dg, du, eg, eu = glu_bwd_reference(0, dY, B, Z, F)
+    pf, gf = ref.up(F) * G, ref.up(F)
+    for k, (d, e) in enumerate(((dg, eg), (du, eu))):
+        check_codes(q[:, k * pf:(k + 1) * pf].contiguous(), s[k * gf:(k + 1) * gf].contiguous(), d, e, True)
+        check_codes(q_t[k], s_t[k], d.t().contiguous(), e.t().contiguous(), True)
