@@ -93,7 +93,9 @@ int tp_fp8g_quantize(const tp_fp8g_quant_desc *desc, const void *x, void *q, voi
                      void *s_t, void *stream);
 
 /* M 0 .. 2^30; N a positive multiple of 8 for bf16, 4 for fp32, at most 2^21; K a
- * positive multiple of 128, at most 2^21, for one part (parts 2: 2^20); parts 1 or 2;
+ * multiple of 128, at most 2^21, for one part (parts 2: 2^20), positive for bf16; of
+ * fp32 results K may be 0 (a weight gradient of no tokens: zeros, or C as it was where
+ * accumulate is 1; nothing of A, B or the scales is read); parts 1 or 2;
  * fmt_a, fmt_b: both E4M3, or one of them E5M2; scale of A and B alike; square: of B;
  * dtype of C; accumulate 1: added into C (fp32 only). */
 typedef struct tp_fp8g_gemm_desc {

@@ -103,7 +103,9 @@ int tp_fp8g_gemm(const tp_fp8g_gemm_desc* desc, const void* A, const void* sA, c
   if (d.accumulate && d.dtype != TP_F32) return fail(TP_ERR_DTYPE, "only fp32 is accumulated into");
   if (d.parts != 1 && d.parts != 2) return fail(TP_ERR_SHAPE, "parts must be 1 or 2");
   if (d.M < 0 || d.M > kMaxDim || d.N <= 0 || d.N > kMaxLd) return fail(TP_ERR_SHAPE, "M or N out of range");
-  if (d.K <= 0 || d.K > kMaxLd / d.parts || d.K % kGroup) return fail(TP_ERR_SHAPE, "K must be a positive multiple of 128 in range");
+  if (d.K < 0 || d.K > kMaxLd / d.parts || d.K % kGroup) return fail(TP_ERR_SHAPE, "K must be a multiple of 128 in range");
+  // (the sum over an empty batch: a weight gradient, which is fp32)
+  if (d.K == 0 && d.dtype != TP_F32) return fail(TP_ERR_SHAPE, "K must be positive for bf16 results");
   const int vec = d.dtype == TP_BF16 ? 8 : 4;
   if (d.N % vec) return fail(TP_ERR_SHAPE, "N must be a multiple of %d for this dtype", vec);
   const bool two = d.parts == 2;
@@ -122,11 +124,12 @@ int tp_fp8g_gemm(const tp_fp8g_gemm_desc* desc, const void* A, const void* sA, c
   a.sA = sA; a.sB = sB; a.sB2 = sB2;
   a.M = d.M; a.lda = d.K * d.parts; a.N = (int)d.N; a.K = (int)d.K; a.parts = d.parts;
   a.C = C; a.out_bf16 = d.dtype == TP_BF16; a.accumulate = d.accumulate;
-  if (d.M == 0) return ok();
+  if (d.M == 0 || (d.K == 0 && d.accumulate)) return ok();
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   hipError_t he = timed(st, [&] {
     const bool f32 = !a.out_bf16, large = d.scale == TP_GROUP_E8M0 || d.square;
-    const G8Form form = g8_plan_gemm(d.M, d.N, d.K / kGroup * d.parts, f32, large);
+    // (of no groups FEW reads nothing and stores zeros)
+    const G8Form form = d.K == 0 ? G8_FEW : g8_plan_gemm(d.M, d.N, d.K / kGroup * d.parts, f32, large);
     if (form == G8_FEW) return g8_gemm_few_launch(d.fmt_a, d.fmt_b, d.scale, d.square, a, st);
     return (f32 ? g8_gemm_f32_launch : g8_gemm_bf16_launch)(form == G8_LARGE, d.fmt_a, d.fmt_b, d.scale, d.square, a, st);
   });
