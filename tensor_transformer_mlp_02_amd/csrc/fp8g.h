@@ -29,6 +29,7 @@ struct G8GemmArgs {
   int64_t M, lda;       // lda: bytes of a row of A
   int N, K, parts;      // K: of one part, a multiple of 128; N: rows of B (F for the gated block)
   int tiles_m, tiles_n;
+  int first;            // workgroup of the launch
   void* C;              // EPI 0: [M,N]
   int out_bf16, accumulate;
   // gated block

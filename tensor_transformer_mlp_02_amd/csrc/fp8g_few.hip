@@ -37,8 +37,9 @@ __global__ __launch_bounds__(64 * NW) void gemm_few(G8GemmArgs a) {
   const int p = lane & 15, q = lane >> 4;
   // (blocks of columns first: those that run together read the same rows of A)
   const int blocks_n = (a.N + 16 * NB - 1) / (16 * NB);
-  const int n0 = (int)(blockIdx.x % blocks_n) * 16 * NB;
-  const int64_t m_first = (int64_t)(blockIdx.x / blocks_n) * FEW_ROWS;
+  const uint32_t block = a.first + blockIdx.x;
+  const int n0 = (int)(block % blocks_n) * 16 * NB;
+  const int64_t m_first = (int64_t)(block / blocks_n) * FEW_ROWS;
   const int64_t M = a.M;
   int n[MATS];
 #pragma unroll
@@ -194,9 +195,13 @@ template <int MT, int NB, int SC, bool SQ, int FMT_A, int FMT_B, int EPI>
 static hipError_t few_run(const G8GemmArgs& a, hipStream_t st) {
   const int64_t blocks = g8_over(a.N, 16 * NB) * g8_over(a.M, FEW_ROWS);
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((gemm_few<MT, NB, FEW_WAVES, SC, SQ, FMT_A, FMT_B, EPI>), dim3((unsigned)blocks), dim3(64 * FEW_WAVES), 0,
-                     st, a);
-  return hipGetLastError();
+  return g8_in_launches(blocks, [&](int64_t first, int64_t count) {
+    G8GemmArgs b = a;
+    b.first = (int)first;
+    hipLaunchKernelGGL((gemm_few<MT, NB, FEW_WAVES, SC, SQ, FMT_A, FMT_B, EPI>), dim3((unsigned)count), dim3(64 * FEW_WAVES), 0,
+                       st, b);
+    return hipGetLastError();
+  });
 }
 template <int SC, bool SQ, int FMT_A, int FMT_B, int EPI>
 static hipError_t few(const G8GemmArgs& a, hipStream_t st) {

@@ -25,6 +25,17 @@ enum G8Form { G8_FEW, G8_SMALL, G8_GROUP, G8_LARGE };
 
 inline int64_t g8_over(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
+// A launch has fewer than 2^32 threads in a dimension: workgroups (of 512 at most) go in
+// launches of 2^22, `launch(first, count)` each, until one fails
+constexpr int64_t G8_LAUNCH = (int64_t)1 << 22;
+template <typename F>
+auto g8_in_launches(int64_t blocks, F launch) {
+  decltype(launch(blocks, blocks)) r{};
+  for (int64_t first = 0; first < blocks && r == decltype(r){}; first += G8_LAUNCH)
+    r = launch(first, std::min(G8_LAUNCH, blocks - first));
+  return r;
+}
+
 // FEW: 32 columns a workgroup halve the reads of A, where there are enough
 // workgroups to hide their longer turns (512 x 1024 x 1024: 7.5 against 6.3 us;
 // 1024 x 256 x 4096, 256 workgroups of 16 columns: 12 against 16)

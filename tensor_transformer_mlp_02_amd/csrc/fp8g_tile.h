@@ -451,7 +451,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
   // tile: XCDs take contiguous runs, rastered in groups of 4 tile rows
-  const int tile = xcd_logical_block(blockIdx.x, gridDim.x);
+  const int tile = a.first + xcd_logical_block(blockIdx.x, gridDim.x);
   const int group = tile / (4 * a.tiles_n), first = 4 * group;
   const int gm = min(4, a.tiles_m - first), li = tile - group * 4 * a.tiles_n;
   const int tm = first + li % gm, tn = li / gm;
@@ -809,10 +809,12 @@ static hipError_t launch(G8GemmArgs& a, hipStream_t st) {
   if (tm * tn > 0x7fffffff) return hipErrorInvalidValue;
   a.tiles_m = (int)tm;
   a.tiles_n = (int)tn;
-  if (tm * tn == 0) return hipSuccess;
-  hipLaunchKernelGGL((gemm<WM, WN, FM, FN, NS, SC, SQ, FMT_A, FMT_B, SUM, EPI>), dim3((unsigned)(tm * tn)),
-                     dim3(64 * WM * WN), 0, st, a);
-  return hipGetLastError();
+  return g8_in_launches(tm * tn, [&](int64_t first, int64_t count) {
+    a.first = (int)first;
+    hipLaunchKernelGGL((gemm<WM, WN, FM, FN, NS, SC, SQ, FMT_A, FMT_B, SUM, EPI>), dim3((unsigned)count), dim3(64 * WM * WN), 0,
+                       st, a);
+    return hipGetLastError();
+  });
 }
 
 }  // namespace g8

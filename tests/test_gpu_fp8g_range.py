@@ -5,7 +5,7 @@ import torch
 
 import fp8g_ref as ref
 import tensor_transformer_mlp_02_amd as tp
-from test_gpu_fp8g import (BF16, DEV, G, check_codes, glu_bwd, glu_bwd_reference, glu_fwd,
+from test_gpu_fp8g import (BF16, DEV, G, check_codes, check_product, glu_bwd, glu_bwd_reference, glu_fwd,
                            glu_reference, product, quantized, tokens)
 
 pytestmark = pytest.mark.gpu
@@ -84,3 +84,34 @@ def test_largest_values_glu_bwd(N, H, F):
     for k, (d, e) in enumerate(((dg, eg), (du, eu))):
         check_codes(q[:, k * pf:(k + 1) * pf].contiguous(), s[k * gf:(k + 1) * gf].contiguous(), d, e, True)
         check_codes(q_t[k], s_t[k], d.t().contiguous(), e.t().contiguous(), True)
+
+
+# --- more workgroups than a launch has ----------------------------------------
+def memory_for(gib):
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < gib << 30:
+        pytest.skip(f"{gib} GiB of device memory")
+
+
+# 2^24 workgroups of 256 threads (a launch ends below 2^32 threads), few rows' kernel; 2^23, the 64 x 128 tiles'
+@pytest.mark.parametrize("M,N", [((1 << 30) - 5, 8), ((1 << 28) + 1000, 136)])
+def test_gemm_of_many_workgroups(M, N):
+    memory_for(200)
+    K, tail = G, 200
+    A = torch.zeros(M, K, dtype=torch.uint8, device=DEV)
+    sA = torch.full((1, M), 127, dtype=torch.uint8, device=DEV)
+    B, sB, b = quantized(tokens(2, N, K), True, True)
+    C = torch.full((M, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    # beside the first and the last row, and beside the borders between launches
+    step = (1 << 22) * 64 // ref.up(N)
+    places = [0, M - tail] + [r - tail // 2 for r in range(step, M, step)]
+    rows = {}
+    for i, r in enumerate(p for p in places if 0 <= p <= M - tail):
+        q, s, rows[r] = quantized(tokens(10 + i, tail, K), True)
+        A[r:r + tail], sA[:, r:r + tail] = q, s
+    product(A, sA, B, sB, M, N, K, torch.bfloat16, C, scale=1, square=1)
+    for r, a in rows.items():
+        check_product(C[r:r + tail], a, b, torch.bfloat16)
+        C[r:r + tail] = 0
+    for part in C.split(1 << 26):
+        assert not bool(part.any())
