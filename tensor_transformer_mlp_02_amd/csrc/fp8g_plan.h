@@ -42,7 +42,8 @@ auto g8_in_launches(int64_t blocks, F launch) {
 inline bool g8_wide(int64_t M, int64_t N) { return M > 32 && g8_over(M, 64) * g8_over(N, 16) > 320; }
 
 // kt: groups of the summed index, every part's; ends: what a workgroup's start and end take, in
-// groups (2100 x 2056 x 384: FEW 17.6 us, SMALL 10.6)
+// groups (2100 x 2056 x 384: FEW 17.6 us, SMALL 10.6); in the gated block that is the fp32 values' way through
+// memory and their codes (8192 tokens, 128 -> 3584: forward FEW 175, LARGE 87; backward 194, 128)
 inline double g8_few_ns(int64_t M, int64_t N, int64_t kt, int64_t ends, double wide_unit, double unit, double turn, double wide_turn) {
   const bool wide = g8_wide(M, N);
   const double units = (double)g8_over(M, 64) * g8_over(N, 16) * (kt + ends), turns = (double)g8_over(kt, 8);
@@ -70,7 +71,7 @@ inline G8Form g8_plan_gemm(int64_t M, int64_t N, int64_t kt, bool f32, bool larg
 inline G8Form g8_plan_glu(int64_t N, int64_t F, int64_t kt, bool backward) {
   if (N <= 64) return G8_FEW;
   const int64_t fb = backward ? 128 : 64;  // columns of F a SMALL tile has
-  const double few = backward ? 14000 + g8_few_ns(N, F, kt, 0, 0.95, 1.12, 2000, 2900) : 13000 + g8_few_ns(N, F, kt, 0, 1.45, 1.45, 2300, 2300);
+  const double few = backward ? 9000 + g8_few_ns(N, F, kt, 4, 0.95, 1.12, 2000, 2900) : 10500 + g8_few_ns(N, F, kt, 4, 1.45, 1.45, 2300, 2300);
   const double small = backward ? g8_small_ns(g8_over(N, 64) * g8_over(F, fb), kt, 15000, 870, 16000, 1350)
                                 : g8_small_ns(g8_over(N, 64) * g8_over(F, fb), kt, 13000, 800, 6000, 1200);
   const double group = (backward ? 13500 + kt * 1400.0 : 11000 + kt * 1930.0) * g8_over(g8_over(N, 128) * g8_over(F, 128), 256);
