@@ -421,6 +421,7 @@ typedef __attribute__((address_space(4))) const uint32_t const_u32_t;
 __device__ __forceinline__ float scalar_f32(const void* p, int64_t i) {
   return ((const_float_t*)(uintptr_t)p)[i];
 }
+// (the aligned word that a byte lies in: of a tensor's first and last bytes it holds up to 3 of others')
 __device__ __forceinline__ uint32_t scalar_byte(const void* p, int64_t i) {
   const uintptr_t at = (uintptr_t)p + (uintptr_t)i;
   return (((const_u32_t*)(at & ~(uintptr_t)3))[0] >> (8 * (at & 3))) & 255u;
