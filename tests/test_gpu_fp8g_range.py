@@ -6,7 +6,6 @@ import torch
 import fp8g_big as big
 import fp8g_ref as ref
 import tensor_transformer_mlp_02_amd as tp
-import tensor_transformer_mlp_02_amd as tp
 from test_gpu_fp8g import (BF16, DEV, G, check_codes, check_product, glu_bwd, glu_bwd_reference, glu_fwd,
                            glu_inputs, glu_reference, product, quantized, tokens)
 
