@@ -36,8 +36,8 @@
  * [P(R)/128, P(C)/128].  Every product here runs over groups: it takes
  * two matrices whose rows are grouped along the summed index, C = A B^T.
  *
- * A training step of a gated block, X [N,H], weights Ag, Au [H,F] (up and
- * gate), B [F,H]: quantize X (codes and those of X^T), the weights in squares
+ * A training step of a gated block, X [N,H], weights Ag, Au [H,F] (gate and
+ * up), B [F,H]: quantize X (codes and those of X^T), the weights in squares
  * (codes and those of the transposes), then
  *   glu_fwd   X, Ag^T, Au^T        -> Z, H (along F and along tokens)
  *   gemm      H, B^T               -> Y [N,H]

@@ -1,5 +1,6 @@
 // The product with fp32 results: codes widened to bf16, fp32 sums.
-// 8192 x 3584 x 4096 with E8M0 scales, added into C: 226 us, of them 34 for C.
+// 8192 x 3584 x 4096 with E8M0 scales, added into C: 227 to 240 us, of them 30 for C; with an fp32 scale for
+// each column, which has the 64 x 128 tile alone, 343.
 #include "fp8g_tile.h"
 
 namespace tpmlp {

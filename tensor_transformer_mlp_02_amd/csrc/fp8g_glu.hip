@@ -1,5 +1,5 @@
 // The gated block's launches: fp32 sums, since its scales and codes are made from the fp32
-// values.  4096 tokens, 8192 -> 3584: forward 404 us (1.19 PFLOP/s), backward 245.
+// values.  4096 tokens, 8192 -> 3584: forward 404 to 420 us (1.17 PFLOP/s), backward 245; with E8M0 scales 390, 237.
 #include "fp8g_tile.h"
 
 namespace tpmlp {

@@ -8,7 +8,7 @@
 //            instruction applies the scales itself and accumulates (TP_GROUP_E8M0).
 //   SUM_F32  codes are widened to bf16 (E8M0 scales go into the exponents) for four
 //            v_mfma_f32_16x16x32_bf16, whose sums are fp32's.
-// 4096 x 8192 x 3584: SUM_FP8 119 us (2.0 PFLOP/s; 132 under sustained load), SUM_F32 206.
+// 4096 x 8192 x 3584: SUM_FP8 119 to 125 us (2.0 PFLOP/s; E8M0 scales 112 to 118), SUM_F32 206 (E8M0 194).
 // The matrix cores are busy 42 % of the time; the rest is waiting at the barrier and for the
 // columns of each k-tile, and the widening beside SUM_F32's instructions.
 //
@@ -23,8 +23,9 @@
 // Shared memory holds rows of 128 codes, the 16-byte chunk c of a row at
 // c ^ (the row's index a or b) % 8: the 8 lanes that are served together read 8
 // different chunks.  A lane takes chunks q and q + 4 (the order of the summed index is free,
-// as long as A and B agree; 2 q and 2 q + 1 met half as many bank conflicts again, and
-// 4096 x 8192 x 3584 took 140 us instead of 136.5 then; with none left it is no faster).  Row scales lie by step: that of row FM a + i at 16 i + a.
+// as long as A and B agree; 2 q and 2 q + 1 meet half as many bank conflicts again, 2.5 % of
+// the time of 4096 x 8192 x 3584; with none left it is no faster).  Row scales lie by step: that
+// of row FM a + i at 16 i + a.
 #pragma once
 
 #include "fp8g.h"
@@ -470,7 +471,8 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
 
   // a wavefront's loads, 8 rows each: lane l fills chunk l % 8 of row l / 8.  Each has a
   // buffer of its own, which begins at its first row's group: so the offsets are a
-  // lane's alone (formed at each load, 4096 x 8192 x 3584 took 137 us, so 131), and rows past the last lie behind its end and read as zeros.
+  // lane's alone (formed at each load they cost 4 % of 4096 x 8192 x 3584), and rows past the last
+  // lie behind its end and read as zeros.
   const int lda = (int)a.lda;
   const int rows = (int)min((int64_t)BM, a.M - mt), cols = min(COLS, a.N - at.n0);
   const uint8_t* const from_a = a.A + mt * a.lda;
@@ -761,8 +763,8 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 && FM * FN == 32 || FM =
             }
           });
         }
-        // (the matrix cores are at work meanwhile: before the step's products the gated forward
-        // took 417 us, so 406; the weight gradient 234, so 227)
+        // (the matrix cores are at work meanwhile: before the step's products these loads cost the
+        // gated forward and the weight gradient 3 %)
         if constexpr (i == FM - 1) {
           __builtin_amdgcn_sched_barrier(0);
           if (kt + NS < kt_all) load_tile(kt + NS, buf);
